@@ -487,6 +487,159 @@ int32_t skv_decode_noalloc(const skv_layout *lay, const void *bitstream, uint64_
                            const uint64_t *offsets, const void *mu, const float *sigma,
                            const uint64_t *counts, void *kv_out, int32_t *status, void *stream);
 
+/*
+ * Serving from decoded pages. A decoded cache is used one step at a time: a
+ * predictor drafts a tree of tokens for each request, the model verifies the
+ * whole tree in one pass over the cache, and the accepted path stays in it.
+ * (The source pages name offload and long context as uses of the coder; they
+ * describe none of the calls below.) Three calls share one description of a
+ * paged cache:
+ *   skv_page_map        which page and slot each new token gets, on the GPU
+ *   skv_cache_append    the new K and V rows go to those slots
+ *   skv_tree_attention  the new tokens' queries read the pages
+ *
+ * skv_paged: a K and a V pool of n_pages pages, both with the same strides.
+ * The value of token t of a page, KV head h, channel d is at
+ *     pool[page * page_stride + t * token_stride + h * head_stride + d]
+ * (strides in codes). Pages as skv_decode_chunks writes them (page_tokens =
+ * tokens_per_chunk, canonical order) have token_stride = n_heads * head_dim,
+ * head_stride = head_dim, page_stride = page_tokens * token_stride; a pool
+ * of K and V pages in turn has twice that page_stride, and so on.
+ *  dtype        SKV_BF16, or SKV_E4M3: stored codes of value / scale
+ *  n_heads      KV heads; head_dim a multiple of 16, at most 256
+ *  page_tokens  any length from 1 to 2^20
+ *  k_pages, v_pages, and the three strides: multiples of 16 bytes; the pages
+ *               must not overlap
+ *  k_scale, v_scale  device float32[n_heads], the scale of each head of an e4m3
+ *               cache (value = code * scale), both given or both NULL (1);
+ *               NULL for bf16
+ *  block_table  device int32 [n_requests][table_stride], row r holding the pages
+ *               of request r in order of position; max_pages entries of a row
+ *               may be used (used by skv_tree_attention only)
+ */
+typedef struct skv_paged {
+    uint32_t version;        /* SKV_FORMAT_VERSION */
+    uint32_t dtype;
+    uint32_t n_heads;
+    uint32_t head_dim;
+    uint32_t page_tokens;
+    uint32_t n_pages;
+    void *k_pages;
+    void *v_pages;
+    uint64_t page_stride;
+    uint64_t token_stride;
+    uint64_t head_stride;
+    const float *k_scale;
+    const float *v_scale;
+    const int32_t *block_table;
+    uint64_t table_stride;
+    uint32_t n_requests;
+    uint32_t max_pages;
+} skv_paged;
+
+/* Host-side validation of a paged cache: SKV_OK or SKV_ERR_INVALID_ARG. */
+int32_t skv_paged_check(const skv_paged *cache);
+
+/*
+ * Block tables and slot maps from request lengths, in one launch that reads no
+ * length on the host. Request r holds n_pages_in[r] pages (the first entries
+ * of its block-table row) and ctx_len[r] tokens, and new_len[r] tokens are
+ * about to be added at positions ctx_len[r], ctx_len[r] + 1, ...; ctx_len[r]
+ * < 0 marks a request that has ended (new_len[r] must be 0).
+ *   want[r] = ceil((ctx_len[r] + new_len[r]) / page_tokens), 0 if ended
+ *   the free list is a ring: entry i of the list is free_pages[(head + i) mod
+ *   free_capacity], head = free_in[0], 0 <= i < free_in[1]. Every request with
+ *   want[r] > n_pages_in[r] takes want[r] - n_pages_in[r] pages off its front into
+ *   its row's next entries, and the pages of ended requests go behind its end
+ *   (usable from the next call on), both in order of request, then of page
+ *   n_pages_out[r] = max(want[r], n_pages_in[r]) (0 if ended)
+ *   cu_new[r] = new_len[0] + ... + new_len[r - 1], r = 0 .. n_requests
+ *   slots[cu_new[r] + i] = page * page_tokens + offset of position ctx_len[r] + i;
+ *   slots past cu_new[n_requests] are -1
+ *   free_out = the ring's new head and count
+ * Entries of block_table and free_pages not named above keep their values, and
+ * entries past a request's page count are never read. The counts are written
+ * to other arrays than they are read from (swap the two each step).
+ *  block_table  device int32 [n_requests][table_stride], max_pages usable per row
+ *  pool_pages   pages of the pool: every page number must be below
+ *  free_pages   device int32[free_capacity]
+ *  slots        device int64[slot_capacity], 8-byte aligned
+ * Device errors, with n_pages_out = n_pages_in, free_out = free_in, cu_new 0,
+ * every slot -1 and nothing else written:
+ *   INVALID_ARG  a new_len < 0, tokens of an ended request, a page count outside
+ *                [0, max_pages] or short of ctx_len, a length above 2^31 - 1, a ring
+ *                head outside [0, free_capacity) or count outside [0, free_capacity]
+ *   CAPACITY     not enough free pages, more than max_pages pages in a row, more
+ *                new tokens than slots or than 2^31 - 1, a ring too short for the
+ *                pages of ended requests
+ * CORRUPT: a page number outside [0, pool_pages) among the pages that are moved
+ * or that new tokens fall into; it is moved as it is, and the slots of such
+ * tokens are -1.
+ */
+int32_t skv_page_map(uint32_t page_tokens, uint32_t pool_pages, uint32_t n_requests, const int32_t *ctx_len,
+                     const int32_t *new_len, int32_t *block_table, uint64_t table_stride, uint32_t max_pages,
+                     const int32_t *n_pages_in, int32_t *n_pages_out, int32_t *free_pages,
+                     uint32_t free_capacity, const int32_t *free_in, int32_t *free_out, int32_t *cu_new,
+                     int64_t *slots, uint64_t slot_capacity, int32_t *status, void *stream);
+
+/*
+ * Write new K and V rows into the pages: for i < n with slots[i] >= 0, row
+ * rows[i] (i if rows is NULL) of k and v goes to token slots[i] % page_tokens
+ * of page slots[i] / page_tokens. With rows, the accepted path of a verified
+ * tree is written again, in order, over the tree.
+ *  k, v      device bf16 [n_src][n_heads][head_dim], head_dim contiguous, 16-byte
+ *            aligned; row_stride and row_head_stride in elements, multiples of 8,
+ *            the same for both (slices of a fused projection are fine)
+ *  slots     device int64[n], distinct where >= 0; rows: device int32[n] or NULL
+ * A bf16 cache gets the bits of the rows. An e4m3 cache gets the code nearest to
+ * x / scale[head] (the real quotient, ties to even), saturated at +-448; NaN
+ * gives NaN.
+ * Device errors: INVALID_ARG for a slot beyond the pool (such rows are skipped)
+ * or a row outside [0, n_src).
+ */
+int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, uint64_t row_stride,
+                         uint64_t row_head_stride, uint32_t n_src, const int32_t *rows,
+                         const int64_t *slots, uint32_t n, int32_t *status, void *stream);
+
+/*
+ * Attention of each request's new tokens (a tree of drafted tokens, or the one
+ * next token) over its pages, which already hold the new tokens' K and V.
+ * Request r has the query rows cu_new[r] .. cu_new[r + 1) and kv positions
+ * 0 .. ctx_len[r] + n_r (n_r its rows). Node i of the tree sees every position
+ * below ctx_len[r], and position ctx_len[r] + j iff bit j % 64 of
+ * mask[row][j / 64] is set (for a tree: j is i or an ancestor of i), or iff j
+ * <= i when mask is NULL. Query head g reads KV head g / (n_q_heads / n_heads):
+ *     out[row][g] = sum_p w_p V_p / sum_p w_p,  w_p = exp(scale * q . K_p)
+ * over the positions that the row sees; a row with no position (or none with a
+ * score above -infinity) gives 0. K or V of a position has no effect on rows
+ * that do not see it, whatever it holds.
+ *  q          device bf16, head_dim contiguous, 16-byte aligned; q_row_stride and
+ *             q_head_stride in elements, multiples of 8
+ *  n_rows     rows of q and out; rows outside every request are left alone
+ *  ctx_len    device int32[n_requests]; < 0 with no rows: an idle request
+ *  cu_new     device int32[n_requests + 1]
+ *  mask       device uint64 [n_rows][mask_words], 8-byte aligned, or NULL (mask_words 0)
+ *  max_nodes  about the largest n_r: chooses the kernel and has no effect on the result's
+ *             definition
+ *  out        device bf16 [n_rows][n_q_heads][head_dim], contiguous, 16-byte aligned
+ *  lse        device float32 [n_rows][n_q_heads] or NULL: log sum_p w_p (-infinity if no
+ *             position)
+ *  workspace  device, 256-byte aligned, ws_bytes >= skv_tree_attention_workspace_bytes;
+ *             contents need not be kept or cleared
+ * Sums and maxima are binary32; the weights w_p enter the second product in
+ * bf16 (bf16 cache) or fp16 (e4m3 cache). Repeated calls give the same bits.
+ * Device errors: INVALID_ARG (cu_new descends or passes n_rows, ctx_len < 0 with
+ * rows, more positions than max_pages hold, n_r > 64 mask_words: such a
+ * request's rows are left alone), CORRUPT (a page number outside the pool: that
+ * request's outputs are unspecified).
+ */
+int32_t skv_tree_attention_workspace_bytes(const skv_paged *cache, uint32_t n_q_heads, uint64_t *bytes);
+int32_t skv_tree_attention(const skv_paged *cache, const void *q, uint64_t q_row_stride,
+                           uint64_t q_head_stride, uint32_t n_q_heads, uint32_t n_rows,
+                           const int32_t *ctx_len, const int32_t *cu_new, const uint64_t *mask,
+                           uint32_t mask_words, uint32_t max_nodes, float scale, void *out, float *lse,
+                           int32_t *status, void *workspace, uint64_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

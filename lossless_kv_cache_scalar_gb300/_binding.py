@@ -27,9 +27,19 @@ class skv_layout(C.Structure):
                 ("sigma_block_tokens", C.c_uint32)]
 
 
+class skv_paged(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("dtype", C.c_uint32), ("n_heads", C.c_uint32),
+                ("head_dim", C.c_uint32), ("page_tokens", C.c_uint32), ("n_pages", C.c_uint32),
+                ("k_pages", C.c_void_p), ("v_pages", C.c_void_p), ("page_stride", C.c_uint64),
+                ("token_stride", C.c_uint64), ("head_stride", C.c_uint64), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("block_table", C.c_void_p), ("table_stride", C.c_uint64),
+                ("n_requests", C.c_uint32), ("max_pages", C.c_uint32)]
+
+
 # name -> (restype, argtypes); the exported symbols of include/skv.h
 _u32, _u64, _i32, _vp = C.c_uint32, C.c_uint64, C.c_int32, C.c_void_p
 _LP = C.POINTER(skv_layout)
+_PP = C.POINTER(skv_paged)
 SIGNATURES = {
     "skv_version": (_u32, []),
     "skv_status_string": (C.c_char_p, [_i32]),
@@ -60,6 +70,13 @@ SIGNATURES = {
                                      _vp]),
     "skv_offload_plan": (_i32, [_vp, _u64, _u64, _u64, _vp, _u64, C.POINTER(_u64)]),
     "skv_calibrate_sigma": (_i32, [_LP, _vp, _vp, _vp, _u64, _vp, _vp]),
+    "skv_paged_check": (_i32, [_PP]),
+    "skv_page_map": (_i32, [_u32, _u32, _u32, _vp, _vp, _vp, _u64, _u32, _vp, _vp, _vp, _u32, _vp, _vp, _vp, _vp, _u64,
+                            _vp, _vp]),
+    "skv_cache_append": (_i32, [_PP, _vp, _vp, _u64, _u64, _u32, _vp, _vp, _u32, _vp, _vp]),
+    "skv_tree_attention_workspace_bytes": (_i32, [_PP, _u32, C.POINTER(_u64)]),
+    "skv_tree_attention": (_i32, [_PP, _vp, _u64, _u64, _u32, _u32, _vp, _vp, _vp, _u32, _u32, C.c_float, _vp, _vp,
+                                  _vp, _vp, _u64, _vp]),
 }
 
 _lib = None

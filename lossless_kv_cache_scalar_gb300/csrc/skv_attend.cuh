@@ -1,0 +1,213 @@
+// skv_attend.cuh -- what the tree-attention kernels share: the split of the work
+// over CTAs, the workspace they leave their parts in, and small arithmetic.
+//
+// Work split. The work of a call is a list of units: for every request with
+// rows, for every KV head, for every tile of query rows (R rows: node-major, a
+// node's query heads of that KV head together), for every run of UT positions,
+// one unit. A fixed grid takes equal, consecutive shares of the list (CTA c the
+// units [c U / G, (c + 1) U / G)), so ragged lengths cost no balance and the host
+// needs no length. The units of one (request, head, row tile) are an item; a
+// CTA that holds a whole item writes its output, and one that holds a part
+// leaves maximum, sum and unnormalised output in the workspace, for the joining
+// kernel. A part that starts at the CTA's first unit goes to place 0 of the
+// CTA, any other (it then ends at the CTA's last unit) to place 1.
+#pragma once
+
+#include "skv_paged.h"
+
+namespace skv {
+
+// Grids: persistent CTAs, two per SM of 152 for the small-row kernel, one for
+// the tcgen05 one. Constants, so that the workspace's size depends on no device.
+constexpr uint32_t kCtasSmall = 304, kCtasLarge = 152;
+
+// An item that starts in a CTA and goes on in the next ones.
+struct Desc {
+    uint32_t valid, request, head, rt;
+    uint32_t place, units;
+    uint64_t unit0;
+};
+
+struct Plan {
+    uint64_t total;     // U
+    uint64_t active;    // CTAs with work
+};
+
+struct AttendWs {
+    Plan *plan;
+    int32_t *errs;      // one per CTA
+    Desc *desc;         // one per CTA
+    float *parts;       // [CTA][2] of part_floats: m[R], l[R], o[R][DP]
+};
+
+__host__ __device__ inline uint64_t part_floats(uint32_t R, uint32_t DP) { return (uint64_t)R * (2u + DP); }
+
+constexpr uint64_t kWsHead = 256u + 1536u + 304u * sizeof(Desc);     // plan, errs, descs
+static_assert(sizeof(Desc) == 32 && kCtasSmall * 4u <= 1536u && kCtasLarge <= kCtasSmall && kWsHead % 256u == 0,
+              "workspace head");
+
+inline AttendWs attend_ws(void *base) {
+    uint8_t *p = static_cast<uint8_t *>(base);
+    return AttendWs{reinterpret_cast<Plan *>(p), reinterpret_cast<int32_t *>(p + 256), reinterpret_cast<Desc *>(p + 1792),
+                    reinterpret_cast<float *>(p + kWsHead)};
+}
+
+// Request r's rows and lengths; n = 0 for one without rows, or in error.
+struct ReqOf {
+    uint32_t row0, n, ctx, len;
+    int32_t err;
+};
+
+__device__ __forceinline__ ReqOf request_of(const AttendArgs &a, uint32_t r) {
+    ReqOf o{0u, 0u, 0u, 0u, SKV_OK};
+    const int32_t c = a.ctx_len[r], lo = a.cu_new[r], hi = a.cu_new[r + 1];
+    if (lo < 0 || hi < lo || (uint32_t)hi > a.n_rows) o.err = SKV_ERR_INVALID_ARG;
+    else if (hi > lo) {
+        const int64_t len = (int64_t)c + (hi - lo);
+        if (c < 0 || len > (int64_t)a.c.max_pages * a.c.page.d || len > INT32_MAX ||
+            (a.mask && (uint64_t)(hi - lo) > 64ull * a.mask_words))
+            o.err = SKV_ERR_INVALID_ARG;
+        else o = ReqOf{(uint32_t)lo, (uint32_t)(hi - lo), (uint32_t)c, (uint32_t)len, SKV_OK};
+    }
+    return o;
+}
+
+// Whether node sees position p of its request.
+__device__ __forceinline__ bool sees(const AttendArgs &a, const ReqOf &q, uint32_t node, uint32_t p) {
+    if (p < q.ctx) return true;
+    const uint32_t j = p - q.ctx;
+    if (!a.mask) return j <= node;
+    return (__ldg(a.mask + (uint64_t)(q.row0 + node) * a.mask_words + (j >> 6)) >> (j & 63u)) & 1u;
+}
+
+// Byte offset of position p of request r, head h, in either pool; ~0 for a page
+// number outside the pool.
+__device__ __forceinline__ uint64_t place_of(const PagedView &c, uint32_t r, uint32_t h, uint32_t p) {
+    const uint32_t j = div_by(p, c.page);
+    const uint32_t page = (uint32_t)__ldg(c.table + (uint64_t)r * c.table_stride + j);
+    if (page >= c.n_pages) return ~0ull;
+    return (uint64_t)page * c.page_stride + (uint64_t)(p - j * c.page.d) * c.token_stride + h * c.head_stride;
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) {
+    const uint32_t b = __float_as_uint(x);
+    if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((b >> 16) | 0x40u);
+    return (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+}
+
+__device__ __forceinline__ float e4m3_float(uint32_t b) {
+    const uint32_t e = (b >> 3) & 15u, m = b & 7u;
+    float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : (float)m * 0.001953125f;
+    if ((b & 127u) == 127u) v = __uint_as_float(0x7FC00000u);
+    return (b & 128u) ? -v : v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The weight of a part with maximum m against the whole's M (0 for a part with nothing).
+__device__ __forceinline__ float part_weight(float m, float M) { return m == -INFINITY ? 0.0f : ex2(m - M); }
+
+// A V value that is not finite, at a position that some rows do not see, would
+// reach them through the matrix product as 0 * NaN. The kernels put 0 in
+// its place there, and each row that does see it gets it added at the end: its
+// weight is positive, so the sum is that infinity or NaN whatever its size.
+// This returns what to add to channel d of the row of `node`, from the positions [p0, p1).
+__device__ __forceinline__ float not_finite_sum(const AttendArgs &a, const ReqOf &q, uint32_t r, uint32_t h,
+                                                uint32_t node, uint32_t d, uint32_t p0, uint32_t p1) {
+    float s = 0.0f;
+    for (uint32_t p = max(p0, q.ctx); p < p1; ++p) {
+        if (!sees(a, q, node, p)) continue;
+        const uint64_t at = place_of(a.c, r, h, p);
+        if (at == ~0ull) continue;
+        const float v = a.c.e4m3 ? e4m3_float(a.c.v[at + d])
+                                 : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.c.v + at)[d] << 16);
+        if (!(fabsf(v) < INFINITY)) s += v;
+    }
+    return s;
+}
+
+// Where CTA c's share of the list starts: the request, and the unit within it.
+struct Share {
+    uint64_t u0, u1;      // units [u0, u1)
+    uint32_t r;
+    uint64_t off;
+};
+
+// Units of request r, split into row tiles of R rows and runs of UT positions.
+__device__ __forceinline__ uint64_t units_of(const AttendArgs &a, const ReqOf &q, uint32_t R, uint32_t UT) {
+    if (q.n == 0) return 0;
+    return (uint64_t)((q.len + UT - 1) / UT) * a.c.n_heads * (((uint64_t)q.n * a.group + R - 1) / R);
+}
+
+// Every thread of the block calls this; sm is scratch of blockDim / 32 + 4 words of 8 bytes.
+template <uint32_t THREADS>
+__device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t UT,
+                                          unsigned long long *sm) {
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    constexpr uint32_t W = THREADS / 32u;
+    unsigned long long mine = 0, first = 0;
+    int32_t err = SKV_OK;
+    for (uint32_t r = tid; r < a.c.n_requests; r += THREADS) {
+        const ReqOf q = request_of(a, r);
+        if (q.err) err = q.err;
+        const uint64_t u = units_of(a, q, R, UT);
+        if (r == tid) first = u;
+        mine += u;
+    }
+    unsigned long long t = mine;
+#pragma unroll
+    for (uint32_t d = 16; d; d >>= 1) t += __shfl_xor_sync(~0u, t, d);
+    if (lane == 0) sm[warp] = t;
+    err = __syncthreads_or(err) ? SKV_ERR_INVALID_ARG : SKV_OK;
+    unsigned long long U = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < W; ++w) U += sm[w];
+    const uint64_t active = U < gridDim.x ? U : gridDim.x;
+    Share s{0, 0, 0, 0};
+    if (tid == 0) {
+        ws.errs[blockIdx.x] = err;
+        ws.desc[blockIdx.x].valid = 0u;
+        if (blockIdx.x == 0) *ws.plan = Plan{U, active};
+    }
+    if (blockIdx.x >= active) return s;
+    s.u0 = (uint64_t)blockIdx.x * U / active;
+    s.u1 = (uint64_t)(blockIdx.x + 1) * U / active;
+    unsigned long long carry = 0;
+    for (uint32_t base = 0; base < a.c.n_requests; base += THREADS) {
+        const uint32_t r = base + tid;
+        unsigned long long u = base == 0 ? first : 0ull;
+        if (base && r < a.c.n_requests) u = units_of(a, request_of(a, r), R, UT);
+        unsigned long long x = u;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d <<= 1) {
+            const unsigned long long y = __shfl_up_sync(~0u, x, d);
+            if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sm[warp] = x;
+        __syncthreads();
+        unsigned long long before = carry, whole = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < W; ++w) {
+            if (w < warp) before += sm[w];
+            whole += sm[w];
+        }
+        x += before - u;
+        if (x <= s.u0 && s.u0 < x + u) {
+            sm[W] = r;
+            sm[W + 1] = s.u0 - x;
+        }
+        carry += whole;
+        if (carry > s.u0) break;            // the same for every thread
+    }
+    __syncthreads();
+    s.r = (uint32_t)sm[W];
+    s.off = sm[W + 1];
+    return s;
+}
+
+}  // namespace skv

@@ -1,0 +1,215 @@
+"""Serving from decoded pages: block tables, row writes and tree attention over
+a paged KV cache (skv_page_map, skv_cache_append, skv_tree_attention).
+
+As in api.py, PyTorch only provides device memory and streams. The `_into`
+calls enqueue on the current (or given) stream and return without
+synchronising; check_status() waits and raises what the device reported. The
+calls of one object share its status word and workspace, so they must not run
+at once on different streams.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+
+import torch
+
+from . import _binding as B
+from .api import _check_dev, _ptr, _stream_handle
+
+
+def _check_i32(what: str, numel: int, *ts):
+    for t in ts:
+        if not t.is_cuda or t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous int32 CUDA tensors of {numel} entries")
+
+
+def _table_rows(t):
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) \
+            or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError("block_table must be an int32 CUDA tensor [n_requests][max_pages] with whole rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class _Status:
+    def _new_status(self, device):
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def check_status(self, where: str, stream=None):
+        (stream or torch.cuda.current_stream()).synchronize()
+        st = int(self.status.item())
+        if st:
+            raise B.SKVError(where, st)
+
+
+class PageTable(_Status):
+    """A block table [n_requests][max_pages] (int32) over a pool of `pool_pages`
+    pages of `page_tokens` tokens, kept on the GPU (skv_page_map)."""
+
+    def __init__(self, block_table: torch.Tensor, page_tokens: int, pool_pages: int):
+        self._stride = _table_rows(block_table)
+        self.block_table = block_table
+        self.page_tokens, self.pool_pages = int(page_tokens), int(pool_pages)
+        self.n_requests, self.max_pages = block_table.shape
+        self._new_status(block_table.device)
+
+    def map_into(self, ctx_len, new_len, n_pages, free_pages, free_state, cu_new, slots, n_pages_out,
+                 free_state_out, stream=None):
+        """Enqueue skv_page_map: pages for each request's new tokens off the ring
+        (free_pages, free_state = [head, count]), their table entries, cu_new and the
+        slot map; a request of ctx_len < 0 gives its pages back. The new page counts and
+        ring state go to n_pages_out and free_state_out (other tensors than the inputs)."""
+        n = self.n_requests
+        _check_i32("ctx_len, new_len, n_pages and n_pages_out", n, ctx_len, new_len, n_pages, n_pages_out)
+        _check_i32("free_state and free_state_out", 2, free_state, free_state_out)
+        _check_i32("cu_new", n + 1, cu_new)
+        _check_dev(free_pages, "free_pages", torch.int32)
+        _check_dev(slots, "slots", torch.int64)
+        rc = B.lib().skv_page_map(self.page_tokens, self.pool_pages, n, ctx_len.data_ptr(), new_len.data_ptr(),
+                                  self.block_table.data_ptr(), self._stride, self.max_pages, n_pages.data_ptr(),
+                                  n_pages_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+                                  free_state.data_ptr(), free_state_out.data_ptr(), cu_new.data_ptr(),
+                                  slots.data_ptr(), slots.numel(), self.status.data_ptr(), _stream_handle(stream))
+        B.check("skv_page_map", rc)
+
+
+class PagePool(PageTable):
+    """A PageTable with its page counts and its ring of free pages: all pages free
+    at first, counts swapped by every step."""
+
+    def __init__(self, n_requests: int, max_pages: int, page_tokens: int, pool_pages: int, device="cuda"):
+        super().__init__(torch.full((n_requests, max_pages), -1, dtype=torch.int32, device=device), page_tokens,
+                         pool_pages)
+        self.n_pages = torch.zeros(n_requests, dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(pool_pages, dtype=torch.int32, device=device)
+        self.free_state = torch.tensor([0, pool_pages], dtype=torch.int32, device=device)
+        self._next = (torch.empty_like(self.n_pages), torch.empty_like(self.free_state))
+
+    def step(self, ctx_len, new_len, max_new: int, check: bool = True, stream=None):
+        """Map one step's new tokens (max_new: room for so many slots). Returns
+        (cu_new, slots), slots past the step's tokens -1."""
+        dev = self.block_table.device
+        cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty(max_new, dtype=torch.int64, device=dev)
+        self.map_into(ctx_len, new_len, self.n_pages, self.free_pages, self.free_state, cu, slots, *self._next,
+                      stream=stream)
+        now = (self.n_pages, self.free_state)
+        self.n_pages, self.free_state = self._next
+        self._next = now
+        if check:
+            self.check_status("skv_page_map", stream)
+        return cu, slots
+
+
+class PagedKV(_Status):
+    """K and V pools [n_pages][page_tokens][n_heads][head_dim] of codes (2-byte: bf16,
+    1-byte: e4m3), of any strides that are multiples of 16 bytes and the same for both
+    (pages as decode_chunks returns them, viewed in four dimensions, are such pools).
+
+    block_table: int32 [n_requests][max_pages], needed by attend; k_scale, v_scale:
+    float32 [n_heads] of an e4m3 cache. q_heads > 0 makes the workspace of attend."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor | None = None,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, q_heads: int = 0):
+        for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not t.is_cuda or t.dim() != 4 or t.element_size() not in (1, 2) or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise ValueError(f"{what} must be a CUDA tensor [n_pages][page_tokens][n_heads][head_dim] of codes")
+        if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
+                or k_pages.element_size() != v_pages.element_size() or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must have the same shape, strides, code size and device")
+        n_pages, page_tokens, n_heads, head_dim = k_pages.shape
+        for s in (k_scale, v_scale):
+            if s is not None:
+                _check_dev(s, "k_scale and v_scale", torch.float32, numel=n_heads)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.block_table, self.n_heads, self.head_dim = block_table, n_heads, head_dim
+        stride, n_requests, max_pages = 0, 0, 0
+        if block_table is not None:
+            stride = _table_rows(block_table)
+            n_requests, max_pages = block_table.shape
+        self.n_requests = n_requests
+        ps, ts, hs = k_pages.stride()[:3]
+        self._c = B.skv_paged(B.SKV_FORMAT_VERSION, B.SKV_BF16 if k_pages.element_size() == 2 else B.SKV_E4M3,
+                              n_heads, head_dim, page_tokens, n_pages, k_pages.data_ptr(), v_pages.data_ptr(),
+                              ps if n_pages > 1 else 0, ts if page_tokens > 1 else 0, hs if n_heads > 1 else 0,
+                              _ptr(k_scale), _ptr(v_scale), _ptr(block_table), stride, n_requests, max_pages)
+        self._ref = C.byref(self._c)
+        B.check("skv_paged_check", B.lib().skv_paged_check(self._ref))
+        self._new_status(k_pages.device)
+        self.q_heads, self.workspace = 0, None
+        if q_heads:
+            self._make_workspace(q_heads)
+
+    def _make_workspace(self, q_heads: int):
+        v = C.c_uint64()
+        B.check("skv_tree_attention_workspace_bytes",
+                B.lib().skv_tree_attention_workspace_bytes(self._ref, q_heads, C.byref(v)))
+        self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
+        self.q_heads = q_heads
+
+    def append_into(self, k, v, slots, rows=None, stream=None):
+        """Enqueue skv_cache_append: rows of k and v (bf16 [n_src][n_heads][head_dim], any
+        row and head strides that are multiples of 8) into the slots (int64, -1 skips)."""
+        for t, what in ((k, "k"), (v, "v")):
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != self.n_heads \
+                    or t.shape[2] != self.head_dim or t.stride(2) != 1:
+                raise ValueError(f"{what} must be a bf16 CUDA tensor [n_src][{self.n_heads}][{self.head_dim}]")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must have the same shape and strides")
+        _check_dev(slots, "slots", torch.int64)
+        if rows is not None:
+            _check_dev(rows, "rows", torch.int32, numel=slots.numel())
+        rc = B.lib().skv_cache_append(self._ref, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.shape[0],
+                                      None if rows is None else rows.data_ptr(), slots.data_ptr(), slots.numel(),
+                                      self.status.data_ptr(), _stream_handle(stream))
+        B.check("skv_cache_append", rc)
+
+    def append(self, k, v, slots, rows=None, stream=None):
+        """append_into, waited for and checked."""
+        self.append_into(k, v, slots, rows, stream)
+        self.check_status("skv_cache_append", stream)
+
+    def attend_into(self, q, ctx_len, cu_new, out, mask=None, max_nodes: int | None = None,
+                    scale: float | None = None, lse=None, stream=None):
+        """Enqueue skv_tree_attention. q: bf16 [n_rows][q_heads][head_dim] (row and head
+        strides multiples of 8); out: the same shape, contiguous; mask: int64 [n_rows][words]
+        of visibility bits among a request's new tokens, None: each sees the ones before it;
+        max_nodes: about the most new tokens of a request (default n_rows); scale defaults
+        to 1 / sqrt(head_dim); lse: float32 [n_rows][q_heads] or None."""
+        if self.block_table is None:
+            raise ValueError("attend needs a block_table")
+        if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != self.head_dim \
+                or q.stride(2) != 1 or q.shape[1] == 0 or q.shape[1] % self.n_heads:
+            raise ValueError(f"q must be a bf16 CUDA tensor [n_rows][a multiple of {self.n_heads}][{self.head_dim}]")
+        n, heads = q.shape[0], q.shape[1]
+        if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 CUDA tensor of q's shape")
+        _check_i32("ctx_len", self.n_requests, ctx_len)
+        _check_i32("cu_new", self.n_requests + 1, cu_new)
+        words = 0
+        if mask is not None:
+            if not mask.is_cuda or mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] != n \
+                    or not mask.is_contiguous() or mask.shape[1] == 0:
+                raise ValueError("mask must be a contiguous int64 CUDA tensor [n_rows][words]")
+            words = mask.shape[1]
+        if lse is not None:
+            _check_dev(lse, "lse", torch.float32, numel=n * heads)
+        if heads != self.q_heads:
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("give PagedKV its q_heads before a capture")
+            self._make_workspace(heads)
+        rc = B.lib().skv_tree_attention(
+            self._ref, q.data_ptr(), q.stride(0), q.stride(1), heads, n, ctx_len.data_ptr(), cu_new.data_ptr(),
+            None if mask is None else mask.data_ptr(), words, n if max_nodes is None else max_nodes,
+            1.0 / math.sqrt(self.head_dim) if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), self.status.data_ptr(), self.workspace.data_ptr(),
+            self.workspace.numel(), _stream_handle(stream))
+        B.check("skv_tree_attention", rc)
+
+    def attend(self, q, ctx_len, cu_new, mask=None, max_nodes: int | None = None, scale: float | None = None,
+               stream=None):
+        """attend_into a new tensor (rows outside every request 0), waited for and checked."""
+        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+        self.attend_into(q, ctx_len, cu_new, out, mask, max_nodes, scale, stream=stream)
+        self.check_status("skv_tree_attention", stream)
+        return out
