@@ -3,117 +3,591 @@
 // For query row i (node j of request r) and query head g, over the positions p
 // that the row sees: s_p = scale q . K_p, out = sum w_p V_p / sum w_p with
 // w_p = exp(s_p - m), m the running maximum; what was summed under an older
-// maximum is scaled by exp(m_old - m) (the ratio is unchanged).
+// maximum is scaled by exp(m_old - m) (the ratio is unchanged). All in base 2:
+// the scores are scaled by log2 e once.
 //
-// One CTA per (row, query head), 128 positions at a time: a thread per score,
-// then a thread per channel.
-#include "skv_paged.h"
+// attend_small serves up to 16 query rows per KV head (single tokens, small
+// trees). It is bound by reading the pages: every K and V value enters one
+// 16-row product, 2 x 16 multiply-adds per code, far below what even the
+// warp-level matrix instructions need to keep up with HBM. So each warp is a
+// stream of its own: it takes every fourth run of 16 positions of its CTA's
+// share through a private ring in shared memory, filled 16 bytes at a time by
+// asynchronous copies that look the page up per position (a page may end
+// anywhere, a row may lie at any 16-byte multiple), and keeps its own maximum,
+// sum and output; no barrier inside the loop. The four are joined at the end of
+// a part. Two CTAs of 4 warps per SM: the ring of each SM holds up to 192 KB, of
+// which two thirds are in flight.
+//
+// An e4m3 cache is raised to fp16 in registers (every e4m3 value is an fp16
+// value). The order of the channels inside a product is free as long as both
+// operands agree, and so is the order of the output's columns: both are chosen so
+// that a thread's 16 bytes of K, and of V per position, are what its fragments
+// need. The queries become fp16 after a power-of-two scale per row that brings the
+// largest magnitude to [1, 2): bf16's 8 bits fit, and what is below 2^-14 of the
+// largest is off by at most 2^-25 of it. Weights are rounded to the type of the
+// product (fp16: half a step 2^-11, bf16: 2^-8); their sum stays binary32.
+#include <atomic>
+
+#include "skv_attend.cuh"
 
 namespace skv {
 
-constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr uint32_t kWarps = 4, kRun = 16, kUnit = kWarps * kRun;
 
-__device__ __forceinline__ float code_value(const PagedView &c, const uint8_t *p, uint32_t d) {
-    if (!c.e4m3) return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(p)[d] << 16);
-    const uint32_t b = p[d], e = (b >> 3) & 15u, m = b & 7u;
-    float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : (float)m * 0.001953125f;
-    if ((b & 127u) == 127u) v = __uint_as_float(0x7FC00000u);
-    return (b & 128u) ? -v : v;
-}
-
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-    uint32_t b = __float_as_uint(x);
-    if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((b >> 16) | 0x40u);
-    return (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
-}
-
-// Request r's rows and lengths; SKV_OK with n = 0 for one without rows.
-struct ReqOf {
-    uint32_t row0, n, ctx, len;
-    int32_t err;
+template <int DP, bool E>
+struct SmallShape {
+    static constexpr uint32_t bytes = E ? 1 : 2;
+    static constexpr uint32_t row = DP * bytes;            // bytes of a position's row in the ring
+    static constexpr uint32_t chunks = row / 16;
+    static constexpr uint32_t half = kRun * row;           // K, then V
+    static constexpr uint32_t stage = 2 * half;
+    static constexpr uint32_t want = 24576 / stage;        // 24 KB per warp
+    static constexpr uint32_t stages = want < 2 ? 2 : want > 8 ? 8 : want;
+    static constexpr uint32_t ring = stages * stage;
+    static constexpr uint32_t joined = kWarps * (16 * (DP + 4) + 32) * 4;
+    static constexpr uint32_t smem = kWarps * ring > joined ? kWarps * ring : joined;
 };
 
-__device__ __forceinline__ ReqOf request_of(const AttendArgs &a, uint32_t r) {
-    ReqOf o{0u, 0u, 0u, 0u, SKV_OK};
-    const int32_t c = a.ctx_len[r], lo = a.cu_new[r], hi = a.cu_new[r + 1];
-    if (lo < 0 || hi < lo || (uint32_t)hi > a.n_rows) o.err = SKV_ERR_INVALID_ARG;
-    else if (hi > lo) {
-        const int64_t len = (int64_t)c + (hi - lo);
-        if (c < 0 || len > (int64_t)a.c.max_pages * a.c.page.d || len > INT32_MAX ||
-            (a.mask && (uint64_t)(hi - lo) > 64ull * a.mask_words))
-            o.err = SKV_ERR_INVALID_ARG;
-        else o = ReqOf{(uint32_t)lo, (uint32_t)(hi - lo), (uint32_t)c, (uint32_t)len, SKV_OK};
-    }
-    return o;
+__device__ __forceinline__ uint32_t smem_of(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ bool sees(const AttendArgs &a, const ReqOf &q, uint32_t node, uint32_t p) {
-    if (p < q.ctx) return true;
-    const uint32_t j = p - q.ctx;
-    if (!a.mask) return j <= node;
-    return (a.mask[(uint64_t)(q.row0 + node) * a.mask_words + (j >> 6)] >> (j & 63u)) & 1u;
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
-__global__ void __launch_bounds__(128) attend_simple(AttendArgs a) {
-    __shared__ float s_q[256], s_w[128], s_red[4];
-    __shared__ uint64_t s_at[128];
-    const uint32_t tid = threadIdx.x, row = blockIdx.x, g = blockIdx.y, h = g / a.group;
-    uint32_t r = 0;
-    ReqOf q{0u, 0u, 0u, 0u, SKV_OK};
-    for (; r < a.c.n_requests; ++r) {
-        q = request_of(a, r);
-        if (q.err && tid == 0) set_first(a.status, q.err);
-        if (q.n && row >= q.row0 && row < q.row0 + q.n) break;
-    }
-    if (r == a.c.n_requests) return;
-    const uint32_t node = row - q.row0, D = a.c.head_dim;
-    for (uint32_t d = tid; d < D; d += 128u)
-        s_q[d] = __uint_as_float((uint32_t)a.q[(uint64_t)row * a.q_row_stride + (uint64_t)g * a.q_head_stride + d] << 16);
-    __syncthreads();
-    const float mul = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.0f);
-    float m = -INFINITY, l = 0.0f, o[2] = {0.0f, 0.0f};
-    for (uint32_t p0 = 0; p0 < q.len; p0 += 128u) {
-        const uint32_t p = p0 + tid;
-        uint64_t at = ~0ull;
-        float s = -INFINITY;
-        if (p < q.len && sees(a, q, node, p)) {
-            const uint32_t j = div_by(p, a.c.page);
-            const int32_t page = a.c.table[(uint64_t)r * a.c.table_stride + j];
-            if ((uint32_t)page < a.c.n_pages) {
-                at = (uint64_t)page * a.c.page_stride + (uint64_t)(p - j * a.c.page.d) * a.c.token_stride +
-                     h * a.c.head_stride;
-                s = 0.0f;
-                for (uint32_t d = 0; d < D; ++d) s = fmaf(s_q[d], code_value(a.c, a.c.k + at, d), s);
-                s *= mul;
-            } else set_first(a.status, SKV_ERR_CORRUPT);
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+template <bool E>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (E)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool E>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (E) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two e4m3 codes (low 16 bits) as fp16.
+__device__ __forceinline__ uint32_t raise2(uint32_t codes) {
+    uint32_t r;
+    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(codes));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+    return r;
+}
+
+// Chunk order inside a row of the ring, so that what the eight lanes of one
+// shared-memory phase read lies in eight different 16-byte columns: bf16 matrices
+// take the same chunk of 8 rows; e4m3 K takes chunks 0-3 of two rows, e4m3 V two
+// chunks of every other row.
+template <int DP, bool E>
+__device__ __forceinline__ uint32_t swz_k(uint32_t row, uint32_t chunk) {
+    if (!E) return chunk ^ (row & 7u);
+    return DP >= 128 ? chunk ^ ((row & 1u) << 2) : chunk;
+}
+template <int DP, bool E>
+__device__ __forceinline__ uint32_t swz_v(uint32_t row, uint32_t chunk) {
+    if (!E) return chunk ^ (row & 7u);
+    return DP >= 128 ? chunk ^ (row & 6u) : chunk ^ ((row >> 1) & 3u);
+}
+
+// The rows (two per thread: lane / 4 and 8 more) of a part's query tile as matrix fragments.
+template <int DP, bool E>
+struct QueryFrags {
+    uint32_t f[DP / 16][4];
+    float mul[2];          // score of the product -> score in base 2
+};
+
+template <int DP, bool E>
+__device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q, uint32_t h, uint32_t rt,
+                                             QueryFrags<DP, E> &x) {
+    const uint32_t lane = threadIdx.x & 31u, c = lane & 3u;
+    const float mul = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + h) : 1.0f) * 1.4426950408889634f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t r = rt * 16u + (lane >> 2) + 8u * half, node = r / a.group, g = r - node * a.group;
+        const bool live = node < q.n;
+        const uint16_t *src = a.q + (uint64_t)(q.row0 + node) * a.q_row_stride + (uint64_t)(h * a.group + g) * a.q_head_stride;
+        float top = 0.0f;
+        if (!E) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t d = 16u * k + 8u * s + 2u * c;
+                    x.f[k][half + 2 * s] = live && d < a.c.head_dim ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u;
+                }
+            }
+            x.mul[half] = mul;
+        } else {
+#pragma unroll
+            for (int b = 0; b < DP / 64; ++b) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // channels 64 b + 16 c + 4 j + {0, 1} and + {2, 3}
+                    const uint32_t d = 64u * b + 16u * c + 4u * j;
+                    const uint2 w = live && d < a.c.head_dim ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
+                    x.f[4 * b + j][half] = w.x;
+                    x.f[4 * b + j][half + 2] = w.y;
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xFFFF0000u))),
+                                           fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xFFFF0000u)))));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            // 2^-e with e the exponent of the largest magnitude; 1 for 0, tiny and infinite rows
+            const uint32_t e = __float_as_uint(top) >> 23;
+            const bool usual = e > 2u && e < 252u;
+            const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
+            x.mul[half] = usual ? mul * __uint_as_float(e << 23) : mul;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t w = x.f[k][half + 2 * s];
+                    x.f[k][half + 2 * s] = pack2<true>(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xFFFF0000u) * down);
+                }
+            }
         }
-        s_at[tid] = at;
-        float t = s;
-        for (uint32_t d = 16; d; d >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, d));
-        if ((tid & 31u) == 0) s_red[tid >> 5] = t;
-        __syncthreads();
-        const float top = fmaxf(m, fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])));
-        const float base = top == -INFINITY ? 0.0f : top;
-        s_w[tid] = at == ~0ull ? 0.0f : expf(s - base);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - base);
-        m = top;
-        __syncthreads();
-        l *= keep;
-        o[0] *= keep;
-        o[1] *= keep;
-        for (uint32_t i = 0; i < 128u; ++i) {
-            if (s_at[i] == ~0ull) continue;
-            l += s_w[i];
-            if (tid < D) o[0] = fmaf(s_w[i], code_value(a.c, a.c.v + s_at[i], tid), o[0]);
-            if (tid + 128u < D) o[1] = fmaf(s_w[i], code_value(a.c, a.c.v + s_at[i], tid + 128u), o[1]);
+    }
+}
+
+template <int DP, bool E>
+__global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(AttendArgs a, AttendWs ws) {
+    using S = SmallShape<DP, E>;
+    extern __shared__ __align__(1024) uint8_t ring_all[];
+    __shared__ unsigned long long sm_plan[kWarps + 4];
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, c4 = lane & 3u, g8 = lane >> 2;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Share sh = share_of<kWarps * 32>(a, ws, 16u, kUnit, sm_plan);
+    if (sh.u0 == sh.u1) return;
+    const uint32_t ring = smem_of(ring_all) + warp * S::ring;
+    const uint32_t row_bytes = a.c.head_dim * S::bytes;
+    bool corrupt = false;
+
+    uint32_t r = sh.r;
+    ReqOf q = request_of(a, r);
+    uint32_t tiles = (q.len + kUnit - 1) / kUnit, rts = (q.n * a.group + 15u) / 16u;
+    uint64_t item = sh.off / tiles;
+    uint32_t tile = (uint32_t)(sh.off - item * tiles);
+    for (uint64_t u = sh.u0; u < sh.u1;) {
+        // one part: head h, row tile rt, tiles [tile, tile_end) of the request
+        const uint32_t h = (uint32_t)(item / rts), rt = (uint32_t)(item - (uint64_t)h * rts);
+        const uint32_t tile_end = (uint32_t)min((uint64_t)tiles, tile + (sh.u1 - u));
+        const uint32_t p_begin = tile * kUnit, p_end = min(q.len, tile_end * kUnit);
+        const uint32_t runs = (p_end - p_begin + kRun - 1) / kRun;
+        const uint32_t mine = runs > warp ? (runs - warp + kWarps - 1) / kWarps : 0u;
+        bool hurt = false;                       // this warp put 0 for a value that is not finite
+
+        // The page of this lane's position (lanes 0-15) in run i of this warp, one run ahead of its copies.
+        uint64_t next_at = ~0ull;
+        auto look_up = [&](uint32_t i) {
+            next_at = ~0ull;
+            const uint32_t p = p_begin + (warp + i * kWarps) * kRun + (lane & 15u);
+            if (i < mine && p < p_end) {
+                next_at = place_of(a.c, r, h, p);
+                corrupt |= next_at == ~0ull;
+            }
+        };
+        auto issue = [&](uint32_t i) {
+            if (i < mine) {
+                const uint32_t st = ring + (i % S::stages) * S::stage;
+#pragma unroll
+                for (uint32_t n = 0; n < (kRun * S::chunks + 31) / 32; ++n) {
+                    const uint32_t x = n * 32u + lane, row = x / S::chunks, ch = x % S::chunks;
+                    const uint64_t at = __shfl_sync(~0u, next_at, row & 15u);
+                    if (row < kRun) {
+                        const bool live = at != ~0ull && ch * 16u < row_bytes;
+                        const uint64_t off = live ? at + ch * 16u : 0ull;
+                        copy16(st + row * S::row + swz_k<DP, E>(row, ch) * 16u, a.c.k + off, live ? 16u : 0u);
+                        copy16(st + S::half + row * S::row + swz_v<DP, E>(row, ch) * 16u, a.c.v + off, live ? 16u : 0u);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            look_up(i + 1);
+        };
+        look_up(0);
+#pragma unroll
+        for (uint32_t i = 0; i + 1 < S::stages; ++i) issue(i);
+
+        QueryFrags<DP, E> qf;
+        load_queries<DP, E>(a, q, h, rt, qf);
+        float o[DP / 8][4];
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+        for (uint32_t i = 0; i < mine; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::stages - 2) : "memory");
+            __syncwarp();
+            issue(i + S::stages - 1);
+            const uint32_t st = ring + (i % S::stages) * S::stage, sv = st + S::half;
+            const uint32_t p0 = p_begin + (warp + i * kWarps) * kRun;
+            const bool edge = p0 + kRun > q.ctx || p0 + kRun > p_end;
+            if (edge && p0 + kRun > q.ctx) {
+                // drafted positions: values that are not finite leave the product
+                bool found = false;
+                for (uint32_t x = lane; x < kRun * S::chunks; x += 32u) {
+                    const uint32_t row = x / S::chunks;
+                    if (p0 + row < q.ctx) continue;
+                    const uint32_t at = sv + x * 16u;
+                    const uint4 w4 = lds128(at);
+                    uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    bool hit = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int b = 0; b < (E ? 4 : 2); ++b) {
+                            const uint32_t bits = E ? 0x7Fu << (8 * b) : 0x7F80u << (16 * b), all = E ? 0xFFu << (8 * b) : 0xFFFFu << (16 * b);
+                            if ((w[j] & bits) == bits) {
+                                w[j] &= ~all;
+                                hit = true;
+                            }
+                        }
+                    }
+                    if (hit)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                    found |= hit;
+                }
+                hurt |= found;
+                __syncwarp();
+            }
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (!E) {
+                const uint32_t row = (lane & 7u) + ((lane >> 4) << 3), hi = (lane >> 3) & 1u;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    uint32_t b[4];
+                    ldm4(b, st + row * S::row + swz_k<DP, E>(row, 2u * k + hi) * 16u);
+                    mma16<E>(s[0], qf.f[k], b[0], b[1]);
+                    mma16<E>(s[1], qf.f[k], b[2], b[3]);
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < DP / 64; ++b) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t row = 8u * n + g8;
+                        const uint4 w4 = lds128(st + row * S::row + swz_k<DP, E>(row, 4u * b + c4) * 16u);
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma16<E>(s[n], qf.f[4 * b + j], raise2(w[j]), raise2(w[j] >> 16));
+                    }
+                }
+            }
+            // scores in base 2; positions a row does not see are -infinity
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int half = e >> 1;
+                    float t = s[n][e] * qf.mul[half];
+                    if (edge) {
+                        const uint32_t p = p0 + 8u * n + 2u * c4 + (e & 1), row = rt * 16u + g8 + 8u * half;
+                        const uint32_t node = row / a.group;
+                        if (p >= p_end || (node < q.n && !sees(a, q, node, p))) t = -INFINITY;
+                    }
+                    s[n][e] = t;
+                    top[half] = fmaxf(top[half], t);
+                }
+            }
+            bool grew = false;
+            float keep[2], base[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 1));
+                top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 2));
+                const float now = fmaxf(m[half], top[half]);
+                grew |= now > m[half];
+                keep[half] = part_weight(m[half], now);
+                m[half] = now;
+                base[half] = now == -INFINITY ? 0.0f : now;
+            }
+            if (__any_sync(~0u, grew)) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) l[half] *= keep[half];
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j) {
+                    o[j][0] *= keep[0];
+                    o[j][1] *= keep[0];
+                    o[j][2] *= keep[1];
+                    o[j][3] *= keep[1];
+                }
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[n][e] = ex2(s[n][e] - base[e >> 1]);
+                    l[e >> 1] += s[n][e];
+                }
+                pa[2 * n] = pack2<E>(s[n][0], s[n][1]);
+                pa[2 * n + 1] = pack2<E>(s[n][2], s[n][3]);
+            }
+            if (!E) {
+                const uint32_t row = lane & 15u, hi = lane >> 4;
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j) {
+                    uint32_t b[4];
+                    ldm4t(b, sv + row * S::row + swz_v<DP, E>(row, 2u * j + hi) * 16u);
+                    mma16<E>(o[2 * j], pa, b[0], b[1]);
+                    mma16<E>(o[2 * j + 1], pa, b[2], b[3]);
+                }
+            } else {
+                // column n of the output tile i is channel (DP / 8) n + i: a thread's bytes of four positions
+                constexpr int CW = DP / 32;                  // words of one position
+                constexpr int PW = CW < 4 ? CW : 4;          // at a time
+#pragma unroll
+                for (int part = 0; part < CW; part += PW) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t row = 2u * c4 + (t & 1) + 8u * (t >> 1);
+                        const uint32_t byte = g8 * (DP / 8) + part * 4u;
+                        const uint32_t at = sv + row * S::row + swz_v<DP, E>(row, byte >> 4) * 16u + (byte & 15u);
+                        if (PW == 4) {
+                            const uint4 x = lds128(at);
+                            w[t][0] = x.x, w[t][1] = x.y, w[t][2] = x.z, w[t][3] = x.w;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < PW; ++j) w[t][j] = lds32(at + 4u * j);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < PW; ++j) {
+                        const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), lo1 = __byte_perm(w[0][j], w[1][j], 0x7362);
+                        const uint32_t hi0 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+                        const int i = (part + j) * 4;
+                        mma16<E>(o[i], pa, raise2(lo0), raise2(hi0));
+                        mma16<E>(o[i + 1], pa, raise2(lo0 >> 16), raise2(hi0 >> 16));
+                        mma16<E>(o[i + 2], pa, raise2(lo1), raise2(hi1));
+                        mma16<E>(o[i + 3], pa, raise2(lo1 >> 16), raise2(hi1 >> 16));
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            l[half] += __shfl_xor_sync(~0u, l[half], 1);
+            l[half] += __shfl_xor_sync(~0u, l[half], 2);
+        }
+        // the rings become the place where the four warps meet
+        const bool any_hurt = __syncthreads_or(hurt);
+        float *so = reinterpret_cast<float *>(ring_all) + warp * 16u * (DP + 4);
+        float *sml = reinterpret_cast<float *>(ring_all) + kWarps * 16u * (DP + 4);     // [warp][2][16]
+        if (c4 == 0) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                sml[warp * 32u + g8 + 8u * half] = m[half];
+                sml[warp * 32u + 16u + g8 + 8u * half] = l[half];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t row = g8 + 8u * (e >> 1), n = 2u * c4 + (e & 1);
+                so[row * (DP + 4) + (E ? n * (DP / 8) + j : 8u * j + n)] = o[j][e];
+            }
         }
         __syncthreads();
+        const bool whole = tile == 0 && tile_end == tiles;
+        const uint32_t place = u == sh.u0 ? 0u : 1u;
+        float *part = ws.parts + ((uint64_t)blockIdx.x * 2u + place) * part_floats(16u, DP);
+        const float vs = a.c.v_scale ? __ldg(a.c.v_scale + h) : 1.0f;
+        // thread: 4 channels of every (512 / DP)th row
+        for (uint32_t x = tid; x < 16u * (DP / 4); x += kWarps * 32) {
+            const uint32_t row = x / (DP / 4), d = (x % (DP / 4)) * 4u;
+            const uint32_t all = rt * 16u + row, node = all / a.group, g = h * a.group + all - node * a.group;
+            if (node >= q.n) continue;
+            float M = -INFINITY, L = 0.0f, f[kWarps];
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w * 32u + row]);
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w) {
+                f[w] = part_weight(sml[w * 32u + row], M);
+                L += f[w] * sml[w * 32u + 16u + row];
+            }
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(ring_all) +
+                                                                   (w * 16u + row) * (DP + 4) + d);
+                v[0] += f[w] * y.x, v[1] += f[w] * y.y, v[2] += f[w] * y.z, v[3] += f[w] * y.w;
+            }
+            if (any_hurt && d < a.c.head_dim) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += not_finite_sum(a, q, r, h, node, d + j, p_begin, p_end);
+            }
+            if (whole) {
+                const float inv = L == 0.0f ? 0.0f : vs / L;
+                if (d < a.c.head_dim) {
+                    uint2 y;
+                    y.x = L == 0.0f ? 0u : pack2<false>(v[0] * inv, v[1] * inv);
+                    y.y = L == 0.0f ? 0u : pack2<false>(v[2] * inv, v[3] * inv);
+                    *reinterpret_cast<uint2 *>(a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim + d) = y;
+                }
+                if (a.lse && d == 0)
+                    a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            } else {
+                if (d == 0) {
+                    part[row] = M;
+                    part[16u + row] = L;
+                }
+                *reinterpret_cast<float4 *>(part + 32u + row * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        if (tid == 0 && tile == 0 && !whole)
+            ws.desc[blockIdx.x] = Desc{1u, r, h, rt, place, tiles, u};
+        u += tile_end - tile;
+        tile = 0;
+        ++item;
+        if (u < sh.u1 && item == (uint64_t)a.c.n_heads * rts) {
+            do q = request_of(a, ++r);
+            while (q.n == 0);
+            tiles = (q.len + kUnit - 1) / kUnit;
+            rts = (q.n * a.group + 15u) / 16u;
+            item = 0;
+        }
+        __syncthreads();                         // the rings are free again
     }
-    const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (a.c.v_scale ? a.c.v_scale[h] : 1.0f);
-    uint16_t *out = a.out + ((uint64_t)row * a.n_q_heads + g) * D;
-    if (tid < D) out[tid] = bf16_bits(l == 0.0f ? 0.0f : o[0] * inv);
-    if (tid + 128u < D) out[tid + 128u] = bf16_bits(l == 0.0f ? 0.0f : o[1] * inv);
-    if (a.lse && tid == 0) a.lse[(uint64_t)row * a.n_q_heads + g] = l == 0.0f ? -INFINITY : m + logf(l);
+    if (__syncthreads_or(corrupt) && tid == 0 && ws.errs[blockIdx.x] == SKV_OK) ws.errs[blockIdx.x] = SKV_ERR_CORRUPT;
+}
+
+// Joins the parts of items that lie in several CTAs, one warp per row: block
+// (c, y) the rows 8 y .. 8 y + 7 of the item that starts in CTA c and goes on.
+// Each part weighs exp2(m - M) with M the largest m, in the order of the CTAs.
+// Block (0, 0) turns the CTAs' error words into the status: the first that has one.
+__global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, uint32_t R, uint32_t DP, uint32_t ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+        int32_t err = SKV_OK;
+        for (uint32_t i = lane; i < ctas && !err; i += 32u) err = ws.errs[i];
+        const uint32_t any = __ballot_sync(~0u, err != SKV_OK);
+        err = __shfl_sync(~0u, err, any ? __ffs(any) - 1 : 0);
+        if (lane == 0) *a.status = err;
+    }
+    const Desc d = ws.desc[c];
+    if (!d.valid) return;
+    const ReqOf q = request_of(a, d.request);
+    const uint32_t row = blockIdx.y * 8u + warp, all = d.rt * R + row, node = all / a.group;
+    if (node >= q.n) return;
+    const uint32_t g = d.head * a.group + all - node * a.group;
+    const Plan plan = *ws.plan;
+    const uint64_t end = d.unit0 + d.units;
+    // parts: CTA c's, then place 0 of the next CTAs up to the one whose share holds unit
+    // end - 1, the last j with j total / active < end
+    const uint32_t n = (uint32_t)((end * plan.active - 1) / plan.total) - c + 1u;
+    const uint64_t size = part_floats(R, DP);
+    const float *first = ws.parts + ((uint64_t)c * 2u + d.place) * size;
+    const auto part = [&](uint32_t j) { return j ? ws.parts + (uint64_t)(c + j) * 2u * size : first; };
+    float M = -INFINITY, L = 0.0f;
+    for (uint32_t j = lane; j < n; j += 32u) M = fmaxf(M, part(j)[row]);
+    for (uint32_t x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (uint32_t j0 = 0; j0 < n; j0 += 32u) {
+        float f = 0.0f;
+        if (j0 + lane < n) {
+            f = part_weight(part(j0 + lane)[row], M);
+            L += f * part(j0 + lane)[R + row];
+        }
+        const uint32_t here = min(32u, n - j0);
+#pragma unroll 4
+        for (uint32_t j = 0; j < here; ++j) {
+            const float w = __shfl_sync(~0u, f, j);
+            const float *src = part(j0 + j) + 2u * R + (uint64_t)row * DP;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x = 4u * lane + 128u * k;
+                if (x < DP) {
+                    const float4 y = *reinterpret_cast<const float4 *>(src + x);
+                    o[4 * k] += w * y.x, o[4 * k + 1] += w * y.y, o[4 * k + 2] += w * y.z, o[4 * k + 3] += w * y.w;
+                }
+            }
+        }
+    }
+    for (uint32_t x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+    const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + d.head) : 1.0f) / L;
+    uint16_t *out = a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t x = 4u * lane + 128u * k;
+        if (x < a.c.head_dim) {
+            uint2 y;
+            y.x = L == 0.0f ? 0u : pack2<false>(o[4 * k] * inv, o[4 * k + 1] * inv);
+            y.y = L == 0.0f ? 0u : pack2<false>(o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+            *reinterpret_cast<uint2 *>(out + x) = y;
+        }
+    }
+    if (a.lse && lane == 0)
+        a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// Dynamic shared memory above 48 KB is asked for once per kernel and device.
+static bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (ready.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+static bool launch_join(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t DP, uint32_t ctas, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, R / 8u);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_join, a, ws, R, DP, ctas) == cudaSuccess;
+}
+
+template <int DP, bool E>
+static bool launch_small(const AttendArgs &a, const AttendWs &ws, cudaStream_t st) {
+    using S = SmallShape<DP, E>;
+    static_assert(S::smem <= 232448, "shared memory of a CTA");
+    static std::atomic<uint64_t> ready{0};                 // devices where the limit is set
+    if (!raise_smem(reinterpret_cast<const void *>(attend_small<DP, E>), S::smem, ready)) return false;
+    attend_small<DP, E><<<kCtasSmall, kWarps * 32, S::smem, st>>>(a, ws);
+    return cudaGetLastError() == cudaSuccess && launch_join(a, ws, 16u, DP, kCtasSmall, st);
 }
 
 }  // namespace skv
@@ -124,7 +598,8 @@ extern "C" int32_t skv_tree_attention_workspace_bytes(const skv_paged *cache, ui
     const int32_t r = skv_paged_check(cache);
     if (r != SKV_OK) return r;
     if (!bytes || n_q_heads == 0 || n_q_heads % cache->n_heads) return SKV_ERR_INVALID_ARG;
-    *bytes = 256;
+    const uint32_t DP = cache->head_dim <= 64 ? 64 : cache->head_dim <= 128 ? 128 : 256;
+    *bytes = kWsHead + sizeof(float) * 2u * kCtasSmall * part_floats(16u, DP);
     return SKV_OK;
 }
 
@@ -149,12 +624,18 @@ extern "C" int32_t skv_tree_attention(const skv_paged *cache, const void *q, uin
          off(cu_new, 4) || off(cache->block_table, 4) || off(mask, 8) || off(lse, 4)))
         return SKV_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    if (cache->n_requests == 0 || n_rows == 0) return SKV_OK;
+    if (cache->n_requests == 0 || n_rows == 0)
+        return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     (void)max_nodes;
-    AttendArgs a{paged_view(*cache), static_cast<const uint16_t *>(q), q_row_stride, q_head_stride, n_q_heads,
-                 n_q_heads / cache->n_heads, n_rows, ctx_len, cu_new, mask, mask_words, scale,
-                 static_cast<uint16_t *>(out), lse, status};
-    attend_simple<<<dim3(n_rows, n_q_heads), 128, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
+    const AttendArgs a{paged_view(*cache), static_cast<const uint16_t *>(q), q_row_stride, q_head_stride, n_q_heads,
+                       n_q_heads / cache->n_heads, n_rows, ctx_len, cu_new, mask, mask_words, scale,
+                       static_cast<uint16_t *>(out), lse, status};
+    const AttendWs ws = attend_ws(workspace);
+    const uint32_t d = cache->head_dim;
+    bool ok;
+    if (cache->dtype == SKV_E4M3)
+        ok = d <= 64 ? launch_small<64, true>(a, ws, st) : d <= 128 ? launch_small<128, true>(a, ws, st) : launch_small<256, true>(a, ws, st);
+    else
+        ok = d <= 64 ? launch_small<64, false>(a, ws, st) : d <= 128 ? launch_small<128, false>(a, ws, st) : launch_small<256, false>(a, ws, st);
+    return ok ? SKV_OK : SKV_ERR_CUDA;
 }
