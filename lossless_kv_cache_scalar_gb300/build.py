@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libskv.so")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["skv_api.cu", "skv_encode.cu", "skv_decode.cu", "skv_calib.cu", "skv_rq.cu", "skv_peak.cu", "skv_noalloc.cu",
-           "skv_paged.cu", "skv_attend.cu"]
+           "skv_paged.cu", "skv_attend.cu", "skv_attend_tc.cu"]
 HEADERS = ["skv_model.cuh", "skv_internal.h", "skv_paged.h", "skv_attend.cuh", "phi_q24.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-ftz=false", "-prec-div=true",

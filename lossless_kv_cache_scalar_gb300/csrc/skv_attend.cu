@@ -26,8 +26,6 @@
 // largest magnitude to [1, 2): bf16's 8 bits fit, and what is below 2^-14 of the
 // largest is off by at most 2^-25 of it. Weights are rounded to the type of the
 // product (fp16: half a step 2^-11, bf16: 2^-8); their sum stays binary32.
-#include <atomic>
-
 #include "skv_attend.cuh"
 
 namespace skv {
@@ -557,7 +555,7 @@ __global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, ui
 }
 
 // Dynamic shared memory above 48 KB is asked for once per kernel and device.
-static bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready) {
+bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
@@ -567,7 +565,7 @@ static bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t>
     return true;
 }
 
-static bool launch_join(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t DP, uint32_t ctas, cudaStream_t st) {
+bool launch_join(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t DP, uint32_t ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, R / 8u);
     cfg.blockDim = dim3(256);
@@ -599,7 +597,8 @@ extern "C" int32_t skv_tree_attention_workspace_bytes(const skv_paged *cache, ui
     if (r != SKV_OK) return r;
     if (!bytes || n_q_heads == 0 || n_q_heads % cache->n_heads) return SKV_ERR_INVALID_ARG;
     const uint32_t DP = cache->head_dim <= 64 ? 64 : cache->head_dim <= 128 ? 128 : 256;
-    *bytes = kWsHead + sizeof(float) * 2u * kCtasSmall * part_floats(16u, DP);
+    const uint64_t small = 2u * kCtasSmall * part_floats(16u, DP), large = DP <= 128 ? 2u * kCtasLarge * part_floats(kLargeRows, DP) : 0;
+    *bytes = kWsHead + sizeof(float) * (small > large ? small : large);
     return SKV_OK;
 }
 
@@ -626,14 +625,15 @@ extern "C" int32_t skv_tree_attention(const skv_paged *cache, const void *q, uin
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cache->n_requests == 0 || n_rows == 0)
         return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
-    (void)max_nodes;
     const AttendArgs a{paged_view(*cache), static_cast<const uint16_t *>(q), q_row_stride, q_head_stride, n_q_heads,
                        n_q_heads / cache->n_heads, n_rows, ctx_len, cu_new, mask, mask_words, scale,
                        static_cast<uint16_t *>(out), lse, status};
     const AttendWs ws = attend_ws(workspace);
     const uint32_t d = cache->head_dim;
     bool ok;
-    if (cache->dtype == SKV_E4M3)
+    if ((uint64_t)max_nodes * a.group > 16u && d <= 128)
+        ok = launch_large(a, ws, st);
+    else if (cache->dtype == SKV_E4M3)
         ok = d <= 64 ? launch_small<64, true>(a, ws, st) : d <= 128 ? launch_small<128, true>(a, ws, st) : launch_small<256, true>(a, ws, st);
     else
         ok = d <= 64 ? launch_small<64, false>(a, ws, st) : d <= 128 ? launch_small<128, false>(a, ws, st) : launch_small<256, false>(a, ws, st);

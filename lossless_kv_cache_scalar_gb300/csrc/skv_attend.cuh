@@ -13,6 +13,8 @@
 // CTA, any other (it then ends at the CTA's last unit) to place 1.
 #pragma once
 
+#include <atomic>
+
 #include "skv_paged.h"
 
 namespace skv {
@@ -209,5 +211,12 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     s.off = sm[W + 1];
     return s;
 }
+
+// skv_attend.cu
+bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready);
+bool launch_join(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t DP, uint32_t ctas, cudaStream_t st);
+// skv_attend_tc.cu: head_dim up to 128
+bool launch_large(const AttendArgs &a, const AttendWs &ws, cudaStream_t st);
+constexpr uint32_t kLargeRows = 256;
 
 }  // namespace skv

@@ -1,0 +1,746 @@
+// skv_attend_tc.cu -- tree attention for more than 16 query rows per KV head, on
+// the fifth-generation tensor cores (the mathematics: skv_attend.cu; the split of
+// the work: skv_attend.cuh).
+//
+// A part has up to 256 query rows (node-major, the query heads of one KV head)
+// and runs over its positions in tiles of 128. Two streams share the tensor
+// cores so that one computes weights while the other multiplies:
+//   more than 128 rows   stream s holds rows 128 s .. 128 s + 127 and every tile
+//                        enters both: a K or V tile is read once for 256 rows
+//   up to 128 rows       both streams hold the same rows and take the tiles in
+//                        turn; their two results are joined at the end
+// A job is one stream with one tile; jobs alternate between the streams.
+//   warps 0-3, 4-7  the weights of stream 0 and 1, one thread per row
+//   warps 8-11      fill the ring of K and V tiles
+//   warp 12         one thread issues the matrix products
+// Per job: S = Q K^T (128 x 128, accumulated in tensor memory), the row's thread
+// turns S into weights and writes them over S as 16-bit values, O += W V with the
+// weights read from tensor memory. K lies in shared memory as [position][channel],
+// channels contiguous (K-major operand); V lies the same way and is the
+// MN-major operand of the second product, so neither is transposed. Both in
+// rows of 128 bytes with the 128-byte swizzle.
+//
+// The maximum that a row's weights refer to lags: it moves only when the row's
+// largest score exceeds it by more than 2^8 in weight, so the output in tensor
+// memory is rarely scaled anew (weights reach 256 at most, sums stay binary32, and
+// the quotient does not depend on the reference).
+//
+// Bound: 2 x 128 x 128 x DP products per job against 2^13 multiply-adds per clock,
+// two jobs per 128 positions from 129 rows on; below that by the pages' bytes.
+#include "skv_attend.cuh"
+
+namespace skv {
+
+constexpr uint32_t kTcThreads = 416, kTcRows = kLargeRows, kTile = 128;
+
+template <int DP>
+struct TcShape {
+    static constexpr uint32_t block = kTile * 128;              // 128 rows of 128 bytes: 64 channels
+    static constexpr uint32_t tile = block * (DP / 64);         // one K, V or 128-row Q tile in 16-bit values
+    static constexpr uint32_t ring = DP == 128 ? 4 : 8;         // tiles
+    static constexpr uint32_t smem = 2 * tile + ring * tile + 1024;
+};
+
+struct TcShared {
+    unsigned long long plan[kTcThreads / 32 + 4];
+    unsigned long long full[8], empty[8];        // ring
+    unsigned long long s_full[2], p_ready[2], o_done[2], q_full, q_empty, drain;
+    unsigned long long at[4][kTile];             // byte offsets of a tile's positions
+    float mul[2][kTcRows];                       // e4m3: what each row's scores are multiplied by
+    float m1[kTile], l1[kTile];                  // stream 1's maxima and sums, for the join
+    uint32_t hurt[4];                            // part by part: a V value that is not finite was put to 0
+    uint32_t tmem;
+    uint32_t gave_up;
+};
+
+__device__ __forceinline__ uint32_t s32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(const void *b, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(s32(b)), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(const void *b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(s32(b)) : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(const void *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p;}"
+                 : "=r"(ok) : "r"(s32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+// Waits for the phase of that parity, at most about two seconds; from the first wait
+// that runs out on, every wait of the CTA returns at once and the CTA runs to its end
+// on whatever it holds (all addresses stay in bounds), to report TIMEOUT.
+__device__ __forceinline__ void bar_wait(TcShared &sm, const void *b, uint32_t parity) {
+    if (bar_try(b, parity)) return;
+    const long long t0 = clock64();
+    while (!bar_try(b, parity)) {
+        if (*reinterpret_cast<volatile uint32_t *>(&sm.gave_up)) return;
+        if (clock64() - t0 > 4000000000ll) {
+            *reinterpret_cast<volatile uint32_t *>(&sm.gave_up) = 1u;
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(const void *b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(s32(b)) : "memory");
+}
+
+// Shared-memory operand: 128-byte swizzle, 8-row groups 1024 bytes apart (bits 32-45);
+// lead: distance of 64-channel blocks where the contiguous dimension is not the
+// product's (bits 16-29).
+__device__ __forceinline__ uint64_t tc_operand(uint32_t at, uint32_t lead) {
+    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add) : "memory");
+}
+
+#define SKV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define SKV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+
+// 32 columns of this warp's 32 rows of tensor memory.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : SKV_R4(r, 0), SKV_R4(r, 4), SKV_R4(r, 8), SKV_R4(r, 12), SKV_R4(r, 16), SKV_R4(r, 20), SKV_R4(r, 24), SKV_R4(r, 28)
+        : "r"(at) : "memory");
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SKV_I4(r, 0), SKV_I4(r, 4), SKV_I4(r, 8), SKV_I4(r, 12),
+        SKV_I4(r, 16), SKV_I4(r, 20), SKV_I4(r, 24), SKV_I4(r, 28), "r"(at) : "memory");
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SKV_I4(r, 0),
+        SKV_I4(r, 4), SKV_I4(r, 8), SKV_I4(r, 12), "r"(at) : "memory");
+}
+
+template <bool E>
+__device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
+    uint32_t r;
+    if (E) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t tc_raise2(uint32_t codes) {
+    uint32_t r;
+    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(codes));
+    return r;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The parts of a CTA's share, in order; every thread walks them for itself.
+struct Walk {
+    uint64_t u, u1, item;
+    uint32_t r, tiles, rts, tile;
+    ReqOf q;
+    uint32_t n;                                     // parts so far
+    // the part
+    uint32_t h, rt, tile_end, rows;                 // rows: of this row tile
+
+    __device__ __forceinline__ void request(const AttendArgs &a) {
+        tiles = (q.len + kTile - 1) / kTile;
+        rts = (q.n * a.group + kTcRows - 1) / kTcRows;
+    }
+    __device__ __forceinline__ void part(const AttendArgs &a) {
+        h = (uint32_t)(item / rts);
+        rt = (uint32_t)(item - (uint64_t)h * rts);
+        tile_end = (uint32_t)min((uint64_t)tiles, tile + (u1 - u));
+        rows = min(kTcRows, q.n * a.group - rt * kTcRows);
+    }
+    __device__ __forceinline__ Walk(const AttendArgs &a, const Share &s) {
+        u = s.u0;
+        u1 = s.u1;
+        r = s.r;
+        n = 0;
+        q = request_of(a, r);
+        request(a);
+        item = s.off / tiles;
+        tile = (uint32_t)(s.off - item * tiles);
+        part(a);
+    }
+    __device__ __forceinline__ bool more() const { return u < u1; }
+    __device__ __forceinline__ bool both() const { return rows > kTile; }          // 129 rows on: every tile in both streams
+    __device__ __forceinline__ uint32_t count() const { return tile_end - tile; }
+    __device__ __forceinline__ void next(const AttendArgs &a) {
+        u += tile_end - tile;
+        tile = 0;
+        ++item;
+        ++n;
+        if (u >= u1) return;
+        if (item == (uint64_t)a.c.n_heads * rts) {
+            do q = request_of(a, ++r);
+            while (q.n == 0);
+            request(a);
+            item = 0;
+        }
+        part(a);
+    }
+};
+
+// Which tile fills the e-th place of a part of T tiles, in the order in which the
+// products need them: K0 V0 K1 V1 ... where both streams take every tile, else
+// K0 K1 V0 K2 V1 K3 ... V(T-2) V(T-1).
+__device__ __forceinline__ uint32_t fill_of(bool both, uint32_t T, uint32_t e, bool &is_v) {
+    if (both || T == 1) {
+        is_v = e & 1u;
+        return e >> 1;
+    }
+    if (e < 2) {
+        is_v = false;
+        return e;
+    }
+    is_v = !(e & 1u) || e == 2 * T - 1;
+    return e == 2 * T - 1 ? T - 1 : is_v ? (e - 2) / 2 : (e - 2) / 2 + 2;
+}
+
+template <int DP, bool E>
+__device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t q_at, uint32_t ring_at,
+                                          bool &corrupt) {
+    using S = TcShape<DP>;
+    const uint32_t t = threadIdx.x - 256u;
+    const uint32_t row_bytes = a.c.head_dim * (E ? 1u : 2u);
+    uint32_t pos = 0;                                                // tiles begun, over all parts
+    for (Walk w(a, sh); w.more(); w.next(a)) {
+        const bool both = w.both();
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        if (w.n) bar_wait(sm, &sm.q_empty, (w.n - 1) & 1u);
+        if (t == 0) sm.hurt[w.n & 3u] = 0u;
+        asm volatile("bar.sync 2, 128;" ::: "memory");               // the last part's offsets are read, the flag is down
+        // ---- queries
+        const uint32_t q_rows = both ? 256u : 128u;
+        if (!E) {
+            constexpr uint32_t CH = DP / 8;                          // 16-byte chunks of a row
+            for (uint32_t x = t; x < q_rows * CH; x += 128u) {
+                const uint32_t row = x / CH, ch = x % CH, all = w.rt * kTcRows + row, node = all / a.group, g = all - node * a.group;
+                const bool live = node < w.q.n && ch * 8u < a.c.head_dim;
+                const uint16_t *src = live ? a.q + (uint64_t)(w.q.row0 + node) * a.q_row_stride +
+                                                 (uint64_t)(w.h * a.group + g) * a.q_head_stride + ch * 8u : a.q;
+                const uint32_t dst = q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else {
+            // fp16 after a power-of-two scale per row (skv_attend.cu): one thread per row
+            for (uint32_t row = t; row < q_rows; row += 128u) {
+                const uint32_t all = w.rt * kTcRows + row, node = all / a.group, g = all - node * a.group;
+                const bool live = node < w.q.n;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    live ? a.q + (uint64_t)(w.q.row0 + node) * a.q_row_stride + (uint64_t)(w.h * a.group + g) * a.q_head_stride : a.q);
+                float top = 0.0f;
+                const uint32_t chunks = live ? a.c.head_dim / 8u : 0u;
+                for (uint32_t ch = 0; ch < chunks; ++ch) {
+                    const uint4 v = __ldg(src + ch);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+                }
+                const uint32_t e = __float_as_uint(top) >> 23;
+                const bool usual = e > 2u && e < 252u;
+                const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
+                sm.mul[w.n & 1u][row] = usual ? __uint_as_float(e << 23) : 1.0f;
+                for (uint32_t ch = 0; ch < DP / 8u; ++ch) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (ch < chunks) {
+                        v = __ldg(src + ch);
+                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = tc_pack<true>(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xFFFF0000u) * down);
+                        v = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    st_shared16(q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4), v);
+                }
+            }
+        }
+        proxy_fence();
+        bar_arrive(&sm.q_full);
+        // ---- K and V tiles
+        // Offsets of a tile's positions: a thread each, into one of four places, a tile ahead.
+        uint64_t next_at = ~0ull;
+        const auto look_up = [&](uint32_t k) {
+            next_at = ~0ull;
+            const uint32_t p = (w.tile + k) * kTile + t;
+            if (k < T && p < p_end) {
+                next_at = place_of(a.c, w.r, w.h, p);
+                corrupt |= next_at == ~0ull;
+            }
+        };
+        look_up(0);
+        const auto offsets = [&](uint32_t k) {
+            sm.at[k & 3u][t] = next_at;
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+            look_up(k + 1);
+        };
+        if (!E) {
+            constexpr uint32_t CH = DP / 8, PER = kTile * CH / 128;   // chunks per row, copies per thread
+            constexpr uint32_t LAG = 2;                               // tiles in flight behind the newest
+            // Tile e of the part has landed: clear what is not finite among drafted V, tell the products.
+            const auto landed = [&](uint32_t e) {
+                bool is_v;
+                const uint32_t k = fill_of(both, T, e, is_v), slot = (pos + e) % S::ring;
+                const uint32_t p0 = (w.tile + k) * kTile;
+                if (is_v && p0 + kTile > w.q.ctx) {
+                    bool found = false;
+                    for (uint32_t i = 0; i < PER; ++i) {
+                        const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
+                        if (p0 + row < w.q.ctx) continue;
+                        const uint32_t at = ring_at + slot * S::tile + (ch >> 3) * S::block + row * 128u + (((ch ^ row) & 7u) << 4);
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+                        bool hit = false;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if ((v[j] & 0x7F80u) == 0x7F80u) v[j] &= 0xFFFF0000u, hit = true;
+                            if ((v[j] & 0x7F800000u) == 0x7F800000u) v[j] &= 0xFFFFu, hit = true;
+                        }
+                        if (hit) st_shared16(at, make_uint4(v[0], v[1], v[2], v[3]));
+                        found |= hit;
+                    }
+                    if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
+                }
+                proxy_fence();
+                bar_arrive(&sm.full[slot]);
+            };
+            for (uint32_t e = 0; e < 2 * T; ++e) {
+                bool is_v;
+                const uint32_t k = fill_of(both, T, e, is_v), slot = (pos + e) % S::ring;
+                if (!is_v) offsets(k);
+                bar_wait(sm, &sm.empty[slot], (((pos + e) / S::ring) & 1u) ^ 1u);
+                const uint8_t *base = is_v ? a.c.v : a.c.k;
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i) {
+                    const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
+                    const uint64_t at = sm.at[k & 3u][row];
+                    const bool live = at != ~0ull && ch * 16u < row_bytes;
+                    const uint32_t dst = ring_at + slot * S::tile + (ch >> 3) * S::block + row * 128u + (((ch ^ row) & 7u) << 4);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(base + (live ? at + ch * 16u : 0ull)),
+                                 "r"(live ? 16u : 0u) : "memory");
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (e >= LAG) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+                    landed(e - LAG);
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            for (uint32_t e = 2 * T > LAG ? 2 * T - LAG : 0u; e < 2 * T; ++e) landed(e);
+        } else {
+            constexpr uint32_t CH = DP / 16, PER = kTile * CH / 128;  // 16 codes each
+            uint4 now[PER], next[PER];
+            const auto load = [&](uint32_t e, uint4(&v)[PER]) {
+                bool is_v;
+                const uint32_t k = fill_of(both, T, e, is_v);
+                if (!is_v) offsets(k);
+                const uint8_t *base = is_v ? a.c.v : a.c.k;
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i) {
+                    const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
+                    const uint64_t at = sm.at[k & 3u][row];
+                    v[i] = at != ~0ull && ch * 16u < row_bytes ? __ldg(reinterpret_cast<const uint4 *>(base + at + ch * 16u))
+                                                               : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            load(0, now);
+            for (uint32_t e = 0; e < 2 * T; ++e) {
+                if (e + 1 < 2 * T) load(e + 1, next);
+                bool is_v;
+                const uint32_t k = fill_of(both, T, e, is_v), slot = (pos + e) % S::ring;
+                const uint32_t p0 = (w.tile + k) * kTile;
+                bar_wait(sm, &sm.empty[slot], (((pos + e) / S::ring) & 1u) ^ 1u);
+                bool found = false;
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i) {
+                    const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
+                    uint32_t c[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+                    if (is_v && p0 + row >= w.q.ctx) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int b = 0; b < 32; b += 8)
+                                if (((c[j] >> b) & 0x7Fu) == 0x7Fu) c[j] &= ~(0xFFu << b), found = true;
+                    }
+                    const uint32_t at = ring_at + slot * S::tile + (ch >> 2) * S::block + row * 128u;
+                    const uint32_t c0 = 2u * ch;
+                    st_shared16(at + (((c0 ^ row) & 7u) << 4),
+                                make_uint4(tc_raise2(c[0]), tc_raise2(c[0] >> 16), tc_raise2(c[1]), tc_raise2(c[1] >> 16)));
+                    st_shared16(at + ((((c0 + 1u) ^ row) & 7u) << 4),
+                                make_uint4(tc_raise2(c[2]), tc_raise2(c[2] >> 16), tc_raise2(c[3]), tc_raise2(c[3] >> 16)));
+                }
+                if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
+                proxy_fence();
+                bar_arrive(&sm.full[slot]);
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i) now[i] = next[i];
+            }
+        }
+        pos += 2 * T;
+    }
+}
+
+template <int DP, bool E>
+__device__ __forceinline__ void product_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t q_at, uint32_t ring_at,
+                                             uint32_t tmem) {
+    using S = TcShape<DP>;
+    // binary32 accumulators; both inputs fp16 (0) or bf16 (1); 128 rows
+    constexpr uint32_t kind0 = (1u << 4) | ((E ? 0u : 1u) << 7) | ((E ? 0u : 1u) << 10) | (8u << 24);
+    constexpr uint32_t kind_s = kind0 | ((kTile >> 3) << 17), kind_o = kind0 | (1u << 16) | (((uint32_t)DP >> 3) << 17);
+    uint32_t pos = 0, jobs[2] = {0u, 0u};
+    for (Walk w(a, sh); w.more(); w.next(a)) {
+        const bool both = w.both();
+        const uint32_t T = w.count(), J = both ? 2 * T : T;
+        bar_wait(sm, &sm.q_full, w.n & 1u);
+        uint32_t k_slot = 0, v_slot = 0;
+        const auto take = [&](uint32_t &slot) {
+            slot = pos % S::ring;
+            bar_wait(sm, &sm.full[slot], (pos / S::ring) & 1u);
+            ++pos;
+        };
+        const auto scores = [&](uint32_t j) {
+            const uint32_t s = j & 1u;
+            if (!both || s == 0) take(k_slot);
+            tc_fence_after();
+            const uint32_t qa = q_at + (both && s ? S::tile : 0u), ka = ring_at + k_slot * S::tile;
+#pragma unroll
+            for (uint32_t k = 0; k < DP / 16; ++k) {
+                const uint32_t off = (k >> 2) * S::block + (k & 3u) * 32u;
+                tc_mma_ss(tmem + s * kTile, tc_operand(qa + off, 16u), tc_operand(ka + off, 16u), kind_s, k != 0);
+            }
+            tc_commit(&sm.s_full[s]);
+            if (!both || s) tc_commit(&sm.empty[k_slot]);
+            if (j + 1 == J) tc_commit(&sm.q_empty);
+        };
+        scores(0);
+        if (J > 1) scores(1);
+        for (uint32_t j = 0; j < J; ++j) {
+            const uint32_t s = j & 1u;
+            if (!both || s == 0) take(v_slot);
+            bar_wait(sm, &sm.p_ready[s], jobs[s] & 1u);
+            ++jobs[s];
+            tc_fence_after();
+            const uint32_t va = ring_at + v_slot * S::tile;
+#pragma unroll
+            for (uint32_t k = 0; k < kTile / 16; ++k)
+                tc_mma_ts(tmem + 256u + s * DP, tmem + s * kTile + k * 8u, tc_operand(va + k * 2048u, S::block), kind_o, j > 1 || k != 0);
+            tc_commit(&sm.o_done[s]);
+            if (!both || s) tc_commit(&sm.empty[v_slot]);
+            if (j + 2 < J) scores(j + 2);
+        }
+    }
+    // Nothing of this CTA is left in the tensor cores when the roles meet at the end.
+    tc_commit(&sm.drain);
+    const long long t0 = clock64();
+    while (!bar_try(&sm.drain, 0u) && clock64() - t0 < 4000000000ll) {}
+}
+
+// Which of the 32 positions p0 .. p0 + 31 the row sees.
+__device__ __forceinline__ uint32_t sees32(const AttendArgs &a, const ReqOf &q, uint32_t node, uint32_t p0, uint32_t p_end) {
+    uint32_t bits = 0u;
+    if (p0 >= p_end) return 0u;
+    const uint32_t live = p_end - p0 >= 32u ? ~0u : (1u << (p_end - p0)) - 1u;
+    const int64_t j0 = (int64_t)p0 - q.ctx;                          // drafted index of bit 0
+    if (j0 < 0) bits = j0 <= -32 ? ~0u : (1u << (uint32_t)(-j0)) - 1u;
+    if (j0 > -32) {
+        if (!a.mask) {
+            const int64_t n = (int64_t)node - j0 + 1;                // j <= node
+            bits |= n >= 32 ? ~0u : n <= 0 ? 0u : (1u << (uint32_t)n) - 1u;
+        } else {
+            const uint64_t *m = a.mask + (uint64_t)(q.row0 + node) * a.mask_words;
+            const uint32_t first = j0 < 0 ? 0u : (uint32_t)j0, word = first >> 6, sh = first & 63u;
+            uint64_t x = word < a.mask_words ? __ldg(m + word) >> sh : 0ull;
+            if (sh > 32u && word + 1 < a.mask_words) x |= __ldg(m + word + 1) << (64u - sh);
+            bits |= j0 < 0 ? (uint32_t)x << (uint32_t)(-j0) : (uint32_t)x;
+        }
+    }
+    return bits & live;
+}
+
+template <int DP, bool E>
+__device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs &ws, const Share &sh, TcShared &sm, uint32_t tmem) {
+    const uint32_t s = threadIdx.x >> 7, t = threadIdx.x & 127u, lanes = (t & ~31u) << 16;
+    const uint32_t at_s = tmem + lanes + s * kTile, at_o = tmem + lanes + 256u + s * DP;
+    uint32_t jobs = 0, others = 0;                                   // of this stream and of stream 1, over all parts
+    for (Walk w(a, sh); w.more(); w.next(a)) {
+        const bool both = w.both();
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        const uint32_t row = both ? s * kTile + t : t;               // of the row tile
+        const uint32_t all = w.rt * kTcRows + row, node = all / a.group, g = w.h * a.group + all - node * a.group;
+        const bool live = row < w.rows, warp_live = (row & ~31u) < w.rows;
+        // (no wait for the queries here: a part of few jobs can be two phases behind the filling warps)
+        float mul = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + w.h) : 1.0f) * 1.4426950408889634f;
+        const bool falls = mul < 0.0f;
+        float m = -INFINITY, l = 0.0f;
+        uint32_t done = 0;                                           // jobs of this part
+        for (uint32_t k = both ? 0u : s; k < T; k += both ? 1u : 2u, ++done, ++jobs) {
+            bar_wait(sm, &sm.s_full[s], jobs & 1u);
+            __syncwarp();
+            tc_fence_after();
+            if (E && done == 0) mul *= sm.mul[w.n & 1u][row];
+            const uint32_t p0 = (w.tile + k) * kTile;
+            const bool edge = p0 + kTile > w.q.ctx || p0 + kTile > p_end;
+            if (warp_live) {
+                uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+                if (edge && live) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) bits[c] = sees32(a, w.q, node, p0 + 32u * c, p_end);
+                }
+                __syncwarp();
+                float top = -INFINITY;                               // of the scores in base 2
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tc_ld32(x, at_s + 32u * c);
+                    tc_wait_ld();
+                    float lo = INFINITY, hi = -INFINITY;
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (!((bits[c] >> i) & 1u)) continue;
+                            lo = fminf(lo, __uint_as_float(x[i]));
+                            hi = fmaxf(hi, __uint_as_float(x[i]));
+                        }
+                    } else if (!falls) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) hi = fmaxf(hi, __uint_as_float(x[i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) lo = fminf(lo, __uint_as_float(x[i]));
+                    }
+                    // nothing seen (or only NaN): no product with an infinity of the start value
+                    const float far = falls ? lo : hi;
+                    if (!edge || bits[c]) top = fmaxf(top, far == (falls ? INFINITY : -INFINITY) && mul == 0.0f ? -INFINITY : far * mul);
+                }
+                // the reference moves only for a weight of 2^8 or more against it
+                const bool move = top > m + 8.0f || (m == -INFINITY && top > m);
+                const float keep = move ? part_weight(m, top) : 1.0f;
+                if (move) m = top;
+                l *= keep;
+                if (__any_sync(~0u, move) && done) {
+                    bar_wait(sm, &sm.o_done[s], (jobs - 1u) & 1u);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t x[32];
+                        tc_ld32(x, at_o + 32u * c);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
+                        tc_st32(at_o + 32u * c, x);
+                    }
+                    tc_wait_st();
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32], y[16];
+                    tc_ld32(x, at_s + 32u * c);
+                    tc_wait_ld();
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float w0 = ex2(fmaf(__uint_as_float(x[i]), mul, -base)), w1 = ex2(fmaf(__uint_as_float(x[i + 1]), mul, -base));
+                        if (edge) {
+                            if (!((bits[c] >> i) & 1u)) w0 = 0.0f;
+                            if (!((bits[c] >> (i + 1)) & 1u)) w1 = 0.0f;
+                        }
+                        sum[0] += w0;
+                        sum[1] += w1;
+                        y[i / 2] = tc_pack<E>(w0, w1);
+                    }
+                    l += sum[0] + sum[1];
+                    tc_st16(at_s + 16u * c, y);
+                }
+                tc_wait_st();
+            }
+            tc_fence_before();
+            bar_arrive(&sm.p_ready[s]);
+        }
+        // ---- the part's result
+        if (!both) {
+            if (s == 1) {
+                sm.m1[t] = done ? m : -INFINITY;
+                sm.l1[t] = l;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        others += both ? T : T / 2;
+        if (done && (both || s == 0)) {
+            bar_wait(sm, &sm.o_done[s], (jobs - 1u) & 1u);
+            if (!both && T > 1) bar_wait(sm, &sm.o_done[1], (others - 1u) & 1u);
+            __syncwarp();
+            tc_fence_after();
+            if (warp_live) {
+                const bool whole = w.tile == 0 && w.tile_end == w.tiles, two = !both && T > 1;
+                const bool hurt = *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) != 0u;
+                float f0 = 1.0f, f1 = 0.0f;
+                if (two) {
+                    const float m1 = sm.m1[t], M = fmaxf(m, m1);
+                    f0 = part_weight(m, M);
+                    f1 = part_weight(m1, M);
+                    l = f0 * l + f1 * sm.l1[t];
+                    m = M;
+                }
+                const float norm = !whole ? 1.0f : l == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + w.h) : 1.0f) / l;
+                f0 *= norm;
+                f1 *= norm;
+                const uint32_t place = w.u == sh.u0 ? 0u : 1u;
+                float *part = ws.parts + ((uint64_t)blockIdx.x * 2u + place) * part_floats(kTcRows, DP);
+                uint16_t *out = a.out + ((uint64_t)(w.q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t x[32];
+                    __syncwarp();
+                    tc_ld32(x, at_o + 32u * c);
+                    tc_wait_ld();
+                    if (two) {
+                        uint32_t y[32];
+                        tc_ld32(y, at_o + DP + 32u * c);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
+                    }
+                    if (hurt && live) {
+                        for (int i = 0; i < 32; ++i) {
+                            if (32u * c + i >= a.c.head_dim) break;
+                            const float add = not_finite_sum(a, w.q, w.r, w.h, node, 32u * c + i, w.tile * kTile, p_end);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)             // registers have no index of their own
+                                if (j == i) x[j] = __float_as_uint(__uint_as_float(x[j]) + add);
+                        }
+                    }
+                    if (live && whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            if (32u * c + i >= a.c.head_dim) break;
+                            uint4 y;
+                            y.x = tc_pack<false>(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                            y.y = tc_pack<false>(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                            y.z = tc_pack<false>(__uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
+                            y.w = tc_pack<false>(__uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
+                            if (l == 0.0f) y = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(out + 32u * c + i) = y;
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4 *>(part + 2u * kTcRows + row * DP + 32u * c + i) =
+                                make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    }
+                }
+                if (live && whole && a.lse)
+                    a.lse[(uint64_t)(w.q.row0 + node) * a.n_q_heads + g] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                if (live && !whole) {
+                    part[row] = m;
+                    part[kTcRows + row] = l;
+                }
+                if (threadIdx.x == 0 && w.tile == 0 && !whole)
+                    ws.desc[blockIdx.x] = Desc{1u, w.r, w.h, w.rt, place, w.tiles, w.u};
+            }
+            tc_fence_before();
+        }
+        // stream 1 goes on once its output has been read
+        if (!both) asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+}
+
+template <int DP, bool E>
+__global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, AttendWs ws) {
+    using S = TcShape<DP>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ TcShared sm;
+    const uint32_t tid = threadIdx.x, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Share sh = share_of<kTcThreads>(a, ws, kTcRows, kTile, sm.plan);
+    if (sh.u0 == sh.u1) return;
+    const uint32_t q_at = (s32(dyn) + 1023u) & ~1023u, ring_at = q_at + 2u * S::tile;
+    if (tid == 0) {
+        for (uint32_t i = 0; i < S::ring; ++i) {
+            bar_init(&sm.full[i], 128u);
+            bar_init(&sm.empty[i], 1u);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            bar_init(&sm.s_full[i], 1u);
+            bar_init(&sm.p_ready[i], 128u);
+            bar_init(&sm.o_done[i], 1u);
+        }
+        bar_init(&sm.q_full, 128u);
+        bar_init(&sm.q_empty, 1u);
+        bar_init(&sm.drain, 1u);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sm.gave_up = 0u;
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s32(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    bool corrupt = false;
+    if (warp < 8) weight_role<DP, E>(a, ws, sh, sm, tmem);
+    else if (warp < 12) fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
+    else if ((tid & 31u) == 0) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
+    __syncwarp();
+    tc_fence_before();
+    corrupt = __syncthreads_or(corrupt);
+    if (warp == 12) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+    if (tid == 0) {
+        if (sm.gave_up) ws.errs[blockIdx.x] = SKV_ERR_TIMEOUT;
+        else if (corrupt && ws.errs[blockIdx.x] == SKV_OK) ws.errs[blockIdx.x] = SKV_ERR_CORRUPT;
+    }
+}
+
+template <int DP, bool E>
+static bool launch(const AttendArgs &a, const AttendWs &ws, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    constexpr uint32_t bytes = TcShape<DP>::smem;
+    static_assert(bytes + sizeof(TcShared) <= 232448, "shared memory of a CTA");
+    if (!raise_smem(reinterpret_cast<const void *>(attend_large<DP, E>), bytes, ready)) return false;
+    attend_large<DP, E><<<kCtasLarge, kTcThreads, bytes, st>>>(a, ws);
+    return cudaGetLastError() == cudaSuccess && launch_join(a, ws, kTcRows, DP, kCtasLarge, st);
+}
+
+bool launch_large(const AttendArgs &a, const AttendWs &ws, cudaStream_t st) {
+    if (a.c.e4m3) return a.c.head_dim <= 64 ? launch<64, true>(a, ws, st) : launch<128, true>(a, ws, st);
+    return a.c.head_dim <= 64 ? launch<64, false>(a, ws, st) : launch<128, false>(a, ws, st);
+}
+
+}  // namespace skv
