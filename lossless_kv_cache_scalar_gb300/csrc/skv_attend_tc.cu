@@ -12,7 +12,7 @@
 // A job is one stream with one tile; jobs alternate between the streams.
 //   warps 0-3, 4-7  the weights of stream 0 and 1, one thread per row
 //   warps 8-11      fill the ring of K and V tiles
-//   warp 12         one thread issues the matrix products
+//   warp 12         one thread issues the matrix products (13-15 only give up their registers)
 // Per job: S = Q K^T (128 x 128, accumulated in tensor memory), the row's thread
 // turns S into weights and writes them over S as 16-bit values, O += W V with the
 // weights read from tensor memory. K lies in shared memory as [position][channel],
@@ -31,7 +31,7 @@
 
 namespace skv {
 
-constexpr uint32_t kTcThreads = 416, kTcRows = kLargeRows, kTile = 128;
+constexpr uint32_t kTcThreads = 512, kTcRows = kLargeRows, kTile = 128;
 
 template <int DP>
 struct TcShape {
@@ -39,6 +39,55 @@ struct TcShape {
     static constexpr uint32_t tile = block * (DP / 64);         // one K, V or 128-row Q tile in 16-bit values
     static constexpr uint32_t ring = DP == 128 ? 4 : 8;         // tiles
     static constexpr uint32_t smem = 2 * tile + ring * tile + 1024;
+};
+
+// The parts of a CTA's share, in order; every role walks them for itself.
+struct Walk {
+    uint64_t u, u1, item;
+    uint32_t r, tiles, rts, tile;
+    ReqOf q;
+    uint32_t n;                                     // parts so far
+    // the part
+    uint32_t h, rt, tile_end, rows;                 // rows: of this row tile
+
+    __device__ __forceinline__ void request(const AttendArgs &a) {
+        tiles = (q.len + kTile - 1) / kTile;
+        rts = (q.n * a.group + kTcRows - 1) / kTcRows;
+    }
+    __device__ __forceinline__ void part(const AttendArgs &a) {
+        h = (uint32_t)(item / rts);
+        rt = (uint32_t)(item - (uint64_t)h * rts);
+        tile_end = (uint32_t)min((uint64_t)tiles, tile + (u1 - u));
+        rows = min(kTcRows, q.n * a.group - rt * kTcRows);
+    }
+    __device__ __forceinline__ void start(const AttendArgs &a, const Share &s) {
+        u = s.u0;
+        u1 = s.u1;
+        r = s.r;
+        n = 0;
+        q = request_of(a, r);
+        request(a);
+        item = s.off / tiles;
+        tile = (uint32_t)(s.off - item * tiles);
+        part(a);
+    }
+    __device__ __forceinline__ bool more() const { return u < u1; }
+    __device__ __forceinline__ bool both() const { return rows > kTile; }          // 129 rows on: every tile in both streams
+    __device__ __forceinline__ uint32_t count() const { return tile_end - tile; }
+    __device__ __forceinline__ void next(const AttendArgs &a) {
+        u += tile_end - tile;
+        tile = 0;
+        ++item;
+        ++n;
+        if (u >= u1) return;
+        if (item == (uint64_t)a.c.n_heads * rts) {
+            do q = request_of(a, ++r);
+            while (q.n == 0);
+            request(a);
+            item = 0;
+        }
+        part(a);
+    }
 };
 
 struct TcShared {
@@ -51,6 +100,7 @@ struct TcShared {
     uint32_t hurt[4];                            // part by part: a V value that is not finite was put to 0
     uint32_t tmem;
     uint32_t gave_up;
+    Walk walk[2];                                // the weights' threads keep their registers for scores
 };
 
 __device__ __forceinline__ uint32_t s32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -125,11 +175,10 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t at) {
         : "r"(at) : "memory");
 }
 
-__device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t at) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SKV_I4(r, 0), SKV_I4(r, 4), SKV_I4(r, 8), SKV_I4(r, 12),
-        SKV_I4(r, 16), SKV_I4(r, 20), SKV_I4(r, 24), SKV_I4(r, 28), "r"(at) : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : SKV_R4(r, 0), SKV_R4(r, 4), SKV_R4(r, 8), SKV_R4(r, 12) : "r"(at) : "memory");
 }
 
 __device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
@@ -137,6 +186,32 @@ __device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SKV_I4(r, 0),
         SKV_I4(r, 4), SKV_I4(r, 8), SKV_I4(r, 12), "r"(at) : "memory");
 }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two binary32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The 128 threads of one stream's weights.
+__device__ __forceinline__ void group_sync(uint32_t s) { asm volatile("bar.sync %0, 128;" ::"r"(3u + s) : "memory"); }
 
 template <bool E>
 __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
@@ -155,55 +230,6 @@ __device__ __forceinline__ uint32_t tc_raise2(uint32_t codes) {
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-
-// The parts of a CTA's share, in order; every thread walks them for itself.
-struct Walk {
-    uint64_t u, u1, item;
-    uint32_t r, tiles, rts, tile;
-    ReqOf q;
-    uint32_t n;                                     // parts so far
-    // the part
-    uint32_t h, rt, tile_end, rows;                 // rows: of this row tile
-
-    __device__ __forceinline__ void request(const AttendArgs &a) {
-        tiles = (q.len + kTile - 1) / kTile;
-        rts = (q.n * a.group + kTcRows - 1) / kTcRows;
-    }
-    __device__ __forceinline__ void part(const AttendArgs &a) {
-        h = (uint32_t)(item / rts);
-        rt = (uint32_t)(item - (uint64_t)h * rts);
-        tile_end = (uint32_t)min((uint64_t)tiles, tile + (u1 - u));
-        rows = min(kTcRows, q.n * a.group - rt * kTcRows);
-    }
-    __device__ __forceinline__ Walk(const AttendArgs &a, const Share &s) {
-        u = s.u0;
-        u1 = s.u1;
-        r = s.r;
-        n = 0;
-        q = request_of(a, r);
-        request(a);
-        item = s.off / tiles;
-        tile = (uint32_t)(s.off - item * tiles);
-        part(a);
-    }
-    __device__ __forceinline__ bool more() const { return u < u1; }
-    __device__ __forceinline__ bool both() const { return rows > kTile; }          // 129 rows on: every tile in both streams
-    __device__ __forceinline__ uint32_t count() const { return tile_end - tile; }
-    __device__ __forceinline__ void next(const AttendArgs &a) {
-        u += tile_end - tile;
-        tile = 0;
-        ++item;
-        ++n;
-        if (u >= u1) return;
-        if (item == (uint64_t)a.c.n_heads * rts) {
-            do q = request_of(a, ++r);
-            while (q.n == 0);
-            request(a);
-            item = 0;
-        }
-        part(a);
-    }
-};
 
 // Which tile fills the e-th place of a part of T tiles, in the order in which the
 // products need them: K0 V0 K1 V1 ... where both streams take every tile, else
@@ -228,7 +254,8 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
     const uint32_t t = threadIdx.x - 256u;
     const uint32_t row_bytes = a.c.head_dim * (E ? 1u : 2u);
     uint32_t pos = 0;                                                // tiles begun, over all parts
-    for (Walk w(a, sh); w.more(); w.next(a)) {
+    Walk w;
+    for (w.start(a, sh); w.more(); w.next(a)) {
         const bool both = w.both();
         const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
         if (w.n) bar_wait(sm, &sm.q_empty, (w.n - 1) & 1u);
@@ -415,7 +442,8 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
     constexpr uint32_t kind0 = (1u << 4) | ((E ? 0u : 1u) << 7) | ((E ? 0u : 1u) << 10) | (8u << 24);
     constexpr uint32_t kind_s = kind0 | ((kTile >> 3) << 17), kind_o = kind0 | (1u << 16) | (((uint32_t)DP >> 3) << 17);
     uint32_t pos = 0, jobs[2] = {0u, 0u};
-    for (Walk w(a, sh); w.more(); w.next(a)) {
+    Walk w;
+    for (w.start(a, sh); w.more(); w.next(a)) {
         const bool both = w.both();
         const uint32_t T = w.count(), J = both ? 2 * T : T;
         bar_wait(sm, &sm.q_full, w.n & 1u);
@@ -489,7 +517,10 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
     const uint32_t s = threadIdx.x >> 7, t = threadIdx.x & 127u, lanes = (t & ~31u) << 16;
     const uint32_t at_s = tmem + lanes + s * kTile, at_o = tmem + lanes + 256u + s * DP;
     uint32_t jobs = 0, others = 0;                                   // of this stream and of stream 1, over all parts
-    for (Walk w(a, sh); w.more(); w.next(a)) {
+    Walk &w = sm.walk[s];
+    if (t == 0) w.start(a, sh);
+    group_sync(s);
+    while (w.more()) {
         const bool both = w.both();
         const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
         const uint32_t row = both ? s * kTile + t : t;               // of the row tile
@@ -498,6 +529,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
         // (no wait for the queries here: a part of few jobs can be two phases behind the filling warps)
         float mul = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + w.h) : 1.0f) * 1.4426950408889634f;
         const bool falls = mul < 0.0f;
+        mul = fabsf(mul);
         float m = -INFINITY, l = 0.0f;
         uint32_t done = 0;                                           // jobs of this part
         for (uint32_t k = both ? 0u : s; k < T; k += both ? 1u : 2u, ++done, ++jobs) {
@@ -514,31 +546,31 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     for (int c = 0; c < 4; ++c) bits[c] = sees32(a, w.q, node, p0 + 32u * c, p_end);
                 }
                 __syncwarp();
-                float top = -INFINITY;                               // of the scores in base 2
+                // the row's 128 scores, all in registers; those it does not see are NaN, which max leaves out
+                uint32_t x[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tc_ld32(x, at_s + 32u * c);
-                    tc_wait_ld();
-                    float lo = INFINITY, hi = -INFINITY;
-                    if (edge) {
+                for (int c = 0; c < 4; ++c) tc_ld32(x[c], at_s + 32u * c);
+                tc_wait_ld();
+                if (falls) {                                         // a negative scale: largest of -score
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (!((bits[c] >> i) & 1u)) continue;
-                            lo = fminf(lo, __uint_as_float(x[i]));
-                            hi = fmaxf(hi, __uint_as_float(x[i]));
-                        }
-                    } else if (!falls) {
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) hi = fmaxf(hi, __uint_as_float(x[i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) lo = fminf(lo, __uint_as_float(x[i]));
-                    }
-                    // nothing seen (or only NaN): no product with an infinity of the start value
-                    const float far = falls ? lo : hi;
-                    if (!edge || bits[c]) top = fmaxf(top, far == (falls ? INFINITY : -INFINITY) && mul == 0.0f ? -INFINITY : far * mul);
+                        for (int i = 0; i < 32; ++i) x[c][i] ^= 0x80000000u;
                 }
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((bits[c] >> i) & 1u)) x[c][i] = 0x7FFFFFFFu;
+                }
+                float far[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) far[c] = max3(far[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                far[0] = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3]));
+                const float top = far[0] == -INFINITY ? -INFINITY : far[0] * mul;      // in base 2
                 // the reference moves only for a weight of 2^8 or more against it
                 const bool move = top > m + 8.0f || (m == -INFINITY && top > m);
                 const float keep = move ? part_weight(m, top) : 1.0f;
@@ -549,37 +581,37 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t x[32];
-                        tc_ld32(x, at_o + 32u * c);
+                    for (int c = 0; c < DP / 16; ++c) {              // 16 at a time: the scores stay in registers
+                        uint32_t y[16];
+                        tc_ld16(y, at_o + 16u * c);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
-                        tc_st32(at_o + 32u * c, x);
+                        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * keep);
+                        tc_st16(at_o + 16u * c, y);
                     }
                     tc_wait_st();
                 }
                 const float base = m == -INFINITY ? 0.0f : m;
+                const uint64_t mul2 = pair_of(mul, mul), base2 = pair_of(-base, -base);
+                uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32], y[16];
-                    tc_ld32(x, at_s + 32u * c);
-                    tc_wait_ld();
-                    float sum[2] = {0.0f, 0.0f};
+                    uint32_t y[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        float w0 = ex2(fmaf(__uint_as_float(x[i]), mul, -base)), w1 = ex2(fmaf(__uint_as_float(x[i + 1]), mul, -base));
+                        uint64_t z = fma2((uint64_t)x[c][i] | ((uint64_t)x[c][i + 1] << 32), mul2, base2);
+                        float w0 = ex2(__uint_as_float((uint32_t)z)), w1 = ex2(__uint_as_float((uint32_t)(z >> 32)));
                         if (edge) {
                             if (!((bits[c] >> i) & 1u)) w0 = 0.0f;
                             if (!((bits[c] >> (i + 1)) & 1u)) w1 = 0.0f;
                         }
-                        sum[0] += w0;
-                        sum[1] += w1;
+                        sum2[(i >> 1) & 1] = add2(sum2[(i >> 1) & 1], pair_of(w0, w1));
                         y[i / 2] = tc_pack<E>(w0, w1);
                     }
-                    l += sum[0] + sum[1];
                     tc_st16(at_s + 16u * c, y);
                 }
+                sum2[0] = add2(sum2[0], sum2[1]);
+                l += __uint_as_float((uint32_t)sum2[0]) + __uint_as_float((uint32_t)(sum2[0] >> 32));
                 tc_wait_st();
             }
             tc_fence_before();
@@ -674,6 +706,9 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
         }
         // stream 1 goes on once its output has been read
         if (!both) asm volatile("bar.sync 1, 256;" ::: "memory");
+        else group_sync(s);
+        if (t == 0) w.next(a);
+        group_sync(s);
     }
 }
 
@@ -712,9 +747,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, Atte
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     bool corrupt = false;
-    if (warp < 8) weight_role<DP, E>(a, ws, sh, sm, tmem);
-    else if (warp < 12) fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
-    else if ((tid & 31u) == 0) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
+    // 512 threads of 128 registers, dealt out anew: 2 x 176 + 112 + 48 = 4 x 128 per lane of the four groups.
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        weight_role<DP, E>(a, ws, sh, sm, tmem);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (tid == 384) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
+    }
     __syncwarp();
     tc_fence_before();
     corrupt = __syncthreads_or(corrupt);
