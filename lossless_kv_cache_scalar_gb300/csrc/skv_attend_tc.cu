@@ -113,6 +113,12 @@ __device__ __forceinline__ void bar_arrive(const void *b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(s32(b)) : "memory");
 }
 
+// One arrival for a warp: what its lanes did before is ordered before it.
+__device__ __forceinline__ void warp_arrive(const void *b) {
+    __syncwarp();
+    if ((threadIdx.x & 31u) == 0u) bar_arrive(b);
+}
+
 __device__ __forceinline__ bool bar_try(const void *b, uint32_t parity) {
     uint32_t ok;
     asm volatile("{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p;}"
@@ -143,6 +149,13 @@ __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.
 
 __device__ __forceinline__ void tc_commit(const void *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(s32(b)) : "memory");
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elected() {
+    uint32_t ok;
+    asm volatile("{.reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.b32 %0, 1, 0, p;}" : "=r"(ok));
+    return ok != 0;
 }
 
 // Shared-memory operand: 128-byte swizzle, 8-row groups 1024 bytes apart (bits 32-45);
@@ -310,7 +323,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
             }
         }
         proxy_fence();
-        bar_arrive(&sm.q_full);
+        warp_arrive(&sm.q_full);
         // ---- K and V tiles
         // Offsets of a tile's positions: a thread each, into one of four places, a tile ahead.
         uint64_t next_at = ~0ull;
@@ -356,7 +369,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
                     if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
                 }
                 proxy_fence();
-                bar_arrive(&sm.full[slot]);
+                warp_arrive(&sm.full[slot]);
             };
             for (uint32_t e = 0; e < 2 * T; ++e) {
                 bool is_v;
@@ -425,7 +438,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
                 }
                 if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
                 proxy_fence();
-                bar_arrive(&sm.full[slot]);
+                warp_arrive(&sm.full[slot]);
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i) now[i] = next[i];
             }
@@ -441,11 +454,16 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
     // binary32 accumulators; both inputs fp16 (0) or bf16 (1); 128 rows
     constexpr uint32_t kind0 = (1u << 4) | ((E ? 0u : 1u) << 7) | ((E ? 0u : 1u) << 10) | (8u << 24);
     constexpr uint32_t kind_s = kind0 | ((kTile >> 3) << 17), kind_o = kind0 | (1u << 16) | (((uint32_t)DP >> 3) << 17);
+    // The whole warp walks the jobs and one lane issues: what the operands' descriptors are
+    // made of is the same in every lane, so it stays in uniform registers (a branch
+    // for one thread moves every descriptor there anew).
+    tmem = __shfl_sync(~0u, tmem, 0);
+    const uint64_t q_op = tc_operand(q_at, 16u), k_op = tc_operand(ring_at, 16u), v_op = tc_operand(ring_at, S::block);
     uint32_t pos = 0, jobs[2] = {0u, 0u};
     Walk w;
-    for (w.start(a, sh); w.more(); w.next(a)) {
-        const bool both = w.both();
-        const uint32_t T = w.count(), J = both ? 2 * T : T;
+    for (w.start(a, sh); __shfl_sync(~0u, (int)w.more(), 0); w.next(a)) {
+        const bool both = __shfl_sync(~0u, (int)w.both(), 0);
+        const uint32_t T = __shfl_sync(~0u, w.count(), 0), J = both ? 2 * T : T;
         bar_wait(sm, &sm.q_full, w.n & 1u);
         uint32_t k_slot = 0, v_slot = 0;
         const auto take = [&](uint32_t &slot) {
@@ -456,16 +474,20 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
         const auto scores = [&](uint32_t j) {
             const uint32_t s = j & 1u;
             if (!both || s == 0) take(k_slot);
+            __syncwarp();
             tc_fence_after();
-            const uint32_t qa = q_at + (both && s ? S::tile : 0u), ka = ring_at + k_slot * S::tile;
+            if (elected()) {
+                const uint64_t qa = q_op + (both && s ? S::tile >> 4 : 0u), ka = k_op + ((k_slot * S::tile) >> 4);
 #pragma unroll
-            for (uint32_t k = 0; k < DP / 16; ++k) {
-                const uint32_t off = (k >> 2) * S::block + (k & 3u) * 32u;
-                tc_mma_ss(tmem + s * kTile, tc_operand(qa + off, 16u), tc_operand(ka + off, 16u), kind_s, k != 0);
+                for (uint32_t k = 0; k < DP / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * S::block + (k & 3u) * 32u) >> 4;
+                    tc_mma_ss(tmem + s * kTile, qa + off, ka + off, kind_s, k != 0);
+                }
+                tc_commit(&sm.s_full[s]);
+                if (!both || s) tc_commit(&sm.empty[k_slot]);
+                if (j + 1 == J) tc_commit(&sm.q_empty);
             }
-            tc_commit(&sm.s_full[s]);
-            if (!both || s) tc_commit(&sm.empty[k_slot]);
-            if (j + 1 == J) tc_commit(&sm.q_empty);
+            __syncwarp();
         };
         scores(0);
         if (J > 1) scores(1);
@@ -474,18 +496,23 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
             if (!both || s == 0) take(v_slot);
             bar_wait(sm, &sm.p_ready[s], jobs[s] & 1u);
             ++jobs[s];
+            __syncwarp();
             tc_fence_after();
-            const uint32_t va = ring_at + v_slot * S::tile;
+            if (elected()) {
+                const uint64_t va = v_op + ((v_slot * S::tile) >> 4);
 #pragma unroll
-            for (uint32_t k = 0; k < kTile / 16; ++k)
-                tc_mma_ts(tmem + 256u + s * DP, tmem + s * kTile + k * 8u, tc_operand(va + k * 2048u, S::block), kind_o, j > 1 || k != 0);
-            tc_commit(&sm.o_done[s]);
-            if (!both || s) tc_commit(&sm.empty[v_slot]);
+                for (uint32_t k = 0; k < kTile / 16; ++k)
+                    tc_mma_ts(tmem + 256u + s * DP, tmem + s * kTile + k * 8u, va + ((k * 2048u) >> 4), kind_o, j > 1 || k != 0);
+                tc_commit(&sm.o_done[s]);
+                if (!both || s) tc_commit(&sm.empty[v_slot]);
+            }
+            __syncwarp();
             if (j + 2 < J) scores(j + 2);
         }
     }
     // Nothing of this CTA is left in the tensor cores when the roles meet at the end.
-    tc_commit(&sm.drain);
+    if (elected()) tc_commit(&sm.drain);
+    __syncwarp();
     const long long t0 = clock64();
     while (!bar_try(&sm.drain, 0u) && clock64() - t0 < 4000000000ll) {}
 }
@@ -615,7 +642,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                 tc_wait_st();
             }
             tc_fence_before();
-            bar_arrive(&sm.p_ready[s]);
+            warp_arrive(&sm.p_ready[s]);
         }
         // ---- the part's result
         if (!both) {
@@ -724,15 +751,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, Atte
     const uint32_t q_at = (s32(dyn) + 1023u) & ~1023u, ring_at = q_at + 2u * S::tile;
     if (tid == 0) {
         for (uint32_t i = 0; i < S::ring; ++i) {
-            bar_init(&sm.full[i], 128u);
+            bar_init(&sm.full[i], 4u);
             bar_init(&sm.empty[i], 1u);
         }
         for (uint32_t i = 0; i < 2; ++i) {
             bar_init(&sm.s_full[i], 1u);
-            bar_init(&sm.p_ready[i], 128u);
+            bar_init(&sm.p_ready[i], 4u);
             bar_init(&sm.o_done[i], 1u);
         }
-        bar_init(&sm.q_full, 128u);
+        bar_init(&sm.q_full, 4u);
         bar_init(&sm.q_empty, 1u);
         bar_init(&sm.drain, 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -756,7 +783,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, Atte
         fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (tid == 384) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
+        if (warp == 12) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
     }
     __syncwarp();
     tc_fence_before();
