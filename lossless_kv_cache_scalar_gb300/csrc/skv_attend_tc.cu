@@ -11,8 +11,10 @@
 //                        turn; their two results are joined at the end
 // A job is one stream with one tile; jobs alternate between the streams.
 //   warps 0-3, 4-7  the weights of stream 0 and 1, one thread per row
-//   warps 8-11      fill the ring of K and V tiles
-//   warp 12         one thread issues the matrix products (13-15 only give up their registers)
+//   warps 8-11      queries; 8-bit tiles raised to fp16; pages of other lengths, row by row
+//   warp 12         one lane issues the matrix products
+//   warp 13         tensor copies of K and V into the ring, page by page
+//   warps 14, 15    only give up their registers
 // Per job: S = Q K^T (128 x 128, accumulated in tensor memory), the row's thread
 // turns S into weights and writes them over S as 16-bit values, O += W V with the
 // weights read from tensor memory. K lies in shared memory as [position][channel],
@@ -27,18 +29,23 @@
 //
 // Bound: 2 x 128 x 128 x DP products per job against 2^13 multiply-adds per clock,
 // two jobs per 128 positions from 129 rows on; below that by the pages' bytes.
+#include <cuda.h>
+
 #include "skv_attend.cuh"
 
 namespace skv {
 
 constexpr uint32_t kTcThreads = 512, kTcRows = kLargeRows, kTile = 128;
 
-template <int DP>
+template <int DP, bool E>
 struct TcShape {
     static constexpr uint32_t block = kTile * 128;              // 128 rows of 128 bytes: 64 channels
     static constexpr uint32_t tile = block * (DP / 64);         // one K, V or 128-row Q tile in 16-bit values
-    static constexpr uint32_t ring = DP == 128 ? 4 : 8;         // tiles
-    static constexpr uint32_t smem = 2 * tile + ring * tile + 1024;
+    static constexpr uint32_t ring = (E ? 3 : 4) * (128 / DP);  // tiles
+    static constexpr uint32_t raw = E ? ring : 0;               // tiles of 8-bit codes on their way to the ring
+    static constexpr uint32_t raw_tile = kTile * DP;
+    static constexpr uint32_t raw_at = (2 + ring) * tile;       // from the queries' start
+    static constexpr uint32_t smem = raw_at + raw * raw_tile + 1024;
 };
 
 // The parts of a CTA's share, in order; every role walks them for itself.
@@ -93,6 +100,8 @@ struct Walk {
 struct TcShared {
     unsigned long long plan[kTcThreads / 32 + 4];
     unsigned long long full[8], empty[8];        // ring
+    unsigned long long landed[8], taken[8];      // tensor copies that the filling warps finish
+    int32_t pages[4][16];                        // page numbers of a tile's boxes
     unsigned long long s_full[2], p_ready[2], o_done[2], q_full, q_empty, drain;
     unsigned long long at[4][kTile];             // byte offsets of a tile's positions
     float mul[2][kTcRows];                       // e4m3: what each row's scores are multiplied by
@@ -179,6 +188,13 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 #define SKV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 #define SKV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
 
+// One box of a pool: `rows` positions of one page and head, from channel x on.
+__device__ __forceinline__ void tc_box(uint32_t dst, const CUtensorMap *map, uint32_t x, uint32_t h, uint32_t token, int32_t page,
+                                       const void *bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                 ::"r"(dst), "l"(map), "r"(s32(bar)), "r"(x), "r"(h), "r"(token), "r"(page) : "memory");
+}
+
 // 32 columns of this warp's 32 rows of tensor memory.
 __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t at) {
     asm volatile(
@@ -260,10 +276,71 @@ __device__ __forceinline__ uint32_t fill_of(bool both, uint32_t T, uint32_t e, b
     return e == 2 * T - 1 ? T - 1 : is_v ? (e - 2) / 2 : (e - 2) / 2 + 2;
 }
 
+// The part's query rows as the first product's operand, by the 128 filling threads.
+template <int DP, bool E>
+__device__ __forceinline__ void fill_queries(const AttendArgs &a, const Walk &w, TcShared &sm, uint32_t q_at) {
+    using S = TcShape<DP, E>;
+    const uint32_t t = threadIdx.x - 256u;
+    const bool both = w.both();
+    if (w.n) bar_wait(sm, &sm.q_empty, (w.n - 1) & 1u);
+    if (t == 0) sm.hurt[w.n & 3u] = 0u;
+    asm volatile("bar.sync 2, 128;" ::: "memory");                   // the last part's offsets are read, the flag is down
+    const uint32_t q_rows = both ? 256u : 128u;
+    if (!E) {
+        constexpr uint32_t CH = DP / 8;                          // 16-byte chunks of a row
+        for (uint32_t x = t; x < q_rows * CH; x += 128u) {
+            const uint32_t row = x / CH, ch = x % CH, all = w.rt * kTcRows + row, node = all / a.group, g = all - node * a.group;
+            const bool live = node < w.q.n && ch * 8u < a.c.head_dim;
+            const uint16_t *src = live ? a.q + (uint64_t)(w.q.row0 + node) * a.q_row_stride +
+                                             (uint64_t)(w.h * a.group + g) * a.q_head_stride + ch * 8u : a.q;
+            const uint32_t dst = q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+        // fp16 after a power-of-two scale per row (skv_attend.cu): one thread per row
+        for (uint32_t row = t; row < q_rows; row += 128u) {
+            const uint32_t all = w.rt * kTcRows + row, node = all / a.group, g = all - node * a.group;
+            const bool live = node < w.q.n;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                live ? a.q + (uint64_t)(w.q.row0 + node) * a.q_row_stride + (uint64_t)(w.h * a.group + g) * a.q_head_stride : a.q);
+            float top = 0.0f;
+            const uint32_t chunks = live ? a.c.head_dim / 8u : 0u;
+            for (uint32_t ch = 0; ch < chunks; ++ch) {
+                const uint4 v = __ldg(src + ch);
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+            }
+            const uint32_t e = __float_as_uint(top) >> 23;
+            const bool usual = e > 2u && e < 252u;
+            const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
+            sm.mul[w.n & 1u][row] = usual ? __uint_as_float(e << 23) : 1.0f;
+            for (uint32_t ch = 0; ch < DP / 8u; ++ch) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (ch < chunks) {
+                    v = __ldg(src + ch);
+                    uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = tc_pack<true>(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xFFFF0000u) * down);
+                    v = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+                st_shared16(q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4), v);
+            }
+        }
+    }
+    proxy_fence();
+    warp_arrive(&sm.q_full);
+}
+
+// Pages whose length is no multiple of 8: every row is looked up and copied by itself.
 template <int DP, bool E>
 __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t q_at, uint32_t ring_at,
                                           bool &corrupt) {
-    using S = TcShape<DP>;
+    using S = TcShape<DP, E>;
     const uint32_t t = threadIdx.x - 256u;
     const uint32_t row_bytes = a.c.head_dim * (E ? 1u : 2u);
     uint32_t pos = 0;                                                // tiles begun, over all parts
@@ -271,59 +348,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
     for (w.start(a, sh); w.more(); w.next(a)) {
         const bool both = w.both();
         const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
-        if (w.n) bar_wait(sm, &sm.q_empty, (w.n - 1) & 1u);
-        if (t == 0) sm.hurt[w.n & 3u] = 0u;
-        asm volatile("bar.sync 2, 128;" ::: "memory");               // the last part's offsets are read, the flag is down
-        // ---- queries
-        const uint32_t q_rows = both ? 256u : 128u;
-        if (!E) {
-            constexpr uint32_t CH = DP / 8;                          // 16-byte chunks of a row
-            for (uint32_t x = t; x < q_rows * CH; x += 128u) {
-                const uint32_t row = x / CH, ch = x % CH, all = w.rt * kTcRows + row, node = all / a.group, g = all - node * a.group;
-                const bool live = node < w.q.n && ch * 8u < a.c.head_dim;
-                const uint16_t *src = live ? a.q + (uint64_t)(w.q.row0 + node) * a.q_row_stride +
-                                                 (uint64_t)(w.h * a.group + g) * a.q_head_stride + ch * 8u : a.q;
-                const uint32_t dst = q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        } else {
-            // fp16 after a power-of-two scale per row (skv_attend.cu): one thread per row
-            for (uint32_t row = t; row < q_rows; row += 128u) {
-                const uint32_t all = w.rt * kTcRows + row, node = all / a.group, g = all - node * a.group;
-                const bool live = node < w.q.n;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    live ? a.q + (uint64_t)(w.q.row0 + node) * a.q_row_stride + (uint64_t)(w.h * a.group + g) * a.q_head_stride : a.q);
-                float top = 0.0f;
-                const uint32_t chunks = live ? a.c.head_dim / 8u : 0u;
-                for (uint32_t ch = 0; ch < chunks; ++ch) {
-                    const uint4 v = __ldg(src + ch);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
-                }
-                const uint32_t e = __float_as_uint(top) >> 23;
-                const bool usual = e > 2u && e < 252u;
-                const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
-                sm.mul[w.n & 1u][row] = usual ? __uint_as_float(e << 23) : 1.0f;
-                for (uint32_t ch = 0; ch < DP / 8u; ++ch) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (ch < chunks) {
-                        v = __ldg(src + ch);
-                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = tc_pack<true>(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xFFFF0000u) * down);
-                        v = make_uint4(x[0], x[1], x[2], x[3]);
-                    }
-                    st_shared16(q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4), v);
-                }
-            }
-        }
-        proxy_fence();
-        warp_arrive(&sm.q_full);
+        fill_queries<DP, E>(a, w, sm, q_at);
         // ---- K and V tiles
         // Offsets of a tile's positions: a thread each, into one of four places, a tile ahead.
         uint64_t next_at = ~0ull;
@@ -447,10 +472,161 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
     }
 }
 
+// Pages of a multiple of 8 positions: a tile is 128 / box boxes, box the largest power of
+// two up to 128 that divides the page length, so that no box crosses a page. A lane
+// per box looks the page up one tile ahead and starts the box's copies; a page number
+// outside the pool is outside the tensor and reads 0. Boxes past the part's end are
+// not copied: their scores are not used and finish_role clears their V.
+template <int DP, bool E>
+__device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t ring_at, uint32_t raw_at,
+                                         const CUtensorMap *kmap, const CUtensorMap *vmap, bool &corrupt) {
+    using S = TcShape<DP, E>;
+    const uint32_t lane = threadIdx.x & 31u, boxes = kTile / a.box;
+    uint32_t pos = 0;
+    Walk w;
+    for (w.start(a, sh); w.more(); w.next(a)) {
+        const bool both = w.both();
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        int32_t next_page = 0;
+        const auto look_up = [&](uint32_t k) {
+            const uint32_t p = (w.tile + k) * kTile + lane * a.box;
+            if (k < T && lane < boxes && p < p_end) {
+                next_page = __ldg(a.c.table + (uint64_t)w.r * a.c.table_stride + div_by(p, a.c.page));
+                if ((uint32_t)next_page >= a.c.n_pages) {
+                    corrupt = true;
+                    next_page = (int32_t)a.c.n_pages;
+                }
+            }
+        };
+        look_up(0);
+        for (uint32_t e = 0; e < 2 * T; ++e) {
+            bool is_v;
+            const uint32_t k = fill_of(both, T, e, is_v), n = pos + e, p0 = (w.tile + k) * kTile;
+            if (!is_v) {
+                if (lane < 16u) sm.pages[k & 3u][lane] = next_page;
+                __syncwarp();
+                look_up(k + 1);
+            }
+            const uint32_t slot = n % S::ring;
+            const void *bar;
+            uint32_t dst;
+            if (E) {
+                bar_wait(sm, &sm.taken[slot], ((n / S::ring) & 1u) ^ 1u);
+                bar = &sm.landed[slot];
+                dst = raw_at + slot * S::raw_tile;
+            } else {
+                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
+                bar = is_v && p0 + kTile > w.q.ctx ? &sm.landed[slot] : &sm.full[slot];
+                dst = ring_at + slot * S::tile;
+            }
+            const uint32_t live = min(boxes, (p_end - p0 + a.box - 1) / a.box);
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(s32(bar)), "r"(live * a.box * DP * (E ? 1u : 2u)) : "memory");
+            __syncwarp();
+            if (lane < live) {
+                const int32_t page = sm.pages[k & 3u][lane];
+                const uint32_t p = p0 + lane * a.box, token = p - div_by(p, a.c.page) * a.c.page.d;
+                const CUtensorMap *map = is_v ? vmap : kmap;
+                if (E) {
+                    tc_box(dst + lane * a.box * DP, map, 0u, w.h, token, page, bar);
+                } else {
+#pragma unroll
+                    for (uint32_t b = 0; b < DP / 64; ++b)
+                        tc_box(dst + b * S::block + lane * a.box * 128u, map, 64u * b, w.h, token, page, bar);
+                }
+            }
+            __syncwarp();
+        }
+        pos += 2 * T;
+    }
+}
+
+// Beside box_role: queries; every tile of an 8-bit cache raised to fp16; and in V tiles with
+// drafted positions, what is not finite there, and what lies past the end, put to 0.
+template <int DP, bool E>
+__device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t q_at, uint32_t ring_at,
+                                            uint32_t raw_at) {
+    using S = TcShape<DP, E>;
+    const uint32_t t = threadIdx.x - 256u;
+    uint32_t pos = 0, turns = 0;                                     // turns: parity of landed[] by slot (bf16)
+    Walk w;
+    for (w.start(a, sh); w.more(); w.next(a)) {
+        const bool both = w.both();
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        fill_queries<DP, E>(a, w, sm, q_at);
+        for (uint32_t e = 0; e < 2 * T; ++e) {
+            bool is_v;
+            const uint32_t k = fill_of(both, T, e, is_v), n = pos + e, p0 = (w.tile + k) * kTile, slot = n % S::ring;
+            const bool edge = is_v && p0 + kTile > w.q.ctx;
+            if (!E && !edge) continue;
+            const uint32_t first = w.q.ctx > p0 ? w.q.ctx - p0 : 0u, last = min(kTile, p_end - p0);     // drafted rows [first, last)
+            bool found = false;
+            if (!E) {
+                bar_wait(sm, &sm.landed[slot], (turns >> slot) & 1u);
+                turns ^= 1u << slot;
+                constexpr uint32_t CH = DP / 8;
+                for (uint32_t x = first * CH + t; x < kTile * CH; x += 128u) {
+                    const uint32_t row = x / CH, ch = x % CH;
+                    const uint32_t at = ring_at + slot * S::tile + (ch >> 3) * S::block + row * 128u + (((ch ^ row) & 7u) << 4);
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+                    bool hit = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if ((v[j] & 0x7F80u) == 0x7F80u) v[j] &= 0xFFFF0000u, hit = true;
+                        if ((v[j] & 0x7F800000u) == 0x7F800000u) v[j] &= 0xFFFFu, hit = true;
+                    }
+                    if (row >= last) st_shared16(at, make_uint4(0u, 0u, 0u, 0u));
+                    else if (hit) st_shared16(at, make_uint4(v[0], v[1], v[2], v[3])), found = true;
+                }
+            } else {
+                bar_wait(sm, &sm.landed[slot], (n / S::ring) & 1u);
+                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
+                constexpr uint32_t CH = DP / 16, PER = kTile * CH / 128;
+                uint32_t c[PER][4];
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i)
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3])
+                                 : "r"(raw_at + slot * S::raw_tile + (i * 128u + t) * 16u) : "memory");
+                warp_arrive(&sm.taken[slot]);
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i) {
+                    const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
+                    if (edge && row >= first) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                            for (int b = 0; b < 32; b += 8)
+                                if (row < last && ((c[i][j] >> b) & 0x7Fu) == 0x7Fu) c[i][j] &= ~(0xFFu << b), found = true;
+                            if (row >= last) c[i][j] = 0u;
+                        }
+                    }
+                    const uint32_t at = ring_at + slot * S::tile + (ch >> 2) * S::block + row * 128u, c0 = 2u * ch;
+                    const uint4 lo = make_uint4(tc_raise2(c[i][0]), tc_raise2(c[i][0] >> 16), tc_raise2(c[i][1]), tc_raise2(c[i][1] >> 16));
+                    const uint4 hi = make_uint4(tc_raise2(c[i][2]), tc_raise2(c[i][2] >> 16), tc_raise2(c[i][3]), tc_raise2(c[i][3] >> 16));
+                    // even chunks of one 64-channel block and odd ones of the other at a time: no two on the same banks
+                    const bool turn = (ch >> 2) & 1u;
+                    st_shared16(at + (((c0 + turn) ^ row) & 7u) * 16u, turn ? hi : lo);
+                    st_shared16(at + (((c0 + 1u - turn) ^ row) & 7u) * 16u, turn ? lo : hi);
+                }
+            }
+            if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
+            proxy_fence();
+            if (E) {
+                warp_arrive(&sm.full[slot]);
+            } else {
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (t == 0) bar_arrive(&sm.full[slot]);
+            }
+        }
+        pos += 2 * T;
+    }
+}
+
 template <int DP, bool E>
 __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t q_at, uint32_t ring_at,
                                              uint32_t tmem) {
-    using S = TcShape<DP>;
+    using S = TcShape<DP, E>;
     // binary32 accumulators; both inputs fp16 (0) or bf16 (1); 128 rows
     constexpr uint32_t kind0 = (1u << 4) | ((E ? 0u : 1u) << 7) | ((E ? 0u : 1u) << 10) | (8u << 24);
     constexpr uint32_t kind_s = kind0 | ((kTile >> 3) << 17), kind_o = kind0 | (1u << 16) | (((uint32_t)DP >> 3) << 17);
@@ -740,19 +916,23 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
 }
 
 template <int DP, bool E>
-__global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, AttendWs ws) {
-    using S = TcShape<DP>;
+__global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a, const AttendWs ws,
+                                                              const __grid_constant__ CUtensorMap kmap,
+                                                              const __grid_constant__ CUtensorMap vmap) {
+    using S = TcShape<DP, E>;
     extern __shared__ uint8_t dyn[];
     __shared__ TcShared sm;
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Share sh = share_of<kTcThreads>(a, ws, kTcRows, kTile, sm.plan);
     if (sh.u0 == sh.u1) return;
-    const uint32_t q_at = (s32(dyn) + 1023u) & ~1023u, ring_at = q_at + 2u * S::tile;
+    const uint32_t q_at = (s32(dyn) + 1023u) & ~1023u, ring_at = q_at + 2u * S::tile, raw_at = q_at + S::raw_at;
     if (tid == 0) {
         for (uint32_t i = 0; i < S::ring; ++i) {
-            bar_init(&sm.full[i], 4u);
+            bar_init(&sm.full[i], a.box && !E ? 1u : 4u);     // the copies' own arrival, or four warps'
             bar_init(&sm.empty[i], 1u);
+            bar_init(&sm.landed[i], 1u);
+            bar_init(&sm.taken[i], 4u);
         }
         for (uint32_t i = 0; i < 2; ++i) {
             bar_init(&sm.s_full[i], 1u);
@@ -780,9 +960,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, Atte
         weight_role<DP, E>(a, ws, sh, sm, tmem);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-        fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
+        if (a.box) finish_role<DP, E>(a, sh, sm, q_at, ring_at, raw_at);
+        else fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 13 && a.box) box_role<DP, E>(a, sh, sm, ring_at, raw_at, &kmap, &vmap, corrupt);
         if (warp == 12) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
     }
     __syncwarp();
@@ -798,13 +980,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(AttendArgs a, Atte
     }
 }
 
+// The driver's tensor-map encoder, through the runtime (the library does not link libcuda).
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encoder() {
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled f = known.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeTiled>(p);
+        known.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
+// A pool as a tensor [page][token][head][channel] read in boxes of `box` tokens of one head.
+static bool pool_map(CUtensorMap *map, const PagedView &c, const uint8_t *pool, uint32_t DP) {
+    const EncodeTiled f = encoder();
+    if (!f) return false;
+    const bool e = c.e4m3;
+    const cuuint64_t dims[4] = {c.head_dim, c.n_heads, c.page.d, c.n_pages};
+    // the stride of a dimension of one entry is never used, but has to be a valid one
+    const cuuint64_t strides[3] = {c.n_heads > 1 ? c.head_stride : 16u, c.page.d > 1 ? c.token_stride : 16u,
+                                   c.n_pages > 1 ? c.page_stride : 16u};
+    const cuuint32_t box[4] = {e ? DP : 64u, 1u, paged_box(c), 1u}, one[4] = {1u, 1u, 1u, 1u};
+    return f(map, e ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t *>(pool), dims, strides,
+             box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, e ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP, bool E>
-static bool launch(const AttendArgs &a, const AttendWs &ws, cudaStream_t st) {
+static bool launch(AttendArgs a, const AttendWs &ws, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
-    constexpr uint32_t bytes = TcShape<DP>::smem;
-    static_assert(bytes + sizeof(TcShared) <= 232448, "shared memory of a CTA");
+    constexpr uint32_t bytes = TcShape<DP, E>::smem;
+    static_assert(bytes + sizeof(TcShared) + 1024 <= 232448 && TcShape<DP, E>::ring <= 8, "shared memory of a CTA");
     if (!raise_smem(reinterpret_cast<const void *>(attend_large<DP, E>), bytes, ready)) return false;
-    attend_large<DP, E><<<kCtasLarge, kTcThreads, bytes, st>>>(a, ws);
+    CUtensorMap kmap = {}, vmap = {};
+    // strides reach 2^41 bytes, a tensor map's less than 2^40
+    a.box = a.c.page_stride < (uint64_t(1) << 40) && a.c.token_stride < (uint64_t(1) << 40) && a.c.head_stride < (uint64_t(1) << 40)
+                ? paged_box(a.c) : 0u;
+    if (a.box && !(pool_map(&kmap, a.c, a.c.k, DP) && pool_map(&vmap, a.c, a.c.v, DP))) a.box = 0u;    // row by row
+    attend_large<DP, E><<<kCtasLarge, kTcThreads, bytes, st>>>(a, ws, kmap, vmap);
     return cudaGetLastError() == cudaSuccess && launch_join(a, ws, kTcRows, DP, kCtasLarge, st);
 }
 

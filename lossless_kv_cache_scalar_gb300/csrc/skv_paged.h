@@ -64,7 +64,14 @@ struct AttendArgs {
     uint16_t *out;
     float *lse;               // or NULL
     int32_t *status;
+    uint32_t box;             // positions of a tensor copy, 0: none fits the page length
 };
+
+// The largest power of two up to 128 that divides the page length, if that is 8 or more.
+inline uint32_t paged_box(const PagedView &c) {
+    const uint32_t low = c.page.d & (~c.page.d + 1u);
+    return low > 128u ? 128u : low >= 8u ? low : 0u;
+}
 
 inline PagedView paged_view(const skv_paged &c) {
     const uint64_t b = c.dtype == SKV_BF16 ? 2u : 1u;
