@@ -10,8 +10,8 @@
 // trees). It is bound by reading the pages: every K and V value enters one
 // 16-row product, 2 x 16 multiply-adds per code, far below what even the
 // warp-level matrix instructions need to keep up with HBM. So each warp is a
-// stream of its own: it takes every fourth run of 16 positions of its CTA's
-// share through a private ring in shared memory, filled 16 bytes at a time by
+// stream of its own: it takes every fourth run of 16 positions (32 of an
+// e4m3 cache) of its CTA's share through a private ring in shared memory, filled 16 bytes at a time by
 // asynchronous copies that look the page up per position (a page may end
 // anywhere, a row may lie at any 16-byte multiple), and keeps its own maximum,
 // sum and output; no barrier inside the loop. The four are joined at the end of
@@ -30,14 +30,17 @@
 
 namespace skv {
 
-constexpr uint32_t kWarps = 4, kRun = 16, kUnit = kWarps * kRun;
+constexpr uint32_t kWarps = 4;
 
 template <int DP, bool E>
 struct SmallShape {
     static constexpr uint32_t bytes = E ? 1 : 2;
+    static constexpr uint32_t run = E ? 32 : 16;           // positions of a warp at a time
+    static constexpr uint32_t unit = kWarps * run;
+    static constexpr uint32_t groups = run / 16;
     static constexpr uint32_t row = DP * bytes;            // bytes of a position's row in the ring
     static constexpr uint32_t chunks = row / 16;
-    static constexpr uint32_t half = kRun * row;           // K, then V
+    static constexpr uint32_t half = run * row;           // K, then V
     static constexpr uint32_t stage = 2 * half;
     static constexpr uint32_t want = 24576 / stage;        // 24 KB per warp
     static constexpr uint32_t stages = want < 2 ? 2 : want > 8 ? 8 : want;
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
     __shared__ unsigned long long sm_plan[kWarps + 4];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, c4 = lane & 3u, g8 = lane >> 2;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share sh = share_of<kWarps * 32>(a, ws, 16u, kUnit, sm_plan);
+    const Share sh = share_of<kWarps * 32>(a, ws, 16u, S::unit, sm_plan);
     if (sh.u0 == sh.u1) return;
     const uint32_t ring = smem_of(ring_all) + warp * S::ring;
     const uint32_t row_bytes = a.c.head_dim * S::bytes;
@@ -192,23 +195,24 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
 
     uint32_t r = sh.r;
     ReqOf q = request_of(a, r);
-    uint32_t tiles = (q.len + kUnit - 1) / kUnit, rts = (q.n * a.group + 15u) / 16u;
+    constexpr uint32_t G = S::groups;
+    uint32_t tiles = (q.len + S::unit - 1) / S::unit, rts = (q.n * a.group + 15u) / 16u;
     uint64_t item = sh.off / tiles;
     uint32_t tile = (uint32_t)(sh.off - item * tiles);
     for (uint64_t u = sh.u0; u < sh.u1;) {
         // one part: head h, row tile rt, tiles [tile, tile_end) of the request
         const uint32_t h = (uint32_t)(item / rts), rt = (uint32_t)(item - (uint64_t)h * rts);
         const uint32_t tile_end = (uint32_t)min((uint64_t)tiles, tile + (sh.u1 - u));
-        const uint32_t p_begin = tile * kUnit, p_end = min(q.len, tile_end * kUnit);
-        const uint32_t runs = (p_end - p_begin + kRun - 1) / kRun;
+        const uint32_t p_begin = tile * S::unit, p_end = min(q.len, tile_end * S::unit);
+        const uint32_t runs = (p_end - p_begin + S::run - 1) / S::run;
         const uint32_t mine = runs > warp ? (runs - warp + kWarps - 1) / kWarps : 0u;
         bool hurt = false;                       // this warp put 0 for a value that is not finite
 
-        // The page of this lane's position (lanes 0-15) in run i of this warp, one run ahead of its copies.
+        // The page of this lane's position in run i of this warp, one run ahead of its copies.
         uint64_t next_at = ~0ull;
         auto look_up = [&](uint32_t i) {
             next_at = ~0ull;
-            const uint32_t p = p_begin + (warp + i * kWarps) * kRun + (lane & 15u);
+            const uint32_t p = p_begin + (warp + i * kWarps) * S::run + (lane & (S::run - 1u));
             if (i < mine && p < p_end) {
                 next_at = place_of(a.c, r, h, p);
                 corrupt |= next_at == ~0ull;
@@ -218,10 +222,10 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
             if (i < mine) {
                 const uint32_t st = ring + (i % S::stages) * S::stage;
 #pragma unroll
-                for (uint32_t n = 0; n < (kRun * S::chunks + 31) / 32; ++n) {
+                for (uint32_t n = 0; n < (S::run * S::chunks + 31) / 32; ++n) {
                     const uint32_t x = n * 32u + lane, row = x / S::chunks, ch = x % S::chunks;
-                    const uint64_t at = __shfl_sync(~0u, next_at, row & 15u);
-                    if (row < kRun) {
+                    const uint64_t at = __shfl_sync(~0u, next_at, row & (S::run - 1u));
+                    if (row < S::run) {
                         const bool live = at != ~0ull && ch * 16u < row_bytes;
                         const uint64_t off = live ? at + ch * 16u : 0ull;
                         copy16(st + row * S::row + swz_k<DP, E>(row, ch) * 16u, a.c.k + off, live ? 16u : 0u);
@@ -248,12 +252,12 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
             __syncwarp();
             issue(i + S::stages - 1);
             const uint32_t st = ring + (i % S::stages) * S::stage, sv = st + S::half;
-            const uint32_t p0 = p_begin + (warp + i * kWarps) * kRun;
-            const bool edge = p0 + kRun > q.ctx || p0 + kRun > p_end;
-            if (edge && p0 + kRun > q.ctx) {
+            const uint32_t p0 = p_begin + (warp + i * kWarps) * S::run;
+            const bool edge = p0 + S::run > q.ctx || p0 + S::run > p_end;
+            if (edge && p0 + S::run > q.ctx) {
                 // drafted positions: values that are not finite leave the product
                 bool found = false;
-                for (uint32_t x = lane; x < kRun * S::chunks; x += 32u) {
+                for (uint32_t x = lane; x < S::run * S::chunks; x += 32u) {
                     const uint32_t row = x / S::chunks;
                     if (p0 + row < q.ctx) continue;
                     const uint32_t at = sv + x * 16u;
@@ -278,21 +282,26 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
                 hurt |= found;
                 __syncwarp();
             }
-            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (!E) {
-                const uint32_t row = (lane & 7u) + ((lane >> 4) << 3), hi = (lane >> 3) & 1u;
+            float s[2 * G][4];
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    uint32_t b[4];
-                    ldm4(b, st + row * S::row + swz_k<DP, E>(row, 2u * k + hi) * 16u);
-                    mma16<E>(s[0], qf.f[k], b[0], b[1]);
-                    mma16<E>(s[1], qf.f[k], b[2], b[3]);
+            for (int n = 0; n < 2 * (int)G; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            if (!E) {
+#pragma unroll
+                for (int y = 0; y < (int)G; ++y) {
+                    const uint32_t row = 16u * y + (lane & 7u) + ((lane >> 4) << 3), hi = (lane >> 3) & 1u;
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        uint32_t b[4];
+                        ldm4(b, st + row * S::row + swz_k<DP, E>(row, 2u * k + hi) * 16u);
+                        mma16<E>(s[2 * y], qf.f[k], b[0], b[1]);
+                        mma16<E>(s[2 * y + 1], qf.f[k], b[2], b[3]);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int b = 0; b < DP / 64; ++b) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int n = 0; n < 2 * (int)G; ++n) {
                         const uint32_t row = 8u * n + g8;
                         const uint4 w4 = lds128(st + row * S::row + swz_k<DP, E>(row, 4u * b + c4) * 16u);
                         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
             // scores in base 2; positions a row does not see are -infinity
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < 2 * (int)G; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int half = e >> 1;
@@ -341,55 +350,58 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
                     o[j][3] *= keep[1];
                 }
             }
-            uint32_t pa[4];
+            uint32_t pa[G][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < 2 * (int)G; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[n][e] = ex2(s[n][e] - base[e >> 1]);
                     l[e >> 1] += s[n][e];
                 }
-                pa[2 * n] = pack2<E>(s[n][0], s[n][1]);
-                pa[2 * n + 1] = pack2<E>(s[n][2], s[n][3]);
+                pa[n >> 1][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
+                pa[n >> 1][2 * (n & 1) + 1] = pack2<E>(s[n][2], s[n][3]);
             }
-            if (!E) {
-                const uint32_t row = lane & 15u, hi = lane >> 4;
 #pragma unroll
-                for (int j = 0; j < DP / 16; ++j) {
-                    uint32_t b[4];
-                    ldm4t(b, sv + row * S::row + swz_v<DP, E>(row, 2u * j + hi) * 16u);
-                    mma16<E>(o[2 * j], pa, b[0], b[1]);
-                    mma16<E>(o[2 * j + 1], pa, b[2], b[3]);
-                }
-            } else {
-                // column n of the output tile i is channel (DP / 8) n + i: a thread's bytes of four positions
-                constexpr int CW = DP / 32;                  // words of one position
-                constexpr int PW = CW < 4 ? CW : 4;          // at a time
+            for (int y = 0; y < (int)G; ++y) {
+                if (!E) {
+                    const uint32_t row = 16u * y + (lane & 15u), hi = lane >> 4;
 #pragma unroll
-                for (int part = 0; part < CW; part += PW) {
-                    uint32_t w[4][4];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t row = 2u * c4 + (t & 1) + 8u * (t >> 1);
-                        const uint32_t byte = g8 * (DP / 8) + part * 4u;
-                        const uint32_t at = sv + row * S::row + swz_v<DP, E>(row, byte >> 4) * 16u + (byte & 15u);
-                        if (PW == 4) {
-                            const uint4 x = lds128(at);
-                            w[t][0] = x.x, w[t][1] = x.y, w[t][2] = x.z, w[t][3] = x.w;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < PW; ++j) w[t][j] = lds32(at + 4u * j);
-                        }
+                    for (int j = 0; j < DP / 16; ++j) {
+                        uint32_t b[4];
+                        ldm4t(b, sv + row * S::row + swz_v<DP, E>(row, 2u * j + hi) * 16u);
+                        mma16<E>(o[2 * j], pa[y], b[0], b[1]);
+                        mma16<E>(o[2 * j + 1], pa[y], b[2], b[3]);
                     }
+                } else {
+                    // column n of the output tile i is channel (DP / 8) n + i: a thread's bytes of four positions
+                    constexpr int CW = DP / 32;              // words of one position
+                    constexpr int PW = CW < 4 ? CW : 4;      // at a time
 #pragma unroll
-                    for (int j = 0; j < PW; ++j) {
-                        const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), lo1 = __byte_perm(w[0][j], w[1][j], 0x7362);
-                        const uint32_t hi0 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
-                        const int i = (part + j) * 4;
-                        mma16<E>(o[i], pa, raise2(lo0), raise2(hi0));
-                        mma16<E>(o[i + 1], pa, raise2(lo0 >> 16), raise2(hi0 >> 16));
-                        mma16<E>(o[i + 2], pa, raise2(lo1), raise2(hi1));
-                        mma16<E>(o[i + 3], pa, raise2(lo1 >> 16), raise2(hi1 >> 16));
+                    for (int part = 0; part < CW; part += PW) {
+                        uint32_t w[4][4];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t row = 16u * y + 2u * c4 + (t & 1) + 8u * (t >> 1);
+                            const uint32_t byte = g8 * (DP / 8) + part * 4u;
+                            const uint32_t at = sv + row * S::row + swz_v<DP, E>(row, byte >> 4) * 16u + (byte & 15u);
+                            if (PW == 4) {
+                                const uint4 x = lds128(at);
+                                w[t][0] = x.x, w[t][1] = x.y, w[t][2] = x.z, w[t][3] = x.w;
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < PW; ++j) w[t][j] = lds32(at + 4u * j);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < PW; ++j) {
+                            const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), lo1 = __byte_perm(w[0][j], w[1][j], 0x7362);
+                            const uint32_t hi0 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+                            const int i = (part + j) * 4;
+                            mma16<E>(o[i], pa[y], raise2(lo0), raise2(hi0));
+                            mma16<E>(o[i + 1], pa[y], raise2(lo0 >> 16), raise2(hi0 >> 16));
+                            mma16<E>(o[i + 2], pa[y], raise2(lo1), raise2(hi1));
+                            mma16<E>(o[i + 3], pa[y], raise2(lo1 >> 16), raise2(hi1 >> 16));
+                        }
                     }
                 }
             }
@@ -475,7 +487,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
         if (u < sh.u1 && item == (uint64_t)a.c.n_heads * rts) {
             do q = request_of(a, ++r);
             while (q.n == 0);
-            tiles = (q.len + kUnit - 1) / kUnit;
+            tiles = (q.len + S::unit - 1) / S::unit;
             rts = (q.n * a.group + 15u) / 16u;
             item = 0;
         }
@@ -492,10 +504,15 @@ __global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, ui
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
-        int32_t err = SKV_OK;
-        for (uint32_t i = lane; i < ctas && !err; i += 32u) err = ws.errs[i];
-        const uint32_t any = __ballot_sync(~0u, err != SKV_OK);
-        err = __shfl_sync(~0u, err, any ? __ffs(any) - 1 : 0);
+        int32_t e[(kCtasSmall + 31u) / 32u], err = SKV_OK;
+#pragma unroll
+        for (uint32_t i = 0; i < (kCtasSmall + 31u) / 32u; ++i)      // all in flight at once
+            e[i] = i * 32u + lane < ctas ? __ldcg(ws.errs + i * 32u + lane) : SKV_OK;
+#pragma unroll
+        for (uint32_t i = 0; i < (kCtasSmall + 31u) / 32u; ++i) {
+            const uint32_t any = __ballot_sync(~0u, e[i] != SKV_OK);
+            if (any && err == SKV_OK) err = __shfl_sync(~0u, e[i], __ffs(any) - 1);
+        }
         if (lane == 0) *a.status = err;
     }
     const Desc d = ws.desc[c];
@@ -523,7 +540,7 @@ __global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, ui
             L += f * part(j0 + lane)[R + row];
         }
         const uint32_t here = min(32u, n - j0);
-#pragma unroll 4
+#pragma unroll 8
         for (uint32_t j = 0; j < here; ++j) {
             const float w = __shfl_sync(~0u, f, j);
             const float *src = part(j0 + j) + 2u * R + (uint64_t)row * DP;

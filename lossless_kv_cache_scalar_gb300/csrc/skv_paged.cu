@@ -15,9 +15,13 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "skv_paged.h"
 
 namespace skv {
+
+bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready);      // skv_attend.cu
 
 struct MapArgs {
     FastDiv page;
@@ -64,9 +68,10 @@ __device__ __forceinline__ MapOf map_of(const MapArgs &a, uint32_t r) {
 }
 
 // Exclusive prefix sums of three counts over the block, and their totals.
+template <uint32_t THREADS>
 __device__ __forceinline__ void scan3(uint32_t (&x)[3], uint32_t (&total)[3], uint32_t (*part)[32]) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    uint32_t in[3] = {x[0], x[1], x[2]};
+    const uint32_t in[3] = {x[0], x[1], x[2]};
 #pragma unroll
     for (uint32_t d = 1; d < 32; d <<= 1) {
 #pragma unroll
@@ -80,131 +85,158 @@ __device__ __forceinline__ void scan3(uint32_t (&x)[3], uint32_t (&total)[3], ui
         for (int j = 0; j < 3; ++j) part[j][warp] = x[j];
     }
     __syncthreads();
-    if (warp < 3) {
-        uint32_t p = lane < (blockDim.x >> 5) ? part[warp][lane] : 0u;
-        for (uint32_t d = 1; d < 32; d <<= 1) {
-            const uint32_t y = __shfl_up_sync(~0u, p, d);
-            if (lane >= d) p += y;
-        }
-        part[warp][lane] = p;
-    }
-    __syncthreads();
+    // every warp sums the warps' totals for itself: one barrier less
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-        x[j] += (warp ? part[j][warp - 1] : 0u) - in[j];
-        total[j] = part[j][31];
+        const uint32_t p = lane < THREADS / 32u ? part[j][lane] : 0u;
+        total[j] = __reduce_add_sync(~0u, p);
+        x[j] += __reduce_add_sync(~0u, lane < warp ? p : 0u) - in[j];
     }
-    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kMapThreads) map_kernel(MapArgs a) {
-    __shared__ unsigned long long sum[3];
-    __shared__ int32_t worst;
+// THREADS: 1,024, or 256 for a step so small that barriers are most of its time. A
+// thread keeps ITEMS requests in a row, so that THREADS * ITEMS requests need one scan.
+template <uint32_t THREADS, uint32_t ITEMS>
+__global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
+    constexpr uint32_t CHUNK = THREADS * ITEMS;
+    extern __shared__ uint32_t dyn[];
+    uint32_t *s_cu = dyn, *s_need = dyn + CHUNK + 1;
+    int32_t *s_ctx = reinterpret_cast<int32_t *>(s_need + CHUNK), *s_have = s_ctx + CHUNK;
+    __shared__ unsigned long long sum[3][32];
     __shared__ uint32_t part[3][32];
-    __shared__ uint32_t s_cu[kMapThreads + 1], s_need[kMapThreads];
-    __shared__ int32_t s_ctx[kMapThreads], s_have[kMapThreads];
-    const uint32_t tid = threadIdx.x, lane = tid & 31u;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const int32_t head = a.free_in[0], count = a.free_in[1];
 
     // Totals in 64 bits and every error that the lengths hold, before anything is written.
-    if (tid == 0) {
-        sum[0] = sum[1] = sum[2] = 0ull;
-        worst = 0;
-    }
-    __syncthreads();
+    MapOf mine[ITEMS];
     unsigned long long t[3] = {0ull, 0ull, 0ull};
     bool bad = false, full = false;
-    for (uint32_t r = tid; r < a.n_requests; r += blockDim.x) {
-        const MapOf m = map_of(a, r);
+#pragma unroll
+    for (uint32_t k = 0; k < ITEMS; ++k) mine[k] = map_of(a, tid * ITEMS + k);
+    const auto add = [&](const MapOf &m) {
         bad |= m.err == SKV_ERR_INVALID_ARG;
         full |= m.err == SKV_ERR_CAPACITY;
         t[0] += m.add;
         t[1] += m.need;
         t[2] += m.back;
-    }
+    };
+#pragma unroll
+    for (uint32_t k = 0; k < ITEMS; ++k) add(mine[k]);
+    for (uint32_t r = CHUNK + tid; r < a.n_requests; r += THREADS) add(map_of(a, r));
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         for (uint32_t d = 16; d; d >>= 1) t[j] += __shfl_xor_sync(~0u, t[j], d);
-        if (lane == 0 && t[j]) atomicAdd(&sum[j], t[j]);       // integers: any order gives the same sum
+        if (lane == 0) sum[j][warp] = t[j];
     }
-    if (bad) atomicOr(&worst, 1);
-    if (full) atomicOr(&worst, 2);
-    __syncthreads();
-    const int32_t head = a.free_in[0], count = a.free_in[1];
+    const int worst = __syncthreads_or((bad ? 1 : 0) | (full ? 2 : 0)) ? (__syncthreads_or(bad) ? 1 : 2) : 0;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        t[j] = lane < THREADS / 32u ? sum[j][lane] : 0ull;
+        for (uint32_t d = 16; d; d >>= 1) t[j] += __shfl_xor_sync(~0u, t[j], d);
+    }
     const bool ring_bad = count < 0 || (uint32_t)count > a.free_capacity || head < 0 ||
                           ((uint32_t)head >= a.free_capacity && (head != 0 || a.free_capacity != 0));
     int32_t err = SKV_OK;
-    if ((worst & 1) || ring_bad)
+    if (worst == 1 || ring_bad)
         err = SKV_ERR_INVALID_ARG;
-    else if ((worst & 2) || sum[1] > (unsigned long long)count || sum[0] > a.slot_capacity || sum[0] > INT32_MAX ||
-             (unsigned long long)count + sum[2] > a.free_capacity)
+    else if (worst || t[1] > (unsigned long long)count || t[0] > a.slot_capacity || t[0] > INT32_MAX ||
+             (unsigned long long)count + t[2] > a.free_capacity)
         err = SKV_ERR_CAPACITY;
 
-    // This CTA's slots: a run of pairs.
-    const uint64_t per = ((a.slot_capacity + gridDim.x - 1) / gridDim.x + 1) & ~uint64_t(1);
-    const uint64_t i0 = min((uint64_t)blockIdx.x * per, a.slot_capacity);
-    const uint64_t i1 = min(i0 + per, a.slot_capacity);
-    const uint32_t total = err ? 0u : (uint32_t)sum[0];
-    for (uint64_t i = max(i0, (uint64_t)total) + tid; i < i1; i += blockDim.x) a.slots[i] = -1;
+    // This CTA's share of the tokens' slots, and of the -1 behind them.
+    const uint64_t total = err ? 0u : t[0], tail = a.slot_capacity - total;
+    const uint64_t per = ((total + gridDim.x - 1) / gridDim.x + 1) & ~uint64_t(1);
+    const uint64_t i0 = min((uint64_t)blockIdx.x * per, total), i1 = min(i0 + per, total);
+    {
+        const uint64_t each = ((tail + gridDim.x - 1) / gridDim.x + 1) & ~uint64_t(1);
+        const uint64_t b0 = min((uint64_t)blockIdx.x * each, tail) + total, b1 = min((uint64_t)(blockIdx.x + 1u) * each, tail) + total;
+        // 16 bytes at a time between the first and the last even entry
+        const uint64_t e0 = min((b0 + 1) & ~uint64_t(1), b1), e1 = max(b1 & ~uint64_t(1), e0);
+        const bool wide = ((uintptr_t)a.slots & 15u) == 0;
+        if (wide) {
+            for (uint64_t i = e0 + 2 * tid; i < e1; i += 2 * THREADS)
+                *reinterpret_cast<longlong2 *>(a.slots + i) = make_longlong2(-1ll, -1ll);
+            if (tid == 0 && b0 < e0) a.slots[b0] = -1;
+            if (tid == 1 && e1 < b1) a.slots[e1] = -1;
+        } else {
+            for (uint64_t i = b0 + tid; i < b1; i += THREADS) a.slots[i] = -1;
+        }
+    }
     if (blockIdx.x == 0 && tid == 0) {
         if (gridDim.x == 1) *a.status = err;
         else if (err) set_first(a.status, err);
         const uint32_t cap = max(a.free_capacity, 1u);
-        a.free_out[0] = err ? head : (int32_t)(((uint64_t)head + sum[1]) % cap);
-        a.free_out[1] = err ? count : (int32_t)(count - sum[1] + sum[2]);
+        uint64_t to = (uint64_t)head + t[1];
+        if (to >= cap) to -= cap;                     // head < cap, at most cap taken
+        a.free_out[0] = err ? head : (int32_t)to;
+        a.free_out[1] = err ? count : (int32_t)(count - t[1] + t[2]);
         a.cu[a.n_requests] = (int32_t)total;
     }
     if (err) {
         if (blockIdx.x == 0) {
-            for (uint32_t r = tid; r < a.n_requests; r += blockDim.x) {
+            for (uint32_t r = tid; r < a.n_requests; r += THREADS) {
                 a.n_out[r] = a.n_in[r];
                 a.cu[r] = 0;
             }
         }
         return;
     }
-    if (gridDim.x == 1) __syncthreads();          // the OK above comes before any CORRUPT below
     bool corrupt = false;
     uint32_t carry[3] = {0u, 0u, 0u};
-    for (uint32_t base = 0; base < a.n_requests; base += blockDim.x) {
-        const uint32_t r = base + tid;
-        const MapOf m = map_of(a, r);
-        uint32_t x[3] = {m.add, m.need, m.back}, tot[3];
-        scan3(x, tot, part);
+    for (uint32_t base = 0; base < a.n_requests; base += CHUNK) {
+        if (base) {
+#pragma unroll
+            for (uint32_t k = 0; k < ITEMS; ++k) mine[k] = map_of(a, base + tid * ITEMS + k);
+        }
+        uint32_t x[3] = {0u, 0u, 0u}, tot[3];
+#pragma unroll
+        for (uint32_t k = 0; k < ITEMS; ++k) {
+            x[0] += mine[k].add;
+            x[1] += mine[k].need;
+            x[2] += mine[k].back;
+        }
+        __syncthreads();                              // the last chunk's sums and slots are done
+        scan3<THREADS>(x, tot, part);
 #pragma unroll
         for (int j = 0; j < 3; ++j) x[j] += carry[j];
-        s_cu[tid] = x[0];
-        s_need[tid] = x[1];
-        s_ctx[tid] = m.ctx;
-        s_have[tid] = m.have;
-        if (tid == 0) s_cu[blockDim.x] = carry[0] + tot[0];
-        if (blockIdx.x == 0 && r < a.n_requests) {
-            a.cu[r] = (int32_t)x[0];
-            a.n_out[r] = m.ctx < 0 ? 0 : m.have + (int32_t)m.need;
-        }
-        // Pages of ended requests, one warp per request, requests dealt over the CTAs.
-        uint32_t ended = __ballot_sync(~0u, m.back != 0u && r % gridDim.x == blockIdx.x);
-        while (ended) {
-            const uint32_t l = __ffs(ended) - 1u;
-            ended &= ended - 1u;
-            const uint32_t back = __shfl_sync(~0u, m.back, l), before = __shfl_sync(~0u, x[2], l);
-            const int32_t *row = a.table + (uint64_t)__shfl_sync(~0u, r, l) * a.table_stride;
-            for (uint32_t j = lane; j < back; j += 32u) {
-                const int32_t p = row[j];
-                corrupt |= (uint32_t)p >= a.pool_pages;
-                a.free_pages[((uint64_t)head + (uint32_t)count + before + j) % a.free_capacity] = p;
+        if (tid == 0) s_cu[CHUNK] = carry[0] + tot[0];
+#pragma unroll
+        for (uint32_t k = 0; k < ITEMS; ++k) {
+            const MapOf &m = mine[k];
+            const uint32_t at = tid * ITEMS + k, r = base + at;
+            s_cu[at] = x[0];
+            s_need[at] = x[1];
+            s_ctx[at] = m.ctx;
+            s_have[at] = m.have;
+            if (r < a.n_requests && r % gridDim.x == blockIdx.x) {
+                a.cu[r] = (int32_t)x[0];
+                a.n_out[r] = m.ctx < 0 ? 0 : m.have + (int32_t)m.need;
             }
+            // Pages of ended requests, one warp per request, requests dealt over the CTAs.
+            uint32_t ended = __ballot_sync(~0u, m.back != 0u && r % gridDim.x == blockIdx.x);
+            while (ended) {
+                const uint32_t l = __ffs(ended) - 1u;
+                ended &= ended - 1u;
+                const uint32_t back = __shfl_sync(~0u, m.back, l), before = __shfl_sync(~0u, x[2], l);
+                const int32_t *row = a.table + (uint64_t)__shfl_sync(~0u, r, l) * a.table_stride;
+                for (uint32_t j = lane; j < back; j += 32u) {
+                    const int32_t p = row[j];
+                    corrupt |= (uint32_t)p >= a.pool_pages;
+                    uint64_t to = (uint64_t)head + (uint32_t)count + before + j;      // below 2 free_capacity
+                    if (to >= a.free_capacity) to -= a.free_capacity;
+                    a.free_pages[to] = p;
+                }
+            }
+            x[0] += m.add;
+            x[1] += m.need;
+            x[2] += m.back;
         }
         __syncthreads();
-        // The slots of this chunk of requests that lie in this CTA's run.
-        const uint64_t lo = max(i0, (uint64_t)s_cu[0]), hi = min(i1, (uint64_t)s_cu[blockDim.x]);
-        for (uint64_t i = lo + tid; i < hi; i += blockDim.x) {
-            uint32_t f = 0, n = blockDim.x;                       // last request with cu <= i
-            while (n > 1) {
-                const uint32_t h = n >> 1;
-                if (s_cu[f + h] <= (uint32_t)i) f += h;
-                n -= h;
-            }
-            const uint32_t at = (uint32_t)i - s_cu[f], pos = (uint32_t)s_ctx[f] + at;
+        // The slots of this chunk of requests that lie in this CTA's run, two to a thread.
+        const uint64_t lo = max(i0, (uint64_t)s_cu[0]), hi = min(i1, (uint64_t)s_cu[CHUNK]);
+        const uint32_t live = min(CHUNK, a.n_requests - base);
+        const auto slot_of = [&](uint32_t i, uint32_t f) {
+            const uint32_t pos = (uint32_t)s_ctx[f] + (i - s_cu[f]);
             const uint32_t j = div_by(pos, a.page), off = pos - j * a.page.d;
             int32_t p;
             if (j < (uint32_t)s_have[f]) {
@@ -217,13 +249,47 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(MapArgs a) {
             }
             const bool ok = (uint32_t)p < a.pool_pages;
             corrupt |= !ok;
-            a.slots[i] = ok ? (int64_t)p * a.page.d + off : -1;
+            return ok ? (int64_t)p * a.page.d + off : -1ll;
+        };
+#pragma unroll 2
+        for (uint64_t i = (lo & ~uint64_t(1)) + 2 * tid; i < hi; i += 2 * THREADS) {
+            const uint32_t first = (uint32_t)max(i, lo);
+            uint32_t f = 0, n = live;                             // last request with cu <= first
+            while (n > 1) {
+                const uint32_t h = n >> 1;
+                if (s_cu[f + h] <= first) f += h;
+                n -= h;
+            }
+            int64_t v[2];
+            v[0] = slot_of(first, f);
+            if (i >= lo && i + 1 < hi) {
+                while (s_cu[f + 1] <= first + 1) ++f;             // past requests without tokens
+                v[1] = slot_of(first + 1, f);
+                if (((uintptr_t)a.slots & 15u) == 0) {
+                    *reinterpret_cast<longlong2 *>(a.slots + i) = make_longlong2(v[0], v[1]);
+                } else {
+                    a.slots[i] = v[0];
+                    a.slots[i + 1] = v[1];
+                }
+            } else {
+                a.slots[first] = v[0];
+            }
         }
-        __syncthreads();
 #pragma unroll
         for (int j = 0; j < 3; ++j) carry[j] += tot[j];
     }
     if (corrupt) set_first(a.status, SKV_ERR_CORRUPT);
+}
+
+template <uint32_t THREADS, uint32_t ITEMS>
+static bool launch_map(const MapArgs &a, unsigned grid, cudaStream_t st) {
+    constexpr uint32_t bytes = (4u * THREADS * ITEMS + 1u) * 4u;
+    if (bytes > 48u * 1024u) {
+        static std::atomic<uint64_t> ready{0};
+        if (!raise_smem(reinterpret_cast<const void *>(map_kernel<THREADS, ITEMS>), bytes, ready)) return false;
+    }
+    map_kernel<THREADS, ITEMS><<<grid, THREADS, bytes, st>>>(a);
+    return cudaGetLastError() == cudaSuccess;
 }
 
 struct AppendArgs {
@@ -235,7 +301,8 @@ struct AppendArgs {
     const uint16_t *k_new, *v_new;
     uint64_t row_stride, row_head_stride;             // elements
     uint32_t n_src, n;
-    uint32_t n_heads, units;                          // units of 16 source bytes or 16 channels per head
+    FastDiv units, per_row;                           // units of 16 source bytes or 16 channels, per head and per row
+    uint32_t narrow;                                  // 1: units and slots of this call fit 31 bits
     const int32_t *rows;
     const int64_t *slots;
     int32_t *status;
@@ -244,32 +311,37 @@ struct AppendArgs {
 
 // The e4m3 code nearest to x / s. The binary32 quotient alone can land on a tie
 // that the real quotient only comes near, so it is rounded to odd first: the
-// remainder x - q s is exact in an fma, and where it is not 0 the quotient is
-// cut towards 0 and its last bit set, which keeps it off every border of the
-// much coarser code grid.
-__device__ __forceinline__ uint32_t e4m3_of(float x, float s) {
-    float q = __fdiv_rn(x, s);
-    const float rem = fmaf(-q, s, x);
-    if (fabsf(q) >= 1.0e-30f && fabsf(q) < 1.0e30f && rem != 0.0f) {
+// remainder x - q s is exact in an fma for any q within a step of the quotient, and
+// where it is not 0 the quotient is cut towards 0 and its last bit set, which keeps it
+// off every border of the much coarser code grid. q: one product with the
+// reciprocal r of s and one correction by the remainder; for scales whose
+// reciprocal may not be normal (r = 0) a division.
+__device__ __forceinline__ uint32_t e4m3_of(float x, float s, float r) {
+    float q = r != 0.0f ? x * r : __fdiv_rn(x, s);
+    if (fabsf(q) >= 1.0e-30f && fabsf(q) < 1.0e30f) {
+        q = fmaf(fmaf(-q, s, x), r, q);
+        const float rem = fmaf(-q, s, x);
         uint32_t b = __float_as_uint(q);
         // the remainder's sign against the quotient's (s > 0): q is too large in magnitude
         if ((__float_as_uint(rem) ^ b) >> 31) --b;
-        q = __uint_as_float(b | 1u);
+        if (rem != 0.0f) q = __uint_as_float(b | 1u);
     }
     return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
+__device__ __forceinline__ float reciprocal_of(float s) { return s > 1.0e-30f && s < 1.0e30f ? __fdiv_rn(1.0f, s) : 0.0f; }
+
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 // 16 bytes of codes from 16 channels of a bf16 row (two 16-byte loads).
-__device__ __forceinline__ uint4 quantise16(const uint16_t *src, float s) {
+__device__ __forceinline__ uint4 quantise16(const uint16_t *src, float s, float r) {
     const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        o[i] = e4m3_of(bf16_float(w[2 * i] & 0xFFFFu), s) | (e4m3_of(bf16_float(w[2 * i] >> 16), s) << 8) |
-               (e4m3_of(bf16_float(w[2 * i + 1] & 0xFFFFu), s) << 16) | (e4m3_of(bf16_float(w[2 * i + 1] >> 16), s) << 24);
+        o[i] = e4m3_of(bf16_float(w[2 * i] & 0xFFFFu), s, r) | (e4m3_of(bf16_float(w[2 * i] >> 16), s, r) << 8) |
+               (e4m3_of(bf16_float(w[2 * i + 1] & 0xFFFFu), s, r) << 16) | (e4m3_of(bf16_float(w[2 * i + 1] >> 16), s, r) << 24);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -278,35 +350,40 @@ template <bool E4M3>
 __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
     bool bad = false;
     if (a.checked && blockIdx.x == 0) {
-        for (uint32_t i = threadIdx.x; i < a.n; i += blockDim.x) {
-            const int64_t s = a.slots[i];
-            bad |= s >= 0 && ((uint64_t)s >= a.pool_tokens || (a.rows && (uint32_t)a.rows[i] >= a.n_src) ||
-                              (!a.rows && i >= a.n_src));
+        // loads of eight rounds in flight at once (checked: n <= 2,048)
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            const uint32_t i = k * 256u + threadIdx.x;
+            const int64_t s = i < a.n ? __ldg(a.slots + i) : -1;
+            const uint32_t row = i < a.n && a.rows ? (uint32_t)__ldg(a.rows + i) : i;
+            bad |= s >= 0 && ((uint64_t)s >= a.pool_tokens || row >= a.n_src);
         }
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
         bad = false;
     }
-    const uint32_t per_row = a.n_heads * a.units;
-    const uint64_t work = (uint64_t)a.n * per_row, step = (uint64_t)gridDim.x * blockDim.x;
+    const uint64_t work = (uint64_t)a.n * a.per_row.d, step = (uint64_t)gridDim.x * blockDim.x;
     for (uint64_t w = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; w < work; w += step) {
-        const uint32_t i = (uint32_t)(w / per_row), c = (uint32_t)(w - (uint64_t)i * per_row);
+        const uint32_t i = a.narrow ? div_by((uint32_t)w, a.per_row) : (uint32_t)(w / a.per_row.d);
+        const uint32_t c = (uint32_t)(w - (uint64_t)i * a.per_row.d);
         const int64_t s = __ldg(a.slots + i);
-        if (s < 0) continue;
         const uint32_t row = a.rows ? (uint32_t)__ldg(a.rows + i) : i;
+        if (s < 0) continue;
         if ((uint64_t)s >= a.pool_tokens || row >= a.n_src) {
             bad = true;
             continue;
         }
-        const uint32_t h = c / a.units, u = c - h * a.units;
-        // a slot can pass 2^31 in a long cache: 64-bit division by the page length
-        const uint64_t p = (uint64_t)s / a.page.d, t = (uint64_t)s - p * a.page.d;
+        const uint32_t h = div_by(c, a.units), u = c - h * a.units.d;
+        // a slot can pass 2^31 in a long cache
+        const uint64_t p = a.narrow ? div_by((uint32_t)s, a.page) : (uint64_t)s / a.page.d;
+        const uint64_t t = (uint64_t)s - p * a.page.d;
         const uint64_t dst = p * a.page_stride + t * a.token_stride + h * a.head_stride + 16u * (uint64_t)u;
         const uint64_t src = (uint64_t)row * a.row_stride + h * a.row_head_stride + (E4M3 ? 16u : 8u) * (uint64_t)u;
         uint4 kc, vc;
         if (E4M3) {
-            kc = quantise16(a.k_new + src, a.k_scale ? __ldg(a.k_scale + h) : 1.0f);
-            vc = quantise16(a.v_new + src, a.v_scale ? __ldg(a.v_scale + h) : 1.0f);
+            const float ks = a.k_scale ? __ldg(a.k_scale + h) : 1.0f, vs = a.v_scale ? __ldg(a.v_scale + h) : 1.0f;
+            kc = quantise16(a.k_new + src, ks, reciprocal_of(ks));
+            vc = quantise16(a.v_new + src, vs, reciprocal_of(vs));
         } else {
             kc = __ldg(reinterpret_cast<const uint4 *>(a.k_new + src));
             vc = __ldg(reinterpret_cast<const uint4 *>(a.v_new + src));
@@ -377,11 +454,13 @@ extern "C" int32_t skv_page_map(uint32_t page_tokens, uint32_t pool_pages, uint3
     MapArgs a{fast_div(page_tokens), pool_pages, n_requests, max_pages, free_capacity, ctx_len, new_len, n_pages_in,
               free_in, block_table, n_pages_out, free_pages, free_out, cu_new, table_stride, slots, slot_capacity,
               status};
+    // One CTA of 256 threads up to 1,024 requests and 2,048 slots, else a CTA of 1,024 per
+    // 4,096 slots up to one per SM; several CTAs need the status cleared before them.
+    if (n_requests <= 1024u && slot_capacity <= 2048u) return launch_map<256, 4>(a, 1, st) ? SKV_OK : SKV_ERR_CUDA;
     uint64_t grid = (slot_capacity + 4u * kMapThreads - 1) / (4u * kMapThreads);
     grid = grid < 1 ? 1 : grid > sms ? sms : grid;
     if (grid > 1 && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    map_kernel<<<(unsigned)grid, kMapThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
+    return launch_map<kMapThreads, 4>(a, (unsigned)grid, st) ? SKV_OK : SKV_ERR_CUDA;
 }
 
 extern "C" int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, uint64_t row_stride,
@@ -403,10 +482,12 @@ extern "C" int32_t skv_cache_append(const skv_paged *cache, const void *k, const
     AppendArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride,
                  c.token_stride, c.head_stride, c.k_scale, c.v_scale, c.page,
                  (uint64_t)cache->n_pages * cache->page_tokens, static_cast<const uint16_t *>(k),
-                 static_cast<const uint16_t *>(v), row_stride, row_head_stride, n_src, n, cache->n_heads,
-                 cache->head_dim / (c.e4m3 ? 16u : 8u), rows, slots, status, n <= 2048u};
+                 static_cast<const uint16_t *>(v), row_stride, row_head_stride, n_src, n,
+                 fast_div(cache->head_dim / (c.e4m3 ? 16u : 8u)), fast_div(cache->n_heads * (cache->head_dim / (c.e4m3 ? 16u : 8u))),
+                 0u, rows, slots, status, n <= 2048u};
+    const uint64_t work = (uint64_t)n * a.per_row.d;
+    a.narrow = work < (uint64_t(1) << 31) && a.pool_tokens < (uint64_t(1) << 31);
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    const uint64_t work = (uint64_t)n * a.n_heads * a.units;
     uint64_t grid = (work + 255u) / 256u;
     if (grid > (uint64_t)sms * 8u) grid = (uint64_t)sms * 8u;
     if (c.e4m3) append_kernel<true><<<(unsigned)grid, 256, 0, st>>>(a);

@@ -15,7 +15,15 @@ import math
 import torch
 
 from . import _binding as B
-from .api import _check_dev, _ptr, _stream_handle
+from .api import _check_dev, _ptr
+
+
+def _stream_of(stream, device) -> int:
+    """The handle of `stream`, or of the current stream of the tensors' device (the
+    raw query: a Stream object costs several microseconds of a short step)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check_i32(what: str, numel: int, *ts):
@@ -69,7 +77,7 @@ class PageTable(_Status):
                                   self.block_table.data_ptr(), self._stride, self.max_pages, n_pages.data_ptr(),
                                   n_pages_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
                                   free_state.data_ptr(), free_state_out.data_ptr(), cu_new.data_ptr(),
-                                  slots.data_ptr(), slots.numel(), self.status.data_ptr(), _stream_handle(stream))
+                                  slots.data_ptr(), slots.numel(), self.status.data_ptr(), _stream_of(stream, self.status.device))
         B.check("skv_page_map", rc)
 
 
@@ -161,7 +169,7 @@ class PagedKV(_Status):
             _check_dev(rows, "rows", torch.int32, numel=slots.numel())
         rc = B.lib().skv_cache_append(self._ref, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.shape[0],
                                       None if rows is None else rows.data_ptr(), slots.data_ptr(), slots.numel(),
-                                      self.status.data_ptr(), _stream_handle(stream))
+                                      self.status.data_ptr(), _stream_of(stream, self.status.device))
         B.check("skv_cache_append", rc)
 
     def append(self, k, v, slots, rows=None, stream=None):
@@ -203,7 +211,7 @@ class PagedKV(_Status):
             None if mask is None else mask.data_ptr(), words, n if max_nodes is None else max_nodes,
             1.0 / math.sqrt(self.head_dim) if scale is None else scale, out.data_ptr(),
             None if lse is None else lse.data_ptr(), self.status.data_ptr(), self.workspace.data_ptr(),
-            self.workspace.numel(), _stream_handle(stream))
+            self.workspace.numel(), _stream_of(stream, self.status.device))
         B.check("skv_tree_attention", rc)
 
     def attend(self, q, ctx_len, cu_new, mask=None, max_nodes: int | None = None, scale: float | None = None,
