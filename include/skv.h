@@ -624,8 +624,9 @@ int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, u
  *  out        device bf16 [n_rows][n_q_heads][head_dim], contiguous, 16-byte aligned
  *  lse        device float32 [n_rows][n_q_heads] or NULL: log sum_p w_p (-infinity if no
  *             position)
- *  workspace  device, 256-byte aligned, ws_bytes >= skv_tree_attention_workspace_bytes;
- *             contents need not be kept or cleared
+ *  workspace  device, 256-byte aligned, ws_bytes >= skv_tree_attention_workspace_bytes.
+ *             Its first SKV_ATTENTION_ZERO_BYTES hold counters: they must be 0 before
+ *             the first call, and every call leaves them 0; the rest may hold anything
  * Sums and maxima are binary32; the weights w_p enter the second product in
  * bf16 (bf16 cache) or fp16 (e4m3 cache). Repeated calls give the same bits.
  * Device errors: INVALID_ARG (cu_new descends or passes n_rows, ctx_len < 0 with
@@ -633,6 +634,7 @@ int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, u
  * request's rows are left alone), CORRUPT (a page number outside the pool: that
  * request's outputs are unspecified).
  */
+#define SKV_ATTENTION_ZERO_BYTES 2048u
 int32_t skv_tree_attention_workspace_bytes(const skv_paged *cache, uint32_t n_q_heads, uint64_t *bytes);
 int32_t skv_tree_attention(const skv_paged *cache, const void *q, uint64_t q_row_stride,
                            uint64_t q_head_stride, uint32_t n_q_heads, uint32_t n_rows,

@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(HERE, "libskv.so")
 
 SKV_BF16, SKV_E4M3 = 0, 1
 SKV_FORMAT_VERSION = 1
+SKV_ATTENTION_ZERO_BYTES = 2048
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "CUDA", 3: "NONFINITE_MU", 4: "BAD_SIGMA",
                 5: "EMPTY_MARGINAL", 6: "CAPACITY", 7: "CORRUPT", 8: "TIMEOUT"}
 

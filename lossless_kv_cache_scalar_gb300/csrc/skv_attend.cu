@@ -180,15 +180,29 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
     }
 }
 
+// A CTA's end: its error, if it is the first; the last CTA writes the status and clears both words.
+__device__ __forceinline__ void finish(const AttendArgs &a, const AttendWs &ws, int32_t err) {
+    if (err) atomicCAS(ws.error, SKV_OK, err);
+    __threadfence();
+    if (atomicAdd(ws.finished, 1u) == gridDim.x - 1u) {
+        __threadfence();
+        *a.status = atomicExch(ws.error, SKV_OK);
+        *ws.finished = 0u;
+    }
+}
+
 template <int DP, bool E>
 __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(AttendArgs a, AttendWs ws) {
     using S = SmallShape<DP, E>;
     extern __shared__ __align__(1024) uint8_t ring_all[];
     __shared__ unsigned long long sm_plan[kWarps + 4];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, c4 = lane & 3u, g8 = lane >> 2;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share sh = share_of<kWarps * 32>(a, ws, 16u, S::unit, sm_plan);
-    if (sh.u0 == sh.u1) return;
+    __shared__ uint32_t sm_last;
+    const Share sh = share_of<kWarps * 32, false>(a, ws, 16u, S::unit, sm_plan);
+    if (sh.u0 == sh.u1) {
+        if (tid == 0) finish(a, ws, SKV_OK);
+        return;
+    }
     const uint32_t ring = smem_of(ring_all) + warp * S::ring;
     const uint32_t row_bytes = a.c.head_dim * S::bytes;
     bool corrupt = false;
@@ -479,8 +493,23 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
                 *reinterpret_cast<float4 *>(part + 32u + row * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
-        if (tid == 0 && tile == 0 && !whole)
-            ws.desc[blockIdx.x] = Desc{1u, r, h, rt, place, tiles, u};
+        if (!whole) {
+            // the CTA that brings the item's last part joins them all
+            const uint64_t unit0 = u - tile;
+            const uint32_t c0 = cta_of(unit0, sh.U, sh.active), n = cta_of(unit0 + tiles - 1, sh.U, sh.active) - c0 + 1u;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                sm_last = atomicAdd(ws.arrived + c0, 1u) == n - 1u;
+                if (sm_last) ws.arrived[c0] = 0u;
+            }
+            __syncthreads();
+            if (sm_last) {
+                __threadfence();
+                const uint32_t first = (uint64_t)c0 * sh.U / sh.active == unit0 ? 0u : 1u;
+                for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
+            }
+        }
         u += tile_end - tile;
         tile = 0;
         ++item;
@@ -493,13 +522,13 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
         }
         __syncthreads();                         // the rings are free again
     }
-    if (__syncthreads_or(corrupt) && tid == 0 && ws.errs[blockIdx.x] == SKV_OK) ws.errs[blockIdx.x] = SKV_ERR_CORRUPT;
+    corrupt = __syncthreads_or(corrupt);
+    if (tid == 0) finish(a, ws, corrupt ? SKV_ERR_CORRUPT : SKV_OK);
 }
 
-// Joins the parts of items that lie in several CTAs, one warp per row: block
-// (c, y) the rows 8 y .. 8 y + 7 of the item that starts in CTA c and goes on.
-// Each part weighs exp2(m - M) with M the largest m, in the order of the CTAs.
-// Block (0, 0) turns the CTAs' error words into the status: the first that has one.
+// Joins the parts that attend_large leaves, one warp per row: block (c, y) the rows
+// 8 y .. 8 y + 7 of the item that starts in CTA c and goes on. Block (0, 0) turns the
+// CTAs' error words into the status: the first that has one.
 __global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, uint32_t R, uint32_t DP, uint32_t ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x;
@@ -516,59 +545,11 @@ __global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, ui
         if (lane == 0) *a.status = err;
     }
     const Desc d = ws.desc[c];
+    const Plan plan = *ws.plan;
     if (!d.valid) return;
     const ReqOf q = request_of(a, d.request);
-    const uint32_t row = blockIdx.y * 8u + warp, all = d.rt * R + row, node = all / a.group;
-    if (node >= q.n) return;
-    const uint32_t g = d.head * a.group + all - node * a.group;
-    const Plan plan = *ws.plan;
-    const uint64_t end = d.unit0 + d.units;
-    // parts: CTA c's, then place 0 of the next CTAs up to the one whose share holds unit
-    // end - 1, the last j with j total / active < end
-    const uint32_t n = (uint32_t)((end * plan.active - 1) / plan.total) - c + 1u;
-    const uint64_t size = part_floats(R, DP);
-    const float *first = ws.parts + ((uint64_t)c * 2u + d.place) * size;
-    const auto part = [&](uint32_t j) { return j ? ws.parts + (uint64_t)(c + j) * 2u * size : first; };
-    float M = -INFINITY, L = 0.0f;
-    for (uint32_t j = lane; j < n; j += 32u) M = fmaxf(M, part(j)[row]);
-    for (uint32_t x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (uint32_t j0 = 0; j0 < n; j0 += 32u) {
-        float f = 0.0f;
-        if (j0 + lane < n) {
-            f = part_weight(part(j0 + lane)[row], M);
-            L += f * part(j0 + lane)[R + row];
-        }
-        const uint32_t here = min(32u, n - j0);
-#pragma unroll 8
-        for (uint32_t j = 0; j < here; ++j) {
-            const float w = __shfl_sync(~0u, f, j);
-            const float *src = part(j0 + j) + 2u * R + (uint64_t)row * DP;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t x = 4u * lane + 128u * k;
-                if (x < DP) {
-                    const float4 y = *reinterpret_cast<const float4 *>(src + x);
-                    o[4 * k] += w * y.x, o[4 * k + 1] += w * y.y, o[4 * k + 2] += w * y.z, o[4 * k + 3] += w * y.w;
-                }
-            }
-        }
-    }
-    for (uint32_t x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-    const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + d.head) : 1.0f) / L;
-    uint16_t *out = a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t x = 4u * lane + 128u * k;
-        if (x < a.c.head_dim) {
-            uint2 y;
-            y.x = L == 0.0f ? 0u : pack2<false>(o[4 * k] * inv, o[4 * k + 1] * inv);
-            y.y = L == 0.0f ? 0u : pack2<false>(o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-            *reinterpret_cast<uint2 *>(out + x) = y;
-        }
-    }
-    if (a.lse && lane == 0)
-        a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    const uint32_t last = cta_of(d.unit0 + d.units - 1, plan.total, plan.active);
+    join_row(a, ws, q, d.head, d.rt, blockIdx.y * 8u + warp, R, DP, c, d.place, last - c + 1u);
 }
 
 // Dynamic shared memory above 48 KB is asked for once per kernel and device.
@@ -602,7 +583,7 @@ static bool launch_small(const AttendArgs &a, const AttendWs &ws, cudaStream_t s
     static std::atomic<uint64_t> ready{0};                 // devices where the limit is set
     if (!raise_smem(reinterpret_cast<const void *>(attend_small<DP, E>), S::smem, ready)) return false;
     attend_small<DP, E><<<kCtasSmall, kWarps * 32, S::smem, st>>>(a, ws);
-    return cudaGetLastError() == cudaSuccess && launch_join(a, ws, 16u, DP, kCtasSmall, st);
+    return cudaGetLastError() == cudaSuccess;
 }
 
 }  // namespace skv

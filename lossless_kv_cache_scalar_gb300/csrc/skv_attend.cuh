@@ -8,8 +8,10 @@
 // units [c U / G, (c + 1) U / G)), so ragged lengths cost no balance and the host
 // needs no length. The units of one (request, head, row tile) are an item; a
 // CTA that holds a whole item writes its output, and one that holds a part
-// leaves maximum, sum and unnormalised output in the workspace, for the joining
-// kernel. A part that starts at the CTA's first unit goes to place 0 of the
+// leaves maximum, sum and unnormalised output in the workspace. The small-row
+// kernel's CTA that comes last to an item joins its parts (counters in the
+// workspace, 0 between calls); the large-row kernel's parts are joined by a second
+// kernel, whose rows are spread over the GPU. A part that starts at the CTA's first unit goes to place 0 of the
 // CTA, any other (it then ends at the CTA's last unit) to place 1.
 #pragma once
 
@@ -36,6 +38,9 @@ struct Plan {
 };
 
 struct AttendWs {
+    uint32_t *arrived;  // [CTA]: parts done of the item that starts in the CTA and goes on
+    uint32_t *finished; // CTAs done
+    int32_t *error;     // the first error of a CTA
     Plan *plan;
     int32_t *errs;      // one per CTA
     Desc *desc;         // one per CTA
@@ -44,13 +49,17 @@ struct AttendWs {
 
 __host__ __device__ inline uint64_t part_floats(uint32_t R, uint32_t DP) { return (uint64_t)R * (2u + DP); }
 
-constexpr uint64_t kWsHead = 256u + 1536u + 304u * sizeof(Desc);     // plan, errs, descs
-static_assert(sizeof(Desc) == 32 && kCtasSmall * 4u <= 1536u && kCtasLarge <= kCtasSmall && kWsHead % 256u == 0,
-              "workspace head");
+// Counters (SKV_ATTENTION_ZERO_BYTES), then plan, errs, descs.
+constexpr uint64_t kWsPlan = SKV_ATTENTION_ZERO_BYTES, kWsErrs = kWsPlan + 256u, kWsDesc = kWsErrs + 1536u;
+constexpr uint64_t kWsHead = kWsDesc + 304u * sizeof(Desc);
+static_assert(sizeof(Desc) == 32 && kCtasSmall * 4u <= 1536u && kCtasSmall * 4u + 8u <= SKV_ATTENTION_ZERO_BYTES &&
+              kCtasLarge <= kCtasSmall && kWsHead % 256u == 0, "workspace head");
 
 inline AttendWs attend_ws(void *base) {
     uint8_t *p = static_cast<uint8_t *>(base);
-    return AttendWs{reinterpret_cast<Plan *>(p), reinterpret_cast<int32_t *>(p + 256), reinterpret_cast<Desc *>(p + 1792),
+    uint32_t *n = reinterpret_cast<uint32_t *>(p);
+    return AttendWs{n + 2, n, reinterpret_cast<int32_t *>(n + 1), reinterpret_cast<Plan *>(p + kWsPlan),
+                    reinterpret_cast<int32_t *>(p + kWsErrs), reinterpret_cast<Desc *>(p + kWsDesc),
                     reinterpret_cast<float *>(p + kWsHead)};
 }
 
@@ -134,6 +143,7 @@ __device__ __forceinline__ float not_finite_sum(const AttendArgs &a, const ReqOf
 
 // Where CTA c's share of the list starts: the request, and the unit within it.
 struct Share {
+    uint64_t U, active;
     uint64_t u0, u1;      // units [u0, u1)
     uint32_t r;
     uint64_t off;
@@ -146,7 +156,8 @@ __device__ __forceinline__ uint64_t units_of(const AttendArgs &a, const ReqOf &q
 }
 
 // Every thread of the block calls this; sm is scratch of blockDim / 32 + 4 words of 8 bytes.
-template <uint32_t THREADS>
+// JOINED: the kernel with a joining kernel behind it leaves plan, error and descriptor for it.
+template <uint32_t THREADS, bool JOINED>
 __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t UT,
                                           unsigned long long *sm) {
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -169,12 +180,13 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
 #pragma unroll
     for (uint32_t w = 0; w < W; ++w) U += sm[w];
     const uint64_t active = U < gridDim.x ? U : gridDim.x;
-    Share s{0, 0, 0, 0};
-    if (tid == 0) {
+    Share s{U, active, 0, 0, 0, 0};
+    if (JOINED && tid == 0) {
         ws.errs[blockIdx.x] = err;
         ws.desc[blockIdx.x].valid = 0u;
         if (blockIdx.x == 0) *ws.plan = Plan{U, active};
     }
+    if (!JOINED && tid == 0 && blockIdx.x == 0 && err) atomicCAS(ws.error, SKV_OK, err);
     if (blockIdx.x >= active) return s;
     s.u0 = (uint64_t)blockIdx.x * U / active;
     s.u1 = (uint64_t)(blockIdx.x + 1) * U / active;
@@ -210,6 +222,76 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     s.r = (uint32_t)sm[W];
     s.off = sm[W + 1];
     return s;
+}
+
+// The last CTA whose share starts at or before unit u: where u lies.
+__device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t U, uint64_t active) {
+    return (uint32_t)(((u + 1) * active - 1) / U);
+}
+
+// One row of an item whose parts lie in CTAs c .. c + n - 1 (place of the first, then 0), by one warp: each
+// part weighs exp2(m - M) with M the largest m, in the order of the CTAs.
+__device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws, const ReqOf &q, uint32_t head, uint32_t rt,
+                                         uint32_t row, uint32_t R, uint32_t DP, uint32_t c, uint32_t place, uint32_t n) {
+    const uint32_t lane = threadIdx.x & 31u, all = rt * R + row, node = all / a.group;
+    if (node >= q.n) return;
+    const uint32_t g = head * a.group + all - node * a.group;
+    const uint64_t size = part_floats(R, DP);
+    const float *first = ws.parts + ((uint64_t)c * 2u + place) * size, *next = ws.parts + (uint64_t)c * 2u * size;
+    const auto part = [&](uint32_t j) { return j ? next + (uint64_t)j * 2u * size : first; };
+    // lane j: part j's maximum and sum (a first 32 in registers, what is beyond read again)
+    float mj = -INFINITY, lj = 0.0f;
+    if (lane < n) {
+        mj = __ldcg(part(lane) + row);
+        lj = __ldcg(part(lane) + R + row);
+    }
+    float M = mj, L = 0.0f;
+    for (uint32_t j = 32u + lane; j < n; j += 32u) M = fmaxf(M, __ldcg(part(j) + row));
+    for (uint32_t x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (uint32_t j0 = 0; j0 < n; j0 += 32u) {
+        float f = 0.0f;
+        if (j0 + lane < n) {
+            if (j0) {
+                mj = __ldcg(part(j0 + lane) + row);
+                lj = __ldcg(part(j0 + lane) + R + row);
+            }
+            f = part_weight(mj, M);
+            L += f * lj;
+        }
+        const uint32_t here = min(32u, n - j0);
+#pragma unroll 8
+        for (uint32_t j = 0; j < here; ++j) {
+            const float w = __shfl_sync(~0u, f, j);
+            const float *src = part(j0 + j) + 2u * R + (uint64_t)row * DP;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x = 4u * lane + 128u * k;
+                if (x < DP) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + x));
+                    o[4 * k] += w * y.x, o[4 * k + 1] += w * y.y, o[4 * k + 2] += w * y.z, o[4 * k + 3] += w * y.w;
+                }
+            }
+        }
+    }
+    for (uint32_t x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+    const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + head) : 1.0f) / L;
+    uint16_t *out = a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t x = 4u * lane + 128u * k;
+        if (x < a.c.head_dim) {
+            const bool none = L == 0.0f;
+            ushort4 y;
+            y.x = none ? 0 : bf16_bits(o[4 * k] * inv);
+            y.y = none ? 0 : bf16_bits(o[4 * k + 1] * inv);
+            y.z = none ? 0 : bf16_bits(o[4 * k + 2] * inv);
+            y.w = none ? 0 : bf16_bits(o[4 * k + 3] * inv);
+            *reinterpret_cast<ushort4 *>(out + x) = y;
+        }
+    }
+    if (a.lse && lane == 0)
+        a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // skv_attend.cu

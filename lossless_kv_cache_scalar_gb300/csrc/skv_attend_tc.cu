@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
     __shared__ TcShared sm;
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share sh = share_of<kTcThreads>(a, ws, kTcRows, kTile, sm.plan);
+    const Share sh = share_of<kTcThreads, true>(a, ws, kTcRows, kTile, sm.plan);
     if (sh.u0 == sh.u1) return;
     const uint32_t q_at = (s32(dyn) + 1023u) & ~1023u, ring_at = q_at + 2u * S::tile, raw_at = q_at + S::raw_at;
     if (tid == 0) {

@@ -153,6 +153,7 @@ class PagedKV(_Status):
         B.check("skv_tree_attention_workspace_bytes",
                 B.lib().skv_tree_attention_workspace_bytes(self._ref, q_heads, C.byref(v)))
         self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
+        self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
         self.q_heads = q_heads
 
     def append_into(self, k, v, slots, rows=None, stream=None):
