@@ -180,11 +180,14 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
     }
 }
 
-// A CTA's end: its error, if it is the first; the last CTA writes the status and clears both words.
-__device__ __forceinline__ void finish(const AttendArgs &a, const AttendWs &ws, int32_t err) {
-    if (err) atomicCAS(ws.error, SKV_OK, err);
-    __threadfence();
-    if (atomicAdd(ws.finished, 1u) == gridDim.x - 1u) {
+// The end of a CTA with work: its error, if it is the first; the last one writes the
+// status and clears both words.
+__device__ __forceinline__ void finish(const AttendArgs &a, const AttendWs &ws, int32_t err, uint32_t active) {
+    if (err) {
+        atomicCAS(ws.error, SKV_OK, err);
+        __threadfence();
+    }
+    if (atomicAdd(ws.finished, 1u) == active - 1u) {
         __threadfence();
         *a.status = atomicExch(ws.error, SKV_OK);
         *ws.finished = 0u;
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
     __shared__ uint32_t sm_last;
     const Share sh = share_of<kWarps * 32, false>(a, ws, 16u, S::unit, sm_plan);
     if (sh.u0 == sh.u1) {
-        if (tid == 0) finish(a, ws, SKV_OK);
+        if (sh.active == 0 && blockIdx.x == 0 && tid == 0) *a.status = atomicExch(ws.error, SKV_OK);
         return;
     }
     const uint32_t ring = smem_of(ring_all) + warp * S::ring;
@@ -211,11 +214,11 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
     ReqOf q = request_of(a, r);
     constexpr uint32_t G = S::groups;
     uint32_t tiles = (q.len + S::unit - 1) / S::unit, rts = (q.n * a.group + 15u) / 16u;
-    uint64_t item = sh.off / tiles;
+    uint64_t item = quotient(sh.off, tiles);
     uint32_t tile = (uint32_t)(sh.off - item * tiles);
     for (uint64_t u = sh.u0; u < sh.u1;) {
         // one part: head h, row tile rt, tiles [tile, tile_end) of the request
-        const uint32_t h = (uint32_t)(item / rts), rt = (uint32_t)(item - (uint64_t)h * rts);
+        const uint32_t h = (uint32_t)quotient(item, rts), rt = (uint32_t)(item - (uint64_t)h * rts);
         const uint32_t tile_end = (uint32_t)min((uint64_t)tiles, tile + (sh.u1 - u));
         const uint32_t p_begin = tile * S::unit, p_end = min(q.len, tile_end * S::unit);
         const uint32_t runs = (p_end - p_begin + S::run - 1) / S::run;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
             __syncthreads();
             if (sm_last) {
                 __threadfence();
-                const uint32_t first = (uint64_t)c0 * sh.U / sh.active == unit0 ? 0u : 1u;
+                const uint32_t first = quotient((uint64_t)c0 * sh.U, sh.active) == unit0 ? 0u : 1u;
                 for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
             }
         }
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
         __syncthreads();                         // the rings are free again
     }
     corrupt = __syncthreads_or(corrupt);
-    if (tid == 0) finish(a, ws, corrupt ? SKV_ERR_CORRUPT : SKV_OK);
+    if (tid == 0) finish(a, ws, corrupt ? SKV_ERR_CORRUPT : SKV_OK, (uint32_t)sh.active);
 }
 
 // Joins the parts that attend_large leaves, one warp per row: block (c, y) the rows

@@ -141,6 +141,11 @@ __device__ __forceinline__ float not_finite_sum(const AttendArgs &a, const ReqOf
     return s;
 }
 
+// n / d; a 64-bit division takes some hundred instructions, and most lists are short.
+__device__ __forceinline__ uint64_t quotient(uint64_t n, uint64_t d) {
+    return (n | d) >> 32 ? n / d : (uint64_t)((uint32_t)n / (uint32_t)d);
+}
+
 // Where CTA c's share of the list starts: the request, and the unit within it.
 struct Share {
     uint64_t U, active;
@@ -186,10 +191,13 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
         ws.desc[blockIdx.x].valid = 0u;
         if (blockIdx.x == 0) *ws.plan = Plan{U, active};
     }
-    if (!JOINED && tid == 0 && blockIdx.x == 0 && err) atomicCAS(ws.error, SKV_OK, err);
+    if (!JOINED && tid == 0 && blockIdx.x == 0 && err) {
+        atomicCAS(ws.error, SKV_OK, err);
+        __threadfence();
+    }
     if (blockIdx.x >= active) return s;
-    s.u0 = (uint64_t)blockIdx.x * U / active;
-    s.u1 = (uint64_t)(blockIdx.x + 1) * U / active;
+    s.u0 = quotient((uint64_t)blockIdx.x * U, active);
+    s.u1 = quotient((uint64_t)(blockIdx.x + 1) * U, active);
     unsigned long long carry = 0;
     for (uint32_t base = 0; base < a.c.n_requests; base += THREADS) {
         const uint32_t r = base + tid;
@@ -226,7 +234,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
 
 // The last CTA whose share starts at or before unit u: where u lies.
 __device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t U, uint64_t active) {
-    return (uint32_t)(((u + 1) * active - 1) / U);
+    return (uint32_t)quotient((u + 1) * active - 1, U);
 }
 
 // One row of an item whose parts lie in CTAs c .. c + n - 1 (place of the first, then 0), by one warp: each
@@ -245,10 +253,21 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws
         mj = __ldcg(part(lane) + row);
         lj = __ldcg(part(lane) + R + row);
     }
+    // the first eight parts' outputs are on their way before the weights are known
+    constexpr uint32_t AHEAD = 8;
+    float4 ahead[AHEAD];
+#pragma unroll
+    for (uint32_t j = 0; j < AHEAD; ++j) {
+        ahead[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n && 4u * lane < DP) ahead[j] = __ldcg(reinterpret_cast<const float4 *>(part(j) + 2u * R + (uint64_t)row * DP + 4u * lane));
+    }
     float M = mj, L = 0.0f;
     for (uint32_t j = 32u + lane; j < n; j += 32u) M = fmaxf(M, __ldcg(part(j) + row));
     for (uint32_t x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const auto add = [&](int k, float w, const float4 &y) {
+        o[4 * k] += w * y.x, o[4 * k + 1] += w * y.y, o[4 * k + 2] += w * y.z, o[4 * k + 3] += w * y.w;
+    };
     for (uint32_t j0 = 0; j0 < n; j0 += 32u) {
         float f = 0.0f;
         if (j0 + lane < n) {
@@ -260,18 +279,21 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws
             L += f * lj;
         }
         const uint32_t here = min(32u, n - j0);
-#pragma unroll 8
-        for (uint32_t j = 0; j < here; ++j) {
-            const float w = __shfl_sync(~0u, f, j);
-            const float *src = part(j0 + j) + 2u * R + (uint64_t)row * DP;
+        uint32_t j = 0;
+        if (j0 == 0) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t x = 4u * lane + 128u * k;
-                if (x < DP) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + x));
-                    o[4 * k] += w * y.x, o[4 * k + 1] += w * y.y, o[4 * k + 2] += w * y.z, o[4 * k + 3] += w * y.w;
-                }
-            }
+            for (; j < AHEAD; ++j)
+                if (j < here) add(0, __shfl_sync(~0u, f, j), ahead[j]);      // here is the same for the warp
+        }
+#pragma unroll 8
+        for (; j < here; ++j) {
+            const float w = __shfl_sync(~0u, f, j);
+            if (4u * lane < DP) add(0, w, __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + (uint64_t)row * DP + 4u * lane)));
+        }
+        if (DP > 128u) {
+#pragma unroll 8
+            for (j = 0; j < here; ++j)
+                add(1, __shfl_sync(~0u, f, j), __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + (uint64_t)row * DP + 128u + 4u * lane)));
         }
     }
     for (uint32_t x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);

@@ -62,7 +62,7 @@ struct Walk {
         rts = (q.n * a.group + kTcRows - 1) / kTcRows;
     }
     __device__ __forceinline__ void part(const AttendArgs &a) {
-        h = (uint32_t)(item / rts);
+        h = (uint32_t)quotient(item, rts);
         rt = (uint32_t)(item - (uint64_t)h * rts);
         tile_end = (uint32_t)min((uint64_t)tiles, tile + (u1 - u));
         rows = min(kTcRows, q.n * a.group - rt * kTcRows);
@@ -74,7 +74,7 @@ struct Walk {
         n = 0;
         q = request_of(a, r);
         request(a);
-        item = s.off / tiles;
+        item = quotient(s.off, tiles);
         tile = (uint32_t)(s.off - item * tiles);
         part(a);
     }
