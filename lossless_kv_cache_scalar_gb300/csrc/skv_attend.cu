@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
             if (sm_last) {
                 __threadfence();
                 const uint32_t first = quotient((uint64_t)c0 * sh.U, sh.active) == unit0 ? 0u : 1u;
-                for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
+                for (uint32_t row = warp; row < 16u; row += kWarps) join_row<8>(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
             }
         }
         u += tile_end - tile;
@@ -529,10 +529,14 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
     if (tid == 0) finish(a, ws, corrupt ? SKV_ERR_CORRUPT : SKV_OK, (uint32_t)sh.active);
 }
 
-// Joins the parts that attend_large leaves, one warp per row: block (c, y) the rows
-// 8 y .. 8 y + 7 of the item that starts in CTA c and goes on. Block (0, 0) turns the
-// CTAs' error words into the status: the first that has one.
-__global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, uint32_t R, uint32_t DP, uint32_t ctas) {
+// Joins the parts that attend_large leaves: block (c, y) every fourth eight rows of the
+// item that starts in CTA c and goes on, a warp per row. All blocks are resident at
+// once, so that descriptor and request are waited for once, not once per eight rows
+// (152 x 32 blocks of eight rows took 31 us behind a 515 us call, these 13). Block (0, 0)
+// turns the CTAs' error words into the status: the first that has one.
+constexpr uint32_t kJoinBlocks = 4;
+
+__global__ void __launch_bounds__(256, 4) attend_join(AttendArgs a, AttendWs ws, uint32_t R, uint32_t DP, uint32_t ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
@@ -552,7 +556,9 @@ __global__ void __launch_bounds__(256) attend_join(AttendArgs a, AttendWs ws, ui
     if (!d.valid) return;
     const ReqOf q = request_of(a, d.request);
     const uint32_t last = cta_of(d.unit0 + d.units - 1, plan.total, plan.active);
-    join_row(a, ws, q, d.head, d.rt, blockIdx.y * 8u + warp, R, DP, c, d.place, last - c + 1u);
+    const uint32_t rows = min(R, q.n * a.group - d.rt * R);
+    for (uint32_t row = blockIdx.y * 8u + warp; row < rows; row += kJoinBlocks * 8u)
+        join_row<4>(a, ws, q, d.head, d.rt, row, R, DP, c, d.place, last - c + 1u);
 }
 
 // Dynamic shared memory above 48 KB is asked for once per kernel and device.
@@ -568,7 +574,7 @@ bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready
 
 bool launch_join(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t DP, uint32_t ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R / 8u);
+    cfg.gridDim = dim3(ctas, kJoinBlocks);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];

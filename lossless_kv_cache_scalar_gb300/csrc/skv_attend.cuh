@@ -52,7 +52,7 @@ __host__ __device__ inline uint64_t part_floats(uint32_t R, uint32_t DP) { retur
 // Counters (SKV_ATTENTION_ZERO_BYTES), then plan, errs, descs.
 constexpr uint64_t kWsPlan = SKV_ATTENTION_ZERO_BYTES, kWsErrs = kWsPlan + 256u, kWsDesc = kWsErrs + 1536u;
 constexpr uint64_t kWsHead = kWsDesc + 304u * sizeof(Desc);
-static_assert(sizeof(Desc) == 32 && kCtasSmall * 4u <= 1536u && kCtasSmall * 4u + 8u <= SKV_ATTENTION_ZERO_BYTES &&
+static_assert(kWsHead % 32u == 0 && sizeof(Desc) == 32 && kCtasSmall * 4u <= 1536u && kCtasSmall * 4u + 8u <= SKV_ATTENTION_ZERO_BYTES &&
               kCtasLarge <= kCtasSmall && kWsHead % 256u == 0, "workspace head");
 
 inline AttendWs attend_ws(void *base) {
@@ -239,6 +239,7 @@ __device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t U, uint64_t acti
 
 // One row of an item whose parts lie in CTAs c .. c + n - 1 (place of the first, then 0), by one warp: each
 // part weighs exp2(m - M) with M the largest m, in the order of the CTAs.
+template <uint32_t AHEAD>
 __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws, const ReqOf &q, uint32_t head, uint32_t rt,
                                          uint32_t row, uint32_t R, uint32_t DP, uint32_t c, uint32_t place, uint32_t n) {
     const uint32_t lane = threadIdx.x & 31u, all = rt * R + row, node = all / a.group;
@@ -253,8 +254,7 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws
         mj = __ldcg(part(lane) + row);
         lj = __ldcg(part(lane) + R + row);
     }
-    // the first eight parts' outputs are on their way before the weights are known
-    constexpr uint32_t AHEAD = 8;
+    // the first parts' outputs are on their way before the weights are known
     float4 ahead[AHEAD];
 #pragma unroll
     for (uint32_t j = 0; j < AHEAD; ++j) {
@@ -285,13 +285,13 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws
             for (; j < AHEAD; ++j)
                 if (j < here) add(0, __shfl_sync(~0u, f, j), ahead[j]);      // here is the same for the warp
         }
-#pragma unroll 8
+#pragma unroll 4
         for (; j < here; ++j) {
             const float w = __shfl_sync(~0u, f, j);
             if (4u * lane < DP) add(0, w, __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + (uint64_t)row * DP + 4u * lane)));
         }
         if (DP > 128u) {
-#pragma unroll 8
+#pragma unroll 4
             for (j = 0; j < here; ++j)
                 add(1, __shfl_sync(~0u, f, j), __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + (uint64_t)row * DP + 128u + 4u * lane)));
         }

@@ -239,6 +239,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void store32(void *at, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                        uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f),
+                 "r"(g), "r"(h) : "memory");
+}
+
 // The 128 threads of one stream's weights.
 __device__ __forceinline__ void group_sync(uint32_t s) { asm volatile("bar.sync %0, 128;" ::"r"(3u + s) : "memory"); }
 
@@ -878,22 +885,25 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                         }
                     }
                     if (live && whole) {
+                        uint32_t y[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            if (32u * c + i >= a.c.head_dim) break;
-                            uint4 y;
-                            y.x = tc_pack<false>(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                            y.y = tc_pack<false>(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-                            y.z = tc_pack<false>(__uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
-                            y.w = tc_pack<false>(__uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
-                            if (l == 0.0f) y = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(out + 32u * c + i) = y;
+                        for (int i = 0; i < 16; ++i)
+                            y[i] = l == 0.0f ? 0u : tc_pack<false>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8) {
+                            if (32u * c + 2 * i >= a.c.head_dim) break;
+                            if (((uintptr_t)out & 31u) == 0) {
+                                store32(out + 32u * c + 2 * i, y[i], y[i + 1], y[i + 2], y[i + 3], y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
+                            } else {
+                                *reinterpret_cast<uint4 *>(out + 32u * c + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                                *reinterpret_cast<uint4 *>(out + 32u * c + 2 * i + 8) = make_uint4(y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
+                            }
                         }
                     } else if (live) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(part + 2u * kTcRows + row * DP + 32u * c + i) =
-                                make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        for (int i = 0; i < 32; i += 8)              // a whole 32-byte sector per lane and store
+                            store32(part + 2u * kTcRows + row * DP + 32u * c + i, x[i], x[i + 1], x[i + 2], x[i + 3], x[i + 4],
+                                    x[i + 5], x[i + 6], x[i + 7]);
                     }
                 }
                 if (live && whole && a.lse)

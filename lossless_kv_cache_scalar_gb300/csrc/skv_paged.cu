@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
 
     // This CTA's share of the tokens' slots, and of the -1 behind them.
     const uint64_t total = err ? 0u : t[0], tail = a.slot_capacity - total;
-    const uint64_t per = ((total + gridDim.x - 1) / gridDim.x + 1) & ~uint64_t(1);
+    const uint64_t per = ((total + gridDim.x - 1) / gridDim.x + 3) & ~uint64_t(3);
     const uint64_t i0 = min((uint64_t)blockIdx.x * per, total), i1 = min(i0 + per, total);
     {
         const uint64_t each = ((tail + gridDim.x - 1) / gridDim.x + 1) & ~uint64_t(1);
@@ -219,8 +219,9 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
                 ended &= ended - 1u;
                 const uint32_t back = __shfl_sync(~0u, m.back, l), before = __shfl_sync(~0u, x[2], l);
                 const int32_t *row = a.table + (uint64_t)__shfl_sync(~0u, r, l) * a.table_stride;
+#pragma unroll 4
                 for (uint32_t j = lane; j < back; j += 32u) {
-                    const int32_t p = row[j];
+                    const int32_t p = __ldg(row + j);        // not written in this call
                     corrupt |= (uint32_t)p >= a.pool_pages;
                     uint64_t to = (uint64_t)head + (uint32_t)count + before + j;      // below 2 free_capacity
                     if (to >= a.free_capacity) to -= a.free_capacity;
@@ -232,47 +233,55 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
             x[2] += m.back;
         }
         __syncthreads();
-        // The slots of this chunk of requests that lie in this CTA's run, two to a thread.
+        // The slots of this chunk of requests that lie in this CTA's run.
         const uint64_t lo = max(i0, (uint64_t)s_cu[0]), hi = min(i1, (uint64_t)s_cu[CHUNK]);
         const uint32_t live = min(CHUNK, a.n_requests - base);
-        const auto slot_of = [&](uint32_t i, uint32_t f) {
-            const uint32_t pos = (uint32_t)s_ctx[f] + (i - s_cu[f]);
-            const uint32_t j = div_by(pos, a.page), off = pos - j * a.page.d;
-            int32_t p;
-            if (j < (uint32_t)s_have[f]) {
-                p = a.table[(uint64_t)(base + f) * a.table_stride + j];
-            } else {
-                uint64_t e = (uint64_t)head + s_need[f] + (j - (uint32_t)s_have[f]);
-                if (e >= a.free_capacity) e -= a.free_capacity;
-                p = a.free_pages[e];
-                if (off == 0u) a.table[(uint64_t)(base + f) * a.table_stride + j] = p;
-            }
-            const bool ok = (uint32_t)p < a.pool_pages;
-            corrupt |= !ok;
-            return ok ? (int64_t)p * a.page.d + off : -1ll;
-        };
-#pragma unroll 2
-        for (uint64_t i = (lo & ~uint64_t(1)) + 2 * tid; i < hi; i += 2 * THREADS) {
-            const uint32_t first = (uint32_t)max(i, lo);
-            uint32_t f = 0, n = live;                             // last request with cu <= first
+        // Four tokens to a thread: their pages are all looked up before anything is stored. (Entries that
+        // are read, old ones of the table and the ring's front, are not written in this call.)
+        for (uint64_t i = (lo & ~uint64_t(3)) + 4 * tid; i < hi; i += 4 * THREADS) {
+            const uint32_t from = (uint32_t)max(i, lo), to = (uint32_t)min(i + 4, hi);
+            uint32_t f = 0, n = live;                             // last request with cu <= from
             while (n > 1) {
                 const uint32_t h = n >> 1;
-                if (s_cu[f + h] <= first) f += h;
+                if (s_cu[f + h] <= from) f += h;
                 n -= h;
             }
-            int64_t v[2];
-            v[0] = slot_of(first, f);
-            if (i >= lo && i + 1 < hi) {
-                while (s_cu[f + 1] <= first + 1) ++f;             // past requests without tokens
-                v[1] = slot_of(first + 1, f);
-                if (((uintptr_t)a.slots & 15u) == 0) {
-                    *reinterpret_cast<longlong2 *>(a.slots + i) = make_longlong2(v[0], v[1]);
-                } else {
-                    a.slots[i] = v[0];
-                    a.slots[i + 1] = v[1];
-                }
+            int64_t v[4];
+            int32_t page[4];
+            int32_t *entry[4];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t x = (uint32_t)i + k;
+                entry[k] = nullptr;
+                page[k] = 0;
+                v[k] = -1;
+                if (x < from || x >= to) continue;
+                while (s_cu[f + 1] <= x) ++f;                     // past requests without tokens
+                const uint32_t pos = (uint32_t)s_ctx[f] + (x - s_cu[f]);
+                const uint32_t j = div_by(pos, a.page), off = pos - j * a.page.d, have = (uint32_t)s_have[f];
+                int32_t *row = a.table + (uint64_t)(base + f) * a.table_stride + j;
+                uint64_t e = (uint64_t)head + s_need[f] + (j - have);
+                if (e >= a.free_capacity) e -= a.free_capacity;
+                if (k > 0 && x > from && off != 0u && pos != (uint32_t)s_ctx[f]) page[k] = page[k - 1];   // the token before it is on the same page
+                else page[k] = __ldg(j < have ? row : a.free_pages + e);
+                if (j >= have && off == 0u) entry[k] = row;
+                v[k] = off;
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                if (entry[k]) *entry[k] = page[k];
+                if (v[k] < 0) continue;
+                const bool ok = (uint32_t)page[k] < a.pool_pages;
+                corrupt |= !ok;
+                v[k] = ok ? (int64_t)page[k] * a.page.d + v[k] : -1ll;
+            }
+            if (from == i && to == i + 4 && ((uintptr_t)a.slots & 15u) == 0) {
+                *reinterpret_cast<longlong2 *>(a.slots + i) = make_longlong2(v[0], v[1]);
+                *reinterpret_cast<longlong2 *>(a.slots + i + 2) = make_longlong2(v[2], v[3]);
             } else {
-                a.slots[first] = v[0];
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k)
+                    if (i + k >= from && i + k < to) a.slots[i + k] = v[k];
             }
         }
 #pragma unroll
