@@ -529,12 +529,12 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
     if (tid == 0) finish(a, ws, corrupt ? SKV_ERR_CORRUPT : SKV_OK, (uint32_t)sh.active);
 }
 
-// Joins the parts that attend_large leaves: block (c, y) every fourth eight rows of the
+// Joins the parts that attend_large leaves: block (c, y) every eighth eight rows of the
 // item that starts in CTA c and goes on, a warp per row. All blocks are resident at
 // once, so that descriptor and request are waited for once, not once per eight rows
 // (152 x 32 blocks of eight rows took 31 us behind a 515 us call, these 13). Block (0, 0)
 // turns the CTAs' error words into the status: the first that has one.
-constexpr uint32_t kJoinBlocks = 4;
+constexpr uint32_t kJoinBlocks = 8;
 
 __global__ void __launch_bounds__(256, 4) attend_join(AttendArgs a, AttendWs ws, uint32_t R, uint32_t DP, uint32_t ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -41,11 +41,13 @@ template <int DP, bool E>
 struct TcShape {
     static constexpr uint32_t block = kTile * 128;              // 128 rows of 128 bytes: 64 channels
     static constexpr uint32_t tile = block * (DP / 64);         // one K, V or 128-row Q tile in 16-bit values
-    static constexpr uint32_t ring = (E ? 3 : 4) * (128 / DP);  // tiles
-    static constexpr uint32_t raw = E ? ring : 0;               // tiles of 8-bit codes on their way to the ring
+    static constexpr uint32_t ring = 4 * (128 / DP);            // tiles
+    static constexpr uint32_t raw = E ? 2 * (128 / DP) : 0;     // tiles of 8-bit codes on their way to the ring
     static constexpr uint32_t raw_tile = kTile * DP;
     static constexpr uint32_t raw_at = (2 + ring) * tile;       // from the queries' start
-    static constexpr uint32_t smem = raw_at + raw * raw_tile + 1024;
+    // where rows are copied one by one, their offsets: four tiles' (then no codes are on their way)
+    static constexpr uint32_t offsets = 4 * kTile * 8;
+    static constexpr uint32_t smem = raw_at + (E ? raw * raw_tile : offsets);
 };
 
 // The parts of a CTA's share, in order; every role walks them for itself.
@@ -103,8 +105,7 @@ struct TcShared {
     unsigned long long landed[8], taken[8];      // tensor copies that the filling warps finish
     int32_t pages[4][16];                        // page numbers of a tile's boxes
     unsigned long long s_full[2], p_ready[2], o_done[2], q_full, q_empty, drain;
-    unsigned long long at[4][kTile];             // byte offsets of a tile's positions
-    float mul[2][kTcRows];                       // e4m3: what each row's scores are multiplied by
+    uint8_t scaled[2][kTcRows];                  // e4m3: exponent of each row's scale, 127 + e
     float m1[kTile], l1[kTile];                  // stream 1's maxima and sums, for the join
     uint32_t hurt[4];                            // part by part: a V value that is not finite was put to 0
     uint32_t tmem;
@@ -324,7 +325,7 @@ __device__ __forceinline__ void fill_queries(const AttendArgs &a, const Walk &w,
             const uint32_t e = __float_as_uint(top) >> 23;
             const bool usual = e > 2u && e < 252u;
             const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
-            sm.mul[w.n & 1u][row] = usual ? __uint_as_float(e << 23) : 1.0f;
+            sm.scaled[w.n & 1u][row] = (uint8_t)(usual ? e : 127u);
             for (uint32_t ch = 0; ch < DP / 8u; ++ch) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (ch < chunks) {
@@ -346,7 +347,7 @@ __device__ __forceinline__ void fill_queries(const AttendArgs &a, const Walk &w,
 // Pages whose length is no multiple of 8: every row is looked up and copied by itself.
 template <int DP, bool E>
 __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t q_at, uint32_t ring_at,
-                                          bool &corrupt) {
+                                          uint64_t (*at_of)[kTile], bool &corrupt) {
     using S = TcShape<DP, E>;
     const uint32_t t = threadIdx.x - 256u;
     const uint32_t row_bytes = a.c.head_dim * (E ? 1u : 2u);
@@ -369,7 +370,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
         };
         look_up(0);
         const auto offsets = [&](uint32_t k) {
-            sm.at[k & 3u][t] = next_at;
+            at_of[k & 3u][t] = next_at;
             asm volatile("bar.sync 2, 128;" ::: "memory");
             look_up(k + 1);
         };
@@ -412,7 +413,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i) {
                     const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
-                    const uint64_t at = sm.at[k & 3u][row];
+                    const uint64_t at = at_of[k & 3u][row];
                     const bool live = at != ~0ull && ch * 16u < row_bytes;
                     const uint32_t dst = ring_at + slot * S::tile + (ch >> 3) * S::block + row * 128u + (((ch ^ row) & 7u) << 4);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(base + (live ? at + ch * 16u : 0ull)),
@@ -437,7 +438,7 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i) {
                     const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
-                    const uint64_t at = sm.at[k & 3u][row];
+                    const uint64_t at = at_of[k & 3u][row];
                     v[i] = at != ~0ull && ch * 16u < row_bytes ? __ldg(reinterpret_cast<const uint4 *>(base + at + ch * 16u))
                                                                : make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -489,6 +490,7 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
                                          const CUtensorMap *kmap, const CUtensorMap *vmap, bool &corrupt) {
     using S = TcShape<DP, E>;
     const uint32_t lane = threadIdx.x & 31u, boxes = kTile / a.box;
+    constexpr uint32_t kRaw = E ? S::raw : 1;
     uint32_t pos = 0;
     Walk w;
     for (w.start(a, sh); w.more(); w.next(a)) {
@@ -518,9 +520,10 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
             const void *bar;
             uint32_t dst;
             if (E) {
-                bar_wait(sm, &sm.taken[slot], ((n / S::ring) & 1u) ^ 1u);
-                bar = &sm.landed[slot];
-                dst = raw_at + slot * S::raw_tile;
+                const uint32_t raw = n % kRaw;
+                bar_wait(sm, &sm.taken[raw], ((n / kRaw) & 1u) ^ 1u);
+                bar = &sm.landed[raw];
+                dst = raw_at + raw * S::raw_tile;
             } else {
                 bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
                 bar = is_v && p0 + kTile > w.q.ctx ? &sm.landed[slot] : &sm.full[slot];
@@ -587,15 +590,18 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
                     else if (hit) st_shared16(at, make_uint4(v[0], v[1], v[2], v[3])), found = true;
                 }
             } else {
-                bar_wait(sm, &sm.landed[slot], (n / S::ring) & 1u);
-                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
+                constexpr uint32_t kRaw = E ? S::raw : 1;
+                const uint32_t raw = n % kRaw;
+                bar_wait(sm, &sm.landed[raw], (n / kRaw) & 1u);
+                __syncwarp();
                 constexpr uint32_t CH = DP / 16, PER = kTile * CH / 128;
                 uint32_t c[PER][4];
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i)
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3])
-                                 : "r"(raw_at + slot * S::raw_tile + (i * 128u + t) * 16u) : "memory");
-                warp_arrive(&sm.taken[slot]);
+                                 : "r"(raw_at + raw * S::raw_tile + (i * 128u + t) * 16u) : "memory");
+                warp_arrive(&sm.taken[raw]);
+                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i) {
                     const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
@@ -746,7 +752,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
             bar_wait(sm, &sm.s_full[s], jobs & 1u);
             __syncwarp();
             tc_fence_after();
-            if (E && done == 0) mul *= sm.mul[w.n & 1u][row];
+            if (E && done == 0) mul *= __uint_as_float((uint32_t)sm.scaled[w.n & 1u][row] << 23);
             const uint32_t p0 = (w.tile + k) * kTile;
             const bool edge = p0 + kTile > w.q.ctx || p0 + kTile > p_end;
             if (warp_live) {
@@ -930,13 +936,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
                                                               const __grid_constant__ CUtensorMap kmap,
                                                               const __grid_constant__ CUtensorMap vmap) {
     using S = TcShape<DP, E>;
-    extern __shared__ uint8_t dyn[];
+    extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ TcShared sm;
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Share sh = share_of<kTcThreads, true>(a, ws, kTcRows, kTile, sm.plan);
     if (sh.u0 == sh.u1) return;
-    const uint32_t q_at = (s32(dyn) + 1023u) & ~1023u, ring_at = q_at + 2u * S::tile, raw_at = q_at + S::raw_at;
+    const uint32_t q_at = s32(dyn), ring_at = q_at + 2u * S::tile, raw_at = q_at + S::raw_at;
     if (tid == 0) {
         for (uint32_t i = 0; i < S::ring; ++i) {
             bar_init(&sm.full[i], a.box && !E ? 1u : 4u);     // the copies' own arrival, or four warps'
@@ -971,7 +977,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         if (a.box) finish_role<DP, E>(a, sh, sm, q_at, ring_at, raw_at);
-        else fill_role<DP, E>(a, sh, sm, q_at, ring_at, corrupt);
+        else fill_role<DP, E>(a, sh, sm, q_at, ring_at, reinterpret_cast<uint64_t(*)[kTile]>(dyn + S::raw_at), corrupt);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 13 && a.box) box_role<DP, E>(a, sh, sm, ring_at, raw_at, &kmap, &vmap, corrupt);
@@ -1029,7 +1035,7 @@ template <int DP, bool E>
 static bool launch(AttendArgs a, const AttendWs &ws, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     constexpr uint32_t bytes = TcShape<DP, E>::smem;
-    static_assert(bytes + sizeof(TcShared) + 1024 <= 232448 && TcShape<DP, E>::ring <= 8, "shared memory of a CTA");
+    static_assert(bytes + (sizeof(TcShared) + 1023) / 1024 * 1024 <= 232448 && TcShape<DP, E>::ring <= 8, "shared memory of a CTA");
     if (!raise_smem(reinterpret_cast<const void *>(attend_large<DP, E>), bytes, ready)) return false;
     CUtensorMap kmap = {}, vmap = {};
     // strides reach 2^41 bytes, a tensor map's less than 2^40
