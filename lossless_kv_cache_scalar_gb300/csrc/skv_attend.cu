@@ -180,16 +180,13 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
     }
 }
 
-// The end of a CTA with work: its error, if it is the first; the last one writes the
-// status and clears both words.
+// The end of a CTA with work: one word counts the CTAs in its low half and holds the kinds of
+// error above; the last CTA writes the status and clears it.
 __device__ __forceinline__ void finish(const AttendArgs &a, const AttendWs &ws, int32_t err, uint32_t active) {
-    if (err) {
-        atomicCAS(ws.error, SKV_OK, err);
-        __threadfence();
-    }
-    if (atomicAdd(ws.finished, 1u) == active - 1u) {
-        __threadfence();
-        *a.status = atomicExch(ws.error, SKV_OK);
+    if (err) atomicOr(ws.finished, err == SKV_ERR_CORRUPT ? kSawCorrupt : kSawInvalid);
+    const uint32_t was = atomicAdd(ws.finished, 1u);
+    if ((was & 0xFFFFu) == active - 1u) {
+        *a.status = status_of(was);
         *ws.finished = 0u;
     }
 }
@@ -203,7 +200,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 256 ? 1 : 2) attend_small(A
     __shared__ uint32_t sm_last;
     const Share sh = share_of<kWarps * 32, false>(a, ws, 16u, S::unit, sm_plan);
     if (sh.u0 == sh.u1) {
-        if (sh.active == 0 && blockIdx.x == 0 && tid == 0) *a.status = atomicExch(ws.error, SKV_OK);
+        if (sh.active == 0 && blockIdx.x == 0 && tid == 0) *a.status = status_of(atomicExch(ws.finished, 0u));
         return;
     }
     const uint32_t ring = smem_of(ring_all) + warp * S::ring;

@@ -39,8 +39,7 @@ struct Plan {
 
 struct AttendWs {
     uint32_t *arrived;  // [CTA]: parts done of the item that starts in the CTA and goes on
-    uint32_t *finished; // CTAs done
-    int32_t *error;     // the first error of a CTA
+    uint32_t *finished; // CTAs done, and the errors seen
     Plan *plan;
     int32_t *errs;      // one per CTA
     Desc *desc;         // one per CTA
@@ -48,6 +47,11 @@ struct AttendWs {
 };
 
 __host__ __device__ inline uint64_t part_floats(uint32_t R, uint32_t DP) { return (uint64_t)R * (2u + DP); }
+
+constexpr uint32_t kSawInvalid = 1u << 16, kSawCorrupt = 1u << 17;
+__host__ __device__ inline int32_t status_of(uint32_t word) {
+    return word & kSawInvalid ? SKV_ERR_INVALID_ARG : word & kSawCorrupt ? SKV_ERR_CORRUPT : SKV_OK;
+}
 
 // Counters (SKV_ATTENTION_ZERO_BYTES), then plan, errs, descs.
 constexpr uint64_t kWsPlan = SKV_ATTENTION_ZERO_BYTES, kWsErrs = kWsPlan + 256u, kWsDesc = kWsErrs + 1536u;
@@ -58,7 +62,7 @@ static_assert(kWsHead % 32u == 0 && sizeof(Desc) == 32 && kCtasSmall * 4u <= 153
 inline AttendWs attend_ws(void *base) {
     uint8_t *p = static_cast<uint8_t *>(base);
     uint32_t *n = reinterpret_cast<uint32_t *>(p);
-    return AttendWs{n + 2, n, reinterpret_cast<int32_t *>(n + 1), reinterpret_cast<Plan *>(p + kWsPlan),
+    return AttendWs{n + 1, n, reinterpret_cast<Plan *>(p + kWsPlan),
                     reinterpret_cast<int32_t *>(p + kWsErrs), reinterpret_cast<Desc *>(p + kWsDesc),
                     reinterpret_cast<float *>(p + kWsHead)};
 }
@@ -192,8 +196,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
         if (blockIdx.x == 0) *ws.plan = Plan{U, active};
     }
     if (!JOINED && tid == 0 && blockIdx.x == 0 && err) {
-        atomicCAS(ws.error, SKV_OK, err);
-        __threadfence();
+        atomicOr(ws.finished, kSawInvalid);
     }
     if (blockIdx.x >= active) return s;
     s.u0 = quotient((uint64_t)blockIdx.x * U, active);

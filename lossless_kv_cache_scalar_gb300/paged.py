@@ -18,18 +18,23 @@ from . import _binding as B
 from .api import _check_dev, _ptr
 
 
-def _stream_of(stream, device) -> int:
+def _stream_of(stream, device: int) -> int:
     """The handle of `stream`, or of the current stream of the tensors' device (the
     raw query: a Stream object costs several microseconds of a short step)."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _check_i32(what: str, numel: int, *ts):
+_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+def _check_words(what: str, dtype, numel: int, *ts):
+    """Contiguous CUDA tensors of one type and size (a step makes a dozen of these
+    checks, each of a few tenths of a microsecond: no calls that are not needed)."""
     for t in ts:
-        if not t.is_cuda or t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous int32 CUDA tensors of {numel} entries")
+        if t.dtype is not dtype or t.numel() != numel or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous {dtype} CUDA tensors of {numel} entries")
 
 
 def _table_rows(t):
@@ -42,6 +47,7 @@ def _table_rows(t):
 class _Status:
     def _new_status(self, device):
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._status, self._device = self.status.data_ptr(), self.status.device.index
 
     def check_status(self, where: str, stream=None):
         (stream or torch.cuda.current_stream()).synchronize()
@@ -56,7 +62,7 @@ class PageTable(_Status):
 
     def __init__(self, block_table: torch.Tensor, page_tokens: int, pool_pages: int):
         self._stride = _table_rows(block_table)
-        self.block_table = block_table
+        self.block_table, self._table = block_table, block_table.data_ptr()
         self.page_tokens, self.pool_pages = int(page_tokens), int(pool_pages)
         self.n_requests, self.max_pages = block_table.shape
         self._new_status(block_table.device)
@@ -67,17 +73,16 @@ class PageTable(_Status):
         (free_pages, free_state = [head, count]), their table entries, cu_new and the
         slot map; a request of ctx_len < 0 gives its pages back. The new page counts and
         ring state go to n_pages_out and free_state_out (other tensors than the inputs)."""
-        n = self.n_requests
-        _check_i32("ctx_len, new_len, n_pages and n_pages_out", n, ctx_len, new_len, n_pages, n_pages_out)
-        _check_i32("free_state and free_state_out", 2, free_state, free_state_out)
-        _check_i32("cu_new", n + 1, cu_new)
-        _check_dev(free_pages, "free_pages", torch.int32)
-        _check_dev(slots, "slots", torch.int64)
+        n, size, room = self.n_requests, free_pages.numel(), slots.numel()
+        _check_words("ctx_len, new_len, n_pages and n_pages_out", _I32, n, ctx_len, new_len, n_pages, n_pages_out)
+        _check_words("free_state and free_state_out", _I32, 2, free_state, free_state_out)
+        _check_words("cu_new", _I32, n + 1, cu_new)
+        _check_words("free_pages", _I32, size, free_pages)
+        _check_words("slots", _I64, room, slots)
         rc = B.lib().skv_page_map(self.page_tokens, self.pool_pages, n, ctx_len.data_ptr(), new_len.data_ptr(),
-                                  self.block_table.data_ptr(), self._stride, self.max_pages, n_pages.data_ptr(),
-                                  n_pages_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
-                                  free_state.data_ptr(), free_state_out.data_ptr(), cu_new.data_ptr(),
-                                  slots.data_ptr(), slots.numel(), self.status.data_ptr(), _stream_of(stream, self.status.device))
+                                  self._table, self._stride, self.max_pages, n_pages.data_ptr(), n_pages_out.data_ptr(),
+                                  free_pages.data_ptr(), size, free_state.data_ptr(), free_state_out.data_ptr(),
+                                  cu_new.data_ptr(), slots.data_ptr(), room, self._status, _stream_of(stream, self._device))
         B.check("skv_page_map", rc)
 
 
@@ -131,6 +136,7 @@ class PagedKV(_Status):
                 _check_dev(s, "k_scale and v_scale", torch.float32, numel=n_heads)
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.block_table, self.n_heads, self.head_dim = block_table, n_heads, head_dim
+        self._row_shape, self._scale = torch.Size((n_heads, head_dim)), 1.0 / math.sqrt(head_dim)
         stride, n_requests, max_pages = 0, 0, 0
         if block_table is not None:
             stride = _table_rows(block_table)
@@ -154,23 +160,24 @@ class PagedKV(_Status):
                 B.lib().skv_tree_attention_workspace_bytes(self._ref, q_heads, C.byref(v)))
         self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
         self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
+        self._workspace, self._workspace_bytes = self.workspace.data_ptr(), v.value
         self.q_heads = q_heads
 
     def append_into(self, k, v, slots, rows=None, stream=None):
         """Enqueue skv_cache_append: rows of k and v (bf16 [n_src][n_heads][head_dim], any
         row and head strides that are multiples of 8) into the slots (int64, -1 skips)."""
-        for t, what in ((k, "k"), (v, "v")):
-            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != self.n_heads \
-                    or t.shape[2] != self.head_dim or t.stride(2) != 1:
-                raise ValueError(f"{what} must be a bf16 CUDA tensor [n_src][{self.n_heads}][{self.head_dim}]")
-        if k.shape != v.shape or k.stride() != v.stride():
-            raise ValueError("k and v must have the same shape and strides")
-        _check_dev(slots, "slots", torch.int64)
+        shape, stride = k.shape, k.stride()
+        if v.shape != shape or v.stride() != stride or k.dtype is not _BF16 or v.dtype is not _BF16 or not k.is_cuda \
+                or not v.is_cuda or len(shape) != 3 or shape[1:] != self._row_shape or stride[2] != 1:
+            raise ValueError("k and v must be bf16 CUDA tensors [n_src][%d][%d] of the same strides, the last 1"
+                             % tuple(self._row_shape))
+        n = slots.numel()
+        _check_words("slots", _I64, n, slots)
         if rows is not None:
-            _check_dev(rows, "rows", torch.int32, numel=slots.numel())
-        rc = B.lib().skv_cache_append(self._ref, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.shape[0],
-                                      None if rows is None else rows.data_ptr(), slots.data_ptr(), slots.numel(),
-                                      self.status.data_ptr(), _stream_of(stream, self.status.device))
+            _check_words("rows", _I32, n, rows)
+            rows = rows.data_ptr()
+        rc = B.lib().skv_cache_append(self._ref, k.data_ptr(), v.data_ptr(), stride[0], stride[1], shape[0], rows,
+                                      slots.data_ptr(), n, self._status, _stream_of(stream, self._device))
         B.check("skv_cache_append", rc)
 
     def append(self, k, v, slots, rows=None, stream=None):
@@ -187,32 +194,33 @@ class PagedKV(_Status):
         to 1 / sqrt(head_dim); lse: float32 [n_rows][q_heads] or None."""
         if self.block_table is None:
             raise ValueError("attend needs a block_table")
-        if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != self.head_dim \
-                or q.stride(2) != 1 or q.shape[1] == 0 or q.shape[1] % self.n_heads:
+        shape, stride = q.shape, q.stride()
+        if len(shape) != 3 or q.dtype is not _BF16 or not q.is_cuda or stride[2] != 1 or shape[2] != self.head_dim \
+                or shape[1] == 0 or shape[1] % self.n_heads:
             raise ValueError(f"q must be a bf16 CUDA tensor [n_rows][a multiple of {self.n_heads}][{self.head_dim}]")
-        n, heads = q.shape[0], q.shape[1]
-        if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+        n, heads = shape[0], shape[1]
+        if out.shape != shape or out.dtype is not _BF16 or not out.is_cuda or not out.is_contiguous():
             raise ValueError("out must be a contiguous bf16 CUDA tensor of q's shape")
-        _check_i32("ctx_len", self.n_requests, ctx_len)
-        _check_i32("cu_new", self.n_requests + 1, cu_new)
+        _check_words("ctx_len", _I32, self.n_requests, ctx_len)
+        _check_words("cu_new", _I32, self.n_requests + 1, cu_new)
         words = 0
         if mask is not None:
-            if not mask.is_cuda or mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] != n \
-                    or not mask.is_contiguous() or mask.shape[1] == 0:
-                raise ValueError("mask must be a contiguous int64 CUDA tensor [n_rows][words]")
+            if mask.dim() != 2 or mask.shape[0] != n or mask.shape[1] == 0:
+                raise ValueError("mask must be an int64 CUDA tensor [n_rows][words]")
             words = mask.shape[1]
+            _check_words("mask", _I64, n * words, mask)
+            mask = mask.data_ptr()
         if lse is not None:
-            _check_dev(lse, "lse", torch.float32, numel=n * heads)
+            _check_words("lse", _F32, n * heads, lse)
+            lse = lse.data_ptr()
         if heads != self.q_heads:
             if torch.cuda.is_current_stream_capturing():
                 raise ValueError("give PagedKV its q_heads before a capture")
             self._make_workspace(heads)
         rc = B.lib().skv_tree_attention(
-            self._ref, q.data_ptr(), q.stride(0), q.stride(1), heads, n, ctx_len.data_ptr(), cu_new.data_ptr(),
-            None if mask is None else mask.data_ptr(), words, n if max_nodes is None else max_nodes,
-            1.0 / math.sqrt(self.head_dim) if scale is None else scale, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), self.status.data_ptr(), self.workspace.data_ptr(),
-            self.workspace.numel(), _stream_of(stream, self.status.device))
+            self._ref, q.data_ptr(), stride[0], stride[1], heads, n, ctx_len.data_ptr(), cu_new.data_ptr(), mask, words,
+            n if max_nodes is None else max_nodes, self._scale if scale is None else scale, out.data_ptr(), lse,
+            self._status, self._workspace, self._workspace_bytes, _stream_of(stream, self._device))
         B.check("skv_tree_attention", rc)
 
     def attend(self, q, ctx_len, cu_new, mask=None, max_nodes: int | None = None, scale: float | None = None,
