@@ -21,9 +21,9 @@
 
 namespace skv {
 
-// Grids: persistent CTAs, two per SM of 152 for the small-row kernel, one for
+// Grids: persistent CTAs, three per SM of 152 for the small-row kernel, one for
 // the tcgen05 one. Constants, so that the workspace's size depends on no device.
-constexpr uint32_t kCtasSmall = 304, kCtasLarge = 152;
+constexpr uint32_t kCtasSmall = 456, kCtasLarge = 152;
 
 // An item that starts in a CTA and goes on in the next ones.
 struct Desc {
@@ -54,10 +54,10 @@ __host__ __device__ inline int32_t status_of(uint32_t word) {
 }
 
 // Counters (SKV_ATTENTION_ZERO_BYTES), then plan, errs, descs.
-constexpr uint64_t kWsPlan = SKV_ATTENTION_ZERO_BYTES, kWsErrs = kWsPlan + 256u, kWsDesc = kWsErrs + 1536u;
-constexpr uint64_t kWsHead = kWsDesc + 304u * sizeof(Desc);
-static_assert(kWsHead % 32u == 0 && sizeof(Desc) == 32 && kCtasSmall * 4u <= 1536u && kCtasSmall * 4u + 8u <= SKV_ATTENTION_ZERO_BYTES &&
-              kCtasLarge <= kCtasSmall && kWsHead % 256u == 0, "workspace head");
+constexpr uint64_t kWsPlan = SKV_ATTENTION_ZERO_BYTES, kWsErrs = kWsPlan + 256u, kWsDesc = kWsErrs + 768u;
+constexpr uint64_t kWsHead = kWsDesc + 160u * sizeof(Desc);
+static_assert(kWsHead % 32u == 0 && sizeof(Desc) == 32 && kCtasLarge * 4u <= 768u && kCtasSmall * 4u + 4u <= SKV_ATTENTION_ZERO_BYTES &&
+              kCtasLarge <= 160u && kWsHead % 256u == 0, "workspace head");
 
 inline AttendWs attend_ws(void *base) {
     uint8_t *p = static_cast<uint8_t *>(base);
