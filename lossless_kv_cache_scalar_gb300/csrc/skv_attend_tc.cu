@@ -264,6 +264,12 @@ __device__ __forceinline__ uint32_t tc_raise2(uint32_t codes) {
     return r;
 }
 
+__device__ __forceinline__ uint2 ld_shared8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -594,33 +600,38 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
                 const uint32_t raw = n % kRaw;
                 bar_wait(sm, &sm.landed[raw], (n / kRaw) & 1u);
                 __syncwarp();
-                constexpr uint32_t CH = DP / 16, PER = kTile * CH / 128;
-                uint32_t c[PER][4];
-#pragma unroll
-                for (uint32_t i = 0; i < PER; ++i)
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3])
-                                 : "r"(raw_at + raw * S::raw_tile + (i * 128u + t) * 16u) : "memory");
-                warp_arrive(&sm.taken[raw]);
-                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
+                // Thread: 16 codes of channels 16 ch .. of every (128 / CH)th row. The eight bytes that go first
+                // differ between the two 64-channel blocks, so that eight lanes' stores lie on different banks.
+                constexpr uint32_t CH = DP / 16, PER = kTile * CH / 128, STEP = 128 / CH;
+                const uint32_t ch = t % CH, row0 = t / CH, turn = (ch >> 2) & 1u;
+                const uint32_t from = raw_at + raw * S::raw_tile + t * 16u + turn * 8u, to = ring_at + slot * S::tile + (ch >> 2) * S::block + row0 * 128u;
+                const uint32_t to0 = to + (((2u * ch + turn) ^ row0) & 7u) * 16u, to1 = to + (((2u * ch + 1u - turn) ^ row0) & 7u) * 16u;
+                uint2 c[PER][2];
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i) {
-                    const uint32_t x = i * 128u + t, row = x / CH, ch = x % CH;
-                    if (edge && row >= first) {
+                    c[i][0] = ld_shared8(from + i * 2048u);
+                    c[i][1] = ld_shared8((from ^ 8u) + i * 2048u);
+                }
+                warp_arrive(&sm.taken[raw]);
+                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
+                if (edge) {
+#pragma unroll
+                    for (uint32_t i = 0; i < PER; ++i) {
+                        const uint32_t row = row0 + i * STEP;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
+                            uint32_t &x = j & 1 ? c[i][j >> 1].y : c[i][j >> 1].x;
 #pragma unroll
                             for (int b = 0; b < 32; b += 8)
-                                if (row < last && ((c[i][j] >> b) & 0x7Fu) == 0x7Fu) c[i][j] &= ~(0xFFu << b), found = true;
-                            if (row >= last) c[i][j] = 0u;
+                                if (row >= first && row < last && ((x >> b) & 0x7Fu) == 0x7Fu) x &= ~(0xFFu << b), found = true;
+                            if (row >= last) x = 0u;
                         }
                     }
-                    const uint32_t at = ring_at + slot * S::tile + (ch >> 2) * S::block + row * 128u, c0 = 2u * ch;
-                    const uint4 lo = make_uint4(tc_raise2(c[i][0]), tc_raise2(c[i][0] >> 16), tc_raise2(c[i][1]), tc_raise2(c[i][1] >> 16));
-                    const uint4 hi = make_uint4(tc_raise2(c[i][2]), tc_raise2(c[i][2] >> 16), tc_raise2(c[i][3]), tc_raise2(c[i][3] >> 16));
-                    // even chunks of one 64-channel block and odd ones of the other at a time: no two on the same banks
-                    const bool turn = (ch >> 2) & 1u;
-                    st_shared16(at + (((c0 + turn) ^ row) & 7u) * 16u, turn ? hi : lo);
-                    st_shared16(at + (((c0 + 1u - turn) ^ row) & 7u) * 16u, turn ? lo : hi);
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < PER; ++i) {
+                    st_shared16(to0 + i * STEP * 128u, make_uint4(tc_raise2(c[i][0].x), tc_raise2(c[i][0].x >> 16), tc_raise2(c[i][0].y), tc_raise2(c[i][0].y >> 16)));
+                    st_shared16(to1 + i * STEP * 128u, make_uint4(tc_raise2(c[i][1].x), tc_raise2(c[i][1].x >> 16), tc_raise2(c[i][1].y), tc_raise2(c[i][1].y >> 16)));
                 }
             }
             if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
@@ -944,7 +955,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
     if (sh.u0 == sh.u1) return;
     const uint32_t q_at = s32(dyn), ring_at = q_at + 2u * S::tile, raw_at = q_at + S::raw_at;
     if (tid == 0) {
-        for (uint32_t i = 0; i < S::ring; ++i) {
+        for (uint32_t i = 0; i < 8; ++i) {
             bar_init(&sm.full[i], a.box && !E ? 1u : 4u);     // the copies' own arrival, or four warps'
             bar_init(&sm.empty[i], 1u);
             bar_init(&sm.landed[i], 1u);
@@ -1035,7 +1046,7 @@ template <int DP, bool E>
 static bool launch(AttendArgs a, const AttendWs &ws, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     constexpr uint32_t bytes = TcShape<DP, E>::smem;
-    static_assert(bytes + (sizeof(TcShared) + 1023) / 1024 * 1024 <= 232448 && TcShape<DP, E>::ring <= 8, "shared memory of a CTA");
+    static_assert(bytes + (sizeof(TcShared) + 1023) / 1024 * 1024 <= 232448 && TcShape<DP, E>::ring <= 8 && TcShape<DP, E>::raw <= 8, "shared memory of a CTA");
     if (!raise_smem(reinterpret_cast<const void *>(attend_large<DP, E>), bytes, ready)) return false;
     CUtensorMap kmap = {}, vmap = {};
     // strides reach 2^41 bytes, a tensor map's less than 2^40
