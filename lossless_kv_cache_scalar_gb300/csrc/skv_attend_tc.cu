@@ -60,7 +60,7 @@ struct Walk {
     uint32_t h, rt, tile_end, rows;                 // rows: of this row tile
 
     __device__ __forceinline__ void request(const AttendArgs &a) {
-        tiles = (q.len + kTile - 1) / kTile;
+        tiles = (q.len + a.span - 1) / a.span;
         rts = (q.n * a.group + kTcRows - 1) / kTcRows;
     }
     __device__ __forceinline__ void part(const AttendArgs &a) {
@@ -300,6 +300,8 @@ __device__ __forceinline__ void fill_queries(const AttendArgs &a, const Walk &w,
     if (t == 0) sm.hurt[w.n & 3u] = 0u;
     asm volatile("bar.sync 2, 128;" ::: "memory");                   // the last part's offsets are read, the flag is down
     const uint32_t q_rows = both ? 256u : 128u;
+    // a negative scale turns the queries, so that the weights' threads look for the largest score in any case
+    const bool turned = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + w.h) : 1.0f) < 0.0f;
     if (!E) {
         constexpr uint32_t CH = DP / 8;                          // 16-byte chunks of a row
         for (uint32_t x = t; x < q_rows * CH; x += 128u) {
@@ -312,6 +314,14 @@ __device__ __forceinline__ void fill_queries(const AttendArgs &a, const Walk &w,
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (turned) {
+            for (uint32_t x = t; x < q_rows * CH; x += 128u) {       // this thread's own copies
+                const uint32_t row = x / CH, ch = x % CH;
+                const uint32_t at = q_at + (row >> 7) * S::tile + (ch >> 3) * S::block + (row & 127u) * 128u + (((ch ^ row) & 7u) << 4);
+                const uint2 lo = ld_shared8(at), hi = ld_shared8(at + 8u);
+                st_shared16(at, make_uint4(lo.x ^ 0x80008000u, lo.y ^ 0x80008000u, hi.x ^ 0x80008000u, hi.y ^ 0x80008000u));
+            }
+        }
     } else {
         // fp16 after a power-of-two scale per row (skv_attend.cu): one thread per row
         for (uint32_t row = t; row < q_rows; row += 128u) {
@@ -330,7 +340,7 @@ __device__ __forceinline__ void fill_queries(const AttendArgs &a, const Walk &w,
             }
             const uint32_t e = __float_as_uint(top) >> 23;
             const bool usual = e > 2u && e < 252u;
-            const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
+            const float down = (usual ? __uint_as_float((254u - e) << 23) : 1.0f) * (turned ? -1.0f : 1.0f);
             sm.scaled[w.n & 1u][row] = (uint8_t)(usual ? e : 127u);
             for (uint32_t ch = 0; ch < DP / 8u; ++ch) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -486,8 +496,8 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
     }
 }
 
-// Pages of a multiple of 8 positions: a tile is 128 / box boxes, box the largest power of
-// two up to 128 that divides the page length, so that no box crosses a page. A lane
+// Pages of a multiple of 8 positions: a tile holds `span` positions in boxes of `box`, a
+// divisor of the page length, so that no box crosses a page (paged_box). A lane
 // per box looks the page up one tile ahead and starts the box's copies; a page number
 // outside the pool is outside the tensor and reads 0. Boxes past the part's end are
 // not copied: their scores are not used and finish_role clears their V.
@@ -495,16 +505,16 @@ template <int DP, bool E>
 __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, TcShared &sm, uint32_t ring_at, uint32_t raw_at,
                                          const CUtensorMap *kmap, const CUtensorMap *vmap, bool &corrupt) {
     using S = TcShape<DP, E>;
-    const uint32_t lane = threadIdx.x & 31u, boxes = kTile / a.box;
+    const uint32_t lane = threadIdx.x & 31u, boxes = a.span / a.box;
     constexpr uint32_t kRaw = E ? S::raw : 1;
     uint32_t pos = 0;
     Walk w;
     for (w.start(a, sh); w.more(); w.next(a)) {
         const bool both = w.both();
-        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * a.span);
         int32_t next_page = 0;
         const auto look_up = [&](uint32_t k) {
-            const uint32_t p = (w.tile + k) * kTile + lane * a.box;
+            const uint32_t p = (w.tile + k) * a.span + lane * a.box;
             if (k < T && lane < boxes && p < p_end) {
                 next_page = __ldg(a.c.table + (uint64_t)w.r * a.c.table_stride + div_by(p, a.c.page));
                 if ((uint32_t)next_page >= a.c.n_pages) {
@@ -516,7 +526,7 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
         look_up(0);
         for (uint32_t e = 0; e < 2 * T; ++e) {
             bool is_v;
-            const uint32_t k = fill_of(both, T, e, is_v), n = pos + e, p0 = (w.tile + k) * kTile;
+            const uint32_t k = fill_of(both, T, e, is_v), n = pos + e, p0 = (w.tile + k) * a.span;
             if (!is_v) {
                 if (lane < 16u) sm.pages[k & 3u][lane] = next_page;
                 __syncwarp();
@@ -532,7 +542,7 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
                 dst = raw_at + raw * S::raw_tile;
             } else {
                 bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
-                bar = is_v && p0 + kTile > w.q.ctx ? &sm.landed[slot] : &sm.full[slot];
+                bar = is_v && p0 + a.span > w.q.ctx ? &sm.landed[slot] : &sm.full[slot];
                 dst = ring_at + slot * S::tile;
             }
             const uint32_t live = min(boxes, (p_end - p0 + a.box - 1) / a.box);
@@ -568,14 +578,14 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
     Walk w;
     for (w.start(a, sh); w.more(); w.next(a)) {
         const bool both = w.both();
-        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * a.span);
         fill_queries<DP, E>(a, w, sm, q_at);
         for (uint32_t e = 0; e < 2 * T; ++e) {
             bool is_v;
-            const uint32_t k = fill_of(both, T, e, is_v), n = pos + e, p0 = (w.tile + k) * kTile, slot = n % S::ring;
-            const bool edge = is_v && p0 + kTile > w.q.ctx;
+            const uint32_t k = fill_of(both, T, e, is_v), n = pos + e, p0 = (w.tile + k) * a.span, slot = n % S::ring;
+            const bool edge = is_v && p0 + a.span > w.q.ctx;
             if (!E && !edge) continue;
-            const uint32_t first = w.q.ctx > p0 ? w.q.ctx - p0 : 0u, last = min(kTile, p_end - p0);     // drafted rows [first, last)
+            const uint32_t first = w.q.ctx > p0 ? w.q.ctx - p0 : 0u, last = min(a.span, p_end - p0);     // drafted rows [first, last)
             bool found = false;
             if (!E) {
                 bar_wait(sm, &sm.landed[slot], (turns >> slot) & 1u);
@@ -749,47 +759,46 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
     group_sync(s);
     while (w.more()) {
         const bool both = w.both();
-        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * kTile);
+        const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * a.span);
         const uint32_t row = both ? s * kTile + t : t;               // of the row tile
         const uint32_t all = w.rt * kTcRows + row, node = all / a.group, g = w.h * a.group + all - node * a.group;
         const bool live = row < w.rows, warp_live = (row & ~31u) < w.rows;
         // (no wait for the queries here: a part of few jobs can be two phases behind the filling warps)
         float mul = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + w.h) : 1.0f) * 1.4426950408889634f;
-        const bool falls = mul < 0.0f;
-        mul = fabsf(mul);
+        // (a negative scale has turned the queries;) at least 2^-100, so that -infinity times it stays that
+        if (!E) mul = fmaxf(fabsf(mul), 0x1p-100f);
         float m = -INFINITY, l = 0.0f;
         uint32_t done = 0;                                           // jobs of this part
         for (uint32_t k = both ? 0u : s; k < T; k += both ? 1u : 2u, ++done, ++jobs) {
             bar_wait(sm, &sm.s_full[s], jobs & 1u);
             __syncwarp();
             tc_fence_after();
-            if (E && done == 0) mul *= __uint_as_float((uint32_t)sm.scaled[w.n & 1u][row] << 23);
-            const uint32_t p0 = (w.tile + k) * kTile;
-            const bool edge = p0 + kTile > w.q.ctx || p0 + kTile > p_end;
+            if (E && done == 0) mul = fmaxf(fabsf(mul) * __uint_as_float((uint32_t)sm.scaled[w.n & 1u][row] << 23), 0x1p-100f);
+            const uint32_t p0 = (w.tile + k) * a.span;
+            const bool edge = p0 + a.span > w.q.ctx || p0 + a.span > p_end, cut = a.span < kTile;
             if (warp_live) {
-                uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+                // a span below 128 positions (at least 112) ends inside the last 32 columns
+                uint32_t bits[4] = {~0u, ~0u, ~0u, cut ? (1u << (a.span - 96u)) - 1u : ~0u};
                 if (edge && live) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) bits[c] = sees32(a, w.q, node, p0 + 32u * c, p_end);
+                    for (int c = 0; c < 4; ++c) bits[c] &= sees32(a, w.q, node, p0 + 32u * c, p_end);
                 }
                 __syncwarp();
-                // the row's 128 scores, all in registers; those it does not see are NaN, which max leaves out
+                // the row's 128 scores, all in registers; -infinity where it does not see
                 uint32_t x[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(x[c], at_s + 32u * c);
                 tc_wait_ld();
-                if (falls) {                                         // a negative scale: largest of -score
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[c][i] ^= 0x80000000u;
-                }
                 if (edge) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!((bits[c] >> i) & 1u)) x[c][i] = 0x7FFFFFFFu;
+                            if (!((bits[c] >> i) & 1u)) x[c][i] = 0xFF800000u;
+                } else if (cut) {
+#pragma unroll
+                    for (int i = 16; i < 32; ++i)
+                        if (!((bits[3] >> i) & 1u)) x[3][i] = 0xFF800000u;
                 }
                 float far[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -797,7 +806,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) far[c] = max3(far[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
                 far[0] = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3]));
-                const float top = far[0] == -INFINITY ? -INFINITY : far[0] * mul;      // in base 2
+                const float top = far[0] * mul;                      // in base 2
                 // the reference moves only for a weight of 2^8 or more against it
                 const bool move = top > m + 8.0f || (m == -INFINITY && top > m);
                 const float keep = move ? part_weight(m, top) : 1.0f;
@@ -827,11 +836,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         uint64_t z = fma2((uint64_t)x[c][i] | ((uint64_t)x[c][i + 1] << 32), mul2, base2);
-                        float w0 = ex2(__uint_as_float((uint32_t)z)), w1 = ex2(__uint_as_float((uint32_t)(z >> 32)));
-                        if (edge) {
-                            if (!((bits[c] >> i) & 1u)) w0 = 0.0f;
-                            if (!((bits[c] >> (i + 1)) & 1u)) w1 = 0.0f;
-                        }
+                        const float w0 = ex2(__uint_as_float((uint32_t)z)), w1 = ex2(__uint_as_float((uint32_t)(z >> 32)));
                         sum2[(i >> 1) & 1] = add2(sum2[(i >> 1) & 1], pair_of(w0, w1));
                         y[i / 2] = tc_pack<E>(w0, w1);
                     }
@@ -895,7 +900,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     if (hurt && live) {
                         for (int i = 0; i < 32; ++i) {
                             if (32u * c + i >= a.c.head_dim) break;
-                            const float add = not_finite_sum(a, w.q, w.r, w.h, node, 32u * c + i, w.tile * kTile, p_end);
+                            const float add = not_finite_sum(a, w.q, w.r, w.h, node, 32u * c + i, w.tile * a.span, p_end);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)             // registers have no index of their own
                                 if (j == i) x[j] = __float_as_uint(__uint_as_float(x[j]) + add);
@@ -951,7 +956,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
     __shared__ TcShared sm;
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share sh = share_of<kTcThreads, true>(a, ws, kTcRows, kTile, sm.plan);
+    const Share sh = share_of<kTcThreads, true>(a, ws, kTcRows, a.span, sm.plan);
     if (sh.u0 == sh.u1) return;
     const uint32_t q_at = s32(dyn), ring_at = q_at + 2u * S::tile, raw_at = q_at + S::raw_at;
     if (tid == 0) {
@@ -977,20 +982,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
+    if (a.span < kTile) {
+        // rows of the ring (and of the codes behind it) that no copy reaches: read as 0, not as what was there
+        const uint32_t rows = kTile - a.span;
+        for (uint32_t x = tid; x < S::ring * (DP / 64u) * rows * 8u; x += kTcThreads)
+            st_shared16(ring_at + x / (rows * 8u) * S::block + (a.span + x / 8u % rows) * 128u + x % 8u * 16u, make_uint4(0u, 0u, 0u, 0u));
+        for (uint32_t x = tid; x < S::raw * rows * (DP / 16u); x += kTcThreads)
+            st_shared16(raw_at + x / (rows * (DP / 16u)) * S::raw_tile + a.span * DP + x % (rows * (DP / 16u)) * 16u, make_uint4(0u, 0u, 0u, 0u));
+        proxy_fence();
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     bool corrupt = false;
-    // 512 threads of 128 registers, dealt out anew: 2 x 176 + 112 + 48 = 4 x 128 per lane of the four groups.
+    // 512 threads of 128 registers, dealt out anew: 2 x 192 + 88 + 40 = 4 x 128 per lane of the four groups.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         weight_role<DP, E>(a, ws, sh, sm, tmem);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (a.box) finish_role<DP, E>(a, sh, sm, q_at, ring_at, raw_at);
         else fill_role<DP, E>(a, sh, sm, q_at, ring_at, reinterpret_cast<uint64_t(*)[kTile]>(dyn + S::raw_at), corrupt);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 13 && a.box) box_role<DP, E>(a, sh, sm, ring_at, raw_at, &kmap, &vmap, corrupt);
         if (warp == 12) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
     }
@@ -1036,7 +1050,7 @@ static bool pool_map(CUtensorMap *map, const PagedView &c, const uint8_t *pool, 
     // the stride of a dimension of one entry is never used, but has to be a valid one
     const cuuint64_t strides[3] = {c.n_heads > 1 ? c.head_stride : 16u, c.page.d > 1 ? c.token_stride : 16u,
                                    c.n_pages > 1 ? c.page_stride : 16u};
-    const cuuint32_t box[4] = {e ? DP : 64u, 1u, paged_box(c), 1u}, one[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t box[4] = {e ? DP : 64u, 1u, paged_box(c.page.d), 1u}, one[4] = {1u, 1u, 1u, 1u};
     return f(map, e ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t *>(pool), dims, strides,
              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, e ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1051,8 +1065,9 @@ static bool launch(AttendArgs a, const AttendWs &ws, cudaStream_t st) {
     CUtensorMap kmap = {}, vmap = {};
     // strides reach 2^41 bytes, a tensor map's less than 2^40
     a.box = a.c.page_stride < (uint64_t(1) << 40) && a.c.token_stride < (uint64_t(1) << 40) && a.c.head_stride < (uint64_t(1) << 40)
-                ? paged_box(a.c) : 0u;
+                ? paged_box(a.c.page.d) : 0u;
     if (a.box && !(pool_map(&kmap, a.c, a.c.k, DP) && pool_map(&vmap, a.c, a.c.v, DP))) a.box = 0u;    // row by row
+    a.span = a.box ? kTile / a.box * a.box : kTile;
     attend_large<DP, E><<<kCtasLarge, kTcThreads, bytes, st>>>(a, ws, kmap, vmap);
     return cudaGetLastError() == cudaSuccess && launch_join(a, ws, kTcRows, DP, kCtasLarge, st);
 }
