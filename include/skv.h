@@ -60,7 +60,7 @@ enum {
     SKV_ERR_EMPTY_MARGINAL = 5, /* w_marginal > 0 but the counts sum to 0                  */
     SKV_ERR_CAPACITY = 6,       /* the encoded stream does not fit out_capacity            */
     SKV_ERR_CORRUPT = 7,        /* bitstream or offsets inconsistent (decode)              */
-    SKV_ERR_TIMEOUT = 8         /* reserved: a bounded device wait ran out                 */
+    SKV_ERR_TIMEOUT = 8         /* a bounded wait inside a kernel ran out (a defect)       */
 };
 
 /*
@@ -592,7 +592,7 @@ int32_t skv_page_map(uint32_t page_tokens, uint32_t pool_pages, uint32_t n_reque
  *            the same for both (slices of a fused projection are fine)
  *  slots     device int64[n], distinct where >= 0; rows: device int32[n] or NULL
  * A bf16 cache gets the bits of the rows. An e4m3 cache gets the code nearest to
- * x / scale[head] (the real quotient, ties to even), saturated at +-448; NaN
+ * x / scale[head] (scale > 0; the real quotient, ties to even), saturated at +-448; NaN
  * gives NaN.
  * Device errors: INVALID_ARG for a slot beyond the pool (such rows are skipped)
  * or a row outside [0, n_src).
@@ -610,8 +610,8 @@ int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, u
  * mask[row][j / 64] is set (for a tree: j is i or an ancestor of i), or iff j
  * <= i when mask is NULL. Query head g reads KV head g / (n_q_heads / n_heads):
  *     out[row][g] = sum_p w_p V_p / sum_p w_p,  w_p = exp(scale * q . K_p)
- * over the positions that the row sees; a row with no position (or none with a
- * score above -infinity) gives 0. K or V of a position has no effect on rows
+ * over the positions that the row sees; a row with no position (or with all
+ * weights 0: every score -infinity) gives 0. K or V of a position has no effect on rows
  * that do not see it, whatever it holds.
  *  q          device bf16, head_dim contiguous, 16-byte aligned; q_row_stride and
  *             q_head_stride in elements, multiples of 8
@@ -632,7 +632,7 @@ int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, u
  * Device errors: INVALID_ARG (cu_new descends or passes n_rows, ctx_len < 0 with
  * rows, more positions than max_pages hold, n_r > 64 mask_words: such a
  * request's rows are left alone), CORRUPT (a page number outside the pool: that
- * request's outputs are unspecified).
+ * request's outputs are unspecified), TIMEOUT (outputs unspecified).
  */
 #define SKV_ATTENTION_ZERO_BYTES 2048u
 int32_t skv_tree_attention_workspace_bytes(const skv_paged *cache, uint32_t n_q_heads, uint64_t *bytes);
