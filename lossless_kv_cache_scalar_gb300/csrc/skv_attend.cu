@@ -254,26 +254,32 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
             look_up(i + 1);
         };
         look_up(0);
-#pragma unroll
-        for (uint32_t i = 0; i + 1 < S::stages; ++i) issue(i);
-
         QueryFrags<DP, E> qf;
-        load_queries<DP, E>(a, q, h, rt, qf);
         float o[DP / 8][4];
 #pragma unroll
         for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-        for (uint32_t i = 0; i < mine; ++i) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::stages - 2) : "memory");
-            __syncwarp();
+        // the first turns only fill the ring
+#pragma unroll 1
+        for (int32_t turn = 1 - (int32_t)S::stages; turn < (int32_t)mine; ++turn) {
+            if (turn >= 0) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::stages - 2) : "memory");
+                __syncwarp();
+            }
+            const uint32_t i = (uint32_t)turn;
             issue(i + S::stages - 1);
+            if (turn < 0) {
+                if (turn == -1) load_queries<DP, E>(a, q, h, rt, qf);
+                continue;
+            }
             const uint32_t st = ring + (i % S::stages) * S::stage, sv = st + S::half;
             const uint32_t p0 = p_begin + (warp + i * kWarps) * S::run;
             const bool edge = p0 + S::run > q.ctx || p0 + S::run > p_end;
             if (edge && p0 + S::run > q.ctx) {
                 // drafted positions: values that are not finite leave the product
                 bool found = false;
+#pragma unroll 1
                 for (uint32_t x = lane; x < S::run * S::chunks; x += 32u) {
                     const uint32_t row = x / S::chunks;
                     if (p0 + row < q.ctx) continue;
@@ -328,6 +334,15 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                 }
             }
             // scores in base 2; positions a row does not see are -infinity
+            uint32_t seen[2] = {0u, 0u};
+            if (edge) {
+#pragma unroll 1
+                for (uint32_t half = 0; half < 2; ++half) {
+                    const uint32_t bits = sees32(a, q, min((rt * 16u + g8 + 8u * half) / a.group, q.n - 1u), p0, p_end);
+                    if (half) seen[1] = bits;
+                    else seen[0] = bits;
+                }
+            }
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < 2 * (int)G; ++n) {
@@ -335,11 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                 for (int e = 0; e < 4; ++e) {
                     const int half = e >> 1;
                     float t = s[n][e] * qf.mul[half];
-                    if (edge) {
-                        const uint32_t p = p0 + 8u * n + 2u * c4 + (e & 1), row = rt * 16u + g8 + 8u * half;
-                        const uint32_t node = row / a.group;
-                        if (p >= p_end || (node < q.n && !sees(a, q, node, p))) t = -INFINITY;
-                    }
+                    if (edge && !((seen[half] >> (8u * n + 2u * c4 + (e & 1))) & 1u)) t = -INFINITY;
                     s[n][e] = t;
                     top[half] = fmaxf(top[half], t);
                 }
@@ -455,6 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
         float *part = ws.parts + ((uint64_t)blockIdx.x * 2u + place) * part_floats(16u, DP);
         const float vs = a.c.v_scale ? __ldg(a.c.v_scale + h) : 1.0f;
         // thread: 4 channels of every (512 / DP)th row
+#pragma unroll 1
         for (uint32_t x = tid; x < 16u * (DP / 4); x += kWarps * 32) {
             const uint32_t row = x / (DP / 4), d = (x % (DP / 4)) * 4u;
             const uint32_t all = rt * 16u + row, node = all / a.group, g = h * a.group + all - node * a.group;
@@ -475,8 +487,13 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                 v[0] += f[w] * y.x, v[1] += f[w] * y.y, v[2] += f[w] * y.z, v[3] += f[w] * y.w;
             }
             if (any_hurt && d < a.c.head_dim) {
+#pragma unroll 1
+                for (uint32_t j = 0; j < 4; ++j) {
+                    const float add = not_finite_sum(a, q, r, h, node, d + j, p_begin, p_end);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] += not_finite_sum(a, q, r, h, node, d + j, p_begin, p_end);
+                    for (uint32_t i = 0; i < 4; ++i)
+                        if (i == j) v[i] += add;
+                }
             }
             if (whole) {
                 const float inv = L == 0.0f ? 0.0f : vs / L;
@@ -510,7 +527,9 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
             if (sm_last) {
                 __threadfence();
                 const uint32_t first = quotient((uint64_t)c0 * sh.U, sh.active) == unit0 ? 0u : 1u;
-                for (uint32_t row = warp; row < 16u; row += kWarps) join_row<8>(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
+
+#pragma unroll 1
+                for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
             }
         }
         u += tile_end - tile;
@@ -558,7 +577,7 @@ __global__ void __launch_bounds__(256, 4) attend_join(AttendArgs a, AttendWs ws,
     const uint32_t last = cta_of(d.unit0 + d.units - 1, plan.total, plan.active);
     const uint32_t rows = min(R, q.n * a.group - d.rt * R);
     for (uint32_t row = blockIdx.y * 8u + warp; row < rows; row += kJoinBlocks * 8u)
-        join_row<4>(a, ws, q, d.head, d.rt, row, R, DP, c, d.place, last - c + 1u);
+        join_row(a, ws, q, d.head, d.rt, row, R, DP, c, d.place, last - c + 1u);
 }
 
 // Dynamic shared memory above 48 KB is asked for once per kernel and device.

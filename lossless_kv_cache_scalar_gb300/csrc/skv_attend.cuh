@@ -95,6 +95,28 @@ __device__ __forceinline__ bool sees(const AttendArgs &a, const ReqOf &q, uint32
     return (__ldg(a.mask + (uint64_t)(q.row0 + node) * a.mask_words + (j >> 6)) >> (j & 63u)) & 1u;
 }
 
+// Which of the 32 positions p0 .. p0 + 31 the row sees.
+__device__ __forceinline__ uint32_t sees32(const AttendArgs &a, const ReqOf &q, uint32_t node, uint32_t p0, uint32_t p_end) {
+    uint32_t bits = 0u;
+    if (p0 >= p_end) return 0u;
+    const uint32_t live = p_end - p0 >= 32u ? ~0u : (1u << (p_end - p0)) - 1u;
+    const int64_t j0 = (int64_t)p0 - q.ctx;                          // drafted index of bit 0
+    if (j0 < 0) bits = j0 <= -32 ? ~0u : (1u << (uint32_t)(-j0)) - 1u;
+    if (j0 > -32) {
+        if (!a.mask) {
+            const int64_t n = (int64_t)node - j0 + 1;                // j <= node
+            bits |= n >= 32 ? ~0u : n <= 0 ? 0u : (1u << (uint32_t)n) - 1u;
+        } else {
+            const uint64_t *m = a.mask + (uint64_t)(q.row0 + node) * a.mask_words;
+            const uint32_t first = j0 < 0 ? 0u : (uint32_t)j0, word = first >> 6, sh = first & 63u;
+            uint64_t x = word < a.mask_words ? __ldg(m + word) >> sh : 0ull;
+            if (sh > 32u && word + 1 < a.mask_words) x |= __ldg(m + word + 1) << (64u - sh);
+            bits |= j0 < 0 ? (uint32_t)x << (uint32_t)(-j0) : (uint32_t)x;
+        }
+    }
+    return bits & live;
+}
+
 // Byte offset of position p of request r, head h, in either pool; ~0 for a page
 // number outside the pool.
 __device__ __forceinline__ uint64_t place_of(const PagedView &c, uint32_t r, uint32_t h, uint32_t p) {
@@ -134,6 +156,7 @@ __device__ __forceinline__ float part_weight(float m, float M) { return m == -IN
 __device__ __forceinline__ float not_finite_sum(const AttendArgs &a, const ReqOf &q, uint32_t r, uint32_t h,
                                                 uint32_t node, uint32_t d, uint32_t p0, uint32_t p1) {
     float s = 0.0f;
+#pragma unroll 1
     for (uint32_t p = max(p0, q.ctx); p < p1; ++p) {
         if (!sees(a, q, node, p)) continue;
         const uint64_t at = place_of(a.c, r, h, p);
@@ -145,9 +168,21 @@ __device__ __forceinline__ float not_finite_sum(const AttendArgs &a, const ReqOf
     return s;
 }
 
-// n / d; a 64-bit division takes some hundred instructions, and most lists are short.
+// n / d. Most lists are short; for the others bit by bit, in a loop: what a short call costs most is
+// fetching instructions that it runs once, and a 64-bit division is a hundred of them.
 __device__ __forceinline__ uint64_t quotient(uint64_t n, uint64_t d) {
-    return (n | d) >> 32 ? n / d : (uint64_t)((uint32_t)n / (uint32_t)d);
+    if (!((n | d) >> 32)) return (uint32_t)n / (uint32_t)d;
+    uint64_t q = 0, r = 0;
+#pragma unroll 1
+    for (int i = 63; i >= 0; --i) {
+        r = (r << 1) | ((n >> i) & 1u);
+        q <<= 1;
+        if (r >= d) {
+            r -= d;
+            q |= 1u;
+        }
+    }
+    return q;
 }
 
 // Where CTA c's share of the list starts: the request, and the unit within it.
@@ -173,6 +208,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     constexpr uint32_t W = THREADS / 32u;
     unsigned long long mine = 0, first = 0;
     int32_t err = SKV_OK;
+#pragma unroll 1
     for (uint32_t r = tid; r < a.c.n_requests; r += THREADS) {
         const ReqOf q = request_of(a, r);
         if (q.err) err = q.err;
@@ -202,6 +238,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     s.u0 = quotient((uint64_t)blockIdx.x * U, active);
     s.u1 = quotient((uint64_t)(blockIdx.x + 1) * U, active);
     unsigned long long carry = 0;
+#pragma unroll 1
     for (uint32_t base = 0; base < a.c.n_requests; base += THREADS) {
         const uint32_t r = base + tid;
         unsigned long long u = base == 0 ? first : 0ull;
@@ -241,82 +278,64 @@ __device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t U, uint64_t acti
 }
 
 // One row of an item whose parts lie in CTAs c .. c + n - 1 (place of the first, then 0), by one warp: each
-// part weighs exp2(m - M) with M the largest m, in the order of the CTAs.
-template <uint32_t AHEAD>
+// part weighs exp2(m - M) with M the largest m, in the order of the CTAs. Four parts' outputs
+// are on their way while the four before them, or the weights, are worked on.
 __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws, const ReqOf &q, uint32_t head, uint32_t rt,
                                          uint32_t row, uint32_t R, uint32_t DP, uint32_t c, uint32_t place, uint32_t n) {
     const uint32_t lane = threadIdx.x & 31u, all = rt * R + row, node = all / a.group;
     if (node >= q.n) return;
     const uint32_t g = head * a.group + all - node * a.group;
-    const uint64_t size = part_floats(R, DP);
-    const float *first = ws.parts + ((uint64_t)c * 2u + place) * size, *next = ws.parts + (uint64_t)c * 2u * size;
-    const auto part = [&](uint32_t j) { return j ? next + (uint64_t)j * 2u * size : first; };
-    // lane j: part j's maximum and sum (a first 32 in registers, what is beyond read again)
-    float mj = -INFINITY, lj = 0.0f;
-    if (lane < n) {
-        mj = __ldcg(part(lane) + row);
-        lj = __ldcg(part(lane) + R + row);
-    }
-    // the first parts' outputs are on their way before the weights are known
-    float4 ahead[AHEAD];
-#pragma unroll
-    for (uint32_t j = 0; j < AHEAD; ++j) {
-        ahead[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < n && 4u * lane < DP) ahead[j] = __ldcg(reinterpret_cast<const float4 *>(part(j) + 2u * R + (uint64_t)row * DP + 4u * lane));
-    }
-    float M = mj, L = 0.0f;
-    for (uint32_t j = 32u + lane; j < n; j += 32u) M = fmaxf(M, __ldcg(part(j) + row));
-    for (uint32_t x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const auto add = [&](int k, float w, const float4 &y) {
-        o[4 * k] += w * y.x, o[4 * k + 1] += w * y.y, o[4 * k + 2] += w * y.z, o[4 * k + 3] += w * y.w;
-    };
-    for (uint32_t j0 = 0; j0 < n; j0 += 32u) {
-        float f = 0.0f;
-        if (j0 + lane < n) {
-            if (j0) {
-                mj = __ldcg(part(j0 + lane) + row);
-                lj = __ldcg(part(j0 + lane) + R + row);
-            }
-            f = part_weight(mj, M);
-            L += f * lj;
-        }
-        const uint32_t here = min(32u, n - j0);
-        uint32_t j = 0;
-        if (j0 == 0) {
-#pragma unroll
-            for (; j < AHEAD; ++j)
-                if (j < here) add(0, __shfl_sync(~0u, f, j), ahead[j]);      // here is the same for the warp
-        }
-#pragma unroll 4
-        for (; j < here; ++j) {
-            const float w = __shfl_sync(~0u, f, j);
-            if (4u * lane < DP) add(0, w, __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + (uint64_t)row * DP + 4u * lane)));
-        }
-        if (DP > 128u) {
-#pragma unroll 4
-            for (j = 0; j < here; ++j)
-                add(1, __shfl_sync(~0u, f, j), __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + (uint64_t)row * DP + 128u + 4u * lane)));
-        }
-    }
-    for (uint32_t x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-    const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + head) : 1.0f) / L;
+    const uint32_t size = (uint32_t)part_floats(R, DP);
+    const float *next = ws.parts + (uint64_t)c * 2u * size, *first = next + place * size;
+    const auto part = [&](uint32_t j) { return j ? next + (uint64_t)(2u * j) * size : first; };
     uint16_t *out = a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
+#pragma unroll 1
+    for (uint32_t x0 = 0; x0 < DP; x0 += 128u) {                     // 256 channels: two rounds; 64: half of the lanes
+        const uint32_t x = x0 + 4u * lane;
+        float4 y[4];
+        const auto fetch = [&](uint32_t j0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t x = 4u * lane + 128u * k;
-        if (x < a.c.head_dim) {
-            const bool none = L == 0.0f;
-            ushort4 y;
-            y.x = none ? 0 : bf16_bits(o[4 * k] * inv);
-            y.y = none ? 0 : bf16_bits(o[4 * k + 1] * inv);
-            y.z = none ? 0 : bf16_bits(o[4 * k + 2] * inv);
-            y.w = none ? 0 : bf16_bits(o[4 * k + 3] * inv);
-            *reinterpret_cast<ushort4 *>(out + x) = y;
+            for (uint32_t j = 0; j < 4; ++j)
+                y[j] = j0 + j < n && x < DP ? __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + row * DP + x)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        fetch(0);
+        float M = -INFINITY;
+#pragma unroll 1
+        for (uint32_t j = lane; j < n; j += 32u) M = fmaxf(M, __ldcg(part(j) + row));
+#pragma unroll
+        for (uint32_t d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.0f, f = 0.0f;
+#pragma unroll 1
+        for (uint32_t j0 = 0; j0 < n; j0 += 4u) {
+            if ((j0 & 31u) == 0) {                                   // lane j: the weight of part j0 + j
+                f = 0.0f;
+                if (j0 + lane < n) {
+                    f = part_weight(__ldcg(part(j0 + lane) + row), M);
+                    L += f * __ldcg(part(j0 + lane) + R + row);
+                }
+            }
+            const float4 z[4] = {y[0], y[1], y[2], y[3]};
+            if (j0 + 4u < n) fetch(j0 + 4u);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const float w = __shfl_sync(~0u, f, (j0 + j) & 31u);
+                o.x += w * z[j].x, o.y += w * z[j].y, o.z += w * z[j].z, o.w += w * z[j].w;
+            }
         }
+#pragma unroll
+        for (uint32_t d = 16; d; d >>= 1) L += __shfl_xor_sync(~0u, L, d);
+        const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + head) : 1.0f) / L;
+        if (x < a.c.head_dim) {
+            uint2 b;
+            b.x = (uint32_t)bf16_bits(o.x * inv) | (uint32_t)bf16_bits(o.y * inv) << 16;
+            b.y = (uint32_t)bf16_bits(o.z * inv) | (uint32_t)bf16_bits(o.w * inv) << 16;
+            if (L == 0.0f) b = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2 *>(out + x) = b;
+        }
+        if (a.lse && x == 0)
+            a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
-    if (a.lse && lane == 0)
-        a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // skv_attend.cu

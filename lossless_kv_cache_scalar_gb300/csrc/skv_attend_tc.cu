@@ -727,28 +727,6 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
     while (!bar_try(&sm.drain, 0u) && clock64() - t0 < 4000000000ll) {}
 }
 
-// Which of the 32 positions p0 .. p0 + 31 the row sees.
-__device__ __forceinline__ uint32_t sees32(const AttendArgs &a, const ReqOf &q, uint32_t node, uint32_t p0, uint32_t p_end) {
-    uint32_t bits = 0u;
-    if (p0 >= p_end) return 0u;
-    const uint32_t live = p_end - p0 >= 32u ? ~0u : (1u << (p_end - p0)) - 1u;
-    const int64_t j0 = (int64_t)p0 - q.ctx;                          // drafted index of bit 0
-    if (j0 < 0) bits = j0 <= -32 ? ~0u : (1u << (uint32_t)(-j0)) - 1u;
-    if (j0 > -32) {
-        if (!a.mask) {
-            const int64_t n = (int64_t)node - j0 + 1;                // j <= node
-            bits |= n >= 32 ? ~0u : n <= 0 ? 0u : (1u << (uint32_t)n) - 1u;
-        } else {
-            const uint64_t *m = a.mask + (uint64_t)(q.row0 + node) * a.mask_words;
-            const uint32_t first = j0 < 0 ? 0u : (uint32_t)j0, word = first >> 6, sh = first & 63u;
-            uint64_t x = word < a.mask_words ? __ldg(m + word) >> sh : 0ull;
-            if (sh > 32u && word + 1 < a.mask_words) x |= __ldg(m + word + 1) << (64u - sh);
-            bits |= j0 < 0 ? (uint32_t)x << (uint32_t)(-j0) : (uint32_t)x;
-        }
-    }
-    return bits & live;
-}
-
 template <int DP, bool E>
 __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs &ws, const Share &sh, TcShared &sm, uint32_t tmem) {
     const uint32_t s = threadIdx.x >> 7, t = threadIdx.x & 127u, lanes = (t & ~31u) << 16;
@@ -780,8 +758,13 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                 // a span below 128 positions (at least 112) ends inside the last 32 columns
                 uint32_t bits[4] = {~0u, ~0u, ~0u, cut ? (1u << (a.span - 96u)) - 1u : ~0u};
                 if (edge && live) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t seen = sees32(a, w.q, node, p0 + 32u * c, p_end);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) bits[c] &= sees32(a, w.q, node, p0 + 32u * c, p_end);
+                        for (int k = 0; k < 4; ++k)
+                            if (k == c) bits[k] &= seen;
+                    }
                 }
                 __syncwarp();
                 // the row's 128 scores, all in registers; -infinity where it does not see
@@ -816,7 +799,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     bar_wait(sm, &sm.o_done[s], (jobs - 1u) & 1u);
                     __syncwarp();
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < DP / 16; ++c) {              // 16 at a time: the scores stay in registers
                         uint32_t y[16];
                         tc_ld16(y, at_o + 16u * c);
@@ -880,7 +863,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                 const uint32_t place = w.u == sh.u0 ? 0u : 1u;
                 float *part = ws.parts + ((uint64_t)blockIdx.x * 2u + place) * part_floats(kTcRows, DP);
                 uint16_t *out = a.out + ((uint64_t)(w.q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
                     uint32_t x[32];
                     __syncwarp();
@@ -898,6 +881,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                         for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
                     }
                     if (hurt && live) {
+#pragma unroll 1
                         for (int i = 0; i < 32; ++i) {
                             if (32u * c + i >= a.c.head_dim) break;
                             const float add = not_finite_sum(a, w.q, w.r, w.h, node, 32u * c + i, w.tile * a.span, p_end);
