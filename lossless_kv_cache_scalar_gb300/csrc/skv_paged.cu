@@ -94,9 +94,10 @@ __device__ __forceinline__ void scan3(uint32_t (&x)[3], uint32_t (&total)[3], ui
     }
 }
 
-// THREADS: 1,024, or 256 for a step so small that barriers are most of its time. A
-// thread keeps ITEMS requests in a row, so that THREADS * ITEMS requests need one scan.
-template <uint32_t THREADS, uint32_t ITEMS>
+// A thread keeps ITEMS requests in a row, so that THREADS * ITEMS requests need one scan, and
+// maps TOK tokens in a row. A step of a few hundred requests and slots is bound by barriers and by
+// fetching instructions that run once: it takes 256 threads, one request and one token each.
+template <uint32_t THREADS, uint32_t ITEMS, uint32_t TOK>
 __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
     constexpr uint32_t CHUNK = THREADS * ITEMS;
     extern __shared__ uint32_t dyn[];
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
     };
 #pragma unroll
     for (uint32_t k = 0; k < ITEMS; ++k) add(mine[k]);
+#pragma unroll 1
     for (uint32_t r = CHUNK + tid; r < a.n_requests; r += THREADS) add(map_of(a, r));
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -154,11 +156,13 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
         const uint64_t e0 = min((b0 + 1) & ~uint64_t(1), b1), e1 = max(b1 & ~uint64_t(1), e0);
         const bool wide = ((uintptr_t)a.slots & 15u) == 0;
         if (wide) {
+#pragma unroll 1
             for (uint64_t i = e0 + 2 * tid; i < e1; i += 2 * THREADS)
                 *reinterpret_cast<longlong2 *>(a.slots + i) = make_longlong2(-1ll, -1ll);
             if (tid == 0 && b0 < e0) a.slots[b0] = -1;
             if (tid == 1 && e1 < b1) a.slots[e1] = -1;
         } else {
+#pragma unroll 1
             for (uint64_t i = b0 + tid; i < b1; i += THREADS) a.slots[i] = -1;
         }
     }
@@ -183,6 +187,7 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
     }
     bool corrupt = false;
     uint32_t carry[3] = {0u, 0u, 0u};
+#pragma unroll 1
     for (uint32_t base = 0; base < a.n_requests; base += CHUNK) {
         if (base) {
 #pragma unroll
@@ -214,6 +219,7 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
             }
             // Pages of ended requests, one warp per request, requests dealt over the CTAs.
             uint32_t ended = __ballot_sync(~0u, m.back != 0u && r % gridDim.x == blockIdx.x);
+#pragma unroll 1
             while (ended) {
                 const uint32_t l = __ffs(ended) - 1u;
                 ended &= ended - 1u;
@@ -236,21 +242,23 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
         // The slots of this chunk of requests that lie in this CTA's run.
         const uint64_t lo = max(i0, (uint64_t)s_cu[0]), hi = min(i1, (uint64_t)s_cu[CHUNK]);
         const uint32_t live = min(CHUNK, a.n_requests - base);
-        // Four tokens to a thread: their pages are all looked up before anything is stored. (Entries that
+        // TOK tokens to a thread: their pages are all looked up before anything is stored. (Entries that
         // are read, old ones of the table and the ring's front, are not written in this call.)
-        for (uint64_t i = (lo & ~uint64_t(3)) + 4 * tid; i < hi; i += 4 * THREADS) {
-            const uint32_t from = (uint32_t)max(i, lo), to = (uint32_t)min(i + 4, hi);
+        #pragma unroll 1
+        for (uint64_t i = (lo & ~uint64_t(TOK - 1)) + TOK * tid; i < hi; i += TOK * THREADS) {
+            const uint32_t from = (uint32_t)max(i, lo), to = (uint32_t)min(i + TOK, hi);
             uint32_t f = 0, n = live;                             // last request with cu <= from
+#pragma unroll 1
             while (n > 1) {
                 const uint32_t h = n >> 1;
                 if (s_cu[f + h] <= from) f += h;
                 n -= h;
             }
-            int64_t v[4];
-            int32_t page[4];
-            int32_t *entry[4];
+            int64_t v[TOK];
+            int32_t page[TOK];
+            int32_t *entry[TOK];
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
+            for (uint32_t k = 0; k < TOK; ++k) {
                 const uint32_t x = (uint32_t)i + k;
                 entry[k] = nullptr;
                 page[k] = 0;
@@ -262,25 +270,26 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
                 int32_t *row = a.table + (uint64_t)(base + f) * a.table_stride + j;
                 uint64_t e = (uint64_t)head + s_need[f] + (j - have);
                 if (e >= a.free_capacity) e -= a.free_capacity;
-                if (k > 0 && x > from && off != 0u && pos != (uint32_t)s_ctx[f]) page[k] = page[k - 1];   // the token before it is on the same page
+                if (k > 0 && x > from && off != 0u && pos != (uint32_t)s_ctx[f]) page[k] = page[k ? k - 1 : 0];   // the token before it is on the same page
                 else page[k] = __ldg(j < have ? row : a.free_pages + e);
                 if (j >= have && off == 0u) entry[k] = row;
                 v[k] = off;
             }
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
+            for (uint32_t k = 0; k < TOK; ++k) {
                 if (entry[k]) *entry[k] = page[k];
                 if (v[k] < 0) continue;
                 const bool ok = (uint32_t)page[k] < a.pool_pages;
                 corrupt |= !ok;
                 v[k] = ok ? (int64_t)page[k] * a.page.d + v[k] : -1ll;
             }
-            if (from == i && to == i + 4 && ((uintptr_t)a.slots & 15u) == 0) {
-                *reinterpret_cast<longlong2 *>(a.slots + i) = make_longlong2(v[0], v[1]);
-                *reinterpret_cast<longlong2 *>(a.slots + i + 2) = make_longlong2(v[2], v[3]);
+            if (TOK % 2 == 0 && from == i && to == i + TOK && ((uintptr_t)a.slots & 15u) == 0) {
+#pragma unroll
+                for (uint32_t k = 0; k + 1 < TOK; k += 2)
+                    *reinterpret_cast<longlong2 *>(a.slots + i + k) = make_longlong2(v[k], v[k + 1 < TOK ? k + 1 : k]);
             } else {
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k)
+                for (uint32_t k = 0; k < TOK; ++k)
                     if (i + k >= from && i + k < to) a.slots[i + k] = v[k];
             }
         }
@@ -290,14 +299,14 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
     if (corrupt) set_first(a.status, SKV_ERR_CORRUPT);
 }
 
-template <uint32_t THREADS, uint32_t ITEMS>
+template <uint32_t THREADS, uint32_t ITEMS, uint32_t TOK>
 static bool launch_map(const MapArgs &a, unsigned grid, cudaStream_t st) {
     constexpr uint32_t bytes = (4u * THREADS * ITEMS + 1u) * 4u;
     if (bytes > 48u * 1024u) {
         static std::atomic<uint64_t> ready{0};
-        if (!raise_smem(reinterpret_cast<const void *>(map_kernel<THREADS, ITEMS>), bytes, ready)) return false;
+        if (!raise_smem(reinterpret_cast<const void *>(map_kernel<THREADS, ITEMS, TOK>), bytes, ready)) return false;
     }
-    map_kernel<THREADS, ITEMS><<<grid, THREADS, bytes, st>>>(a);
+    map_kernel<THREADS, ITEMS, TOK><<<grid, THREADS, bytes, st>>>(a);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -342,9 +351,8 @@ __device__ __forceinline__ float reciprocal_of(float s) { return s > 1.0e-30f &&
 
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-// 16 bytes of codes from 16 channels of a bf16 row (two 16-byte loads).
-__device__ __forceinline__ uint4 quantise16(const uint16_t *src, float s, float r) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+// 16 bytes of codes from 16 channels of a bf16 row.
+__device__ __forceinline__ uint4 quantise16(const uint4 a, const uint4 b, float s, float r) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t o[4];
 #pragma unroll
@@ -388,17 +396,21 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
         const uint64_t t = (uint64_t)s - p * a.page.d;
         const uint64_t dst = p * a.page_stride + t * a.token_stride + h * a.head_stride + 16u * (uint64_t)u;
         const uint64_t src = (uint64_t)row * a.row_stride + h * a.row_head_stride + (E4M3 ? 16u : 8u) * (uint64_t)u;
-        uint4 kc, vc;
         if (E4M3) {
             const float ks = a.k_scale ? __ldg(a.k_scale + h) : 1.0f, vs = a.v_scale ? __ldg(a.v_scale + h) : 1.0f;
-            kc = quantise16(a.k_new + src, ks, reciprocal_of(ks));
-            vc = quantise16(a.v_new + src, vs, reciprocal_of(vs));
+            const uint4 k0 = __ldg(reinterpret_cast<const uint4 *>(a.k_new + src)), k1 = __ldg(reinterpret_cast<const uint4 *>(a.k_new + src) + 1);
+            const uint4 v0 = __ldg(reinterpret_cast<const uint4 *>(a.v_new + src)), v1 = __ldg(reinterpret_cast<const uint4 *>(a.v_new + src) + 1);
+            // one code for both pools: half the instructions to fetch
+#pragma unroll 1
+            for (uint32_t pool = 0; pool < 2; ++pool) {
+                const float scale = pool ? vs : ks;
+                *reinterpret_cast<uint4 *>((pool ? a.v : a.k) + dst) = quantise16(pool ? v0 : k0, pool ? v1 : k1, scale, reciprocal_of(scale));
+            }
         } else {
-            kc = __ldg(reinterpret_cast<const uint4 *>(a.k_new + src));
-            vc = __ldg(reinterpret_cast<const uint4 *>(a.v_new + src));
+            const uint4 kc = __ldg(reinterpret_cast<const uint4 *>(a.k_new + src)), vc = __ldg(reinterpret_cast<const uint4 *>(a.v_new + src));
+            *reinterpret_cast<uint4 *>(a.k + dst) = kc;
+            *reinterpret_cast<uint4 *>(a.v + dst) = vc;
         }
-        *reinterpret_cast<uint4 *>(a.k + dst) = kc;
-        *reinterpret_cast<uint4 *>(a.v + dst) = vc;
     }
     if (bad && !a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
 }
@@ -463,13 +475,13 @@ extern "C" int32_t skv_page_map(uint32_t page_tokens, uint32_t pool_pages, uint3
     MapArgs a{fast_div(page_tokens), pool_pages, n_requests, max_pages, free_capacity, ctx_len, new_len, n_pages_in,
               free_in, block_table, n_pages_out, free_pages, free_out, cu_new, table_stride, slots, slot_capacity,
               status};
-    // One CTA of 256 threads up to 1,024 requests and 2,048 slots, else a CTA of 1,024 per
+    // One CTA of 256 threads up to 256 requests and 2,048 slots, else a CTA of 1,024 per
     // 4,096 slots up to one per SM; several CTAs need the status cleared before them.
-    if (n_requests <= 1024u && slot_capacity <= 2048u) return launch_map<256, 4>(a, 1, st) ? SKV_OK : SKV_ERR_CUDA;
+    if (n_requests <= 256u && slot_capacity <= 2048u) return launch_map<256, 1, 1>(a, 1, st) ? SKV_OK : SKV_ERR_CUDA;
     uint64_t grid = (slot_capacity + 4u * kMapThreads - 1) / (4u * kMapThreads);
     grid = grid < 1 ? 1 : grid > sms ? sms : grid;
     if (grid > 1 && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    return launch_map<kMapThreads, 4>(a, (unsigned)grid, st) ? SKV_OK : SKV_ERR_CUDA;
+    return launch_map<kMapThreads, 4, 4>(a, (unsigned)grid, st) ? SKV_OK : SKV_ERR_CUDA;
 }
 
 extern "C" int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, uint64_t row_stride,
