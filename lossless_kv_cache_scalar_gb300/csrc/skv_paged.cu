@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
         // The slots of this chunk of requests that lie in this CTA's run.
         const uint64_t lo = max(i0, (uint64_t)s_cu[0]), hi = min(i1, (uint64_t)s_cu[CHUNK]);
         const uint32_t live = min(CHUNK, a.n_requests - base);
-        // TOK tokens to a thread: their pages are all looked up before anything is stored. (Entries that
-        // are read, old ones of the table and the ring's front, are not written in this call.)
+        // TOK tokens to a thread. (Entries that are read, old ones of the table and the ring's front, are
+        // not written in this call.)
         #pragma unroll 1
         for (uint64_t i = (lo & ~uint64_t(TOK - 1)) + TOK * tid; i < hi; i += TOK * THREADS) {
             const uint32_t from = (uint32_t)max(i, lo), to = (uint32_t)min(i + TOK, hi);
@@ -254,43 +254,48 @@ __global__ void __launch_bounds__(THREADS) map_kernel(MapArgs a) {
                 if (s_cu[f + h] <= from) f += h;
                 n -= h;
             }
-            int64_t v[TOK];
-            int32_t page[TOK];
-            int32_t *entry[TOK];
+            if (TOK == 4 && a.page.d >= 4u && i >= lo && s_cu[f + 1] >= (uint32_t)i + 4u && i + 4 <= hi &&
+                ((uintptr_t)a.slots & 31u) == 0) {
+                // four tokens of one request lie on at most two pages
+                const uint32_t pos = (uint32_t)s_ctx[f] + (from - s_cu[f]), have = (uint32_t)s_have[f];
+                const uint32_t j = div_by(pos, a.page), off = pos - j * a.page.d;
+                int32_t *row = a.table + (uint64_t)(base + f) * a.table_stride + j;
+                const bool over = off + 3u >= a.page.d;
+                int32_t p[2];
 #pragma unroll
-            for (uint32_t k = 0; k < TOK; ++k) {
-                const uint32_t x = (uint32_t)i + k;
-                entry[k] = nullptr;
-                page[k] = 0;
-                v[k] = -1;
-                if (x < from || x >= to) continue;
+                for (uint32_t k = 0; k < 2; ++k) {
+                    uint64_t e = (uint64_t)head + s_need[f] + (j + k - have);
+                    if (e >= a.free_capacity) e -= a.free_capacity;
+                    p[k] = k == 0 || over ? __ldg(j + k < have ? row + k : a.free_pages + e) : 0;
+                }
+                if (off == 0u && j >= have) row[0] = p[0];
+                if (over && j + 1u >= have) row[1] = p[1];
+                const bool ok0 = (uint32_t)p[0] < a.pool_pages, ok1 = (uint32_t)p[1] < a.pool_pages;
+                corrupt |= !ok0 || (over && !ok1);
+                const int64_t s0 = (int64_t)p[0] * a.page.d + off, s1 = (int64_t)p[1] * a.page.d + off - a.page.d;
+                int64_t v[4];
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const bool next = off + k >= a.page.d;
+                    v[k] = (next ? ok1 : ok0) ? (next ? s1 : s0) + k : -1ll;
+                }
+                // a whole 32-byte sector at a time
+                asm volatile("st.global.v4.b64 [%0], {%1,%2,%3,%4};" ::"l"(a.slots + i), "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]) : "memory");
+                continue;
+            }
+#pragma unroll 1
+            for (uint32_t x = from; x < to; ++x) {
                 while (s_cu[f + 1] <= x) ++f;                     // past requests without tokens
-                const uint32_t pos = (uint32_t)s_ctx[f] + (x - s_cu[f]);
-                const uint32_t j = div_by(pos, a.page), off = pos - j * a.page.d, have = (uint32_t)s_have[f];
+                const uint32_t pos = (uint32_t)s_ctx[f] + (x - s_cu[f]), have = (uint32_t)s_have[f];
+                const uint32_t j = div_by(pos, a.page), off = pos - j * a.page.d;
                 int32_t *row = a.table + (uint64_t)(base + f) * a.table_stride + j;
                 uint64_t e = (uint64_t)head + s_need[f] + (j - have);
                 if (e >= a.free_capacity) e -= a.free_capacity;
-                if (k > 0 && x > from && off != 0u && pos != (uint32_t)s_ctx[f]) page[k] = page[k ? k - 1 : 0];   // the token before it is on the same page
-                else page[k] = __ldg(j < have ? row : a.free_pages + e);
-                if (j >= have && off == 0u) entry[k] = row;
-                v[k] = off;
-            }
-#pragma unroll
-            for (uint32_t k = 0; k < TOK; ++k) {
-                if (entry[k]) *entry[k] = page[k];
-                if (v[k] < 0) continue;
-                const bool ok = (uint32_t)page[k] < a.pool_pages;
+                const int32_t p = __ldg(j < have ? row : a.free_pages + e);
+                if (j >= have && off == 0u) *row = p;
+                const bool ok = (uint32_t)p < a.pool_pages;
                 corrupt |= !ok;
-                v[k] = ok ? (int64_t)page[k] * a.page.d + v[k] : -1ll;
-            }
-            if (TOK % 2 == 0 && from == i && to == i + TOK && ((uintptr_t)a.slots & 15u) == 0) {
-#pragma unroll
-                for (uint32_t k = 0; k + 1 < TOK; k += 2)
-                    *reinterpret_cast<longlong2 *>(a.slots + i + k) = make_longlong2(v[k], v[k + 1 < TOK ? k + 1 : k]);
-            } else {
-#pragma unroll
-                for (uint32_t k = 0; k < TOK; ++k)
-                    if (i + k >= from && i + k < to) a.slots[i + k] = v[k];
+                a.slots[x] = ok ? (int64_t)p * a.page.d + off : -1ll;
             }
         }
 #pragma unroll
