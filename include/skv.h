@@ -615,7 +615,8 @@ int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, u
  * that do not see it, whatever it holds.
  *  q          device bf16, head_dim contiguous, 16-byte aligned; q_row_stride and
  *             q_head_stride in elements, multiples of 8
- *  n_rows     rows of q and out; rows outside every request are left alone
+ *  n_rows     rows of q and out, n_rows * n_q_heads / n_heads at most 2^31 - 1; rows outside
+ *             every request are left alone
  *  ctx_len    device int32[n_requests]; < 0 with no rows: an idle request
  *  cu_new     device int32[n_requests + 1]
  *  mask       device uint64 [n_rows][mask_words], 8-byte aligned, or NULL (mask_words 0)

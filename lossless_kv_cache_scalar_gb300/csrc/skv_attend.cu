@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
         }
         __syncthreads();
         const bool whole = tile == 0 && tile_end == tiles;
-        const uint32_t place = u == sh.u0 ? 0u : 1u;
+        const uint32_t place = tile ? 0u : 1u;
         float *part = ws.parts + ((uint64_t)blockIdx.x * 2u + place) * part_floats(16u, DP);
         const float vs = a.c.v_scale ? __ldg(a.c.v_scale + h) : 1.0f;
         // thread: 4 channels of every (512 / DP)th row
@@ -526,10 +526,9 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
             __syncthreads();
             if (sm_last) {
                 __threadfence();
-                const uint32_t first = quotient((uint64_t)c0 * sh.U, sh.active) == unit0 ? 0u : 1u;
 
 #pragma unroll 1
-                for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, first, n);
+                for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, n);
             }
         }
         u += tile_end - tile;
@@ -574,10 +573,10 @@ __global__ void __launch_bounds__(256, 4) attend_join(AttendArgs a, AttendWs ws,
     const Plan plan = *ws.plan;
     if (!d.valid) return;
     const ReqOf q = request_of(a, d.request);
-    const uint32_t last = cta_of(d.unit0 + d.units - 1, plan.total, plan.active);
+    const uint32_t last = cta_of(d.last, plan.total, plan.active);
     const uint32_t rows = min(R, q.n * a.group - d.rt * R);
     for (uint32_t row = blockIdx.y * 8u + warp; row < rows; row += kJoinBlocks * 8u)
-        join_row(a, ws, q, d.head, d.rt, row, R, DP, c, d.place, last - c + 1u);
+        join_row(a, ws, q, d.head, d.rt, row, R, DP, c, last - c + 1u);
 }
 
 // Dynamic shared memory above 48 KB is asked for once per kernel and device.
@@ -638,7 +637,8 @@ extern "C" int32_t skv_tree_attention(const skv_paged *cache, const void *q, uin
     if (r != SKV_OK) return r;
     const auto off = [](const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) != 0; };
     if (!status || off(status, 4) || !workspace || off(workspace, 256) || ws_bytes < need) return SKV_ERR_INVALID_ARG;
-    if (cache->n_requests > 0x7FFFFFFEu || n_rows > 0x7FFFFFFFu || n_q_heads > 65535u || cache->max_pages > 0x7FFFFFFFu ||
+    if (cache->n_requests > 0x7FFFFFFEu || n_q_heads > 65535u ||
+        (uint64_t)n_rows * (n_q_heads / cache->n_heads) > 0x7FFFFFFFu || cache->max_pages > 0x7FFFFFFFu ||
         (cache->n_requests > 1 && cache->table_stride < cache->max_pages) || !(scale == scale) ||
         (mask != nullptr) != (mask_words != 0) || mask_words > (1u << 20))
         return SKV_ERR_INVALID_ARG;

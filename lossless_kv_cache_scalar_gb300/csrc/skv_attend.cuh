@@ -11,8 +11,13 @@
 // leaves maximum, sum and unnormalised output in the workspace. The small-row
 // kernel's CTA that comes last to an item joins its parts (counters in the
 // workspace, 0 between calls); the large-row kernel's parts are joined by a second
-// kernel, whose rows are spread over the GPU. A part that starts at the CTA's first unit goes to place 0 of the
-// CTA, any other (it then ends at the CTA's last unit) to place 1.
+// kernel, whose rows are spread over the GPU. A part that goes on from an earlier CTA goes to
+// place 0 of its CTA, one that starts its item (and is cut off by the share's end) to place 1.
+//
+// In the large-row kernel a run of positions counts kWide units with more than 128 rows and
+// kNarrow with up to 128: half of the products, the same bytes (256 against 128 rows took 1.28
+// to 1.42 times as long, in bf16 and e4m3, with 64 and 128 channels). A run belongs to the CTA
+// in whose share its first unit lies.
 #pragma once
 
 #include <atomic>
@@ -24,12 +29,12 @@ namespace skv {
 // Grids: persistent CTAs, three per SM of 152 for the small-row kernel, one for
 // the tcgen05 one. Constants, so that the workspace's size depends on no device.
 constexpr uint32_t kCtasSmall = 456, kCtasLarge = 152;
+constexpr uint32_t kWide = 4, kNarrow = 3;
 
 // An item that starts in a CTA and goes on in the next ones.
 struct Desc {
     uint32_t valid, request, head, rt;
-    uint32_t place, units;
-    uint64_t unit0;
+    uint64_t first, last;                // units at which its first and its last run begin
 };
 
 struct Plan {
@@ -194,14 +199,18 @@ struct Share {
 };
 
 // Units of request r, split into row tiles of R rows and runs of UT positions.
+template <bool LARGE>
 __device__ __forceinline__ uint64_t units_of(const AttendArgs &a, const ReqOf &q, uint32_t R, uint32_t UT) {
     if (q.n == 0) return 0;
-    return (uint64_t)((q.len + UT - 1) / UT) * a.c.n_heads * (((uint64_t)q.n * a.group + R - 1) / R);
+    const uint32_t rows = q.n * a.group, rts = (rows + R - 1) / R;
+    const uint32_t per_run = LARGE ? rts * kWide - (rows - (rts - 1) * R > 128u ? 0u : kWide - kNarrow) : rts;
+    return (uint64_t)((q.len + UT - 1) / UT) * ((uint64_t)a.c.n_heads * per_run);
 }
 
 // Every thread of the block calls this; sm is scratch of blockDim / 32 + 4 words of 8 bytes.
-// JOINED: the kernel with a joining kernel behind it leaves plan, error and descriptor for it.
-template <uint32_t THREADS, bool JOINED>
+// LARGE: the kernel with weighted runs and a joining kernel behind it, for which it leaves plan, error and
+// descriptor.
+template <uint32_t THREADS, bool LARGE>
 __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &ws, uint32_t R, uint32_t UT,
                                           unsigned long long *sm) {
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -212,7 +221,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     for (uint32_t r = tid; r < a.c.n_requests; r += THREADS) {
         const ReqOf q = request_of(a, r);
         if (q.err) err = q.err;
-        const uint64_t u = units_of(a, q, R, UT);
+        const uint64_t u = units_of<LARGE>(a, q, R, UT);
         if (r == tid) first = u;
         mine += u;
     }
@@ -224,14 +233,15 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     unsigned long long U = 0;
 #pragma unroll
     for (uint32_t w = 0; w < W; ++w) U += sm[w];
-    const uint64_t active = U < gridDim.x ? U : gridDim.x;
+    // every share is at least a run
+    const uint64_t runs = LARGE ? (U > kWide ? U / kWide : U != 0) : U, active = runs < gridDim.x ? runs : gridDim.x;
     Share s{U, active, 0, 0, 0, 0};
-    if (JOINED && tid == 0) {
+    if (LARGE && tid == 0) {
         ws.errs[blockIdx.x] = err;
         ws.desc[blockIdx.x].valid = 0u;
         if (blockIdx.x == 0) *ws.plan = Plan{U, active};
     }
-    if (!JOINED && tid == 0 && blockIdx.x == 0 && err) {
+    if (!LARGE && tid == 0 && blockIdx.x == 0 && err) {
         atomicOr(ws.finished, kSawInvalid);
     }
     if (blockIdx.x >= active) return s;
@@ -242,7 +252,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     for (uint32_t base = 0; base < a.c.n_requests; base += THREADS) {
         const uint32_t r = base + tid;
         unsigned long long u = base == 0 ? first : 0ull;
-        if (base && r < a.c.n_requests) u = units_of(a, request_of(a, r), R, UT);
+        if (base && r < a.c.n_requests) u = units_of<LARGE>(a, request_of(a, r), R, UT);
         unsigned long long x = u;
 #pragma unroll
         for (uint32_t d = 1; d < 32; d <<= 1) {
@@ -277,16 +287,16 @@ __device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t U, uint64_t acti
     return (uint32_t)quotient((u + 1) * active - 1, U);
 }
 
-// One row of an item whose parts lie in CTAs c .. c + n - 1 (place of the first, then 0), by one warp: each
+// One row of an item whose parts lie in CTAs c .. c + n - 1 (place 1 of the first, then 0), by one warp: each
 // part weighs exp2(m - M) with M the largest m, in the order of the CTAs. Four parts' outputs
 // are on their way while the four before them, or the weights, are worked on.
 __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws, const ReqOf &q, uint32_t head, uint32_t rt,
-                                         uint32_t row, uint32_t R, uint32_t DP, uint32_t c, uint32_t place, uint32_t n) {
+                                         uint32_t row, uint32_t R, uint32_t DP, uint32_t c, uint32_t n) {
     const uint32_t lane = threadIdx.x & 31u, all = rt * R + row, node = all / a.group;
     if (node >= q.n) return;
     const uint32_t g = head * a.group + all - node * a.group;
     const uint32_t size = (uint32_t)part_floats(R, DP);
-    const float *next = ws.parts + (uint64_t)c * 2u * size, *first = next + place * size;
+    const float *next = ws.parts + (uint64_t)c * 2u * size, *first = next + size;
     const auto part = [&](uint32_t j) { return j ? next + (uint64_t)(2u * j) * size : first; };
     uint16_t *out = a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
 #pragma unroll 1

@@ -52,50 +52,67 @@ struct TcShape {
 
 // The parts of a CTA's share, in order; every role walks them for itself.
 struct Walk {
-    uint64_t u, u1, item;
-    uint32_t r, tiles, rts, tile;
+    uint64_t at, u1;                                // units: the item's start, the share's end
+    uint32_t r, tiles, rts, h, rt;
     ReqOf q;
     uint32_t n;                                     // parts so far
-    // the part
-    uint32_t h, rt, tile_end, rows;                 // rows: of this row tile
+    // the part: tiles [tile, tile_end) of the item
+    uint32_t tile, tile_end, rows, weight;          // rows of this row tile, units of a tile
 
     __device__ __forceinline__ void request(const AttendArgs &a) {
         tiles = (q.len + a.span - 1) / a.span;
         rts = (q.n * a.group + kTcRows - 1) / kTcRows;
+        h = rt = 0;
     }
-    __device__ __forceinline__ void part(const AttendArgs &a) {
-        h = (uint32_t)quotient(item, rts);
-        rt = (uint32_t)(item - (uint64_t)h * rts);
-        tile_end = (uint32_t)min((uint64_t)tiles, tile + (u1 - u));
+    __device__ __forceinline__ void item(const AttendArgs &a) {
         rows = min(kTcRows, q.n * a.group - rt * kTcRows);
+        weight = both() ? kWide : kNarrow;
+    }
+    // The tiles that start before the share's end.
+    __device__ __forceinline__ void part() {
+        const uint64_t left = u1 > at ? u1 - at : 0u;
+        tile_end = left >= (uint64_t)tiles * weight ? tiles : ((uint32_t)left + weight - 1) / weight;
+    }
+    __device__ __forceinline__ void advance(const AttendArgs &a) {
+        at += (uint64_t)tiles * weight;
+        tile = tile_end = 0;
+        if (at >= u1) return;
+        if (++rt == rts) {
+            rt = 0;
+            if (++h == a.c.n_heads) {
+                do q = request_of(a, ++r);
+                while (q.n == 0);
+                request(a);
+            }
+        }
+        item(a);
+        part();
     }
     __device__ __forceinline__ void start(const AttendArgs &a, const Share &s) {
-        u = s.u0;
         u1 = s.u1;
         r = s.r;
         n = 0;
         q = request_of(a, r);
         request(a);
-        item = quotient(s.off, tiles);
-        tile = (uint32_t)(s.off - item * tiles);
-        part(a);
+        const uint32_t last = q.n * a.group - (rts - 1) * kTcRows > kTile ? kWide : kNarrow;
+        const uint64_t wide = (uint64_t)tiles * kWide, head = (rts - 1) * wide + (uint64_t)tiles * last;
+        h = (uint32_t)quotient(s.off, head);
+        uint64_t off = s.off - h * head;
+        rt = min((uint32_t)quotient(off, wide), rts - 1);
+        off -= rt * wide;
+        at = s.u0 - off;
+        item(a);
+        tile = (uint32_t)quotient(off + weight - 1, weight);
+        part();
+        if (tile >= tiles) advance(a);
     }
-    __device__ __forceinline__ bool more() const { return u < u1; }
+    __device__ __forceinline__ bool more() const { return tile < tile_end; }
     __device__ __forceinline__ bool both() const { return rows > kTile; }          // 129 rows on: every tile in both streams
     __device__ __forceinline__ uint32_t count() const { return tile_end - tile; }
     __device__ __forceinline__ void next(const AttendArgs &a) {
-        u += tile_end - tile;
-        tile = 0;
-        ++item;
         ++n;
-        if (u >= u1) return;
-        if (item == (uint64_t)a.c.n_heads * rts) {
-            do q = request_of(a, ++r);
-            while (q.n == 0);
-            request(a);
-            item = 0;
-        }
-        part(a);
+        if (tile_end < tiles) tile = tile_end;      // the share ends in this item
+        else advance(a);
     }
 };
 
@@ -860,7 +877,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                 const float norm = !whole ? 1.0f : l == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + w.h) : 1.0f) / l;
                 f0 *= norm;
                 f1 *= norm;
-                const uint32_t place = w.u == sh.u0 ? 0u : 1u;
+                const uint32_t place = w.tile ? 0u : 1u;
                 float *part = ws.parts + ((uint64_t)blockIdx.x * 2u + place) * part_floats(kTcRows, DP);
                 uint16_t *out = a.out + ((uint64_t)(w.q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
 #pragma unroll 1
@@ -919,7 +936,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     part[kTcRows + row] = l;
                 }
                 if (threadIdx.x == 0 && w.tile == 0 && !whole)
-                    ws.desc[blockIdx.x] = Desc{1u, w.r, w.h, w.rt, place, w.tiles, w.u};
+                    ws.desc[blockIdx.x] = Desc{1u, w.r, w.h, w.rt, w.at, w.at + (uint64_t)(w.tiles - 1) * w.weight};
             }
             tc_fence_before();
         }
