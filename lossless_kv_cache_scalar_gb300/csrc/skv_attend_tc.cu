@@ -1052,9 +1052,13 @@ static bool pool_map(CUtensorMap *map, const PagedView &c, const uint8_t *pool, 
     const cuuint64_t strides[3] = {c.n_heads > 1 ? c.head_stride : 16u, c.page.d > 1 ? c.token_stride : 16u,
                                    c.n_pages > 1 ? c.page_stride : 16u};
     const cuuint32_t box[4] = {e ? DP : 64u, 1u, paged_box(c.page.d), 1u}, one[4] = {1u, 1u, 1u, 1u};
+    // L2 fetches no more than a row: what lies behind it is another head's, wanted much later
+    const uint32_t row = c.head_dim * (e ? 1u : 2u);
+    const CUtensorMapL2promotion fetch = row >= 256u ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                       : row >= 128u ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     return f(map, e ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t *>(pool), dims, strides,
              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, e ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP, bool E>
