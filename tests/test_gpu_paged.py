@@ -608,3 +608,40 @@ def test_over_decoded_pages(dtype):
     o, tol, _, _ = P.attention(q, whole[0].view(codes), whole[1].view(codes), scale, scale, i32([[0]]), ctx, cu, mask,
                                1.0 / math.sqrt(dim), **eps)
     assert ((out.cpu().double() - o).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("bf16", 48), ("e4m3", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("page", [1, 8, 12, 40, 48, 72, 104, 120, 136, 256])
+def test_attend_page_lengths(page, dtype, dim):
+    """Tiles of whole pages, of parts of pages, and of rows one by one, over several tiles and
+    with rows past the pages' ends that hold NaN."""
+    s = attend_case(59 + page, [333, 130, 7], [9, 33, 40], page, 2, 4, dim, dtype, garbage=math.nan)
+    check_attend(s, max_nodes=40)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hint", [1, 1000])
+def test_attend_many_requests(hint, dtype):
+    """More requests than a CTA has threads, some idle, and far more than there are shares."""
+    rng = random.Random(61)
+    ctx = [rng.choice([0, 1, 5, 30, 140]) for _ in range(1300)]
+    new = [rng.choice([0, 1, 1, 2]) for _ in range(1300)]
+    ctx = [-1 if n == 0 and c == 5 else c for c, n in zip(ctx, new)]
+    s = attend_case(61, ctx, new, 16, 1, 1, 64, dtype)
+    check_attend(s, max_nodes=hint)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ctx,new", [([0], [1]), ([0, 0, 0], [1, 0, 2]), ([127], [1]), ([128], [1])])
+def test_attend_least_work(ctx, new, dtype):
+    """One or two tiles in all, through the kernel for many rows."""
+    s = attend_case(67, ctx, new, 16, 1, 2, 128, dtype)
+    check_attend(s, max_nodes=1000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attend_wide_and_narrow_row_tiles(dtype):
+    """Row tiles of 256, 129, 128 and 1 rows in one call, cut by the shares' ends."""
+    s = attend_case(71, [3000, 2500, 1400, 700], [96, 43, 32, 65], 64, 1, 4, 64, dtype)
+    check_attend(s, max_nodes=96)
+

@@ -78,7 +78,8 @@ def attend_args(**kw):
 
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(q=A + 8), dict(q_row_stride=4097), dict(q_head_stride=4), dict(n_q_heads=0), dict(n_q_heads=33),
-    dict(n_q_heads=65536), dict(n_rows=1 << 31), dict(ctx_len=None), dict(cu_new=None), dict(cu_new=A + 2), dict(mask=None), dict(mask_words=0), dict(mask=A + 4),
+    dict(n_q_heads=65536), dict(n_rows=1 << 31),
+    dict(n_rows=1 << 29), dict(ctx_len=None), dict(cu_new=None), dict(cu_new=A + 2), dict(mask=None), dict(mask_words=0), dict(mask=A + 4),
     dict(scale=float("nan")), dict(out=None), dict(out=A + 8), dict(lse=A + 2), dict(status=None), dict(workspace=None),
     dict(workspace=A + 128), dict(ws_bytes=0)])
 def test_bad_attention_arguments(kw):
