@@ -88,11 +88,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// Two e4m3 codes (low 16 bits) as fp16.
-__device__ __forceinline__ uint32_t raise2(uint32_t codes) {
-    uint32_t r;
-    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(codes));
-    return r;
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void raise4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
@@ -329,7 +328,11 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                         const uint4 w4 = lds128(st + row * S::row + swz_k<DP, E>(row, 4u * b + c4) * 16u);
                         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma16<E>(s[n], qf.f[4 * b + j], raise2(w[j]), raise2(w[j] >> 16));
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t lo, hi;
+                            raise4(w[j], lo, hi);
+                            mma16<E>(s[n], qf.f[4 * b + j], lo, hi);
+                        }
                     }
                 }
             }
@@ -425,10 +428,13 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                             const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), lo1 = __byte_perm(w[0][j], w[1][j], 0x7362);
                             const uint32_t hi0 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
                             const int i = (part + j) * 4;
-                            mma16<E>(o[i], pa[y], raise2(lo0), raise2(hi0));
-                            mma16<E>(o[i + 1], pa[y], raise2(lo0 >> 16), raise2(hi0 >> 16));
-                            mma16<E>(o[i + 2], pa[y], raise2(lo1), raise2(hi1));
-                            mma16<E>(o[i + 3], pa[y], raise2(lo1 >> 16), raise2(hi1 >> 16));
+                            uint32_t b[4][2];
+                            raise4(lo0, b[0][0], b[1][0]);
+                            raise4(hi0, b[0][1], b[1][1]);
+                            raise4(lo1, b[2][0], b[3][0]);
+                            raise4(hi1, b[2][1], b[3][1]);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) mma16<E>(o[i + x], pa[y], b[x][0], b[x][1]);
                         }
                     }
                 }

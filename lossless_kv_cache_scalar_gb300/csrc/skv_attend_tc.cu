@@ -275,9 +275,11 @@ __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t tc_raise2(uint32_t codes) {
-    uint32_t r;
-    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(codes));
+// Eight e4m3 codes as fp16.
+__device__ __forceinline__ uint4 tc_raise8(uint32_t a, uint32_t b) {
+    uint4 r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(r.z), "=r"(r.w) : "r"(b));
     return r;
 }
 
@@ -498,9 +500,9 @@ __device__ __forceinline__ void fill_role(const AttendArgs &a, const Share &sh, 
                     const uint32_t at = ring_at + slot * S::tile + (ch >> 2) * S::block + row * 128u;
                     const uint32_t c0 = 2u * ch;
                     st_shared16(at + (((c0 ^ row) & 7u) << 4),
-                                make_uint4(tc_raise2(c[0]), tc_raise2(c[0] >> 16), tc_raise2(c[1]), tc_raise2(c[1] >> 16)));
+                                tc_raise8(c[0], c[1]));
                     st_shared16(at + ((((c0 + 1u) ^ row) & 7u) << 4),
-                                make_uint4(tc_raise2(c[2]), tc_raise2(c[2] >> 16), tc_raise2(c[3]), tc_raise2(c[3] >> 16)));
+                                tc_raise8(c[2], c[3]));
                 }
                 if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
                 proxy_fence();
@@ -657,8 +659,8 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
                 }
 #pragma unroll
                 for (uint32_t i = 0; i < PER; ++i) {
-                    st_shared16(to0 + i * STEP * 128u, make_uint4(tc_raise2(c[i][0].x), tc_raise2(c[i][0].x >> 16), tc_raise2(c[i][0].y), tc_raise2(c[i][0].y >> 16)));
-                    st_shared16(to1 + i * STEP * 128u, make_uint4(tc_raise2(c[i][1].x), tc_raise2(c[i][1].x >> 16), tc_raise2(c[i][1].y), tc_raise2(c[i][1].y >> 16)));
+                    st_shared16(to0 + i * STEP * 128u, tc_raise8(c[i][0].x, c[i][0].y));
+                    st_shared16(to1 + i * STEP * 128u, tc_raise8(c[i][1].x, c[i][1].y));
                 }
             }
             if (found) *reinterpret_cast<volatile uint32_t *>(&sm.hurt[w.n & 3u]) = 1u;
