@@ -125,14 +125,16 @@ __device__ __forceinline__ uint32_t swz_v(uint32_t row, uint32_t chunk) {
 template <int DP, bool E>
 struct QueryFrags {
     uint32_t f[DP / 16][4];
-    float mul[2];          // score of the product -> score in base 2
+    float mul[2];          // product -> score in base 2; at least 2^-100, so that -infinity times it stays that
 };
 
 template <int DP, bool E>
 __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q, uint32_t h, uint32_t rt,
                                              QueryFrags<DP, E> &x) {
     const uint32_t lane = threadIdx.x & 31u, c = lane & 3u;
-    const float mul = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + h) : 1.0f) * 1.4426950408889634f;
+    // a negative scale turns the queries, so that the largest product is the largest score
+    const float scale = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + h) : 1.0f) * 1.4426950408889634f, mul = fabsf(scale);
+    const bool turned = scale < 0.0f;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const uint32_t r = rt * 16u + (lane >> 2) + 8u * half, node = r / a.group, g = r - node * a.group;
@@ -145,10 +147,10 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const uint32_t d = 16u * k + 8u * s + 2u * c;
-                    x.f[k][half + 2 * s] = live && d < a.c.head_dim ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u;
+                    x.f[k][half + 2 * s] = (live && d < a.c.head_dim ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u) ^ (turned ? 0x80008000u : 0u);
                 }
             }
-            x.mul[half] = mul;
+            x.mul[half] = fmaxf(mul, 0x1p-100f);
         } else {
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b) {
@@ -168,8 +170,8 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
             // 2^-e with e the exponent of the largest magnitude; 1 for 0, tiny and infinite rows
             const uint32_t e = __float_as_uint(top) >> 23;
             const bool usual = e > 2u && e < 252u;
-            const float down = usual ? __uint_as_float((254u - e) << 23) : 1.0f;
-            x.mul[half] = usual ? mul * __uint_as_float(e << 23) : mul;
+            const float down = (usual ? __uint_as_float((254u - e) << 23) : 1.0f) * (turned ? -1.0f : 1.0f);
+            x.mul[half] = fmaxf(usual ? mul * __uint_as_float(e << 23) : mul, 0x1p-100f);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
 #pragma unroll
@@ -336,43 +338,43 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                     }
                 }
             }
-            // scores in base 2; positions a row does not see are -infinity
-            uint32_t seen[2] = {0u, 0u};
+            // positions a row does not see: -infinity
             if (edge) {
+                uint32_t seen[2] = {0u, 0u};
 #pragma unroll 1
                 for (uint32_t half = 0; half < 2; ++half) {
                     const uint32_t bits = sees32(a, q, min((rt * 16u + g8 + 8u * half) / a.group, q.n - 1u), p0, p_end);
                     if (half) seen[1] = bits;
                     else seen[0] = bits;
                 }
-            }
-            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < 2 * (int)G; ++n) {
+                for (int n = 0; n < 2 * (int)G; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int half = e >> 1;
-                    float t = s[n][e] * qf.mul[half];
-                    if (edge && !((seen[half] >> (8u * n + 2u * c4 + (e & 1))) & 1u)) t = -INFINITY;
-                    s[n][e] = t;
-                    top[half] = fmaxf(top[half], t);
-                }
+                    for (int e = 0; e < 4; ++e)
+                        if (!((seen[e >> 1] >> (8u * n + 2u * c4 + (e & 1))) & 1u)) s[n][e] = -INFINITY;
             }
-            bool grew = false;
-            float keep[2], base[2];
+            float top[2] = {-INFINITY, -INFINITY}, base[2];
+#pragma unroll
+            for (int n = 0; n < 2 * (int)G; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+            // the reference of a row's weights moves only for a weight of 2^8 or more against it (sums are
+            // binary32 and the quotient does not depend on it), so the output is rarely scaled anew
+            bool move[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 1));
-                top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 2));
-                const float now = fmaxf(m[half], top[half]);
-                grew |= now > m[half];
-                keep[half] = part_weight(m[half], now);
-                m[half] = now;
-                base[half] = now == -INFINITY ? 0.0f : now;
+                top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 2)) * qf.mul[half];
+                move[half] = top[half] > m[half] + 8.0f || (m[half] == -INFINITY && top[half] > m[half]);
             }
-            if (__any_sync(~0u, grew)) {
+            if (__any_sync(~0u, move[0] || move[1])) {
+                float keep[2];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) l[half] *= keep[half];
+                for (int half = 0; half < 2; ++half) {
+                    keep[half] = move[half] ? part_weight(m[half], top[half]) : 1.0f;
+                    if (move[half]) m[half] = top[half];
+                    l[half] *= keep[half];
+                }
 #pragma unroll
                 for (int j = 0; j < DP / 8; ++j) {
                     o[j][0] *= keep[0];
@@ -381,12 +383,14 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
                     o[j][3] *= keep[1];
                 }
             }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) base[half] = m[half] == -INFINITY ? 0.0f : -m[half];
             uint32_t pa[G][4];
 #pragma unroll
             for (int n = 0; n < 2 * (int)G; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[n][e] = ex2(s[n][e] - base[e >> 1]);
+                    s[n][e] = ex2(fmaf(s[n][e], qf.mul[e >> 1], base[e >> 1]));
                     l[e >> 1] += s[n][e];
                 }
                 pa[n >> 1][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
