@@ -185,11 +185,11 @@ __device__ __forceinline__ bool elected() {
     return ok != 0;
 }
 
-// Shared-memory operand: 128-byte swizzle, 8-row groups 1024 bytes apart (bits 32-45);
+// Shared-memory operand: 128-byte swizzle, 8-row groups `group` bytes apart (bits 32-45);
 // lead: distance of 64-channel blocks where the contiguous dimension is not the
 // product's (bits 16-29).
-__device__ __forceinline__ uint64_t tc_operand(uint32_t at, uint32_t lead) {
-    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+__device__ __forceinline__ uint64_t tc_operand(uint32_t at, uint32_t lead, uint32_t group) {
+    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
@@ -211,6 +211,13 @@ __device__ __forceinline__ void tc_box(uint32_t dst, const CUtensorMap *map, uin
                                        const void *bar) {
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
                  ::"r"(dst), "l"(map), "r"(s32(bar)), "r"(x), "r"(h), "r"(token), "r"(page) : "memory");
+}
+
+// The same with both 64-channel blocks of a head in one box, eight positions of one, then of the other.
+__device__ __forceinline__ void tc_box_folded(uint32_t dst, const CUtensorMap *map, uint32_t block, uint32_t eight, int32_t page,
+                                              const void *bar) {
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %4, %5, %6}], [%2];"
+                 ::"r"(dst), "l"(map), "r"(s32(bar)), "r"(0), "r"(block), "r"(eight), "r"(page) : "memory");
 }
 
 // 32 columns of this warp's 32 rows of tensor memory.
@@ -308,6 +315,12 @@ __device__ __forceinline__ uint32_t fill_of(bool both, uint32_t T, uint32_t e, b
     is_v = !(e & 1u) || e == 2 * T - 1;
     return e == 2 * T - 1 ? T - 1 : is_v ? (e - 2) / 2 : (e - 2) / 2 + 2;
 }
+
+// A tile's layout in the ring: 64-channel blocks one after the other, or, where a box brings both
+// (a.folded), eight positions of one and of the other in turn.
+template <int DP, bool E>
+__device__ __forceinline__ uint32_t block_of(const AttendArgs &a) { return !E && DP == 128 && a.folded ? 1024u : TcShape<DP, E>::block; }
+__device__ __forceinline__ uint32_t group_of(const AttendArgs &a) { return a.folded ? 2048u : 1024u; }
 
 // The part's query rows as the first product's operand, by the 128 filling threads.
 template <int DP, bool E>
@@ -574,6 +587,8 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
                 const CUtensorMap *map = is_v ? vmap : kmap;
                 if (E) {
                     tc_box(dst + lane * a.box * DP, map, 0u, w.h, token, page, bar);
+                } else if (DP == 128 && a.folded) {
+                    tc_box_folded(dst + lane * a.box * 256u, map, 2u * w.h, token >> 3, page, bar);
                 } else {
 #pragma unroll
                     for (uint32_t b = 0; b < DP / 64; ++b)
@@ -593,6 +608,7 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
                                             uint32_t raw_at) {
     using S = TcShape<DP, E>;
     const uint32_t t = threadIdx.x - 256u;
+    const uint32_t block = block_of<DP, E>(a), group = group_of(a);
     uint32_t pos = 0, turns = 0;                                     // turns: parity of landed[] by slot (bf16)
     Walk w;
     for (w.start(a, sh); w.more(); w.next(a)) {
@@ -612,7 +628,7 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
                 constexpr uint32_t CH = DP / 8;
                 for (uint32_t x = first * CH + t; x < kTile * CH; x += 128u) {
                     const uint32_t row = x / CH, ch = x % CH;
-                    const uint32_t at = ring_at + slot * S::tile + (ch >> 3) * S::block + row * 128u + (((ch ^ row) & 7u) << 4);
+                    const uint32_t at = ring_at + slot * S::tile + (ch >> 3) * block + (row >> 3) * group + (row & 7u) * 128u + (((ch ^ row) & 7u) << 4);
                     uint32_t v[4];
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
                     bool hit = false;
@@ -687,7 +703,8 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
     // made of is the same in every lane, so it stays in uniform registers (a branch
     // for one thread moves every descriptor there anew).
     tmem = __shfl_sync(~0u, tmem, 0);
-    const uint64_t q_op = tc_operand(q_at, 16u), k_op = tc_operand(ring_at, 16u), v_op = tc_operand(ring_at, S::block);
+    const uint32_t block = block_of<DP, E>(a), group = group_of(a);
+    const uint64_t q_op = tc_operand(q_at, 16u, 1024u), k_op = tc_operand(ring_at, 16u, group), v_op = tc_operand(ring_at, block, group);
     uint32_t pos = 0, jobs[2] = {0u, 0u};
     Walk w;
     for (w.start(a, sh); __shfl_sync(~0u, (int)w.more(), 0); w.next(a)) {
@@ -709,8 +726,8 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
                 const uint64_t qa = q_op + (both && s ? S::tile >> 4 : 0u), ka = k_op + ((k_slot * S::tile) >> 4);
 #pragma unroll
                 for (uint32_t k = 0; k < DP / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * S::block + (k & 3u) * 32u) >> 4;
-                    tc_mma_ss(tmem + s * kTile, qa + off, ka + off, kind_s, k != 0);
+                    const uint32_t in = ((k & 3u) * 32u) >> 4;
+                    tc_mma_ss(tmem + s * kTile, qa + (((k >> 2) * S::block) >> 4) + in, ka + (((k >> 2) * block) >> 4) + in, kind_s, k != 0);
                 }
                 tc_commit(&sm.s_full[s]);
                 if (!both || s) tc_commit(&sm.empty[k_slot]);
@@ -731,7 +748,7 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
                 const uint64_t va = v_op + ((v_slot * S::tile) >> 4);
 #pragma unroll
                 for (uint32_t k = 0; k < kTile / 16; ++k)
-                    tc_mma_ts(tmem + 256u + s * DP, tmem + s * kTile + k * 8u, va + ((k * 2048u) >> 4), kind_o, j > 1 || k != 0);
+                    tc_mma_ts(tmem + 256u + s * DP, tmem + s * kTile + k * 8u, va + ((k * 2u * group) >> 4), kind_o, j > 1 || k != 0);
                 tc_commit(&sm.o_done[s]);
                 if (!both || s) tc_commit(&sm.empty[v_slot]);
             }
@@ -988,8 +1005,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
     if (a.span < kTile) {
         // rows of the ring (and of the codes behind it) that no copy reaches: read as 0, not as what was there
         const uint32_t rows = kTile - a.span;
-        for (uint32_t x = tid; x < S::ring * (DP / 64u) * rows * 8u; x += kTcThreads)
-            st_shared16(ring_at + x / (rows * 8u) * S::block + (a.span + x / 8u % rows) * 128u + x % 8u * 16u, make_uint4(0u, 0u, 0u, 0u));
+        for (uint32_t x = tid; x < S::ring * (DP / 64u) * rows * 8u; x += kTcThreads) {
+            const uint32_t row = a.span + x / 8u % rows, of = x / (rows * 8u);
+            st_shared16(ring_at + of / (DP / 64u) * S::tile + of % (DP / 64u) * block_of<DP, E>(a) + (row >> 3) * group_of(a) + (row & 7u) * 128u +
+                            x % 8u * 16u, make_uint4(0u, 0u, 0u, 0u));
+        }
         for (uint32_t x = tid; x < S::raw * rows * (DP / 16u); x += kTcThreads)
             st_shared16(raw_at + x / (rows * (DP / 16u)) * S::raw_tile + a.span * DP + x % (rows * (DP / 16u)) * 16u, make_uint4(0u, 0u, 0u, 0u));
         proxy_fence();
@@ -1044,15 +1064,25 @@ static EncodeTiled encoder() {
     return f;
 }
 
-// A pool as a tensor [page][token][head][channel] read in boxes of `box` tokens of one head.
-static bool pool_map(CUtensorMap *map, const PagedView &c, const uint8_t *pool, uint32_t DP) {
+// A pool as a tensor [page][token][head][channel] read in boxes of `box` tokens of one head; folded: as
+// [page][token / 8][64-channel block][token % 8][channel], both blocks of a head in a box.
+static bool pool_map(CUtensorMap *map, const PagedView &c, const uint8_t *pool, uint32_t DP, bool folded) {
     const EncodeTiled f = encoder();
     if (!f) return false;
     const bool e = c.e4m3;
+    const uint64_t page_stride = c.n_pages > 1 ? c.page_stride : 16u;
+    if (folded) {
+        const cuuint64_t dims[5] = {64u, 8u, 2u * c.n_heads, c.page.d / 8u, c.n_pages};
+        const cuuint64_t strides[4] = {c.token_stride, 128u, 8u * c.token_stride, page_stride};
+        const cuuint32_t box[5] = {64u, 8u, 2u, paged_box(c.page.d) / 8u, 1u}, one[5] = {1u, 1u, 1u, 1u, 1u};
+        return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t *>(pool), dims, strides, box, one,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
     const cuuint64_t dims[4] = {c.head_dim, c.n_heads, c.page.d, c.n_pages};
     // the stride of a dimension of one entry is never used, but has to be a valid one
     const cuuint64_t strides[3] = {c.n_heads > 1 ? c.head_stride : 16u, c.page.d > 1 ? c.token_stride : 16u,
-                                   c.n_pages > 1 ? c.page_stride : 16u};
+                                   page_stride};
     const cuuint32_t box[4] = {e ? DP : 64u, 1u, paged_box(c.page.d), 1u}, one[4] = {1u, 1u, 1u, 1u};
     // L2 fetches no more than a row: what lies behind it is another head's, wanted much later
     const uint32_t row = c.head_dim * (e ? 1u : 2u);
@@ -1073,7 +1103,9 @@ static bool launch(AttendArgs a, const AttendWs &ws, cudaStream_t st) {
     // strides reach 2^41 bytes, a tensor map's less than 2^40
     a.box = a.c.page_stride < (uint64_t(1) << 40) && a.c.token_stride < (uint64_t(1) << 40) && a.c.head_stride < (uint64_t(1) << 40)
                 ? paged_box(a.c.page.d) : 0u;
-    if (a.box && !(pool_map(&kmap, a.c, a.c.k, DP) && pool_map(&vmap, a.c, a.c.v, DP))) a.box = 0u;    // row by row
+    // heads side by side, as the coder lays pages out: half as many boxes, which counts where they are small
+    a.folded = !E && a.c.head_dim == 128u && a.box && a.box < 128u && (a.c.n_heads == 1u || a.c.head_stride == 256u);
+    if (a.box && !(pool_map(&kmap, a.c, a.c.k, DP, a.folded) && pool_map(&vmap, a.c, a.c.v, DP, a.folded))) a.box = a.folded = 0u;    // row by row
     a.span = a.box ? kTile / a.box * a.box : kTile;
     attend_large<DP, E><<<kCtasLarge, kTcThreads, bytes, st>>>(a, ws, kmap, vmap);
     return cudaGetLastError() == cudaSuccess && launch_join(a, ws, kTcRows, DP, kCtasLarge, st);

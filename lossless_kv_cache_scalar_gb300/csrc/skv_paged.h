@@ -66,6 +66,7 @@ struct AttendArgs {
     int32_t *status;
     uint32_t box;             // positions of a tensor copy, 0: none fits the page length
     uint32_t span;            // positions of a tile: 128 / box boxes, or 128
+    uint32_t folded;          // 1: a copy brings both 64-channel blocks of a head of 128 channels
 };
 
 // Positions of a tensor copy for a page length: the largest divisor of it that is a
