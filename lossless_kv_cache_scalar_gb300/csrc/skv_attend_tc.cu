@@ -1018,16 +1018,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     bool corrupt = false;
-    // 512 threads of 128 registers, dealt out anew: 2 x 192 + 88 + 40 = 4 x 128 per lane of the four groups.
+    // 512 threads of 128 registers, dealt out anew: per lane of the four groups 2 x 184 + 88 + 56 (bf16) and
+    // 2 x 184 + 96 + 48 (e4m3, whose second group converts) = 4 x 128.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         weight_role<DP, E>(a, ws, sh, sm, tmem);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (E) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (a.box) finish_role<DP, E>(a, sh, sm, q_at, ring_at, raw_at);
         else fill_role<DP, E>(a, sh, sm, q_at, ring_at, reinterpret_cast<uint64_t(*)[kTile]>(dyn + S::raw_at), corrupt);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (E) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 13 && a.box) box_role<DP, E>(a, sh, sm, ring_at, raw_at, &kmap, &vmap, corrupt);
         if (warp == 12) product_role<DP, E>(a, sh, sm, q_at, ring_at, tmem);
     }
