@@ -199,7 +199,7 @@ template <int DP, bool E>
 __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend_small(AttendArgs a, AttendWs ws) {
     using S = SmallShape<DP, E>;
     extern __shared__ __align__(1024) uint8_t ring_all[];
-    __shared__ unsigned long long sm_plan[kWarps + 4];
+    __shared__ unsigned long long sm_plan[2 * kWarps + 4];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, c4 = lane & 3u, g8 = lane >> 2;
     __shared__ uint32_t sm_last;
     const Share sh = share_of<kWarps * 32, false>(a, ws, 16u, S::unit, sm_plan);

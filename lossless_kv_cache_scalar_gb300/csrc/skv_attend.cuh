@@ -17,7 +17,8 @@
 // In the large-row kernel a run of positions counts kWide units with more than 128 rows and
 // kNarrow with up to 128: half of the products, the same bytes (256 against 128 rows took 1.28
 // to 1.42 times as long, in bf16 and e4m3, with 64 and 128 channels). A run belongs to the CTA
-// in whose share its first unit lies.
+// in whose share its first unit lies. A list of a few runs per CTA counts every run once: then what
+// matters is that no CTA has one more than another.
 #pragma once
 
 #include <atomic>
@@ -196,18 +197,19 @@ struct Share {
     uint64_t u0, u1;      // units [u0, u1)
     uint32_t r;
     uint64_t off;
+    uint32_t wide, narrow;    // units of a run
 };
 
 // Units of request r, split into row tiles of R rows and runs of UT positions.
-template <bool LARGE>
-__device__ __forceinline__ uint64_t units_of(const AttendArgs &a, const ReqOf &q, uint32_t R, uint32_t UT) {
+__device__ __forceinline__ uint64_t units_of(const AttendArgs &a, const ReqOf &q, uint32_t R, uint32_t UT, uint32_t wide,
+                                             uint32_t narrow) {
     if (q.n == 0) return 0;
     const uint32_t rows = q.n * a.group, rts = (rows + R - 1) / R;
-    const uint32_t per_run = LARGE ? rts * kWide - (rows - (rts - 1) * R > 128u ? 0u : kWide - kNarrow) : rts;
+    const uint32_t per_run = rts * wide - (rows - (rts - 1) * R > 128u ? 0u : wide - narrow);
     return (uint64_t)((q.len + UT - 1) / UT) * ((uint64_t)a.c.n_heads * per_run);
 }
 
-// Every thread of the block calls this; sm is scratch of blockDim / 32 + 4 words of 8 bytes.
+// Every thread of the block calls this; sm is scratch of 2 blockDim / 32 + 4 words of 8 bytes.
 // LARGE: the kernel with weighted runs and a joining kernel behind it, for which it leaves plan, error and
 // descriptor.
 template <uint32_t THREADS, bool LARGE>
@@ -215,27 +217,45 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
                                           unsigned long long *sm) {
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     constexpr uint32_t W = THREADS / 32u;
+    constexpr uint32_t wide = LARGE ? kWide : 1u, narrow = LARGE ? kNarrow : 1u;
     unsigned long long mine = 0, first = 0;
+    uint32_t runs = 0, first_runs = 0;          // modulo 2^32: used where the whole is small
     int32_t err = SKV_OK;
 #pragma unroll 1
     for (uint32_t r = tid; r < a.c.n_requests; r += THREADS) {
         const ReqOf q = request_of(a, r);
         if (q.err) err = q.err;
-        const uint64_t u = units_of<LARGE>(a, q, R, UT);
+        const uint64_t u = units_of(a, q, R, UT, wide, narrow);
         if (r == tid) first = u;
         mine += u;
+        if (LARGE) {
+            const uint32_t n = (uint32_t)units_of(a, q, R, UT, 1u, 1u);
+            if (r == tid) first_runs = n;
+            runs += n;
+        }
     }
     unsigned long long t = mine;
 #pragma unroll
     for (uint32_t d = 16; d; d >>= 1) t += __shfl_xor_sync(~0u, t, d);
-    if (lane == 0) sm[warp] = t;
+    if (LARGE) runs = __reduce_add_sync(~0u, runs);
+    if (lane == 0) {
+        sm[warp] = t;
+        if (LARGE) sm[W + 4 + warp] = runs;
+    }
     err = __syncthreads_or(err) ? SKV_ERR_INVALID_ARG : SKV_OK;
     unsigned long long U = 0;
 #pragma unroll
     for (uint32_t w = 0; w < W; ++w) U += sm[w];
-    // every share is at least a run
-    const uint64_t runs = LARGE ? (U > kWide ? U / kWide : U != 0) : U, active = runs < gridDim.x ? runs : gridDim.x;
-    Share s{U, active, 0, 0, 0, 0};
+    const bool even = LARGE && U <= 4u * kWide * gridDim.x;
+    if (even) {
+        U = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < W; ++w) U += sm[W + 4 + w];
+        first = first_runs;
+    }
+    // every share is at least a run (U >= 4 kWide CTAs where runs are weighted)
+    const uint64_t active = U < gridDim.x ? U : gridDim.x;
+    Share s{U, active, 0, 0, 0, 0, even ? 1u : wide, even ? 1u : narrow};
     if (LARGE && tid == 0) {
         ws.errs[blockIdx.x] = err;
         ws.desc[blockIdx.x].valid = 0u;
@@ -252,7 +272,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs &a, const AttendWs &w
     for (uint32_t base = 0; base < a.c.n_requests; base += THREADS) {
         const uint32_t r = base + tid;
         unsigned long long u = base == 0 ? first : 0ull;
-        if (base && r < a.c.n_requests) u = units_of<LARGE>(a, request_of(a, r), R, UT);
+        if (base && r < a.c.n_requests) u = units_of(a, request_of(a, r), R, UT, s.wide, s.narrow);
         unsigned long long x = u;
 #pragma unroll
         for (uint32_t d = 1; d < 32; d <<= 1) {

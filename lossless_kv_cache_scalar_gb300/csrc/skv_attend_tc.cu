@@ -58,6 +58,7 @@ struct Walk {
     uint32_t n;                                     // parts so far
     // the part: tiles [tile, tile_end) of the item
     uint32_t tile, tile_end, rows, weight;          // rows of this row tile, units of a tile
+    uint32_t wide, narrow;
 
     __device__ __forceinline__ void request(const AttendArgs &a) {
         tiles = (q.len + a.span - 1) / a.span;
@@ -66,7 +67,7 @@ struct Walk {
     }
     __device__ __forceinline__ void item(const AttendArgs &a) {
         rows = min(kTcRows, q.n * a.group - rt * kTcRows);
-        weight = both() ? kWide : kNarrow;
+        weight = both() ? wide : narrow;
     }
     // The tiles that start before the share's end.
     __device__ __forceinline__ void part() {
@@ -92,14 +93,16 @@ struct Walk {
         u1 = s.u1;
         r = s.r;
         n = 0;
+        wide = s.wide;
+        narrow = s.narrow;
         q = request_of(a, r);
         request(a);
-        const uint32_t last = q.n * a.group - (rts - 1) * kTcRows > kTile ? kWide : kNarrow;
-        const uint64_t wide = (uint64_t)tiles * kWide, head = (rts - 1) * wide + (uint64_t)tiles * last;
+        const uint32_t last = q.n * a.group - (rts - 1) * kTcRows > kTile ? wide : narrow;
+        const uint64_t full = (uint64_t)tiles * wide, head = (rts - 1) * full + (uint64_t)tiles * last;
         h = (uint32_t)quotient(s.off, head);
         uint64_t off = s.off - h * head;
-        rt = min((uint32_t)quotient(off, wide), rts - 1);
-        off -= rt * wide;
+        rt = min((uint32_t)quotient(off, full), rts - 1);
+        off -= rt * full;
         at = s.u0 - off;
         item(a);
         tile = (uint32_t)quotient(off + weight - 1, weight);
@@ -117,7 +120,7 @@ struct Walk {
 };
 
 struct TcShared {
-    unsigned long long plan[kTcThreads / 32 + 4];
+    unsigned long long plan[2 * kTcThreads / 32 + 4];
     unsigned long long full[8], empty[8];        // ring
     unsigned long long landed[8], taken[8];      // tensor copies that the filling warps finish
     int32_t pages[4][16];                        // page numbers of a tile's boxes
