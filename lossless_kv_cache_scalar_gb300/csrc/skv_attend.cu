@@ -184,6 +184,108 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
     }
 }
 
+// o[k] += weight * output of the warp's k-th row (warp + 4 k), over `here` parts, in their order.
+template <int DP, uint32_t ROWS, class At>
+__device__ __forceinline__ void add_parts(float4 (&o)[4], const float *s_f, uint32_t rows, uint32_t here, At at) {
+    const uint32_t warp = threadIdx.x >> 5;
+    constexpr uint32_t PARTS = 8u / ROWS;
+#pragma unroll 1
+    for (uint32_t j0 = 0; j0 < here; j0 += PARTS) {
+        float4 y[PARTS][ROWS];
+#pragma unroll
+        for (uint32_t j = 0; j < PARTS; ++j)
+#pragma unroll
+            for (uint32_t k = 0; k < ROWS; ++k) {
+                y[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < here && warp + 4u * k < rows)
+                    y[j][k] = __ldcg(reinterpret_cast<const float4 *>(at(j0 + j) + (warp + 4u * k) * DP));
+            }
+#pragma unroll
+        for (uint32_t j = 0; j < PARTS; ++j)
+#pragma unroll
+            for (uint32_t k = 0; k < ROWS; ++k) {
+                const float f = j0 + j < here ? s_f[(warp + 4u * k) * 33u + j0 + j] : 0.0f;
+                o[k].x += f * y[j][k].x, o[k].y += f * y[j][k].y, o[k].z += f * y[j][k].z, o[k].w += f * y[j][k].w;
+            }
+    }
+}
+
+// The 16 rows of an item whose n parts lie in CTAs c .. c + n - 1 (place 1 of the first, then 0), by a CTA:
+// each part weighs exp2(m - M) with M the largest m, in the order of the CTAs. Eight threads per row
+// find the weights of 32 parts at a time; then a thread adds up four channels of four rows, so
+// that the rows wait for L2 together (one after the other a warp's four rows took 5 us of 19).
+template <int DP>
+__device__ __forceinline__ void join_item(const AttendArgs &a, const AttendWs &ws, const ReqOf &q, uint32_t h, uint32_t rt,
+                                          uint32_t c, uint32_t n, float *scratch) {
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, row8 = tid >> 3, sub = tid & 7u;
+    const uint32_t rows = min(16u, q.n * a.group - rt * 16u);
+    constexpr uint32_t size = 16u * (2u + DP);
+    const float *next = ws.parts + (uint64_t)c * 2u * size;
+    const auto part = [&](uint32_t j) { return j ? next + (uint64_t)(2u * j) * size : next + size; };
+    float *s_f = scratch, *s_ml = scratch + 16 * 33;
+    const float vs = a.c.v_scale ? __ldg(a.c.v_scale + h) : 1.0f;
+    float M = -INFINITY, L = 0.0f;
+    if (row8 < rows) {
+#pragma unroll 4
+        for (uint32_t j = sub; j < n; j += 8u) M = fmaxf(M, __ldcg(part(j) + row8));
+    }
+#pragma unroll
+    for (uint32_t d = 4; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+#pragma unroll 1
+    for (uint32_t x0 = 0; x0 < DP; x0 += 128u) {                     // 256 channels: two rounds; 64: half of the lanes
+        const uint32_t x = x0 + 4u * lane;
+        float4 o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (uint32_t j0 = 0; j0 < n; j0 += 32u) {
+            __syncthreads();
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t j = 8u * i + sub;
+                float f = 0.0f;
+                if (j0 + j < n && row8 < rows) {
+                    f = part_weight(__ldcg(part(j0 + j) + row8), M);
+                    if (x0 == 0) L += f * __ldcg(part(j0 + j) + 16u + row8);
+                }
+                s_f[row8 * 33u + j] = f;
+            }
+            __syncthreads();
+            const uint32_t here = min(32u, n - j0);
+            if (x < DP) {
+                // eight loads on their way: four rows of two parts, two of four, or one of eight
+                if (rows > 8u) add_parts<DP, 4>(o, s_f, rows, here, [&](uint32_t j) { return part(j0 + j) + 32u + x; });
+                else if (rows > 4u) add_parts<DP, 2>(o, s_f, rows, here, [&](uint32_t j) { return part(j0 + j) + 32u + x; });
+                else add_parts<DP, 1>(o, s_f, rows, here, [&](uint32_t j) { return part(j0 + j) + 32u + x; });
+            }
+        }
+        if (x0 == 0) {
+#pragma unroll
+            for (uint32_t d = 4; d; d >>= 1) L += __shfl_xor_sync(~0u, L, d);
+            if (sub == 0) {
+                s_ml[row8] = M;
+                s_ml[16u + row8] = L;
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t row = warp + 4u * k;
+            if (row >= rows) continue;
+            const uint32_t all = rt * 16u + row, node = all / a.group, g = h * a.group + all - node * a.group;
+            const float l = s_ml[16u + row], inv = l == 0.0f ? 0.0f : vs / l;
+            if (x < a.c.head_dim) {
+                uint2 y;
+                y.x = l == 0.0f ? 0u : pack2<false>(o[k].x * inv, o[k].y * inv);
+                y.y = l == 0.0f ? 0u : pack2<false>(o[k].z * inv, o[k].w * inv);
+                *reinterpret_cast<uint2 *>(a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim + x) = y;
+            }
+            if (a.lse && x == 0)
+                a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = l == 0.0f ? -INFINITY : (s_ml[row] + log2f(l)) * 0.6931471805599453f;
+        }
+    }
+}
+
 // The end of a CTA with work: one word counts the CTAs in its low half and holds the kinds of
 // error above; the last CTA writes the status and clears it.
 __device__ __forceinline__ void finish(const AttendArgs &a, const AttendWs &ws, int32_t err, uint32_t active) {
@@ -536,9 +638,7 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
             __syncthreads();
             if (sm_last) {
                 __threadfence();
-
-#pragma unroll 1
-                for (uint32_t row = warp; row < 16u; row += kWarps) join_row(a, ws, q, h, rt, row, 16u, DP, c0, n);
+                join_item<DP>(a, ws, q, h, rt, c0, n, reinterpret_cast<float *>(ring_all));
             }
         }
         u += tile_end - tile;
