@@ -17,8 +17,8 @@
 // sum and output; no barrier inside the loop. The four are joined at the end of
 // a part. Three CTAs of 4 warps per SM, 64 KB of ring each, half of it in flight: 64
 // requests x 8,192 positions x 8 heads x 128 channels, one token, 8 query heads each, take 213 us in
-// bf16 (6.36 TB/s, 0.95 of a copy) and 141 us in e4m3 (4.8 TB/s: the conversions); two CTAs of
-// 96 KB took 219 and 151.
+// bf16 (6.36 TB/s, 0.95 of a copy) and 129 us in e4m3 (5.3 TB/s, bound by issue: the conversions);
+// two CTAs of 96 KB took 3% and 6% longer.
 //
 // An e4m3 cache is raised to fp16 in registers (every e4m3 value is an fp16
 // value). The order of the channels inside a product is free as long as both
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
 // Joins the parts that attend_large leaves: block (c, y) every eighth eight rows of the
 // item that starts in CTA c and goes on, a warp per row. All blocks are resident at
 // once, so that descriptor and request are waited for once, not once per eight rows
-// (152 x 32 blocks of eight rows took 31 us behind a 515 us call, these 13). Block (0, 0)
+// (152 x 32 blocks of eight rows each took 31 us behind a 515 us call, 152 x 4 took 21). Block (0, 0)
 // turns the CTAs' error words into the status: the first that has one.
 constexpr uint32_t kJoinBlocks = 8;
 
@@ -767,6 +767,10 @@ extern "C" int32_t skv_tree_attention(const skv_paged *cache, const void *q, uin
     const AttendWs ws = attend_ws(workspace);
     const uint32_t d = cache->head_dim;
     bool ok;
+    // The tcgen05 kernel pays 128 rows whatever their number, the small-row kernel reads the pages once per
+    // 16 rows. us for small / tcgen05, 8 KV heads of 128 channels, 8 query heads each, bf16: 16 requests x
+    // 16,000 positions: 16 rows 172 / 177, 32 rows 329 / 174; 4 x 3,000: 16 rows 24 / 25, 32 rows 29 / 25; e4m3, 16 x
+    // 16,000: 16 rows 106 / 167, 32 rows 202 / 165. Head sizes above 128 do not fit tensor memory twice.
     if ((uint64_t)max_nodes * a.group > 16u && d <= 128)
         ok = launch_large(a, ws, st);
     else if (cache->dtype == SKV_E4M3)

@@ -73,7 +73,7 @@ struct AttendArgs {
 // multiple of 8 (the swizzle's period) and of which whole boxes fill at least 112 of a
 // tile's 128 rows; 0 if the length is no multiple of 8. A copy costs some 45 clocks
 // beside its rows: with boxes of 8 a page of 24 took 410 us where whole pages (five of 24, 120 of
-// 128 rows used) take 253, and a page of 256 191 (19 requests x 16,384 positions x 8 heads x 128 channels, bf16, 64 rows).
+// 128 rows used) take 245, 209 with both blocks of a head in one box, and a page of 256 190 (19 requests x 16,384 positions x 8 heads x 128 channels, bf16, 64 rows).
 inline uint32_t paged_box(uint32_t page) {
     for (uint32_t b = page < 128u ? page : 128u; b >= 8u; --b)
         if (b % 8u == 0 && page % b == 0 && 128u / b * b >= 112u) return b;
