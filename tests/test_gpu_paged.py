@@ -645,3 +645,40 @@ def test_attend_wide_and_narrow_row_tiles(dtype):
     s = attend_case(71, [3000, 2500, 1400, 700], [96, 43, 32, 65], 64, 1, 4, 64, dtype)
     check_attend(s, max_nodes=96)
 
+
+
+def test_wrappers_refuse_wrong_tensors():
+    """Types, shapes, strides and devices that the C ABI cannot see are refused before a call."""
+    s = attend_case(73, [9, 3], [2, 1], 16, 2, 2, 64, "bf16")
+    cache = PagedKV(s["k"], s["v"], s["table"], q_heads=4)
+    q, ctx, cu, mask = s["q"], s["ctx"], s["cu"], s["mask"]
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q.transpose(0, 1)),
+                dict(out=out.float()), dict(out=out[:-1]), dict(out=out.transpose(0, 1)), dict(ctx=ctx.long()), dict(ctx=ctx[:1]),
+                dict(cu=cu[:-1]), dict(cu=cu.cpu()), dict(mask=mask[:-1]), dict(mask=mask.int()), dict(mask=mask[:, :0]),
+                dict(lse=torch.empty(3, device="cuda"))):
+        a = dict(dict(q=q, ctx=ctx, cu=cu, out=out, mask=mask, lse=None), **bad)
+        with pytest.raises(ValueError):
+            cache.attend_into(a["q"], a["ctx"], a["cu"], a["out"], mask=a["mask"], lse=a["lse"])
+    with pytest.raises(ValueError):
+        PagedKV(s["k"], s["v"]).attend_into(q, ctx, cu, out)
+    new, slots = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.arange(3, dtype=torch.int64, device="cuda")
+    rows = i32([0, 1, 2])
+    for k, v, sl, r in ((new.float(), new.float(), slots, None), (new, new[:2], slots, None), (new[:, :1], new[:, :1], slots, None),
+                        (new, new.cpu(), slots, None), (new, new, slots.int(), None), (new, new, slots, rows[:2]),
+                        (new, new, slots, rows.long())):
+        with pytest.raises(ValueError):
+            cache.append_into(k, v, sl, rows=r)
+    for k, v in ((s["k"].float(), s["v"].float()), (s["k"][:-1], s["v"]), (s["k"].view(torch.int16)[..., ::2], s["v"].view(torch.int16)[..., ::2])):
+        with pytest.raises(ValueError):
+            PagedKV(k, v, s["table"])
+    with pytest.raises(ValueError):
+        PagedKV(s["k"], s["v"], s["table"].t())
+    with pytest.raises(SKVError):                      # scales of a bf16 cache
+        one = torch.ones(2, device="cuda")
+        PagedKV(s["k"], s["v"], s["table"], k_scale=one, v_scale=one)
+    pt = PageTable(s["table"], 16, s["k"].shape[0])
+    with pytest.raises(ValueError):
+        pt.map_into(ctx.long(), ctx, ctx, ctx, ctx, cu, slots, ctx, ctx)
+    with pytest.raises(SKVError):                      # counts read and written in place
+        pt.map_into(ctx, ctx, ctx, i32([0]), i32([0, 1]), cu, slots, ctx, i32([0, 0]))
