@@ -226,7 +226,8 @@ class PagedKV(_Status):
     def attend(self, q, ctx_len, cu_new, mask=None, max_nodes: int | None = None, scale: float | None = None,
                stream=None):
         """attend_into a new tensor (rows outside every request 0), waited for and checked."""
-        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+        with torch.cuda.stream(stream):                  # zeros before the call's writes, on its own stream
+            out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
         self.attend_into(q, ctx_len, cu_new, out, mask, max_nodes, scale, stream=stream)
         self.check_status("skv_tree_attention", stream)
         return out
