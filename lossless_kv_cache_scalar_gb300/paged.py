@@ -154,12 +154,14 @@ class PagedKV(_Status):
         if q_heads:
             self._make_workspace(q_heads)
 
-    def _make_workspace(self, q_heads: int):
+    def _make_workspace(self, q_heads: int, stream=None):
+        """The workspace, its counters 0 before what `stream` (None: the current one) does next."""
         v = C.c_uint64()
         B.check("skv_tree_attention_workspace_bytes",
                 B.lib().skv_tree_attention_workspace_bytes(self._ref, q_heads, C.byref(v)))
-        self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
-        self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
+        with torch.cuda.stream(stream):
+            self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
+            self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
         self._workspace, self._workspace_bytes = self.workspace.data_ptr(), v.value
         self.q_heads = q_heads
 
@@ -214,9 +216,11 @@ class PagedKV(_Status):
             _check_words("lse", _F32, n * heads, lse)
             lse = lse.data_ptr()
         if heads != self.q_heads:
-            if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:
                 raise ValueError("give PagedKV its q_heads before a capture")
-            self._make_workspace(heads)
+            self._make_workspace(heads, stream)
         rc = B.lib().skv_tree_attention(
             self._ref, q.data_ptr(), stride[0], stride[1], heads, n, ctx_len.data_ptr(), cu_new.data_ptr(), mask, words,
             n if max_nodes is None else max_nodes, self._scale if scale is None else scale, out.data_ptr(), lse,

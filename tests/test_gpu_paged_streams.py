@@ -3,14 +3,23 @@ between calls: nothing that a call needs may still wait on another stream, and n
 that a captured graph holds may be given away."""
 import pytest
 import torch
+
 from tests.test_gpu_paged import attend_case
 from lossless_kv_cache_scalar_gb300 import PagedKV
+
 pytestmark = pytest.mark.gpu
 
 
 def busy():
     """Keeps the current stream at work for some 0.2 s."""
     torch.cuda._sleep(400_000_000)
+
+
+def dirty(n_bytes, count=1):
+    """Leaves blocks of that size full of ones with the allocator of the current stream."""
+    blocks = [torch.full((n_bytes,), 255, dtype=torch.uint8, device="cuda") for _ in range(count)]
+    torch.cuda.synchronize()
+    return blocks
 
 
 def case(nodes, dtype, seed=81):
@@ -39,3 +48,43 @@ def test_attend_fills_its_output_on_the_given_stream(nodes, dtype):
     got = cache.attend(s["q"], s["ctx"], s["cu"], mask=s["mask"], max_nodes=nodes, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [1, 40])
+def test_attend_makes_its_workspace_on_the_given_stream(nodes, dtype):
+    """A first call without q_heads: the counters are 0 before the kernel reads them."""
+    s = case(nodes, dtype)
+    want, cache, side = expected(s, nodes), cache_of(s), torch.cuda.Stream()
+    n_bytes = cache_of(s, q_heads=8).workspace.numel()
+    blocks = dirty(n_bytes, 3)
+    with torch.cuda.stream(side):
+        blocks += dirty(n_bytes, 3)
+    del blocks
+    got = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    busy()
+    cache.status.fill_(-1)                           # behind the busy stream's work: must not be what stays
+    torch.cuda.synchronize()
+    busy()
+    cache.attend_into(s["q"], s["ctx"], s["cu"], got, mask=s["mask"], max_nodes=nodes, stream=side)
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 0
+    assert torch.equal(got, want)
+    cache.attend_into(s["q"], s["ctx"], s["cu"], got.zero_(), mask=s["mask"], max_nodes=nodes)
+    assert torch.equal(got, want)
+
+
+def test_no_workspace_is_made_in_a_capture_of_the_given_stream():
+    """The capture that counts is the given stream's, not the current one's."""
+    s = case(1, "bf16")
+    cache = cache_of(s)
+    out = torch.zeros_like(s["q"]).contiguous()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            with pytest.raises(ValueError):
+                cache.attend_into(s["q"], s["ctx"], s["cu"], out, mask=s["mask"], max_nodes=1, stream=side)
+    assert cache.workspace is None
