@@ -120,7 +120,8 @@ class PagedKV(_Status):
     (pages as decode_chunks returns them, viewed in four dimensions, are such pools).
 
     block_table: int32 [n_requests][max_pages], needed by attend; k_scale, v_scale:
-    float32 [n_heads] of an e4m3 cache. q_heads > 0 makes the workspace of attend."""
+    float32 [n_heads] of an e4m3 cache. q_heads > 0 makes the workspace of attend, for any
+    number of query heads (a first call makes it otherwise, which a capture cannot)."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor | None = None,
                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, q_heads: int = 0):
@@ -150,12 +151,14 @@ class PagedKV(_Status):
         self._ref = C.byref(self._c)
         B.check("skv_paged_check", B.lib().skv_paged_check(self._ref))
         self._new_status(k_pages.device)
-        self.q_heads, self.workspace = 0, None
+        self.workspace = None
         if q_heads:
             self._make_workspace(q_heads)
 
     def _make_workspace(self, q_heads: int, stream=None):
-        """The workspace, its counters 0 before what `stream` (None: the current one) does next."""
+        """The workspace, its counters 0 before what `stream` (None: the current one) does next. Its
+        size is the same for every number of query heads, and it stays as long as the object: a
+        captured graph holds its address."""
         v = C.c_uint64()
         B.check("skv_tree_attention_workspace_bytes",
                 B.lib().skv_tree_attention_workspace_bytes(self._ref, q_heads, C.byref(v)))
@@ -163,7 +166,6 @@ class PagedKV(_Status):
             self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
             self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
         self._workspace, self._workspace_bytes = self.workspace.data_ptr(), v.value
-        self.q_heads = q_heads
 
     def append_into(self, k, v, slots, rows=None, stream=None):
         """Enqueue skv_cache_append: rows of k and v (bf16 [n_src][n_heads][head_dim], any
@@ -215,7 +217,7 @@ class PagedKV(_Status):
         if lse is not None:
             _check_words("lse", _F32, n * heads, lse)
             lse = lse.data_ptr()
-        if heads != self.q_heads:
+        if self.workspace is None:
             with torch.cuda.stream(stream):
                 capturing = torch.cuda.is_current_stream_capturing()
             if capturing:

@@ -75,6 +75,36 @@ def test_attend_makes_its_workspace_on_the_given_stream(nodes, dtype):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("nodes", [1, 40])
+def test_a_graph_keeps_its_workspace(nodes):
+    """A capture with one number of query heads, then a call with another, then other tensors:
+    a replay gives what it gave, and writes to nobody else's memory."""
+    s = case(nodes, "bf16")
+    cache = cache_of(s, q_heads=8)
+    out = torch.zeros_like(s["q"]).contiguous()
+    half = s["q"][:, ::2]
+
+    def step():
+        cache.attend_into(s["q"], s["ctx"], s["cu"], out, mask=s["mask"], max_nodes=nodes)
+
+    step()
+    torch.cuda.synchronize()
+    want = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    n_bytes = cache.workspace.numel()
+    eager = cache.attend(half, s["ctx"], s["cu"], mask=s["mask"], max_nodes=nodes)
+    others = dirty(n_bytes, 4)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    for t in others:
+        assert (t == 255).all()
+    assert torch.equal(cache.attend(half, s["ctx"], s["cu"], mask=s["mask"], max_nodes=nodes), eager)
+
+
 def test_no_workspace_is_made_in_a_capture_of_the_given_stream():
     """The capture that counts is the given stream's, not the current one's."""
     s = case(1, "bf16")
