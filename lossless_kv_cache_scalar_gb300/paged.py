@@ -49,6 +49,12 @@ class _Status:
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self._status, self._device = self.status.data_ptr(), self.status.device.index
 
+    def _settle(self):
+        """End of a constructor: what it filled is filled, whatever stream calls first (in a capture
+        the fills are part of the graph)."""
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self._device).synchronize()
+
     def check_status(self, where: str, stream=None):
         (stream or torch.cuda.current_stream()).synchronize()
         st = int(self.status.item())
@@ -66,6 +72,7 @@ class PageTable(_Status):
         self.page_tokens, self.pool_pages = int(page_tokens), int(pool_pages)
         self.n_requests, self.max_pages = block_table.shape
         self._new_status(block_table.device)
+        self._settle()
 
     def map_into(self, ctx_len, new_len, n_pages, free_pages, free_state, cu_new, slots, n_pages_out,
                  free_state_out, stream=None):
@@ -97,6 +104,7 @@ class PagePool(PageTable):
         self.free_pages = torch.arange(pool_pages, dtype=torch.int32, device=device)
         self.free_state = torch.tensor([0, pool_pages], dtype=torch.int32, device=device)
         self._next = (torch.empty_like(self.n_pages), torch.empty_like(self.free_state))
+        self._settle()
 
     def step(self, ctx_len, new_len, max_new: int, check: bool = True, stream=None):
         """Map one step's new tokens (max_new: room for so many slots). Returns
@@ -151,9 +159,10 @@ class PagedKV(_Status):
         self._ref = C.byref(self._c)
         B.check("skv_paged_check", B.lib().skv_paged_check(self._ref))
         self._new_status(k_pages.device)
-        self.workspace = None
+        self.q_heads, self.workspace = q_heads, None
         if q_heads:
             self._make_workspace(q_heads)
+        self._settle()
 
     def _make_workspace(self, q_heads: int, stream=None):
         """The workspace, its counters 0 before what `stream` (None: the current one) does next. Its

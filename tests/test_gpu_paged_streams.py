@@ -4,8 +4,8 @@ that a captured graph holds may be given away."""
 import pytest
 import torch
 
-from tests.test_gpu_paged import attend_case
-from lossless_kv_cache_scalar_gb300 import PagedKV
+from tests.test_gpu_paged import attend_case, gen_of, i32, pool_of
+from lossless_kv_cache_scalar_gb300 import PagedKV, PagePool, SKVError
 
 pytestmark = pytest.mark.gpu
 
@@ -76,6 +76,35 @@ def test_attend_makes_its_workspace_on_the_given_stream(nodes, dtype):
 
 
 @pytest.mark.parametrize("nodes", [1, 40])
+def test_a_new_object_is_ready_for_any_stream(nodes):
+    """What a constructor fills is filled when it returns: a status that a call on another stream
+    writes is not wiped by the constructor's zeros."""
+    s = case(nodes, "bf16")
+    s["table"][1, 2] = 10 ** 6                        # outside the pool
+    out, side = torch.zeros_like(s["q"]).contiguous(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    cache = cache_of(s, q_heads=8)
+    cache.attend_into(s["q"], s["ctx"], s["cu"], out, mask=s["mask"], max_nodes=nodes, stream=side)
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 7
+
+
+def test_a_new_pool_is_ready_for_any_stream():
+    ctx, new, side = i32([0, 0]), i32([20, 5]), torch.cuda.Stream()
+    blocks = dirty(512, 20)
+    del blocks
+    torch.cuda.synchronize()
+    busy()
+    pool = PagePool(2, 4, 16, 8)
+    cu, slots = pool.step(ctx, new, 32, stream=side)
+    torch.cuda.synchronize()
+    assert cu.tolist() == [0, 20, 25]
+    assert slots.tolist() == list(range(20)) + list(range(32, 37)) + [-1] * 7
+    assert pool.block_table[:, :2].tolist() == [[0, 1], [2, -1]]
+
+
+@pytest.mark.parametrize("nodes", [1, 40])
 def test_a_graph_keeps_its_workspace(nodes):
     """A capture with one number of query heads, then a call with another, then other tensors:
     a replay gives what it gave, and writes to nobody else's memory."""
@@ -118,3 +147,20 @@ def test_no_workspace_is_made_in_a_capture_of_the_given_stream():
             with pytest.raises(ValueError):
                 cache.attend_into(s["q"], s["ctx"], s["cu"], out, mask=s["mask"], max_nodes=1, stream=side)
     assert cache.workspace is None
+
+
+def test_append_on_a_given_stream():
+    """Rows and their status, with the current stream busy."""
+    g, side = gen_of(83), torch.cuda.Stream()
+    k, v = (pool_of(4, 16, 2, 64, "bf16", g) for _ in range(2))
+    new = torch.randn(9, 2, 64, generator=g, device="cuda").to(torch.bfloat16)
+    slots = torch.arange(9, dtype=torch.int64, device="cuda") * 7
+    slots[8] = 64
+    torch.cuda.synchronize()
+    busy()
+    cache = PagedKV(k, v)
+    with pytest.raises(SKVError):
+        cache.append(new, new, slots, stream=side)
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 1
+    assert torch.equal(k.view(-1, 2, 64)[slots[:8]], new[:8])
