@@ -110,8 +110,9 @@ class PagePool(PageTable):
         """Map one step's new tokens (max_new: room for so many slots). Returns
         (cu_new, slots), slots past the step's tokens -1."""
         dev = self.block_table.device
-        cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
-        slots = torch.empty(max_new, dtype=torch.int64, device=dev)
+        with torch.cuda.stream(stream):                  # memory that this stream has done with
+            cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
+            slots = torch.empty(max_new, dtype=torch.int64, device=dev)
         self.map_into(ctx_len, new_len, self.n_pages, self.free_pages, self.free_state, cu, slots, *self._next,
                       stream=stream)
         now = (self.n_pages, self.free_state)

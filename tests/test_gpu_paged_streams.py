@@ -104,6 +104,21 @@ def test_a_new_pool_is_ready_for_any_stream():
     assert pool.block_table[:, :2].tolist() == [[0, 1], [2, -1]]
 
 
+def test_pool_step_takes_no_memory_that_the_current_stream_still_writes():
+    """cu_new and slots of a step on another stream: not a block whose last use is still on its way."""
+    ctx, new, side, pool = i32([0, 0]), i32([20, 5]), torch.cuda.Stream(), PagePool(2, 4, 16, 8)
+    torch.cuda.synchronize()
+    old = [torch.empty(n, dtype=t, device="cuda") for n, t in ((32, torch.int64), (3, torch.int32)) for _ in range(8)]
+    busy()
+    for t in old:
+        t.fill_(77)
+    del old, t
+    cu, slots = pool.step(ctx, new, 32, stream=side)
+    torch.cuda.synchronize()
+    assert cu.tolist() == [0, 20, 25]
+    assert slots.tolist() == list(range(20)) + list(range(32, 37)) + [-1] * 7
+
+
 @pytest.mark.parametrize("nodes", [1, 40])
 def test_a_graph_keeps_its_workspace(nodes):
     """A capture with one number of query heads, then a call with another, then other tensors:
