@@ -108,9 +108,12 @@ class PagePool(PageTable):
 
     def step(self, ctx_len, new_len, max_new: int, check: bool = True, stream=None):
         """Map one step's new tokens (max_new: room for so many slots). Returns
-        (cu_new, slots), slots past the step's tokens -1."""
+        (cu_new, slots), slots past the step's tokens -1. Not for a capture, whose replays would
+        all start from the same counts: capture map_into, and copy its counts back behind it."""
         dev = self.block_table.device
         with torch.cuda.stream(stream):                  # memory that this stream has done with
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("PagePool.step swaps its counts on the host; capture map_into")
             cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
             slots = torch.empty(max_new, dtype=torch.int64, device=dev)
         self.map_into(ctx_len, new_len, self.n_pages, self.free_pages, self.free_state, cu, slots, *self._next,

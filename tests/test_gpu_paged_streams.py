@@ -164,6 +164,18 @@ def test_no_workspace_is_made_in_a_capture_of_the_given_stream():
     assert cache.workspace is None
 
 
+def test_pool_step_refuses_a_capture():
+    """A step swaps its buffers on the host: replayed, it would read the same counts for ever."""
+    ctx, new, pool = i32([0, 0]), i32([20, 5]), PagePool(2, 4, 16, 8)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError):
+            pool.step(ctx, new, 32, check=False)
+    cu, slots = pool.step(ctx, new, 32)
+    assert cu.tolist() == [0, 20, 25] and pool.n_pages.tolist() == [2, 1]
+
+
 def test_append_on_a_given_stream():
     """Rows and their status, with the current stream busy."""
     g, side = gen_of(83), torch.cuda.Stream()
