@@ -313,7 +313,8 @@ class Coder:
 
     def decode_chunks(self, bitstream, offsets, mu, sigma, counts, chunk_ids, stream=None):
         lay = self.layout
-        pages = torch.zeros((chunk_ids.numel(), lay.page_elems), dtype=mu.dtype, device=mu.device)
+        with torch.cuda.stream(stream):                  # zeros before the call's writes, on its own stream
+            pages = torch.zeros((chunk_ids.numel(), lay.page_elems), dtype=mu.dtype, device=mu.device)
         self.decode_chunks_into(bitstream, offsets, mu, sigma, counts, chunk_ids, pages, stream)
         self.check_status("skv_decode_chunks", stream)
         return pages

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests.test_gpu_paged import attend_case, gen_of, i32, pool_of
-from lossless_kv_cache_scalar_gb300 import PagedKV, PagePool, SKVError
+from lossless_kv_cache_scalar_gb300 import Coder, Layout, PagedKV, PagePool, SKVError, synth
 
 pytestmark = pytest.mark.gpu
 
@@ -174,6 +174,21 @@ def test_pool_step_refuses_a_capture():
             pool.step(ctx, new, 32, check=False)
     cu, slots = pool.step(ctx, new, 32)
     assert cu.tolist() == [0, 20, 25] and pool.n_pages.tolist() == [2, 1]
+
+
+def test_decode_chunks_fills_its_pages_on_the_given_stream():
+    cfg = synth.CONFIGS["tiny"].scaled(n_tokens=600)
+    w = {k: v.cuda() for k, v in synth.generate(cfg).items()}
+    lay = Layout("bf16", cfg.n_layers, cfg.n_kv, cfg.n_heads, cfg.head_dim, 600, tokens_per_chunk=256)
+    coder, side = Coder(lay), torch.cuda.Stream()
+    bits, offs = coder.encode(w["kv"], w["mu"], w["sigma"], w["counts"])
+    ids = i32([2, 0, 1])
+    want = coder.decode_chunks(bits, offs, w["mu"], w["sigma"], w["counts"], ids)
+    torch.cuda.synchronize()
+    busy()
+    got = coder.decode_chunks(bits, offs, w["mu"], w["sigma"], w["counts"], ids, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
 
 
 def test_append_on_a_given_stream():
