@@ -27,6 +27,9 @@ def _stream_of(stream, device: int) -> int:
 
 
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+# what a pool may be kept as: the format's own type, or its bits
+_CODES = {torch.bfloat16: B.SKV_BF16, torch.int16: B.SKV_BF16, torch.uint16: B.SKV_BF16,
+          torch.float8_e4m3fn: B.SKV_E4M3, torch.uint8: B.SKV_E4M3, torch.int8: B.SKV_E4M3}
 
 
 def _check_words(what: str, dtype, numel: int, *ts):
@@ -127,8 +130,8 @@ class PagePool(PageTable):
 
 
 class PagedKV(_Status):
-    """K and V pools [n_pages][page_tokens][n_heads][head_dim] of codes (2-byte: bf16,
-    1-byte: e4m3), of any strides that are multiples of 16 bytes and the same for both
+    """K and V pools [n_pages][page_tokens][n_heads][head_dim] of codes (bf16, or int16
+    and uint16 of its bits; float8_e4m3fn, or uint8 and int8), of any strides that are multiples of 16 bytes and the same for both
     (pages as decode_chunks returns them, viewed in four dimensions, are such pools).
 
     block_table: int32 [n_requests][max_pages], needed by attend; k_scale, v_scale:
@@ -138,11 +141,12 @@ class PagedKV(_Status):
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor | None = None,
                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, q_heads: int = 0):
         for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-            if not t.is_cuda or t.dim() != 4 or t.element_size() not in (1, 2) or (t.shape[3] > 1 and t.stride(3) != 1):
-                raise ValueError(f"{what} must be a CUDA tensor [n_pages][page_tokens][n_heads][head_dim] of codes")
+            if not t.is_cuda or t.dim() != 4 or t.dtype not in _CODES or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise ValueError(f"{what} must be a CUDA tensor [n_pages][page_tokens][n_heads][head_dim] of codes "
+                                 "(bfloat16, int16 or uint16; float8_e4m3fn, uint8 or int8)")
         if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
-                or k_pages.element_size() != v_pages.element_size() or k_pages.device != v_pages.device:
-            raise ValueError("k_pages and v_pages must have the same shape, strides, code size and device")
+                or _CODES[k_pages.dtype] != _CODES[v_pages.dtype] or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must have the same shape, strides, format and device")
         n_pages, page_tokens, n_heads, head_dim = k_pages.shape
         for s in (k_scale, v_scale):
             if s is not None:
@@ -156,8 +160,7 @@ class PagedKV(_Status):
             n_requests, max_pages = block_table.shape
         self.n_requests = n_requests
         ps, ts, hs = k_pages.stride()[:3]
-        self._c = B.skv_paged(B.SKV_FORMAT_VERSION, B.SKV_BF16 if k_pages.element_size() == 2 else B.SKV_E4M3,
-                              n_heads, head_dim, page_tokens, n_pages, k_pages.data_ptr(), v_pages.data_ptr(),
+        self._c = B.skv_paged(B.SKV_FORMAT_VERSION, _CODES[k_pages.dtype], n_heads, head_dim, page_tokens, n_pages, k_pages.data_ptr(), v_pages.data_ptr(),
                               ps if n_pages > 1 else 0, ts if page_tokens > 1 else 0, hs if n_heads > 1 else 0,
                               _ptr(k_scale), _ptr(v_scale), _ptr(block_table), stride, n_requests, max_pages)
         self._ref = C.byref(self._c)
