@@ -20,7 +20,10 @@ from .api import _check_dev, _ptr
 
 def _stream_of(stream, device: int) -> int:
     """The handle of `stream`, or of the current stream of the tensors' device (the
-    raw query: a Stream object costs several microseconds of a short step)."""
+    raw query: a Stream object costs several microseconds of a short step). Kernels are
+    launched on the current device, so that has to be the tensors'."""
+    if torch._C._cuda_getDevice() != device or (stream is not None and stream.device_index != device):
+        raise ValueError(f"the pools are on cuda:{device}: make it the current device and give a stream of it")
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device)
@@ -32,12 +35,12 @@ _CODES = {torch.bfloat16: B.SKV_BF16, torch.int16: B.SKV_BF16, torch.uint16: B.S
           torch.float8_e4m3fn: B.SKV_E4M3, torch.uint8: B.SKV_E4M3, torch.int8: B.SKV_E4M3}
 
 
-def _check_words(what: str, dtype, numel: int, *ts):
-    """Contiguous CUDA tensors of one type and size (a step makes a dozen of these
+def _check_words(what: str, dtype, numel: int, device: int, *ts):
+    """Contiguous tensors of one type and size on that device (a step makes a dozen of these
     checks, each of a few tenths of a microsecond: no calls that are not needed)."""
     for t in ts:
-        if t.dtype is not dtype or t.numel() != numel or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous {dtype} CUDA tensors of {numel} entries")
+        if t.dtype is not dtype or t.numel() != numel or t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous {dtype} tensors of {numel} entries on cuda:{device}")
 
 
 def _table_rows(t):
@@ -83,12 +86,12 @@ class PageTable(_Status):
         (free_pages, free_state = [head, count]), their table entries, cu_new and the
         slot map; a request of ctx_len < 0 gives its pages back. The new page counts and
         ring state go to n_pages_out and free_state_out (other tensors than the inputs)."""
-        n, size, room = self.n_requests, free_pages.numel(), slots.numel()
-        _check_words("ctx_len, new_len, n_pages and n_pages_out", _I32, n, ctx_len, new_len, n_pages, n_pages_out)
-        _check_words("free_state and free_state_out", _I32, 2, free_state, free_state_out)
-        _check_words("cu_new", _I32, n + 1, cu_new)
-        _check_words("free_pages", _I32, size, free_pages)
-        _check_words("slots", _I64, room, slots)
+        n, size, room, dev = self.n_requests, free_pages.numel(), slots.numel(), self._device
+        _check_words("ctx_len, new_len, n_pages and n_pages_out", _I32, n, dev, ctx_len, new_len, n_pages, n_pages_out)
+        _check_words("free_state and free_state_out", _I32, 2, dev, free_state, free_state_out)
+        _check_words("cu_new", _I32, n + 1, dev, cu_new)
+        _check_words("free_pages", _I32, size, dev, free_pages)
+        _check_words("slots", _I64, room, dev, slots)
         rc = B.lib().skv_page_map(self.page_tokens, self.pool_pages, n, ctx_len.data_ptr(), new_len.data_ptr(),
                                   self._table, self._stride, self.max_pages, n_pages.data_ptr(), n_pages_out.data_ptr(),
                                   free_pages.data_ptr(), size, free_state.data_ptr(), free_state_out.data_ptr(),
@@ -130,9 +133,10 @@ class PagePool(PageTable):
 
 
 class PagedKV(_Status):
-    """K and V pools [n_pages][page_tokens][n_heads][head_dim] of codes (bf16, or int16
-    and uint16 of its bits; float8_e4m3fn, or uint8 and int8), of any strides that are multiples of 16 bytes and the same for both
-    (pages as decode_chunks returns them, viewed in four dimensions, are such pools).
+    """K and V pools [n_pages][page_tokens][n_heads][head_dim] of codes (bf16, or int16 and
+    uint16 of its bits; float8_e4m3fn, or uint8 and int8), of any strides that are multiples of
+    16 bytes and the same for both (pages as decode_chunks returns them, viewed in four
+    dimensions, are such pools).
 
     block_table: int32 [n_requests][max_pages], needed by attend; k_scale, v_scale:
     float32 [n_heads] of an e4m3 cache. q_heads > 0 makes the workspace of attend, for any
@@ -151,6 +155,9 @@ class PagedKV(_Status):
         for s in (k_scale, v_scale):
             if s is not None:
                 _check_dev(s, "k_scale and v_scale", torch.float32, numel=n_heads)
+        for t in (k_scale, v_scale, block_table):
+            if t is not None and t.device != k_pages.device:
+                raise ValueError("the scales and the block_table must be on the pools' device")
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.block_table, self.n_heads, self.head_dim = block_table, n_heads, head_dim
         self._row_shape, self._scale = torch.Size((n_heads, head_dim)), 1.0 / math.sqrt(head_dim)
@@ -186,15 +193,15 @@ class PagedKV(_Status):
     def append_into(self, k, v, slots, rows=None, stream=None):
         """Enqueue skv_cache_append: rows of k and v (bf16 [n_src][n_heads][head_dim], any
         row and head strides that are multiples of 8) into the slots (int64, -1 skips)."""
-        shape, stride = k.shape, k.stride()
-        if v.shape != shape or v.stride() != stride or k.dtype is not _BF16 or v.dtype is not _BF16 or not k.is_cuda \
-                or not v.is_cuda or len(shape) != 3 or shape[1:] != self._row_shape or stride[2] != 1:
-            raise ValueError("k and v must be bf16 CUDA tensors [n_src][%d][%d] of the same strides, the last 1"
+        shape, stride, dev = k.shape, k.stride(), self._device
+        if v.shape != shape or v.stride() != stride or k.dtype is not _BF16 or v.dtype is not _BF16 or k.get_device() != dev \
+                or v.get_device() != dev or len(shape) != 3 or shape[1:] != self._row_shape or stride[2] != 1:
+            raise ValueError("k and v must be bf16 tensors [n_src][%d][%d] on the pools' device, of the same strides, the last 1"
                              % tuple(self._row_shape))
         n = slots.numel()
-        _check_words("slots", _I64, n, slots)
+        _check_words("slots", _I64, n, dev, slots)
         if rows is not None:
-            _check_words("rows", _I32, n, rows)
+            _check_words("rows", _I32, n, dev, rows)
             rows = rows.data_ptr()
         rc = B.lib().skv_cache_append(self._ref, k.data_ptr(), v.data_ptr(), stride[0], stride[1], shape[0], rows,
                                       slots.data_ptr(), n, self._status, _stream_of(stream, self._device))
@@ -214,24 +221,24 @@ class PagedKV(_Status):
         to 1 / sqrt(head_dim); lse: float32 [n_rows][q_heads] or None."""
         if self.block_table is None:
             raise ValueError("attend needs a block_table")
-        shape, stride = q.shape, q.stride()
-        if len(shape) != 3 or q.dtype is not _BF16 or not q.is_cuda or stride[2] != 1 or shape[2] != self.head_dim \
+        shape, stride, dev = q.shape, q.stride(), self._device
+        if len(shape) != 3 or q.dtype is not _BF16 or q.get_device() != dev or stride[2] != 1 or shape[2] != self.head_dim \
                 or shape[1] == 0 or shape[1] % self.n_heads:
-            raise ValueError(f"q must be a bf16 CUDA tensor [n_rows][a multiple of {self.n_heads}][{self.head_dim}]")
+            raise ValueError(f"q must be a bf16 tensor [n_rows][a multiple of {self.n_heads}][{self.head_dim}] on cuda:{dev}")
         n, heads = shape[0], shape[1]
-        if out.shape != shape or out.dtype is not _BF16 or not out.is_cuda or not out.is_contiguous():
-            raise ValueError("out must be a contiguous bf16 CUDA tensor of q's shape")
-        _check_words("ctx_len", _I32, self.n_requests, ctx_len)
-        _check_words("cu_new", _I32, self.n_requests + 1, cu_new)
+        if out.shape != shape or out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 tensor of q's shape and device")
+        _check_words("ctx_len", _I32, self.n_requests, dev, ctx_len)
+        _check_words("cu_new", _I32, self.n_requests + 1, dev, cu_new)
         words = 0
         if mask is not None:
             if mask.dim() != 2 or mask.shape[0] != n or mask.shape[1] == 0:
                 raise ValueError("mask must be an int64 CUDA tensor [n_rows][words]")
             words = mask.shape[1]
-            _check_words("mask", _I64, n * words, mask)
+            _check_words("mask", _I64, n * words, dev, mask)
             mask = mask.data_ptr()
         if lse is not None:
-            _check_words("lse", _F32, n * heads, lse)
+            _check_words("lse", _F32, n * heads, dev, lse)
             lse = lse.data_ptr()
         if self.workspace is None:
             with torch.cuda.stream(stream):
