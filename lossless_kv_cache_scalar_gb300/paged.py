@@ -217,7 +217,8 @@ class PagedKV(_Status):
         """Enqueue skv_tree_attention. q: bf16 [n_rows][q_heads][head_dim] (row and head
         strides multiples of 8); out: the same shape, contiguous; mask: int64 [n_rows][words]
         of visibility bits among a request's new tokens, None: each sees the ones before it;
-        max_nodes: about the most new tokens of a request (default n_rows); scale defaults
+        max_nodes: about the most new tokens of a request (default: the mean over the requests,
+        rounded up, so that a batch of single tokens is taken for one); scale defaults
         to 1 / sqrt(head_dim); lse: float32 [n_rows][q_heads] or None."""
         if self.block_table is None:
             raise ValueError("attend needs a block_table")
@@ -248,7 +249,7 @@ class PagedKV(_Status):
             self._make_workspace(heads, stream)
         rc = B.lib().skv_tree_attention(
             self._ref, q.data_ptr(), stride[0], stride[1], heads, n, ctx_len.data_ptr(), cu_new.data_ptr(), mask, words,
-            n if max_nodes is None else max_nodes, self._scale if scale is None else scale, out.data_ptr(), lse,
+            -(-n // max(self.n_requests, 1)) if max_nodes is None else max_nodes, self._scale if scale is None else scale, out.data_ptr(), lse,
             self._status, self._workspace, self._workspace_bytes, _stream_of(stream, self._device))
         B.check("skv_tree_attention", rc)
 

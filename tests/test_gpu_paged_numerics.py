@@ -6,9 +6,20 @@ import pytest
 import torch
 
 from tests import _pagedtest as P
+from tests.test_gpu_paged import attend_case
 from lossless_kv_cache_scalar_gb300 import PagedKV
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attend_takes_single_tokens_for_single_tokens(dtype):
+    """Without max_nodes a batch of single tokens is one, whatever the number of requests: the
+    same bits as with max_nodes=1."""
+    s = attend_case(95, [900 + 37 * i for i in range(40)], [1] * 40, 16, 2, 8, 128, dtype)
+    q = s["q"][:40]
+    cache = PagedKV(s["k"], s["v"], s["table"], k_scale=s["ks"], v_scale=s["vs"], q_heads=16)
+    assert torch.equal(cache.attend(q, s["ctx"], s["cu"]), cache.attend(q, s["ctx"], s["cu"], max_nodes=1))
 
 
 @pytest.mark.parametrize("kind", [torch.float16, torch.float8_e5m2, torch.float8_e4m3fnuz, torch.bool])
