@@ -629,7 +629,8 @@ int32_t skv_cache_append(const skv_paged *cache, const void *k, const void *v, u
  *             Its first SKV_ATTENTION_ZERO_BYTES hold counters: they must be 0 before
  *             the first call, and every call leaves them 0; the rest may hold anything
  * Sums and maxima are binary32; the weights w_p enter the second product in
- * bf16 (bf16 cache) or fp16 (e4m3 cache). Repeated calls give the same bits.
+ * bf16 (bf16 cache) or fp16 (e4m3 cache: off by 2^-11 of a weight, or by 2^-32 of the row's
+ * largest weight where that is more). Repeated calls give the same bits.
  * Device errors: INVALID_ARG (cu_new descends or passes n_rows, ctx_len < 0 with
  * rows, more positions than max_pages hold, n_r > 64 mask_words: such a
  * request's rows are left alone), CORRUPT (a page number outside the pool: that

@@ -27,7 +27,7 @@
 // need. The queries become fp16 after a power-of-two scale per row that brings the
 // largest magnitude to [1, 2): bf16's 8 bits fit, and what is below 2^-14 of the
 // largest is off by at most 2^-25 of it. Weights are rounded to the type of the
-// product (fp16: half a step 2^-11, bf16: 2^-8); their sum stays binary32.
+// product (fp16: half a step 2^-11, or 2^-32 of the row's largest; bf16: 2^-8); their sum stays binary32.
 #include "skv_attend.cuh"
 
 namespace skv {
@@ -460,14 +460,14 @@ __global__ void __launch_bounds__(kWarps * 32, SmallShape<DP, E>::per_sm) attend
             for (int n = 0; n < 2 * (int)G; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
-            // the reference of a row's weights moves only for a weight of 2^8 or more against it (sums are
-            // binary32 and the quotient does not depend on it), so the output is rarely scaled anew
+            // the reference of a row's weights lags (kLag; sums are binary32), so the output is rarely scaled anew
             bool move[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 1));
                 top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 2)) * qf.mul[half];
-                move[half] = top[half] > m[half] + 8.0f || (m[half] == -INFINITY && top[half] > m[half]);
+                move[half] = top[half] > m[half] + (kLag + kLower<E>) || (m[half] == -INFINITY && top[half] > m[half]);
+                top[half] -= kLower<E>;
             }
             if (__any_sync(~0u, move[0] || move[1])) {
                 float keep[2];

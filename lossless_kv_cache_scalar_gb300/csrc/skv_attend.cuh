@@ -151,6 +151,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A row's weights are 2^(score - m) against a reference m that lags behind the row's largest score by
+// up to 2^8 in weight. In fp16 (e4m3 caches) a weight below 2^-14 loses bits and one below 2^-25 is
+// nothing, while a sink's neighbours can hold much of the output at 2^-27 each: there the reference is
+// put 2^7 lower, so that weights reach 2^15 (of fp16's 65,504) and are off by 2^-32 of the row's largest at
+// most. The quotient does not depend on the reference.
+constexpr float kLag = 8.0f;
+template <bool FP16>
+constexpr float kLower = FP16 ? 7.0f : 0.0f;
+
 // The weight of a part with maximum m against the whole's M (0 for a part with nothing).
 __device__ __forceinline__ float part_weight(float m, float M) { return m == -INFINITY ? 0.0f : ex2(m - M); }
 

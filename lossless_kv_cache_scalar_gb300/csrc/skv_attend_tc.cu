@@ -22,10 +22,8 @@
 // MN-major operand of the second product, so neither is transposed. Both in
 // rows of 128 bytes with the 128-byte swizzle.
 //
-// The maximum that a row's weights refer to lags: it moves only when the row's
-// largest score exceeds it by more than 2^8 in weight, so the output in tensor
-// memory is rarely scaled anew (weights reach 256 at most, sums stay binary32, and
-// the quotient does not depend on the reference).
+// The reference of a row's weights lags behind the row's largest score (kLag), so the output in
+// tensor memory is rarely scaled anew; sums stay binary32.
 //
 // Bound: from 129 rows on by the products (2 x 128 x 128 x DP per job, 2^12 multiply-adds per clock) and the
 // first product's shared-memory reads (8 KB for 64 clocks of work); below that by the pages' bytes.
@@ -833,10 +831,9 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     for (int i = 0; i < 32; i += 2) far[c] = max3(far[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
                 far[0] = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3]));
                 const float top = far[0] * mul;                      // in base 2
-                // the reference moves only for a weight of 2^8 or more against it
-                const bool move = top > m + 8.0f || (m == -INFINITY && top > m);
-                const float keep = move ? part_weight(m, top) : 1.0f;
-                if (move) m = top;
+                const bool move = top > m + (kLag + kLower<E>) || (m == -INFINITY && top > m);
+                const float keep = move ? part_weight(m, top - kLower<E>) : 1.0f;
+                if (move) m = top - kLower<E>;
                 l *= keep;
                 if (__any_sync(~0u, move) && done) {
                     bar_wait(sm, &sm.o_done[s], (jobs - 1u) & 1u);

@@ -6,10 +6,56 @@ import pytest
 import torch
 
 from tests import _pagedtest as P
-from tests.test_gpu_paged import attend_case
+from tests.test_gpu_paged import attend_case, gen_of, i32
 from lossless_kv_cache_scalar_gb300 import PagedKV
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes,requests,ctx", [(1, 40, 2000), (40, 16, 2000), (1, 1, 20000)])
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("above", [27.0, 7.9])
+def test_attend_small_weights_beside_a_large_one(above, where, nodes, requests, ctx, dtype):
+    """One position whose score lies `above` powers of two over all others and whose value is
+    0: the output is what the others hold, each with a weight of 2^-above. A batch with as many
+    items as CTAs, so that one CTA has all positions of a head; and one request, split over
+    many. (7.9: the largest weight against a reference that has not moved.)"""
+    g = gen_of(91)
+    page, heads, group, dim = 256, 16, 2, 64
+    pages = -(-(ctx + nodes) // page)
+    kf = torch.randn(pages * page, heads, dim, generator=g, device="cuda") * 0.25
+    vf = 1.0 + 0.5 * torch.rand(pages * page, heads, dim, generator=g, device="cuda")
+    kf[:, :, 0] = 0.0
+    at = 0 if where == "first" else ctx - 1
+    kf[at], vf[at] = 0.0, 0.0
+    kf[at, :, 0] = 8.0
+    kind = torch.bfloat16 if dtype == "bf16" else P.E4M3
+    k, v = (t.to(kind).view(pages, page, heads, dim) for t in (kf, vf))
+    if dtype == "e4m3":
+        k, v = k.view(torch.uint8), v.view(torch.uint8)
+    scale = 0.125
+    rows = requests * nodes
+    q = torch.randn(rows, heads * group, dim, generator=g, device="cuda") * 0.5
+    q[:, :, 0] = above * math.log(2.0) / (8.0 * scale)
+    q = q.to(torch.bfloat16)
+    ones = torch.ones(heads, device="cuda") if dtype == "e4m3" else None
+    # every request reads the same pages
+    table, lens, cu = i32([list(range(pages))] * requests), i32([ctx] * requests), i32(list(range(0, rows + 1, nodes)))
+    out = PagedKV(k, v, table, k_scale=ones, v_scale=ones).attend(q, lens, cu, max_nodes=nodes, scale=scale)
+    eps = dict(q_eps=2.0 ** -16, p_eps=2.0 ** -11) if dtype == "e4m3" else {}
+    for r in {0, requests // 2, requests - 1}:
+        for i in {0, nodes // 2, nodes - 1}:
+            # node i of a chain is a single token over ctx + i positions
+            row = slice(r * nodes + i, r * nodes + i + 1)
+            o, tol, _, _ = P.attention(q[row], k, v, ones, ones, table[:1], i32([ctx + i]), i32([0, 1]), None, scale, **eps)
+            # an e4m3 cache: fp16 weights are off by 2^-32 of the row's largest, or 2^-11 of themselves
+            if dtype == "e4m3":
+                tol = tol + 2.0 ** -32 * (ctx + i + 1) * 1.5
+            if above == 27.0:
+                assert float(o.min()) > 4 * float(tol.max())           # the tolerance tells the output from nothing
+            over = (out[row].cpu().double() - o).abs() - tol
+            assert (over <= 0).all(), float(over.max())
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
