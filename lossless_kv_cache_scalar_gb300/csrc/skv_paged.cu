@@ -334,18 +334,33 @@ struct AppendArgs {
     uint32_t checked;                                 // 1: block 0 reports the errors
 };
 
+// A head's scale s, brought between 2^-85 and 2^64 together with the values (`by`, a power of two):
+// there 1 / s and the remainders below are exact enough at either end of binary32. A value that
+// leaves binary32 on the way saturates, or is 0, like its quotient.
+struct ScaleOf {
+    float by, s, r;
+};
+
+__device__ __forceinline__ ScaleOf scale_of(float s) {
+    ScaleOf o;
+    o.by = s < 0x1p-64f ? 0x1p64f : s > 0x1p64f ? 0x1p-64f : 1.0f;
+    o.s = s * o.by;
+    o.r = __fdiv_rn(1.0f, o.s);
+    return o;
+}
+
 // The e4m3 code nearest to x / s. The binary32 quotient alone can land on a tie
 // that the real quotient only comes near, so it is rounded to odd first: the
 // remainder x - q s is exact in an fma for any q within a step of the quotient, and
 // where it is not 0 the quotient is cut towards 0 and its last bit set, which keeps it
 // off every border of the much coarser code grid. q: one product with the
-// reciprocal r of s and one correction by the remainder; for scales whose
-// reciprocal may not be normal (r = 0) a division.
-__device__ __forceinline__ uint32_t e4m3_of(float x, float s, float r) {
-    float q = r != 0.0f ? x * r : __fdiv_rn(x, s);
+// reciprocal of s and one correction by the remainder.
+__device__ __forceinline__ uint32_t e4m3_of(float value, const ScaleOf &c) {
+    const float x = value * c.by;
+    float q = x * c.r;
     if (fabsf(q) >= 1.0e-30f && fabsf(q) < 1.0e30f) {
-        q = fmaf(fmaf(-q, s, x), r, q);
-        const float rem = fmaf(-q, s, x);
+        q = fmaf(fmaf(-q, c.s, x), c.r, q);
+        const float rem = fmaf(-q, c.s, x);
         uint32_t b = __float_as_uint(q);
         // the remainder's sign against the quotient's (s > 0): q is too large in magnitude
         if ((__float_as_uint(rem) ^ b) >> 31) --b;
@@ -354,18 +369,16 @@ __device__ __forceinline__ uint32_t e4m3_of(float x, float s, float r) {
     return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ float reciprocal_of(float s) { return s > 1.0e-30f && s < 1.0e30f ? __fdiv_rn(1.0f, s) : 0.0f; }
-
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 // 16 bytes of codes from 16 channels of a bf16 row.
-__device__ __forceinline__ uint4 quantise16(const uint4 a, const uint4 b, float s, float r) {
+__device__ __forceinline__ uint4 quantise16(const uint4 a, const uint4 b, const ScaleOf &s) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        o[i] = e4m3_of(bf16_float(w[2 * i] & 0xFFFFu), s, r) | (e4m3_of(bf16_float(w[2 * i] >> 16), s, r) << 8) |
-               (e4m3_of(bf16_float(w[2 * i + 1] & 0xFFFFu), s, r) << 16) | (e4m3_of(bf16_float(w[2 * i + 1] >> 16), s, r) << 24);
+        o[i] = e4m3_of(bf16_float(w[2 * i] & 0xFFFFu), s) | (e4m3_of(bf16_float(w[2 * i] >> 16), s) << 8) |
+               (e4m3_of(bf16_float(w[2 * i + 1] & 0xFFFFu), s) << 16) | (e4m3_of(bf16_float(w[2 * i + 1] >> 16), s) << 24);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -410,8 +423,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
             // one code for both pools: half the instructions to fetch
 #pragma unroll 1
             for (uint32_t pool = 0; pool < 2; ++pool) {
-                const float scale = pool ? vs : ks;
-                *reinterpret_cast<uint4 *>((pool ? a.v : a.k) + dst) = quantise16(pool ? v0 : k0, pool ? v1 : k1, scale, reciprocal_of(scale));
+                *reinterpret_cast<uint4 *>((pool ? a.v : a.k) + dst) = quantise16(pool ? v0 : k0, pool ? v1 : k1, scale_of(pool ? vs : ks));
             }
         } else {
             const uint4 kc = __ldg(reinterpret_cast<const uint4 *>(a.k_new + src)), vc = __ldg(reinterpret_cast<const uint4 *>(a.v_new + src));

@@ -58,6 +58,49 @@ def test_attend_small_weights_beside_a_large_one(above, where, nodes, requests, 
             assert (over <= 0).all(), float(over.max())
 
 
+def near_ties(exponent):
+    """bf16 values of that exponent and scales for which their quotients are ties of the 8-bit
+    grid, or next to one."""
+    x = torch.arange(128, 256, dtype=torch.float64) * 2.0 ** (exponent - 7)
+    x = x[x == x.to(torch.bfloat16).double()]
+    ties = torch.tensor([1.0625, 1.1875, 1.3125, 1.4375, 1.5625, 1.6875, 1.8125], dtype=torch.float64)
+    s = (x[:, None] / ties).flatten().float()
+    x = x.repeat_interleave(7)
+    s = torch.cat([s, torch.nextafter(s, torch.full_like(s, math.inf)), torch.nextafter(s, torch.zeros_like(s))])
+    x = x.repeat(3)
+    keep = (s > 0) & torch.isfinite(s)
+    return x[keep].to(torch.bfloat16), s[keep]
+
+
+@pytest.mark.parametrize("exponent", [-131, -126, -124, -122, -120, -110, -101, -98, 98, 101, 120, 126, 127])
+def test_append_rounds_the_real_quotient_at_the_ends_of_binary32(exponent):
+    x, s = near_ties(exponent)
+    heads = s.numel()
+    k = torch.zeros(1, 1, heads, 16, dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    new = x.view(1, heads, 1).expand(1, heads, 16).contiguous().cuda()
+    PagedKV(k, v, k_scale=s.cuda(), v_scale=s.cuda()).append(new, -new, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    want = P.to_e4m3(x.double() / s.double())
+    assert torch.equal(k[0, 0, :, 0].cpu(), want) and torch.equal(v[0, 0, :, 5].cpu(), want | 128)
+
+
+@pytest.mark.parametrize("scale", [1e-45, 1e-40, 1e-37, 3e-31, 3e31, 1e38, 3.4e38])
+def test_append_with_scales_far_from_the_values(scale):
+    """Values of any size against scales of any size: saturated, or 0 with the value's sign."""
+    x = torch.tensor([0.0, -0.0, 1.0, -1.0, 3e38, -3e38, 1e-38, -1e-38, 9.2e-41, -9.2e-41, math.inf, -math.inf, math.nan, 448.0, 0.01, 7.0],
+                     dtype=torch.float64).to(torch.bfloat16)
+    s = torch.tensor([scale], dtype=torch.float32)
+    k = torch.zeros(1, 1, 1, 16, dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    PagedKV(k, v, k_scale=s.cuda(), v_scale=s.cuda()).append(x.view(1, 1, 16).cuda(), x.view(1, 1, 16).cuda(),
+                                                             torch.zeros(1, dtype=torch.int64, device="cuda"))
+    want = P.to_e4m3(x.double() / s.double())
+    for got in (k, v):
+        got = got.flatten().cpu()
+        nan = (want & 127) == 127
+        assert torch.equal((got & 127) == 127, nan) and torch.equal(got[~nan], want[~nan])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attend_takes_single_tokens_for_single_tokens(dtype):
     """Without max_nodes a batch of single tokens is one, whatever the number of requests: the
