@@ -151,26 +151,47 @@ __device__ __forceinline__ void warp_arrive(const void *b) {
     if ((threadIdx.x & 31u) == 0u) bar_arrive(b);
 }
 
-__device__ __forceinline__ bool bar_try(const void *b, uint32_t parity) {
+// How a wait looks at its barrier (try_wait sleeps on it for a while, test_wait does not) and when it
+// runs out. A test builds the kernel with a limit of its own.
+#ifndef SKV_WAIT_CLOCKS
+#define SKV_WAIT_CLOCKS 4000000000ll
+#define SKV_BAR_TRY "mbarrier.try_wait"
+#else
+#define SKV_BAR_TRY "mbarrier.test_wait"
+#endif
+
+__device__ __forceinline__ bool bar_try(uint32_t at, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p;}"
-                 : "=r"(ok) : "r"(s32(b)), "r"(parity) : "memory");
+    asm volatile("{.reg .pred p; " SKV_BAR_TRY ".parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p;}"
+                 : "=r"(ok) : "r"(at), "r"(parity) : "memory");
     return ok != 0;
 }
 
-// Waits for the phase of that parity, at most about two seconds; from the first wait
-// that runs out on, every wait of the CTA returns at once and the CTA runs to its end
-// on whatever it holds (all addresses stay in bounds), to report TIMEOUT.
+__device__ __forceinline__ bool bar_try(const void *b, uint32_t parity) { return bar_try(s32(b), parity); }
+
+__device__ __forceinline__ bool gave_up(const TcShared &sm) { return *reinterpret_cast<const volatile uint32_t *>(&sm.gave_up) != 0u; }
+
+// Waits for the phase of that parity, at most about two seconds. From the first wait that
+// runs out on, every wait of the CTA that is not over returns at once and the CTA runs to its
+// end on whatever it holds (all addresses stay in bounds), to report TIMEOUT. A barrier may then
+// say free or full where nothing is, so no copy is started any more (box_role), and the
+// copies and products that are on their way are waited for, again with a limit (bar_last).
 __device__ __forceinline__ void bar_wait(TcShared &sm, const void *b, uint32_t parity) {
     if (bar_try(b, parity)) return;
     const long long t0 = clock64();
     while (!bar_try(b, parity)) {
-        if (*reinterpret_cast<volatile uint32_t *>(&sm.gave_up)) return;
-        if (clock64() - t0 > 4000000000ll) {
+        if (gave_up(sm)) return;
+        if (clock64() - t0 > SKV_WAIT_CLOCKS) {
             *reinterpret_cast<volatile uint32_t *>(&sm.gave_up) = 1u;
             return;
         }
     }
+}
+
+// For what is on its way itself, whether the CTA gave up or not.
+__device__ __forceinline__ void bar_last(uint32_t at, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!bar_try(at, parity) && clock64() - t0 < 4000000000ll) {}
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -545,8 +566,11 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
     const uint32_t lane = threadIdx.x & 31u, boxes = a.span / a.box;
     constexpr uint32_t kRaw = E ? S::raw : 1;
     uint32_t pos = 0;
+    // lane i, of place i of the ring: barrier (its address) and phase (bit 0) of its last copies; uses of landed[i] in bf16
+    uint32_t last = 0u, turns = 0u;
+    bool stopped = false;
     Walk w;
-    for (w.start(a, sh); w.more(); w.next(a)) {
+    for (w.start(a, sh); !stopped && w.more(); w.next(a)) {
         const bool both = w.both();
         const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * a.span);
         int32_t next_page = 0;
@@ -582,6 +606,16 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
                 bar = is_v && p0 + a.span > w.q.ctx ? &sm.landed[slot] : &sm.full[slot];
                 dst = ring_at + slot * S::tile;
             }
+            // A place is free for certain only while nobody has given up: whoever gives up says so before it
+            // arrives anywhere. (A barrier armed twice for copies in one phase is undefined.)
+            __syncwarp();
+            stopped = __any_sync(~0u, gave_up(sm));
+            if (stopped) break;
+            if (lane == (E ? n % kRaw : slot)) {
+                const bool counted = !E && bar == &sm.landed[slot];
+                last = s32(bar) | (E ? (n / kRaw) & 1u : counted ? turns : (n / S::ring) & 1u);
+                if (counted) turns ^= 1u;
+            }
             const uint32_t live = min(boxes, (p_end - p0 + a.box - 1) / a.box);
             if (lane == 0)
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(s32(bar)), "r"(live * a.box * DP * (E ? 1u : 2u)) : "memory");
@@ -604,6 +638,9 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
         }
         pos += 2 * T;
     }
+    // No copy is on its way into this CTA's shared memory when the roles meet at the end.
+    if (last) bar_last(last & ~1u, last & 1u);
+    __syncwarp();
 }
 
 // Beside box_role: queries; every tile of an 8-bit cache raised to fp16; and in V tiles with
@@ -764,8 +801,7 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
     // Nothing of this CTA is left in the tensor cores when the roles meet at the end.
     if (elected()) tc_commit(&sm.drain);
     __syncwarp();
-    const long long t0 = clock64();
-    while (!bar_try(&sm.drain, 0u) && clock64() - t0 < 4000000000ll) {}
+    bar_last(s32(&sm.drain), 0u);
 }
 
 template <int DP, bool E>
