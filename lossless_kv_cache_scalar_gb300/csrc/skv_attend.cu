@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t swz_v(uint32_t row, uint32_t chunk) {
 template <int DP, bool E>
 struct QueryFrags {
     uint32_t f[DP / 16][4];
-    float mul[2];          // product -> score in base 2; at least 2^-100, so that -infinity times it stays that
+    float mul[2];          // product -> score in base 2; at least 2^-149, so that -infinity times it stays that
 };
 
 template <int DP, bool E>
@@ -150,7 +150,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
                     x.f[k][half + 2 * s] = (live && d < a.c.head_dim ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u) ^ (turned ? 0x80008000u : 0u);
                 }
             }
-            x.mul[half] = fmaxf(mul, 0x1p-100f);
+            x.mul[half] = fmaxf(mul, 0x1p-149f);
         } else {
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b) {
@@ -171,7 +171,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const ReqOf &q
             const uint32_t e = __float_as_uint(top) >> 23;
             const bool usual = e > 2u && e < 252u;
             const float down = (usual ? __uint_as_float((254u - e) << 23) : 1.0f) * (turned ? -1.0f : 1.0f);
-            x.mul[half] = fmaxf(usual ? mul * __uint_as_float(e << 23) : mul, 0x1p-100f);
+            x.mul[half] = fmaxf(usual ? mul * __uint_as_float(e << 23) : mul, 0x1p-149f);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
 #pragma unroll

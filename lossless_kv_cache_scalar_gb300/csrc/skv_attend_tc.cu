@@ -820,15 +820,15 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
         const bool live = row < w.rows, warp_live = (row & ~31u) < w.rows;
         // (no wait for the queries here: a part of few jobs can be two phases behind the filling warps)
         float mul = a.scale * (a.c.k_scale ? __ldg(a.c.k_scale + w.h) : 1.0f) * 1.4426950408889634f;
-        // (a negative scale has turned the queries;) at least 2^-100, so that -infinity times it stays that
-        if (!E) mul = fmaxf(fabsf(mul), 0x1p-100f);
+        // (a negative scale has turned the queries;) at least 2^-149, so that -infinity times it stays that
+        if (!E) mul = fmaxf(fabsf(mul), 0x1p-149f);
         float m = -INFINITY, l = 0.0f;
         uint32_t done = 0;                                           // jobs of this part
         for (uint32_t k = both ? 0u : s; k < T; k += both ? 1u : 2u, ++done, ++jobs) {
             bar_wait(sm, &sm.s_full[s], jobs & 1u);
             __syncwarp();
             tc_fence_after();
-            if (E && done == 0) mul = fmaxf(fabsf(mul) * __uint_as_float((uint32_t)sm.scaled[w.n & 1u][row] << 23), 0x1p-100f);
+            if (E && done == 0) mul = fmaxf(fabsf(mul) * __uint_as_float((uint32_t)sm.scaled[w.n & 1u][row] << 23), 0x1p-149f);
             const uint32_t p0 = (w.tile + k) * a.span;
             const bool edge = p0 + a.span > w.q.ctx || p0 + a.span > p_end, cut = a.span < kTile;
             if (warp_live) {

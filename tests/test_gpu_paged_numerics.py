@@ -2,11 +2,12 @@
 scales at the ends of binary32, wide and narrow row tiles in one long list of work,
 the kernel that a call takes by default, and pools of other types."""
 import math
+import random
 import pytest
 import torch
 
 from tests import _pagedtest as P
-from tests.test_gpu_paged import attend_case, gen_of, i32
+from tests.test_gpu_paged import attend_case, check_attend, gen_of, i32
 from lossless_kv_cache_scalar_gb300 import PagedKV
 
 pytestmark = pytest.mark.gpu
@@ -127,3 +128,13 @@ def test_pools_of_codes_are_taken(kind):
     PagedKV(k, v).append(new, new, torch.zeros(1, dtype=torch.int64, device="cuda"))
     one = k.view(torch.bfloat16) if kind.itemsize == 2 else k.view(P.E4M3)
     assert (one[0, 0].float() == 1).all()
+
+
+@pytest.mark.parametrize("nodes", [1, 40])
+@pytest.mark.parametrize("scale", [1e-35, -1e-35, 0.0])
+def test_attend_tiny_scales_of_large_values(scale, nodes):
+    """Products of 1e35 and a scale that makes ordinary scores of them, or none at all."""
+    s = attend_case(97, [300, 20], [nodes, nodes], 16, 2, 4, 64, "bf16")
+    for name in ("q", "k"):
+        s[name] = (s[name].float() * 2.0 ** 56).to(torch.bfloat16)
+    check_attend(s, max_nodes=nodes, scale=scale)
