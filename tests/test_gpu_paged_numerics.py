@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import _pagedtest as P
-from tests.test_gpu_paged import attend_case, check_attend, gen_of, i32
+from tests.test_gpu_paged import attend_case, check_attend, gen_of, i32, map_inputs, run_map
 from lossless_kv_cache_scalar_gb300 import PagedKV
 
 pytestmark = pytest.mark.gpu
@@ -102,6 +102,18 @@ def test_append_with_scales_far_from_the_values(scale):
         assert torch.equal((got & 127) == 127, nan) and torch.equal(got[~nan], want[~nan])
 
 
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("bf16", 80), ("e4m3", 64), ("e4m3", 80)])
+def test_attend_wide_and_narrow_row_tiles_in_a_long_list(dtype, dim):
+    """Row tiles of 256, 4, 140 and 6 rows among 3,920 units of work, above the 2,432 from which runs
+    of wide and of narrow tiles count 4 and 3, so that shares end anywhere in either."""
+    ctx, new, heads, group = [3000, 1500, 700], [130, 70, 3], 16, 2
+    units = sum(heads * -(-(c + n) // 128) * (4 * (n * group // 256) + (4 if n * group % 256 > 128 else 3 if n * group % 256 else 0))
+                for c, n in zip(ctx, new))
+    assert units > 4 * 4 * 152
+    s = attend_case(93, ctx, new, 64, heads, group, dim, dtype)
+    check_attend(s, max_nodes=130)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attend_takes_single_tokens_for_single_tokens(dtype):
     """Without max_nodes a batch of single tokens is one, whatever the number of requests: the
@@ -138,3 +150,41 @@ def test_attend_tiny_scales_of_large_values(scale, nodes):
     for name in ("q", "k"):
         s[name] = (s[name].float() * 2.0 ** 56).to(torch.bfloat16)
     check_attend(s, max_nodes=nodes, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [16, 32, 112])
+@pytest.mark.parametrize("page", [16, 24])
+def test_attend_trees_of_other_head_sizes(page, dim, dtype):
+    """Heads that fill a part of a copy's box, one of their blocks or none of the second."""
+    s = attend_case(99 + dim, [333, 130], [40, 9], page, 2, 4, dim, dtype, garbage=math.nan)
+    check_attend(s, max_nodes=40)
+
+
+def test_append_slots_beyond_31_bits():
+    """A pool of 2^32 token slots (pages 16 bytes apart: nothing that is written lies twice)."""
+    base_k, base_v = (torch.zeros((1 << 20) + 4096, 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+    k, v = (t.as_strided((4096, 1 << 20, 1, 16), (16, 16, 16, 1)) for t in (base_k, base_v))
+    pages, tokens = [0, 2047, 2048, 4095, 4000], [5, 77, 1000, (1 << 20) - 1, 9]
+    slots = torch.tensor([p * (1 << 20) + t for p, t in zip(pages, tokens)] + [1 << 32, -1], dtype=torch.int64, device="cuda")
+    new = torch.arange(1, 8, device="cuda").view(7, 1, 1).expand(7, 1, 16).to(torch.bfloat16).contiguous()
+    cache = PagedKV(k, v)
+    cache.append_into(new, -new, slots)
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 1                    # the slot just behind the pool
+    want = torch.zeros_like(base_k).view(P.E4M3).float()
+    for i, (p, t) in enumerate(zip(pages, tokens)):
+        want[p + t] = float(i + 1)
+    assert torch.equal(base_k.view(P.E4M3).float(), want) and torch.equal(base_v.view(P.E4M3).float(), -want)
+
+
+@pytest.mark.parametrize("b,page,max_new,more", [(4096, 16, 3, 7), (4097, 24, 9, 0), (9000, 5, 20, 30000)])
+def test_page_map_of_many_requests(b, page, max_new, more):
+    """More requests than one scan of the block holds."""
+    rng = random.Random(b)
+    ctx, new, have, table, free, state, pool, width = map_inputs(rng, b, page, 60, max_new, 0.2)
+    cap = sum(new) + more
+    want = P.page_map(page, pool, width, cap, ctx, new, table, have, free, state)
+    got = run_map(page, pool, width, cap, ctx, new, table, have, free, state)
+    for name, x, y in zip(("table", "n_pages", "free", "state", "cu", "slots"), got, want):
+        assert x == y, name
