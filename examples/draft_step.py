@@ -29,7 +29,8 @@ def tree_mask(parents):
     return torch.tensor([[b - (1 << 64) if b >> 63 else b] for b in bits], dtype=torch.int64)
 
 
-def main(tokens=1000, group=4):
+def step(tokens=1000, group=4):
+    """The whole step; returns what it made and what it had."""
     heads, dim, page = 8, 128, 256
     # a one-layer cache of `tokens` tokens, compressed against its predictor
     cfg = synth.CONFIGS["tiny"].scaled(n_tokens=tokens)
@@ -77,9 +78,16 @@ def main(tokens=1000, group=4):
     ctx.fill_(tokens + len(path) - 1)
     cu1 = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
     again = cache.attend(q[path[-1]:path[-1] + 1], ctx, cu1, max_nodes=1)
+    return dict(out=out, again=again, path=path, cache=cache, pool=pool, slots=slots, q=q, k=k, v=v, parents=parents,
+                bytes=bits.numel(), values=lay.n_elems)
+
+
+def main(tokens=1000, group=4):
+    s = step(tokens, group)
+    out, again, path = s["out"], s["again"], s["path"]
     off = (again[0].float() - out[path[-1]].float()).abs().max().item()
-    print(f"{tokens} tokens in {bits.numel()} bytes ({8.0 * bits.numel() / lay.n_elems:.2f} bits per value); "
-          f"{n} drafted, {len(path)} accepted; tree and single-token attention differ by {off:.4f} at most")
+    print(f"{tokens} tokens in {s['bytes']} bytes ({8.0 * s['bytes'] / s['values']:.2f} bits per value); "
+          f"{len(s['parents'])} drafted, {len(path)} accepted; tree and single-token attention differ by {off:.4f} at most")
     return out, again, path
 
 
