@@ -35,7 +35,7 @@ constexpr uint32_t kWide = 4, kNarrow = 3;
 // An item that starts in a CTA and goes on in the next ones.
 struct Desc {
     uint32_t valid, request, head, rt;
-    uint64_t first, last;                // units at which its first and its last run begin
+    uint64_t last;                       // unit at which its last run begins
 };
 
 struct Plan {
@@ -62,7 +62,7 @@ __host__ __device__ inline int32_t status_of(uint32_t word) {
 // Counters (SKV_ATTENTION_ZERO_BYTES), then plan, errs, descs.
 constexpr uint64_t kWsPlan = SKV_ATTENTION_ZERO_BYTES, kWsErrs = kWsPlan + 256u, kWsDesc = kWsErrs + 768u;
 constexpr uint64_t kWsHead = kWsDesc + 160u * sizeof(Desc);
-static_assert(kWsHead % 32u == 0 && sizeof(Desc) == 32 && kCtasLarge * 4u <= 768u && kCtasSmall * 4u + 4u <= SKV_ATTENTION_ZERO_BYTES &&
+static_assert(kWsHead % 32u == 0 && sizeof(Desc) == 24 && kCtasLarge * 4u <= 768u && kCtasSmall * 4u + 4u <= SKV_ATTENTION_ZERO_BYTES &&
               kCtasLarge <= 160u && kWsHead % 256u == 0, "workspace head");
 
 inline AttendWs attend_ws(void *base) {
@@ -328,53 +328,50 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, const AttendWs &ws
     const float *next = ws.parts + (uint64_t)c * 2u * size, *first = next + size;
     const auto part = [&](uint32_t j) { return j ? next + (uint64_t)(2u * j) * size : first; };
     uint16_t *out = a.out + ((uint64_t)(q.row0 + node) * a.n_q_heads + g) * a.c.head_dim;
-#pragma unroll 1
-    for (uint32_t x0 = 0; x0 < DP; x0 += 128u) {                     // 256 channels: two rounds; 64: half of the lanes
-        const uint32_t x = x0 + 4u * lane;
-        float4 y[4];
-        const auto fetch = [&](uint32_t j0) {
+    const uint32_t x = 4u * lane;                                    // (64 channels: half of the lanes)
+    float4 y[4];
+    const auto fetch = [&](uint32_t j0) {
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                y[j] = j0 + j < n && x < DP ? __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + row * DP + x)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        fetch(0);
-        float M = -INFINITY;
+        for (uint32_t j = 0; j < 4; ++j)
+            y[j] = j0 + j < n && x < DP ? __ldcg(reinterpret_cast<const float4 *>(part(j0 + j) + 2u * R + row * DP + x)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    fetch(0);
+    float M = -INFINITY;
 #pragma unroll 1
-        for (uint32_t j = lane; j < n; j += 32u) M = fmaxf(M, __ldcg(part(j) + row));
+    for (uint32_t j = lane; j < n; j += 32u) M = fmaxf(M, __ldcg(part(j) + row));
 #pragma unroll
-        for (uint32_t d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.0f, f = 0.0f;
+    for (uint32_t d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.0f, f = 0.0f;
 #pragma unroll 1
-        for (uint32_t j0 = 0; j0 < n; j0 += 4u) {
-            if ((j0 & 31u) == 0) {                                   // lane j: the weight of part j0 + j
-                f = 0.0f;
-                if (j0 + lane < n) {
-                    f = part_weight(__ldcg(part(j0 + lane) + row), M);
-                    L += f * __ldcg(part(j0 + lane) + R + row);
-                }
-            }
-            const float4 z[4] = {y[0], y[1], y[2], y[3]};
-            if (j0 + 4u < n) fetch(j0 + 4u);
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                const float w = __shfl_sync(~0u, f, (j0 + j) & 31u);
-                o.x += w * z[j].x, o.y += w * z[j].y, o.z += w * z[j].z, o.w += w * z[j].w;
+    for (uint32_t j0 = 0; j0 < n; j0 += 4u) {
+        if ((j0 & 31u) == 0) {                                   // lane j: the weight of part j0 + j
+            f = 0.0f;
+            if (j0 + lane < n) {
+                f = part_weight(__ldcg(part(j0 + lane) + row), M);
+                L += f * __ldcg(part(j0 + lane) + R + row);
             }
         }
+        const float4 z[4] = {y[0], y[1], y[2], y[3]};
+        if (j0 + 4u < n) fetch(j0 + 4u);
 #pragma unroll
-        for (uint32_t d = 16; d; d >>= 1) L += __shfl_xor_sync(~0u, L, d);
-        const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + head) : 1.0f) / L;
-        if (x < a.c.head_dim) {
-            uint2 b;
-            b.x = (uint32_t)bf16_bits(o.x * inv) | (uint32_t)bf16_bits(o.y * inv) << 16;
-            b.y = (uint32_t)bf16_bits(o.z * inv) | (uint32_t)bf16_bits(o.w * inv) << 16;
-            if (L == 0.0f) b = make_uint2(0u, 0u);
-            *reinterpret_cast<uint2 *>(out + x) = b;
+        for (uint32_t j = 0; j < 4; ++j) {
+            const float w = __shfl_sync(~0u, f, (j0 + j) & 31u);
+            o.x += w * z[j].x, o.y += w * z[j].y, o.z += w * z[j].z, o.w += w * z[j].w;
         }
-        if (a.lse && x == 0)
-            a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
+#pragma unroll
+    for (uint32_t d = 16; d; d >>= 1) L += __shfl_xor_sync(~0u, L, d);
+    const float inv = L == 0.0f ? 0.0f : (a.c.v_scale ? __ldg(a.c.v_scale + head) : 1.0f) / L;
+    if (x < a.c.head_dim) {
+        uint2 b;
+        b.x = (uint32_t)bf16_bits(o.x * inv) | (uint32_t)bf16_bits(o.y * inv) << 16;
+        b.y = (uint32_t)bf16_bits(o.z * inv) | (uint32_t)bf16_bits(o.w * inv) << 16;
+        if (L == 0.0f) b = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2 *>(out + x) = b;
+    }
+    if (a.lse && x == 0)
+        a.lse[(uint64_t)(q.row0 + node) * a.n_q_heads + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // skv_attend.cu

@@ -995,7 +995,7 @@ __device__ __forceinline__ void weight_role(const AttendArgs &a, const AttendWs 
                     part[kTcRows + row] = l;
                 }
                 if (threadIdx.x == 0 && w.tile == 0 && !whole)
-                    ws.desc[blockIdx.x] = Desc{1u, w.r, w.h, w.rt, w.at, w.at + (uint64_t)(w.tiles - 1) * w.weight};
+                    ws.desc[blockIdx.x] = Desc{1u, w.r, w.h, w.rt, w.at + (uint64_t)(w.tiles - 1) * w.weight};
             }
             tc_fence_before();
         }
