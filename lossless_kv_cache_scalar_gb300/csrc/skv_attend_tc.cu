@@ -131,7 +131,7 @@ struct TcShared {
     float m1[kTile], l1[kTile];                  // stream 1's maxima and sums, for the join
     uint32_t hurt[4];                            // part by part: a V value that is not finite was put to 0
     uint32_t tmem;
-    uint32_t gave_up;
+    uint32_t gave_up, stopped;                   // a wait ran out; no tensor copy is started any more
     Walk walk[2];                                // the weights' threads keep their registers for scores
 };
 
@@ -169,23 +169,28 @@ __device__ __forceinline__ bool bar_try(uint32_t at, uint32_t parity) {
 
 __device__ __forceinline__ bool bar_try(const void *b, uint32_t parity) { return bar_try(s32(b), parity); }
 
-__device__ __forceinline__ bool gave_up(const TcShared &sm) { return *reinterpret_cast<const volatile uint32_t *>(&sm.gave_up) != 0u; }
-
-// Waits for the phase of that parity, at most about two seconds. From the first wait that
-// runs out on, every wait of the CTA that is not over returns at once and the CTA runs to its
-// end on whatever it holds (all addresses stay in bounds), to report TIMEOUT. A barrier may then
-// say free or full where nothing is, so no copy is started any more (box_role), and the
-// copies and products that are on their way are waited for, again with a limit (bar_last).
-__device__ __forceinline__ void bar_wait(TcShared &sm, const void *b, uint32_t parity) {
-    if (bar_try(b, parity)) return;
+// Waits for the phase of that parity, at most about two seconds; false where it gave up. From
+// the first wait that runs out on, every wait of the CTA that is not over gives up at once, and
+// the CTA runs to its end on whatever it holds (all addresses stay in bounds), to report TIMEOUT.
+__device__ __forceinline__ bool bar_wait(TcShared &sm, const void *b, uint32_t parity) {
+    if (bar_try(b, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(b, parity)) {
-        if (gave_up(sm)) return;
+        if (*reinterpret_cast<volatile uint32_t *>(&sm.gave_up)) return false;
         if (clock64() - t0 > SKV_WAIT_CLOCKS) {
             *reinterpret_cast<volatile uint32_t *>(&sm.gave_up) = 1u;
-            return;
+            return false;
         }
     }
+    return true;
+}
+
+// For whoever gave up on a tile and is about to go on as if it had come: the place that it frees then may
+// still be on its way, and a barrier armed twice for copies in one phase is undefined. So
+// first, with a limit, no more copies are started.
+__device__ __forceinline__ void copies_stopped(const TcShared &sm) {
+    const long long t0 = clock64();
+    while (!*reinterpret_cast<const volatile uint32_t *>(&sm.stopped) && clock64() - t0 < 4000000000ll) {}
 }
 
 // For what is on its way itself, whether the CTA gave up or not.
@@ -565,12 +570,10 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
     using S = TcShape<DP, E>;
     const uint32_t lane = threadIdx.x & 31u, boxes = a.span / a.box;
     constexpr uint32_t kRaw = E ? S::raw : 1;
-    uint32_t pos = 0;
-    // lane i, of place i of the ring: barrier (its address) and phase (bit 0) of its last copies; uses of landed[i] in bf16
-    uint32_t last = 0u, turns = 0u;
-    bool stopped = false;
+    uint32_t pos = 0, filled = 0;                                    // tiles begun over all parts; tiles copied
+    bool ok = true;
     Walk w;
-    for (w.start(a, sh); !stopped && w.more(); w.next(a)) {
+    for (w.start(a, sh); ok && w.more(); w.next(a)) {
         const bool both = w.both();
         const uint32_t T = w.count(), p_end = min(w.q.len, w.tile_end * a.span);
         int32_t next_page = 0;
@@ -598,28 +601,22 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
             uint32_t dst;
             if (E) {
                 const uint32_t raw = n % kRaw;
-                bar_wait(sm, &sm.taken[raw], ((n / kRaw) & 1u) ^ 1u);
+                ok = bar_wait(sm, &sm.taken[raw], ((n / kRaw) & 1u) ^ 1u);
                 bar = &sm.landed[raw];
                 dst = raw_at + raw * S::raw_tile;
             } else {
-                bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
+                ok = bar_wait(sm, &sm.empty[slot], ((n / S::ring) & 1u) ^ 1u);
                 bar = is_v && p0 + a.span > w.q.ctx ? &sm.landed[slot] : &sm.full[slot];
                 dst = ring_at + slot * S::tile;
             }
-            // A place is free for certain only while nobody has given up: whoever gives up says so before it
-            // arrives anywhere. (A barrier armed twice for copies in one phase is undefined.)
-            __syncwarp();
-            stopped = __any_sync(~0u, gave_up(sm));
-            if (stopped) break;
-            if (lane == (E ? n % kRaw : slot)) {
-                const bool counted = !E && bar == &sm.landed[slot];
-                last = s32(bar) | (E ? (n / kRaw) & 1u : counted ? turns : (n / S::ring) & 1u);
-                if (counted) turns ^= 1u;
-            }
             const uint32_t live = min(boxes, (p_end - p0 + a.box - 1) / a.box);
-            if (lane == 0)
+            if (lane == 0 && ok)                                     // (at worst armed and then left alone)
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(s32(bar)), "r"(live * a.box * DP * (E ? 1u : 2u)) : "memory");
-            __syncwarp();
+            ok = __all_sync(~0u, ok);
+            if (!ok) {
+                filled = n;
+                break;
+            }
             if (lane < live) {
                 const int32_t page = sm.pages[k & 3u][lane];
                 const uint32_t p = p0 + lane * a.box, token = p - div_by(p, a.c.page) * a.c.page.d;
@@ -638,8 +635,13 @@ __device__ __forceinline__ void box_role(const AttendArgs &a, const Share &sh, T
         }
         pos += 2 * T;
     }
-    // No copy is on its way into this CTA's shared memory when the roles meet at the end.
-    if (last) bar_last(last & ~1u, last & 1u);
+    if (ok) filled = pos;
+    __syncwarp();
+    if (lane == 0) *reinterpret_cast<volatile uint32_t *>(&sm.stopped) = 1u;
+    // No copy is on its way into this CTA's shared memory when the roles meet at the end: lane i waits for the
+    // last of the tiles that went to place i (in bf16 a V tile with drafted positions is full only once it has landed).
+    constexpr uint32_t places = E ? kRaw : S::ring;
+    if (lane < places && lane < filled) bar_last(s32(E ? &sm.landed[lane] : &sm.full[lane]), ((filled - 1u - lane) / places) & 1u);
     __syncwarp();
 }
 
@@ -652,6 +654,7 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
     const uint32_t t = threadIdx.x - 256u;
     const uint32_t block = block_of<DP, E>(a), group = group_of(a);
     uint32_t pos = 0, turns = 0;                                     // turns: parity of landed[] by slot (bf16)
+    bool good = true;                                                // (bf16) no tile was given up
     Walk w;
     for (w.start(a, sh); w.more(); w.next(a)) {
         const bool both = w.both();
@@ -665,7 +668,7 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
             const uint32_t first = w.q.ctx > p0 ? w.q.ctx - p0 : 0u, last = min(a.span, p_end - p0);     // drafted rows [first, last)
             bool found = false;
             if (!E) {
-                bar_wait(sm, &sm.landed[slot], (turns >> slot) & 1u);
+                if (!bar_wait(sm, &sm.landed[slot], (turns >> slot) & 1u)) good = false;
                 turns ^= 1u << slot;
                 constexpr uint32_t CH = DP / 8;
                 for (uint32_t x = first * CH + t; x < kTile * CH; x += 128u) {
@@ -685,7 +688,7 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
             } else {
                 constexpr uint32_t kRaw = E ? S::raw : 1;
                 const uint32_t raw = n % kRaw;
-                bar_wait(sm, &sm.landed[raw], (n / kRaw) & 1u);
+                if (!bar_wait(sm, &sm.landed[raw], (n / kRaw) & 1u)) copies_stopped(sm);
                 __syncwarp();
                 // Thread: 16 codes of channels 16 ch .. of every (128 / CH)th row. The eight bytes that go first
                 // differ between the two 64-channel blocks, so that eight lanes' stores lie on different banks.
@@ -727,7 +730,7 @@ __device__ __forceinline__ void finish_role(const AttendArgs &a, const Share &sh
                 warp_arrive(&sm.full[slot]);
             } else {
                 asm volatile("bar.sync 2, 128;" ::: "memory");
-                if (t == 0) bar_arrive(&sm.full[slot]);
+                if (t == 0 && good) bar_arrive(&sm.full[slot]);
             }
         }
         pos += 2 * T;
@@ -756,7 +759,7 @@ __device__ __forceinline__ void product_role(const AttendArgs &a, const Share &s
         uint32_t k_slot = 0, v_slot = 0;
         const auto take = [&](uint32_t &slot) {
             slot = pos % S::ring;
-            bar_wait(sm, &sm.full[slot], (pos / S::ring) & 1u);
+            if (!bar_wait(sm, &sm.full[slot], (pos / S::ring) & 1u)) copies_stopped(sm);
             ++pos;
         };
         const auto scores = [&](uint32_t j) {
@@ -1036,6 +1039,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_large(const AttendArgs a
         bar_init(&sm.drain, 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.gave_up = 0u;
+        sm.stopped = a.box ? 0u : 1u;
     }
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s32(&sm.tmem)) : "memory");
