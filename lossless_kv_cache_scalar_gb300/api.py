@@ -99,6 +99,14 @@ def _stream_handle(stream: torch.cuda.Stream | None):
     return C.c_void_p(s.cuda_stream)
 
 
+def _after_current(stream: torch.cuda.Stream | None):
+    """For a call on `stream` that makes its result itself: the memory, and the zeros in it, are the
+    current stream's, so what that stream has been given comes first. (The result then belongs to
+    the current stream, where the caller uses and frees it.)"""
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream(stream.device))
+
+
 def _check_model_inputs(lay: Layout, sigma: torch.Tensor, counts: torch.Tensor | None):
     """sigma and counts must be device tensors of the layout's sizes (the C ABI
     takes bare pointers, so a short table would be read past its end)."""
@@ -313,8 +321,8 @@ class Coder:
 
     def decode_chunks(self, bitstream, offsets, mu, sigma, counts, chunk_ids, stream=None):
         lay = self.layout
-        with torch.cuda.stream(stream):                  # zeros before the call's writes, on its own stream
-            pages = torch.zeros((chunk_ids.numel(), lay.page_elems), dtype=mu.dtype, device=mu.device)
+        pages = torch.zeros((chunk_ids.numel(), lay.page_elems), dtype=mu.dtype, device=mu.device)
+        _after_current(stream)
         self.decode_chunks_into(bitstream, offsets, mu, sigma, counts, chunk_ids, pages, stream)
         self.check_status("skv_decode_chunks", stream)
         return pages

@@ -5,7 +5,9 @@ As in api.py, PyTorch only provides device memory and streams. The `_into`
 calls enqueue on the current (or given) stream and return without
 synchronising; check_status() waits and raises what the device reported. The
 calls of one object share its status word and workspace, so they must not run
-at once on different streams.
+at once on different streams. A call that makes its result itself (step, attend)
+comes after what the current stream has been given, and the result is the
+current stream's.
 """
 from __future__ import annotations
 
@@ -15,7 +17,7 @@ import math
 import torch
 
 from . import _binding as B
-from .api import _check_dev, _ptr
+from .api import _after_current, _check_dev, _ptr
 
 
 def _stream_of(stream, device: int) -> int:
@@ -48,6 +50,14 @@ def _table_rows(t):
             or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError("block_table must be an int32 CUDA tensor [n_requests][max_pages] with whole rows")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _capturing(stream) -> bool:
+    """Whether `stream` (None: the current one) or the current stream is being captured."""
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 class _Status:
@@ -117,11 +127,11 @@ class PagePool(PageTable):
         (cu_new, slots), slots past the step's tokens -1. Not for a capture, whose replays would
         all start from the same counts: capture map_into, and copy its counts back behind it."""
         dev = self.block_table.device
-        with torch.cuda.stream(stream):                  # memory that this stream has done with
-            if torch.cuda.is_current_stream_capturing():
-                raise ValueError("PagePool.step swaps its counts on the host; capture map_into")
-            cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
-            slots = torch.empty(max_new, dtype=torch.int64, device=dev)
+        if _capturing(stream):
+            raise ValueError("PagePool.step swaps its counts on the host; capture map_into")
+        cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty(max_new, dtype=torch.int64, device=dev)
+        _after_current(stream)
         self.map_into(ctx_len, new_len, self.n_pages, self.free_pages, self.free_state, cu, slots, *self._next,
                       stream=stream)
         now = (self.n_pages, self.free_state)
@@ -129,6 +139,9 @@ class PagePool(PageTable):
         self._next = now
         if check:
             self.check_status("skv_page_map", stream)
+        elif stream is not None:                         # given up early, they are not handed out early
+            cu.record_stream(stream)
+            slots.record_stream(stream)
         return cu, slots
 
 
@@ -185,9 +198,9 @@ class PagedKV(_Status):
         v = C.c_uint64()
         B.check("skv_tree_attention_workspace_bytes",
                 B.lib().skv_tree_attention_workspace_bytes(self._ref, q_heads, C.byref(v)))
-        with torch.cuda.stream(stream):
-            self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
-            self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
+        self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.k_pages.device)
+        self.workspace[:B.SKV_ATTENTION_ZERO_BYTES].zero_()
+        _after_current(stream)
         self._workspace, self._workspace_bytes = self.workspace.data_ptr(), v.value
 
     def append_into(self, k, v, slots, rows=None, stream=None):
@@ -242,9 +255,7 @@ class PagedKV(_Status):
             _check_words("lse", _F32, n * heads, dev, lse)
             lse = lse.data_ptr()
         if self.workspace is None:
-            with torch.cuda.stream(stream):
-                capturing = torch.cuda.is_current_stream_capturing()
-            if capturing:
+            if _capturing(stream):
                 raise ValueError("give PagedKV its q_heads before a capture")
             self._make_workspace(heads, stream)
         rc = B.lib().skv_tree_attention(
@@ -256,8 +267,8 @@ class PagedKV(_Status):
     def attend(self, q, ctx_len, cu_new, mask=None, max_nodes: int | None = None, scale: float | None = None,
                stream=None):
         """attend_into a new tensor (rows outside every request 0), waited for and checked."""
-        with torch.cuda.stream(stream):                  # zeros before the call's writes, on its own stream
-            out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+        _after_current(stream)
         self.attend_into(q, ctx_len, cu_new, out, mask, max_nodes, scale, stream=stream)
         self.check_status("skv_tree_attention", stream)
         return out

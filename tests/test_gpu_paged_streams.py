@@ -206,3 +206,49 @@ def test_append_on_a_given_stream():
     torch.cuda.synchronize()
     assert int(cache.status.item()) == 1
     assert torch.equal(k.view(-1, 2, 64)[slots[:8]], new[:8])
+
+
+def test_results_may_be_used_on_the_current_stream():
+    """What a call on another stream returned is read on the current one and given up there: the
+    next call on the other stream takes no memory that is still read."""
+    s = case(1, "bf16")
+    cache, side = cache_of(s, q_heads=8), torch.cuda.Stream()
+    args = (s["ctx"], s["cu"], s["mask"])
+    want = cache.attend(s["q"], *args, max_nodes=1, stream=side).clone()
+    pool, ctx, new = PagePool(2, 4, 16, 8), i32([0, 0]), i32([20, 5])
+    cfg = synth.CONFIGS["tiny"].scaled(n_tokens=600)
+    w = {k: v.cuda() for k, v in synth.generate(cfg).items()}
+    coder = Coder(Layout("bf16", cfg.n_layers, cfg.n_kv, cfg.n_heads, cfg.head_dim, 600, tokens_per_chunk=256))
+    bits, offs = coder.encode(w["kv"], w["mu"], w["sigma"], w["counts"])
+    ids, others = i32([2, 0, 1]), i32([0, 1, 2])
+    pages = coder.decode_chunks(bits, offs, w["mu"], w["sigma"], w["counts"], ids).clone()
+    turned = -s["q"]
+    torch.cuda.synchronize()
+
+    out = cache.attend(s["q"], *args, max_nodes=1, stream=side)
+    cu, slots = pool.step(ctx, new, 32, stream=side)
+    got = coder.decode_chunks(bits, offs, w["mu"], w["sigma"], w["counts"], ids, stream=side)
+    busy()
+    read = [t.clone() for t in (out, cu, slots, got)]
+    del out, cu, slots, got
+    later = [cache.attend(turned, *args, max_nodes=1, stream=side), pool.step(i32([20, 5]), i32([1, 9]), 32, stream=side),
+             coder.decode_chunks(bits, offs, w["mu"], w["sigma"], w["counts"], others, stream=side)]
+    torch.cuda.synchronize()
+    assert torch.equal(read[0], want) and torch.equal(read[3], pages)
+    assert read[1].tolist() == [0, 20, 25]
+    assert read[2].tolist() == list(range(20)) + list(range(32, 37)) + [-1] * 7
+    del later
+
+
+def test_pool_step_without_a_check_keeps_its_results():
+    """A step that is not waited for: its results, given up at once, are not handed out while it writes."""
+    pool, side = PagePool(2, 4, 16, 8), torch.cuda.Stream()
+    ctx, new = i32([0, 0]), i32([20, 5])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy()
+    pool.step(ctx, new, 32, check=False, stream=side)
+    later = [torch.full((n,), 77, dtype=t, device="cuda") for n, t in ((32, torch.int64), (3, torch.int32)) for _ in range(4)]
+    torch.cuda.synchronize()
+    for t in later:
+        assert (t == 77).all()
