@@ -9,11 +9,13 @@
 // both only read in this call, and the CTA that holds the first token of a new
 // page writes that page's table entry. The ring's pushes go behind its end, where
 // nothing is read. On the device a step of 8 requests takes 3 to 4 us (launch, two barriers
-// and code fetched once) and one of 2,000 requests with 2.0 M tokens in a map of 4.0 M slots 18.5 us
-// (8 of them launch and reductions; the 32 MB of slots alone are 5 us of HBM).
+// and code fetched once) and one of 2,000 requests with 1.75 M tokens in a map of 4.0 M slots 18.5 us:
+// with a token each it takes 12.4 in a map of 0.6 M slots (152 CTAs, each with all lengths and sums) and
+// 16.4 in the large one (32 MB of slots, 5 us of HBM); the rest are the tokens' searches.
 //
 // append: each K and V row moves once, 16 bytes per thread and step; bound by HBM: 65,536 bf16 rows of
-// 8 x 128 channels take 90 us (5.95 TB/s, 0.89 of a copy), 8 rows 2 us.
+// 8 x 128 channels take 90 us (5.95 TB/s, 0.89 of a copy), 8 rows 2 us. Into e4m3 the same rows take 120 us
+// against 60 of HBM: bound by issue, some 24 instructions per code for the exact quotient.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
