@@ -312,8 +312,8 @@ def _prepare_compact(case, seed):
             m = min(have[i], have[i - 1]) // 2
             table[i, :m] = table[i - 1, :m]
     s = dict(page=page, pool=pool, k=_pool(pool, case, gen), v=_pool(pool, case, gen), table=_i32(table), have=_i32(have),
-             free=_i32([-1] * pool), table_out=_i32(torch.full((b, width), -1)), state_out=_i32([0, 0]), src=_i32([0] * used),
-             dst=_i32([0] * used))
+             free=_i32([-1] * pool), state=_i32([0, 0]), table_out=_i32(torch.full((b, width), -1)), state_out=_i32([0, 0]),
+             src=_i32([0] * used), dst=_i32([0] * used))
     if own:
         from lossless_kv_cache_scalar_gb300 import PagedKV, PageTable
         s["pages"], s["cache"] = PageTable(s["table"], page, pool, workspace=True), PagedKV(s["k"], s["v"])
@@ -548,7 +548,7 @@ def _own_pass(s):
                              s["state_out"], s["src"], s["dst"], s["count"])
         s["cache"].copy_into(s["src"], s["dst"], tokens=s["count"])
     else:
-        s["pages"].compact_into(s["have"], s["free"], s["table_out"], s["state_out"], s["src"], s["dst"])
+        s["pages"].compact_into(s["have"], s["free"], s["state"], s["table_out"], s["state_out"], s["src"], s["dst"])
         s["cache"].copy_into(s["src"], s["dst"])
 
 
