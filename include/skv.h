@@ -644,6 +644,185 @@ int32_t skv_tree_attention(const skv_paged *cache, const void *q, uint64_t q_row
                            uint32_t mask_words, uint32_t max_nodes, float scale, void *out, float *lse,
                            int32_t *status, void *workspace, uint64_t ws_bytes, void *stream);
 
+/*
+ * Heads of queries and keys normalised and rotated by their positions, keys and
+ * values into the pages, in one pass over a projection's rows. For row i:
+ *     n = x / sqrt(mean over the head's channels of x^2 + eps) * w   (x where w is NULL)
+ * for the query heads with w = q_norm, for the key heads with k_norm; then, for the pair
+ * (a, b) of frequency j < rot_dim / 2,
+ *     (a cos t - b sin t, a sin t + b cos t) * amplitude,  t = position * frequency_j
+ * where the position is positions[axis_j][i]. Pairs are the channels (j, j + rot_dim / 2), or
+ * (2 j, 2 j + 1) if interleaved; channels from rot_dim on are not rotated. The queries go to
+ * q_out; keys and the unchanged values go to token slots[i] of the cache as
+ * skv_cache_append writes its rows, an e4m3 cache's codes straight from the binary32 results.
+ * Rows with slots[i] < 0 only have queries.
+ *
+ * skv_rotary:
+ *  head_dim   that of the cache
+ *  rot_dim    channels that are rotated: a multiple of 16, 0 to head_dim
+ *  n_axes     1 to 16 axes of positions (text has one; images and video have time, height
+ *             and width)
+ *  turns      device uint64[rot_dim / 2]: frequency_j / (2 pi) in units of 2^-64 of a
+ *             turn, modulo 1: a position's angle is one product modulo 2^64, exact to
+ *             2^-44 of a turn up to positions of 2^20
+ *  axis       device uint8[rot_dim / 2], each below n_axes, or NULL (all 0)
+ *  q_norm, k_norm  device float32[head_dim], 16-byte aligned, or NULL
+ * skv_rotate_append:
+ *  q          device bf16 [n][n_q_heads][head_dim], head_dim contiguous, 16-byte aligned; strides
+ *             in elements, multiples of 8. NULL with n_q_heads 0: no queries
+ *  k, v       as for skv_cache_append
+ *  positions  device int32 [n_axes][n], of any sign
+ *  slots      device int64[n], distinct where >= 0
+ *  q_out      device bf16 [n][n_q_heads][head_dim], contiguous, 16-byte aligned (q itself
+ *             where q is contiguous)
+ * Everything is binary32 and rounded once, at the end. Device errors: INVALID_ARG for
+ * a slot beyond the pool (that row's keys and values are skipped). An axis from n_axes on
+ * counts as axis 0.
+ */
+typedef struct skv_rotary {
+    uint32_t version;        /* SKV_FORMAT_VERSION */
+    uint32_t head_dim;
+    uint32_t rot_dim;
+    uint32_t n_axes;
+    uint32_t interleaved;
+    float eps;
+    float amplitude;
+    const uint64_t *turns;
+    const uint8_t *axis;
+    const float *q_norm;
+    const float *k_norm;
+} skv_rotary;
+
+int32_t skv_rotary_check(const skv_rotary *rotary);
+int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *rotary, const void *q, uint64_t q_row_stride,
+                          uint64_t q_head_stride, uint32_t n_q_heads, const void *k, const void *v, uint64_t row_stride,
+                          uint64_t row_head_stride, const int32_t *positions, const int64_t *slots, uint32_t n, void *q_out,
+                          int32_t *status, void *stream);
+
+/*
+ * Verification of drafted trees against the target's probabilities, with given
+ * random numbers: the tokens that come out are distributed as the target's own. Request r
+ * has the rows cu_new[r] .. cu_new[r + 1), one per node of its tree: node 0 is the last
+ * token that is certain, parents[row] (a node number below the node's own) is a
+ * node's parent, tokens[row] its drafted token, and row's probabilities are the target's
+ * for what follows the node. The walk starts at node 0. At a node with target row p and draft
+ * row q, its children are tried in order, each with its own u = uniform[row of the child]; with
+ * c = 0, Z = 1, s = 1 before the first, R(y) = max(p(y) - c q(y), 0):
+ *     child x is accepted, and the walk goes on from it, iff  u q(x) Z < R(x) s
+ *     else  c := c + Z / s,  Z := sum over y of R(y) (with the new c),  s := s - q(x) if distinct
+ * (what is left of the target after a rejection, not divided by its sum). Without draft
+ * probabilities (a draft's best tokens) child x is accepted iff u Z < p(x), else Z := Z - p(x) and
+ * p(x) := 0. When no child is left, the next token is the first y with
+ *     sum over y' <= y of R(y')  >  floor(uniform[row of node 0] * sum over all y' of R(y'))
+ * One node is a request without drafted tokens: its token is drawn from its row.
+ *  dtype         SKV_PROB_F32 or SKV_PROB_BF16, of both kinds of probabilities
+ *  probs         device [n_rows][vocab], vocab contiguous, stride in elements (at least vocab)
+ *  draft_probs   the same for the draft, each node's row the one its children were drawn
+ *                from; or NULL
+ *  distinct      1: siblings were drawn without replacement (each after the first from what is
+ *                left of q), 0: independently (two siblings may be the same token)
+ *  vocab         1 to 2^19
+ *  tokens        device int32[n_rows], in [0, vocab) (node 0's is not looked at)
+ *  parents       device int32[n_rows] (node 0's is not looked at), or NULL: every request is a chain
+ *  uniform       device float32[n_rows], in [0, 1)
+ *  accepted      device int32[n_requests]: nodes of the accepted path, node 0 among them;
+ *                0 for a request without rows
+ *  rows          device int32[n_rows]: at cu_new[r] + i the row of the i-th node of the path,
+ *                -1 behind the path
+ *  next          device int32[n_requests]: the next token; -1 without rows, or where p has no weight
+ *  slots, kept   device int64[n_rows], both or neither (NULL): kept is slots where rows is not
+ *                -1, else -1: the places that the path's rows move to (skv_cache_move, or
+ *                skv_cache_append with rows)
+ *  ctx_len, ctx_out  device int32[n_requests], both or neither: ctx_out = ctx_len + accepted
+ * Entries of rows and kept outside every request are left alone. Probabilities outside [0, 1] count as the
+ * nearer end, NaN as 0; where R has no weight left the token is drawn from p. R is
+ * binary32 and summed as whole numbers of 2^-44 (each R rounded to one), Z, s and the test's two
+ * products are binary64, c is binary32: the result does not depend on the order of anything.
+ * Device errors: INVALID_ARG for a request whose cu_new descends or passes n_rows, with a token or parent
+ * outside its range, or with more than 4,096 nodes and no draft probabilities: its accepted is 0, next -1, ctx_out = ctx_len, and its rows and kept -1 if cu_new is in order.
+ */
+enum { SKV_PROB_F32 = 0, SKV_PROB_BF16 = 1 };
+int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t probs_stride, const void *draft_probs,
+                        uint64_t draft_stride, uint32_t vocab, uint32_t distinct, uint32_t n_rows, uint32_t n_requests,
+                        const int32_t *cu_new, const int32_t *tokens, const int32_t *parents, const float *uniform,
+                        const int64_t *slots, const int32_t *ctx_len, int32_t *accepted, int32_t *rows, int64_t *kept,
+                        int32_t *ctx_out, int32_t *next, int32_t *status, void *stream);
+
+/*
+ * Move accepted tokens together: for each request, for i = cu_new[r] .. cu_new[r + 1) - 1 one after
+ * the other, with kept[i] >= 0: the K and V of token slots[rows[i]] become those of token
+ * kept[i], as they lie (codes and bits). With rows and kept of skv_tree_verify the accepted
+ * path comes to lie in order behind the context. Slots of one request must not be those of another.
+ *  rows, slots, kept  device int32, int64, int64 [n_rows]
+ * Device errors: INVALID_ARG for a slot outside the pool, a row outside [0, n_rows) (such entries
+ * are skipped), or cu_new that descends or passes n_rows (such requests are skipped).
+ */
+int32_t skv_cache_move(const skv_paged *cache, uint32_t n_requests, const int32_t *cu_new, uint32_t n_rows,
+                       const int32_t *rows, const int64_t *slots, const int64_t *kept, int32_t *status, void *stream);
+
+/*
+ * Requests that go on from other requests' tokens (samples of one prompt, beams, ends): row s
+ * of the new block table goes on from row parents[s] of the old one (s: from itself; -1, or a row
+ * with ctx_len < 0: it is empty; parents NULL: every row from itself). Of the rows that go on from row r, one is its heir: r itself if it is among
+ * them, else the lowest. The heir keeps all of r's pages (with trim: those that ctx_len[r] tokens
+ * need); each other one shares the pages that r's tokens fill whole and, where the last page is begun,
+ * takes a page off the ring for a copy of it. Pages that no row holds any more go behind the
+ * ring's end, in ascending order (usable from the next call on).
+ *   ctx_out[s] = ctx_len[parents[s]], -1 for an empty row; n_pages_out[s] its pages; the first
+ *   n_pages_out[s] entries of row s of table_out are written
+ *   copy_src[s], copy_dst[s], copy_tokens[s]: the copy that row s needs (for skv_cache_copy, on
+ *   each layer's pools); -1, -1, 0 if none. Pages are taken in order of s
+ * Sharing rows may be forked, trimmed and ended again by this call at will. skv_page_map gives the pages of
+ * an ended request back whoever else holds them: end requests that may share pages by this call. Tokens
+ * that are added to a row fall into no page of another one, as long as its ctx_len does not go back below
+ * what it was when its pages were shared.
+ *  n_pages_in, ring   as for skv_page_map; table_out, n_pages_out, ctx_out, free_out and the copies are other
+ *                     arrays than the inputs
+ *  workspace          device, 16-byte aligned, skv_page_workspace_bytes(n_requests, pool_pages) bytes; any content
+ * Device errors, with table_out, n_pages_out, ctx_out, free_out = the inputs, copies -1, the ring untouched:
+ *   INVALID_ARG  a parent outside [-1, n_requests), a page count outside [0, max_pages] or short of ctx_len, a ring
+ *                head outside [0, free_capacity) or count outside [0, free_capacity]
+ *   CAPACITY     not enough free pages, or a ring too short for those that come free
+ * CORRUPT: a page number outside [0, pool_pages) in a row or taken off the ring; it is handed on as it is, its
+ * copy is left out.
+ */
+int32_t skv_page_workspace_bytes(uint32_t n_requests, uint32_t pool_pages, uint64_t *bytes);
+int32_t skv_page_fork(uint32_t page_tokens, uint32_t pool_pages, uint32_t n_requests, const int32_t *parents,
+                      const int32_t *ctx_len, const int32_t *block_table, uint64_t table_stride, uint32_t max_pages,
+                      const int32_t *n_pages_in, uint32_t trim, int32_t *table_out, uint64_t table_out_stride,
+                      int32_t *n_pages_out, int32_t *ctx_out, int32_t *free_pages, uint32_t free_capacity,
+                      const int32_t *free_in, int32_t *free_out, int32_t *copy_src, int32_t *copy_dst,
+                      int32_t *copy_tokens, int32_t *status, void *workspace, uint64_t ws_bytes, void *stream);
+
+/*
+ * Move the pages that rows hold to the front of the pool. With L the number of different
+ * pages held, the k-th held page from L on (ascending) takes the place of the k-th page below L that no row
+ * holds; table_out is the table with the new numbers (first n_pages[r] entries of each row), the ring becomes
+ * the pages L .. pool_pages - 1 in order, head 0 (pages that neither a row nor the old ring
+ * held are free again). copy_src[k], copy_dst[k]: the k-th move, -1 behind the last (for
+ * skv_cache_copy: no destination is a source).
+ *  copy_capacity  entries of copy_src and copy_dst
+ * Device errors, with table_out and free_out = the inputs, copies -1, the ring untouched: INVALID_ARG (a page
+ * count outside [0, max_pages]), CAPACITY (more moves than copy_capacity, more than free_capacity pages
+ * free). CORRUPT: a page number outside the pool in a row, handed on as it is.
+ */
+int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, const int32_t *block_table, uint64_t table_stride,
+                         uint32_t max_pages, const int32_t *n_pages, int32_t *table_out, uint64_t table_out_stride,
+                         int32_t *free_pages, uint32_t free_capacity, const int32_t *free_in, int32_t *free_out,
+                         int32_t *copy_src, int32_t *copy_dst, uint32_t copy_capacity, int32_t *status, void *workspace,
+                         uint64_t ws_bytes, void *stream);
+
+/*
+ * Copy pages: for i < n with src[i] >= 0, the first tokens[i] tokens (all if tokens is
+ * NULL) of K and V page src[i] to page dst[i] (pages of less than 2^31 - 1,024 units of 16 bytes). The
+ * destinations are distinct, and none of them a source.
+ *  src, dst, tokens  device int32[n]
+ * Device errors: INVALID_ARG for a page outside the pool or tokens outside [0, page_tokens] (such
+ * entries are skipped).
+ */
+int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, const int32_t *dst, const int32_t *tokens, uint32_t n,
+                       int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

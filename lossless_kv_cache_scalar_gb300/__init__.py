@@ -7,6 +7,7 @@ from ._binding import SKVError, SKV_BF16, SKV_E4M3, STATUS_NAMES, lib  # noqa: F
 from .api import (Coder, HostCoder, Layout, calibrate_sigma, cdf_eval, decode,  # noqa: F401
                   decode_chunks, encode, histogram, requantize)
 from .paged import PagedKV, PagePool, PageTable  # noqa: F401
+from .serve import Rotary, Verifier  # noqa: F401
 
-__all__ = ["Coder", "HostCoder", "Layout", "PagePool", "PageTable", "PagedKV", "SKVError", "calibrate_sigma", "cdf_eval", "decode",
+__all__ = ["Coder", "HostCoder", "Layout", "PagePool", "PageTable", "PagedKV", "Rotary", "SKVError", "Verifier", "calibrate_sigma", "cdf_eval", "decode",
            "decode_chunks", "encode", "histogram", "lib", "requantize"]

@@ -13,6 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libskv.so")
 
 SKV_BF16, SKV_E4M3 = 0, 1
+SKV_PROB_F32, SKV_PROB_BF16 = 0, 1
 SKV_FORMAT_VERSION = 1
 SKV_ATTENTION_ZERO_BYTES = 2048
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "CUDA", 3: "NONFINITE_MU", 4: "BAD_SIGMA",
@@ -37,10 +38,17 @@ class skv_paged(C.Structure):
                 ("n_requests", C.c_uint32), ("max_pages", C.c_uint32)]
 
 
+class skv_rotary(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("head_dim", C.c_uint32), ("rot_dim", C.c_uint32), ("n_axes", C.c_uint32),
+                ("interleaved", C.c_uint32), ("eps", C.c_float), ("amplitude", C.c_float), ("turns", C.c_void_p),
+                ("axis", C.c_void_p), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p)]
+
+
 # name -> (restype, argtypes); the exported symbols of include/skv.h
 _u32, _u64, _i32, _vp = C.c_uint32, C.c_uint64, C.c_int32, C.c_void_p
 _LP = C.POINTER(skv_layout)
 _PP = C.POINTER(skv_paged)
+_RP = C.POINTER(skv_rotary)
 SIGNATURES = {
     "skv_version": (_u32, []),
     "skv_status_string": (C.c_char_p, [_i32]),
@@ -78,6 +86,17 @@ SIGNATURES = {
     "skv_tree_attention_workspace_bytes": (_i32, [_PP, _u32, C.POINTER(_u64)]),
     "skv_tree_attention": (_i32, [_PP, _vp, _u64, _u64, _u32, _u32, _vp, _vp, _vp, _u32, _u32, C.c_float, _vp, _vp,
                                   _vp, _vp, _u64, _vp]),
+    "skv_rotary_check": (_i32, [_RP]),
+    "skv_rotate_append": (_i32, [_PP, _RP, _vp, _u64, _u64, _u32, _vp, _vp, _u64, _u64, _vp, _vp, _u32, _vp, _vp, _vp]),
+    "skv_tree_verify": (_i32, [_u32, _vp, _u64, _vp, _u64, _u32, _u32, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _vp, _vp, _vp, _vp, _vp]),
+    "skv_cache_move": (_i32, [_PP, _u32, _vp, _u32, _vp, _vp, _vp, _vp, _vp]),
+    "skv_page_workspace_bytes": (_i32, [_u32, _u32, C.POINTER(_u64)]),
+    "skv_page_fork": (_i32, [_u32, _u32, _u32, _vp, _vp, _vp, _u64, _u32, _vp, _u32, _vp, _u64, _vp, _vp, _vp, _u32, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _vp, _u64, _vp]),
+    "skv_page_compact": (_i32, [_u32, _u32, _vp, _u64, _u32, _vp, _vp, _u64, _vp, _u32, _vp, _vp, _vp, _vp, _u32, _vp, _vp,
+                                _u64, _vp]),
+    "skv_cache_copy": (_i32, [_PP, _vp, _vp, _vp, _u32, _vp, _vp]),
 }
 
 _lib = None

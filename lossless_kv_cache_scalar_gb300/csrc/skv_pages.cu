@@ -1,0 +1,725 @@
+// skv_pages.cu -- pages of a paged cache shared, moved and copied: fork, compact, copy, move.
+//
+// fork and compact plan on block tables alone: one cluster of CTAs walks the tables with a bit per page of the
+// pool in the workspace. A page comes free iff its bit, set for every page that some row held, is not cleared for the
+// rows that go on; no count per page is kept between calls that could drift from the tables. Between its
+// steps the cluster passes a barrier (some hundred nanoseconds, where a launch costs microseconds).
+// Everything comes out in a fixed order: prefix sums over rows and over the words of bits.
+//
+// copy and move bring the K and V: 16 bytes per thread and step, bound by HBM.
+#include <cooperative_groups.h>
+
+#include "skv_rows.cuh"
+
+namespace skv {
+
+namespace cg = cooperative_groups;
+
+constexpr uint32_t kPlanThreads = 512, kPlanWarps = kPlanThreads / 32u, kPlanCluster = 8;
+
+struct PlanArgs {
+    FastDiv page;
+    uint32_t pool_pages, n_requests, max_pages, free_capacity, trim, capacity;
+    const int32_t *parents, *ctx_len, *table, *n_in, *free_in;
+    uint64_t table_stride, out_stride;
+    int32_t *table_out, *n_out, *ctx_out, *free_pages, *free_out, *src, *dst, *count, *status;
+    uint32_t *bits;                     // workspace: a bit per page
+    uint32_t *words;                    // fork: the heir of each row; compact: rank of a far page, then the holes
+};
+
+// What the CTAs of the cluster tell each other: a word each, in every CTA's shared memory.
+struct Told {
+    uint32_t word[2][kPlanCluster];
+};
+
+struct Team {
+    uint32_t C, rank, parity;
+    Told *told;
+
+    // Every thread calls; w is thread 0's. All writes of the cluster before it are seen after it.
+    __device__ __forceinline__ const uint32_t *tell(uint32_t w) {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (threadIdx.x == 0)
+            for (uint32_t j = 0; j < C; ++j) *cluster.map_shared_rank(&told->word[parity][rank], j) = w;
+        __threadfence();
+        cluster.sync();
+        const uint32_t *all = told->word[parity];
+        parity ^= 1u;
+        return all;
+    }
+    __device__ __forceinline__ uint32_t any(uint32_t w) {
+        const uint32_t *all = tell(w);
+        uint32_t x = 0;
+        for (uint32_t j = 0; j < C; ++j) x |= all[j];
+        return x;
+    }
+    // The sum of the CTAs' words, and of those before this one.
+    __device__ __forceinline__ uint32_t sum(uint32_t w, uint32_t *before) {
+        const uint32_t *all = tell(w);
+        uint32_t x = 0;
+        *before = 0;
+        for (uint32_t j = 0; j < C; ++j) {
+            if (j == rank) *before = x;
+            x += all[j];
+        }
+        return x;
+    }
+};
+
+// Exclusive prefix sum over the block, and the total. part: a word per warp.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *total, uint32_t *part) {
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, in = x;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    const uint32_t p = lane < kPlanWarps ? part[lane] : 0u;
+    *total = __reduce_add_sync(~0u, p);
+    return x - in + __reduce_add_sync(~0u, lane < warp ? p : 0u);
+}
+
+__device__ __forceinline__ uint32_t *bit_word(const PlanArgs &a, uint32_t page) { return a.bits + (page >> 5); }
+
+// Sets the bit of every page that a row holds; whether all of them lie in the pool.
+__device__ __forceinline__ bool mark_rows(const PlanArgs &a, const Team &t) {
+    const uint32_t lane = threadIdx.x & 31u;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t r = t.rank * kPlanWarps + (threadIdx.x >> 5); r < a.n_requests; r += t.C * kPlanWarps) {
+        const uint32_t n = (uint32_t)__ldg(a.n_in + r);
+        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < n; j += 32u) {
+            const uint32_t p = (uint32_t)__ldg(row + j);
+            if (p < a.pool_pages) atomicOr(bit_word(a, p), 1u << (p & 31u));
+            else ok = false;
+        }
+    }
+    return ok;
+}
+
+__device__ __forceinline__ void clear_bits(const PlanArgs &a, const Team &t) {
+    const uint32_t n = (a.pool_pages + 31u) >> 5;
+    for (uint32_t i = t.rank * kPlanThreads + threadIdx.x; i < n; i += t.C * kPlanThreads) a.bits[i] = 0u;
+}
+
+// Words of bits of this CTA and, in them, of this thread: runs in order.
+__device__ __forceinline__ void run_of(const PlanArgs &a, const Team &t, uint32_t *from, uint32_t *to) {
+    const uint32_t n = (a.pool_pages + 31u) >> 5, each = (n + t.C * kPlanThreads - 1u) / (t.C * kPlanThreads);
+    const uint64_t at = (uint64_t)(t.rank * kPlanThreads + threadIdx.x) * each;
+    *from = (uint32_t)min(at, (uint64_t)n);
+    *to = (uint32_t)min(at + each, (uint64_t)n);
+}
+
+__device__ __forceinline__ bool ring_bad(const PlanArgs &a, int32_t head, int32_t count) {
+    return count < 0 || (uint32_t)count > a.free_capacity || head < 0 ||
+           ((uint32_t)head >= a.free_capacity && (head != 0 || a.free_capacity != 0));
+}
+
+// The tables handed on as they were, after an error (page counts clamped to the rows).
+__device__ __forceinline__ void hand_on(const PlanArgs &a, const Team &t, int32_t err) {
+    const uint32_t lane = threadIdx.x & 31u;
+    for (uint32_t r = t.rank * kPlanWarps + (threadIdx.x >> 5); r < a.n_requests; r += t.C * kPlanWarps) {
+        const uint32_t n = min((uint32_t)max(__ldg(a.n_in + r), 0), a.max_pages);
+        for (uint32_t j = lane; j < n; j += 32u)
+            a.table_out[(uint64_t)r * a.out_stride + j] = __ldg(a.table + (uint64_t)r * a.table_stride + j);
+        if (lane == 0 && a.n_out) {
+            a.n_out[r] = __ldg(a.n_in + r);
+            a.ctx_out[r] = __ldg(a.ctx_len + r);
+        }
+    }
+    for (uint32_t i = t.rank * kPlanThreads + threadIdx.x; i < a.capacity; i += t.C * kPlanThreads) {
+        a.src[i] = a.dst[i] = -1;
+        if (a.count) a.count[i] = 0;
+    }
+    if (t.rank == 0 && threadIdx.x == 0) {
+        a.free_out[0] = __ldg(a.free_in);
+        a.free_out[1] = __ldg(a.free_in + 1);
+        *a.status = err;
+    }
+}
+
+// ---- fork
+
+// The row that row s goes on from, or ~0 (errors are found before).
+__device__ __forceinline__ uint32_t parent_row(const PlanArgs &a, uint32_t s) {
+    const int32_t p = a.parents ? __ldg(a.parents + s) : (int32_t)s;
+    return p < 0 || __ldg(a.ctx_len + p) < 0 ? ~0u : (uint32_t)p;
+}
+
+struct Fork {
+    uint32_t from;       // ~0: empty
+    uint32_t keep;       // entries of the old row
+    uint32_t copies;     // 1: one more page, a copy of the old row's next
+    uint32_t part;       // tokens of it
+    bool heir;
+};
+
+__device__ __forceinline__ Fork fork_of(const PlanArgs &a, uint32_t s) {
+    Fork f{parent_row(a, s), 0u, 0u, 0u, false};
+    if (f.from == ~0u) return f;
+    const uint32_t c = (uint32_t)__ldg(a.ctx_len + f.from), whole = div_by(c, a.page), part = c - whole * a.page.d;
+    // the workspace holds s + 1 of the lowest row that goes on, 0 for the row itself
+    f.heir = __ldcg(a.words + f.from) == (f.from == s ? 0u : s + 1u);
+    if (f.heir) {
+        f.keep = a.trim ? whole + (part != 0u) : (uint32_t)__ldg(a.n_in + f.from);
+    } else {
+        f.keep = whole;
+        f.copies = part != 0u;
+        f.part = part;
+    }
+    return f;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_pages_kernel(const PlanArgs a) {
+    __shared__ Told told;
+    __shared__ uint32_t part[kPlanWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    Team t{cluster.num_blocks(), cluster.block_rank(), 0u, &told};
+    const uint32_t tid = threadIdx.x, lane = tid & 31u;
+    const int32_t head = __ldg(a.free_in), count = __ldg(a.free_in + 1);
+    cluster.sync();                                       // every CTA has started
+
+    // Errors of the lengths; the workspace is made ready.
+    bool bad = ring_bad(a, head, count);
+    for (uint32_t r = t.rank * kPlanThreads + tid; r < a.n_requests; r += t.C * kPlanThreads) {
+        const int32_t p = a.parents ? __ldg(a.parents + r) : (int32_t)r, c = __ldg(a.ctx_len + r), h = __ldg(a.n_in + r);
+        bad |= p < -1 || p >= (int32_t)a.n_requests || h < 0 || (uint32_t)h > a.max_pages || (int64_t)c > (int64_t)h * a.page.d;
+        a.words[r] = ~0u;
+    }
+    clear_bits(a, t);
+    bad = __syncthreads_or(bad);
+    if (t.any(bad)) {
+        hand_on(a, t, SKV_ERR_INVALID_ARG);
+        return;
+    }
+    // Heirs, and the pages that are held.
+    for (uint32_t s = t.rank * kPlanThreads + tid; s < a.n_requests; s += t.C * kPlanThreads) {
+        const uint32_t p = parent_row(a, s);
+        if (p != ~0u) atomicMin(a.words + p, p == s ? 0u : s + 1u);
+    }
+    bool corrupt = !mark_rows(a, t);
+    __syncthreads();
+    t.tell(0u);
+    // The bits of what rows go on with are cleared (an heir's pages: the others' are among them); the first CTA
+    // ranks the copies, in order of rows, and takes their pages off the ring.
+#pragma unroll 1
+    for (uint32_t s = t.rank * kPlanWarps + (tid >> 5); s < a.n_requests; s += t.C * kPlanWarps) {
+        const Fork f = fork_of(a, s);
+        if (!f.heir) continue;
+        const int32_t *row = a.table + (uint64_t)f.from * a.table_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < f.keep; j += 32u) {
+            const uint32_t p = (uint32_t)__ldg(row + j);
+            if (p < a.pool_pages) atomicAnd(bit_word(a, p), ~(1u << (p & 31u)));
+        }
+    }
+    uint32_t took = 0;
+    if (t.rank == 0) {
+#pragma unroll 1
+        for (uint32_t base = 0; base < a.n_requests; base += kPlanThreads) {
+            const uint32_t s = base + tid;
+            Fork f{~0u, 0u, 0u, 0u, false};
+            if (s < a.n_requests) f = fork_of(a, s);
+            uint32_t all;
+            const uint32_t k = took + block_scan(f.copies, &all, part);
+            took += all;
+            if (s < a.n_requests) {
+                int32_t from = -1, to = -1;
+                if (f.copies && k < (uint32_t)count) {
+                    uint64_t e = (uint64_t)head + k;
+                    if (e >= a.free_capacity) e -= a.free_capacity;
+                    from = __ldg(a.table + (uint64_t)f.from * a.table_stride + f.keep);
+                    to = __ldg(a.free_pages + e);
+                    // (a ring that names a held page is not made worse)
+                    if ((uint32_t)to < a.pool_pages) atomicAnd(bit_word(a, (uint32_t)to), ~(1u << (to & 31)));
+                }
+                // both as they are until the rows are written; a pair outside the pool is left out then
+                a.src[s] = from;
+                a.dst[s] = to;
+                a.count[s] = (int32_t)f.part;
+                a.n_out[s] = (int32_t)(f.keep + f.copies);
+                a.ctx_out[s] = f.from == ~0u ? -1 : __ldg(a.ctx_len + f.from);
+            }
+        }
+    }
+    __syncthreads();
+    took = t.tell(took)[0];
+    // Freed pages, counted.
+    uint32_t from, to, mine = 0, freed_here;
+    run_of(a, t, &from, &to);
+    for (uint32_t i = from; i < to; ++i) mine += __popc(__ldcg(a.bits + i));
+    uint32_t at = block_scan(mine, &freed_here, part), before;
+    const uint32_t freed = t.sum(freed_here, &before);
+    at += before;
+    if (took > (uint32_t)count || (uint64_t)count - took + freed > a.free_capacity) {
+        hand_on(a, t, SKV_ERR_CAPACITY);
+        return;
+    }
+    // Into the ring behind its end, the rows, the counts.
+    for (uint32_t i = from; i < to; ++i) {
+        uint32_t w = __ldcg(a.bits + i);
+        while (w) {
+            uint64_t e = (uint64_t)head + (uint32_t)count + at++;
+            while (e >= a.free_capacity) e -= a.free_capacity;
+            a.free_pages[e] = (int32_t)(32u * i + __ffs(w) - 1u);
+            w &= w - 1u;
+        }
+    }
+#pragma unroll 1
+    for (uint32_t s = t.rank * kPlanWarps + (tid >> 5); s < a.n_requests; s += t.C * kPlanWarps) {
+        const Fork f = fork_of(a, s);
+        if (f.from == ~0u) continue;
+        const int32_t *row = a.table + (uint64_t)f.from * a.table_stride;
+        int32_t *out = a.table_out + (uint64_t)s * a.out_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < f.keep; j += 32u) out[j] = __ldg(row + j);
+        if (f.copies && lane == 0) {
+            const int32_t x = __ldcg(a.src + s), y = __ldcg(a.dst + s);
+            out[f.keep] = y;
+            if ((uint32_t)x >= a.pool_pages || (uint32_t)y >= a.pool_pages) {
+                corrupt = true;
+                a.src[s] = a.dst[s] = -1;
+                a.count[s] = 0;
+            }
+        }
+    }
+    corrupt = __syncthreads_or(corrupt);
+    corrupt = t.any(corrupt);
+    if (t.rank == 0 && tid == 0) {
+        uint64_t e = (uint64_t)head + took;
+        const uint32_t cap = max(a.free_capacity, 1u);
+        if (e >= cap) e -= cap;
+        a.free_out[0] = (int32_t)e;
+        a.free_out[1] = (int32_t)((uint32_t)count - took + freed);
+        *a.status = corrupt ? SKV_ERR_CORRUPT : SKV_OK;
+    }
+}
+
+// ---- compact
+
+// Bits of word i that lie below page `limit`.
+__device__ __forceinline__ uint32_t below(uint32_t i, uint32_t limit) {
+    const uint32_t first = 32u * i;
+    return limit <= first ? 0u : limit - first >= 32u ? ~0u : (1u << (limit - first)) - 1u;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_pages_kernel(const PlanArgs a) {
+    __shared__ Told told;
+    __shared__ uint32_t part[kPlanWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    Team t{cluster.num_blocks(), cluster.block_rank(), 0u, &told};
+    const uint32_t tid = threadIdx.x, lane = tid & 31u;
+    cluster.sync();
+    bool bad = false;
+    for (uint32_t r = t.rank * kPlanThreads + tid; r < a.n_requests; r += t.C * kPlanThreads) {
+        const int32_t h = __ldg(a.n_in + r);
+        bad |= h < 0 || (uint32_t)h > a.max_pages;
+    }
+    clear_bits(a, t);
+    bad = __syncthreads_or(bad);
+    if (t.any(bad)) {
+        hand_on(a, t, SKV_ERR_INVALID_ARG);
+        return;
+    }
+    bool corrupt = !mark_rows(a, t);
+    corrupt = __syncthreads_or(corrupt);
+    corrupt = t.any(corrupt);
+    // Held pages in all, then holes below that number and held pages from it on.
+    uint32_t from, to, mine = 0, here, before;
+    run_of(a, t, &from, &to);
+    for (uint32_t i = from; i < to; ++i) mine += __popc(__ldcg(a.bits + i));
+    block_scan(mine, &here, part);
+    const uint32_t live = t.sum(here, &before);
+    uint32_t holes = 0, far = 0;
+    for (uint32_t i = from; i < to; ++i) {
+        const uint32_t w = __ldcg(a.bits + i), low = below(i, live);
+        holes += __popc(~w & low);
+        far += __popc(w & ~low);
+    }
+    uint32_t here_holes, here_far;
+    holes = block_scan(holes, &here_holes, part);
+    far = block_scan(far, &here_far, part);
+    t.sum(here_holes, &before);
+    holes += before;
+    const uint32_t moves = t.sum(here_far, &before);
+    far += before;
+    if (moves > a.capacity || a.pool_pages - live > a.free_capacity) {
+        hand_on(a, t, SKV_ERR_CAPACITY);
+        return;
+    }
+    uint32_t *rank_of = a.words, *hole = a.words + a.pool_pages;
+    for (uint32_t i = from; i < to; ++i) {
+        const uint32_t w = __ldcg(a.bits + i), low = below(i, live);
+        for (uint32_t m = ~w & low; m; m &= m - 1u) {
+            const uint32_t p = 32u * i + __ffs(m) - 1u;
+            hole[holes] = p;
+            a.dst[holes++] = (int32_t)p;
+        }
+        for (uint32_t m = w & ~low; m; m &= m - 1u) {
+            const uint32_t p = 32u * i + __ffs(m) - 1u;
+            rank_of[p] = far;
+            a.src[far++] = (int32_t)p;
+        }
+    }
+    for (uint32_t i = moves + t.rank * kPlanThreads + tid; i < a.capacity; i += t.C * kPlanThreads) a.src[i] = a.dst[i] = -1;
+    for (uint32_t i = t.rank * kPlanThreads + tid; i < a.pool_pages - live; i += t.C * kPlanThreads) a.free_pages[i] = (int32_t)(live + i);
+    __syncthreads();
+    t.tell(0u);
+#pragma unroll 1
+    for (uint32_t r = t.rank * kPlanWarps + (tid >> 5); r < a.n_requests; r += t.C * kPlanWarps) {
+        const uint32_t n = (uint32_t)__ldg(a.n_in + r);
+        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
+        int32_t *out = a.table_out + (uint64_t)r * a.out_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < n; j += 32u) {
+            int32_t p = __ldg(row + j);
+            if ((uint32_t)p >= live && (uint32_t)p < a.pool_pages) p = (int32_t)__ldcg(hole + __ldcg(rank_of + p));
+            out[j] = p;
+        }
+    }
+    if (t.rank == 0 && tid == 0) {
+        a.free_out[0] = 0;
+        a.free_out[1] = (int32_t)(a.pool_pages - live);
+        *a.status = corrupt ? SKV_ERR_CORRUPT : SKV_OK;
+    }
+}
+
+// ---- copies of pages
+
+struct CopyArgs {
+    uint8_t *k, *v;
+    uint64_t page_stride, token_stride, head_stride;      // bytes
+    uint32_t page_tokens, n_pages, n, chunks;             // chunks of a page, of kCopyUnits units of 16 bytes
+    FastDiv by_chunks, per_token, per_head;               // units of a token and of a head
+    const int32_t *src, *dst, *tokens;
+    int32_t *status;
+    uint32_t checked;
+};
+
+constexpr uint32_t kCopyThreads = 256, kCopyDeep = 4, kCopyUnits = kCopyThreads * kCopyDeep;
+
+// A pair's pages and how many tokens of them; false: nothing to copy (bad: not as it should be).
+__device__ __forceinline__ bool pair_of(const CopyArgs &a, uint32_t i, int32_t *src, int32_t *dst, uint32_t *n, bool *bad) {
+    *src = __ldg(a.src + i);
+    *dst = __ldg(a.dst + i);
+    *n = a.tokens ? (uint32_t)__ldg(a.tokens + i) : a.page_tokens;
+    if (*src < 0) return false;
+    const bool ok = (uint32_t)*src < a.n_pages && (uint32_t)*dst < a.n_pages && *n <= a.page_tokens;
+    *bad |= !ok;
+    return ok && *n != 0u;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs a) {
+    const uint32_t lane = threadIdx.x & 31u;
+    bool bad = false;
+    int32_t src, dst;
+    uint32_t n;
+    if (a.checked && blockIdx.x == 0) {
+        for (uint32_t i = threadIdx.x; i < a.n; i += kCopyThreads) pair_of(a, i, &src, &dst, &n, &bad);
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
+        bad = false;
+    }
+    // Chunks are dealt to the CTAs in turn. A warp looks 32 of its chunks up at once, so that pairs without a copy
+    // cost little; all warps of a CTA find the same.
+    const uint64_t items = (uint64_t)a.n * a.chunks;
+#pragma unroll 1
+    for (uint64_t m0 = blockIdx.x; m0 < items; m0 += 32ull * gridDim.x) {
+        const uint64_t m = m0 + (uint64_t)lane * gridDim.x;
+        bool live = false;
+        uint32_t chunk = 0;
+        src = dst = 0;
+        n = 0;
+        if (m < items) {
+            const uint32_t i = m >> 31 ? (uint32_t)(m / a.chunks) : div_by((uint32_t)m, a.by_chunks);
+            chunk = (uint32_t)(m - (uint64_t)i * a.chunks);
+            live = pair_of(a, i, &src, &dst, &n, &bad) && (uint64_t)chunk * kCopyUnits < (uint64_t)n * a.per_token.d;
+        }
+        uint32_t todo = __ballot_sync(~0u, live);
+#pragma unroll 1
+        while (todo) {
+            const uint32_t l = __ffs(todo) - 1u;
+            todo &= todo - 1u;
+            const uint64_t from = (uint64_t)__shfl_sync(~0u, src, l) * a.page_stride, to = (uint64_t)__shfl_sync(~0u, dst, l) * a.page_stride;
+            const uint32_t u0 = __shfl_sync(~0u, chunk, l) * kCopyUnits, end = __shfl_sync(~0u, n, l) * a.per_token.d;
+            uint4 x[kCopyDeep], y[kCopyDeep];
+            uint64_t at[kCopyDeep];
+#pragma unroll
+            for (uint32_t j = 0; j < kCopyDeep; ++j) {
+                const uint32_t u = u0 + j * kCopyThreads + threadIdx.x;
+                const uint32_t token = div_by(u, a.per_token), rest = u - token * a.per_token.d;
+                const uint32_t h = div_by(rest, a.per_head);
+                at[j] = token * a.token_stride + h * a.head_stride + 16u * (uint64_t)(rest - h * a.per_head.d);
+                if (u < end) {
+                    x[j] = *reinterpret_cast<const uint4 *>(a.k + from + at[j]);
+                    y[j] = *reinterpret_cast<const uint4 *>(a.v + from + at[j]);
+                }
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < kCopyDeep; ++j) {
+                if (u0 + j * kCopyThreads + threadIdx.x < end) {
+                    *reinterpret_cast<uint4 *>(a.k + to + at[j]) = x[j];
+                    *reinterpret_cast<uint4 *>(a.v + to + at[j]) = y[j];
+                }
+            }
+        }
+    }
+    if (bad && !a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
+}
+
+// ---- moves of tokens
+
+struct MoveArgs {
+    uint8_t *k, *v;
+    uint64_t page_stride, token_stride, head_stride;      // bytes
+    FastDiv page, per_head;                               // units of 16 bytes per head
+    uint64_t pool_tokens;
+    uint32_t n_requests, n_rows, units, per_request;      // units of a token; CTAs of a request
+    const int32_t *cu, *rows;
+    const int64_t *slots, *kept;
+    int32_t *status;
+    uint32_t checked;
+};
+
+constexpr uint32_t kMoveThreads = 256, kMoveDeep = 8;
+
+// Entry i's places; false: nothing to move (bad: not as it should be).
+__device__ __forceinline__ bool move_of(const MoveArgs &a, uint32_t i, int64_t *from, int64_t *to, bool *bad) {
+    *to = __ldg(a.kept + i);
+    const uint32_t row = (uint32_t)__ldg(a.rows + i);
+    *from = -1;
+    if (*to < 0) return false;
+    if (row < a.n_rows) *from = __ldg(a.slots + row);
+    const bool ok = (uint64_t)*to < a.pool_tokens && (uint64_t)*from < a.pool_tokens;
+    *bad |= !ok;
+    return ok && *from != *to;
+}
+
+__device__ __forceinline__ uint64_t byte_of(const MoveArgs &a, int64_t slot) {
+    const uint64_t p = a.pool_tokens >> 31 ? (uint64_t)slot / a.page.d : div_by((uint32_t)slot, a.page);
+    return p * a.page_stride + ((uint64_t)slot - p * a.page.d) * a.token_stride;
+}
+
+__device__ __forceinline__ bool move_rows_of(const MoveArgs &a, uint32_t r, uint32_t *lo, uint32_t *hi) {
+    const int32_t x = __ldg(a.cu + r), y = __ldg(a.cu + r + 1);
+    *lo = (uint32_t)x;
+    *hi = (uint32_t)y;
+    if (x >= 0 && y >= x && (uint32_t)y <= a.n_rows) return true;
+    *lo = *hi = 0u;
+    return false;
+}
+
+// A thread keeps one 16-byte column of K or V of a request's tokens and moves them in order, so that
+// a place that is read before it is written over needs no barrier.
+__global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveArgs a) {
+    const uint32_t lane = threadIdx.x & 31u;
+    bool bad = false;
+    int64_t from, to;
+    uint32_t lo, hi;
+    if (blockIdx.x >= a.n_requests * a.per_request) {         // the errors of every request
+        for (uint32_t r = threadIdx.x >> 5; r < a.n_requests; r += kMoveThreads / 32u) {
+            bad |= !move_rows_of(a, r, &lo, &hi);
+            for (uint32_t i = lo + lane; i < hi; i += 32u) move_of(a, i, &from, &to, &bad);
+        }
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
+        return;
+    }
+    const uint32_t r = blockIdx.x / a.per_request;
+    const uint32_t column = (blockIdx.x - r * a.per_request) * kMoveThreads + threadIdx.x;
+    bad |= !move_rows_of(a, r, &lo, &hi);
+    const bool on = column < 2u * a.units;
+    const uint32_t u = column < a.units ? column : column - a.units, h = div_by(u, a.per_head);
+    uint8_t *pool = (column < a.units ? a.k : a.v) + h * a.head_stride + 16u * (uint64_t)(u - h * a.per_head.d);
+#pragma unroll 1
+    for (uint32_t i0 = lo; i0 < hi; i0 += 32u) {
+        const uint32_t i = i0 + lane;
+        from = to = -1;
+        const bool live = i < hi && move_of(a, i, &from, &to, &bad);
+        uint32_t todo = __ballot_sync(~0u, live);
+#pragma unroll 1
+        while (todo) {
+            // up to eight entries whose places are all read before any is written; fewer where one reads
+            // what an entry before it writes
+            uint64_t src[kMoveDeep], dst[kMoveDeep];
+            int64_t wrote[kMoveDeep];
+            uint32_t n = 0;
+#pragma unroll
+            for (uint32_t j = 0; j < kMoveDeep; ++j) {
+                wrote[j] = -1;
+                src[j] = dst[j] = 0;
+                if (!todo || n < j) continue;
+                const uint32_t l = __ffs(todo) - 1u;
+                const int64_t x = __shfl_sync(~0u, from, l), y = __shfl_sync(~0u, to, l);
+                bool after = false;
+#pragma unroll
+                for (uint32_t e = 0; e < j; ++e) after |= wrote[e] == x;
+                if (after) continue;
+                todo &= todo - 1u;
+                wrote[j] = y;
+                src[j] = byte_of(a, x);
+                dst[j] = byte_of(a, y);
+                n = j + 1u;
+            }
+            uint4 x[kMoveDeep];
+#pragma unroll
+            for (uint32_t j = 0; j < kMoveDeep; ++j)
+                if (on && j < n) x[j] = *reinterpret_cast<const uint4 *>(pool + src[j]);
+#pragma unroll
+            for (uint32_t j = 0; j < kMoveDeep; ++j)
+                if (on && j < n) *reinterpret_cast<uint4 *>(pool + dst[j]) = x[j];
+        }
+    }
+    if (bad && !a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
+}
+
+static bool launch_plan(void (*kernel)(PlanArgs), const PlanArgs &a, cudaStream_t st) {
+    // One CTA where a small table and pool leave little for more: a barrier of several costs more.
+    const uint64_t entries = (uint64_t)a.n_requests * a.max_pages;
+    const uint32_t cluster = entries <= 2048u && a.pool_pages <= 32768u ? 1u : kPlanCluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess;
+}
+
+static uint64_t bits_bytes(uint32_t pool_pages) { return ((uint64_t)pool_pages + 511u) / 512u * 64u; }
+
+static uint64_t workspace_bytes(uint32_t n_requests, uint32_t pool_pages) {
+    const uint64_t fork = 4ull * n_requests, compact = 8ull * pool_pages;
+    return (bits_bytes(pool_pages) + (fork > compact ? fork : compact) + 255u) & ~uint64_t(255);
+}
+
+static bool bad_sizes(uint32_t pool_pages, uint32_t n_requests, uint32_t max_pages, uint64_t stride, uint64_t out_stride,
+                      uint32_t free_capacity) {
+    return pool_pages == 0 || pool_pages > 0x7FFFFFFFu || n_requests > 0x7FFFFFFFu || max_pages > 0x7FFFFFFFu ||
+           free_capacity > 0x7FFFFFFFu || (n_requests > 1 && (stride < max_pages || out_stride < max_pages));
+}
+
+}  // namespace skv
+
+using namespace skv;
+
+extern "C" int32_t skv_page_workspace_bytes(uint32_t n_requests, uint32_t pool_pages, uint64_t *bytes) {
+    if (!bytes || pool_pages == 0 || pool_pages > 0x7FFFFFFFu || n_requests > 0x7FFFFFFFu) return SKV_ERR_INVALID_ARG;
+    *bytes = workspace_bytes(n_requests, pool_pages);
+    return SKV_OK;
+}
+
+extern "C" int32_t skv_page_fork(uint32_t page_tokens, uint32_t pool_pages, uint32_t n_requests, const int32_t *parents,
+                                 const int32_t *ctx_len, const int32_t *block_table, uint64_t table_stride, uint32_t max_pages,
+                                 const int32_t *n_pages_in, uint32_t trim, int32_t *table_out, uint64_t table_out_stride,
+                                 int32_t *n_pages_out, int32_t *ctx_out, int32_t *free_pages, uint32_t free_capacity,
+                                 const int32_t *free_in, int32_t *free_out, int32_t *copy_src, int32_t *copy_dst,
+                                 int32_t *copy_tokens, int32_t *status, void *workspace, uint64_t ws_bytes, void *stream) {
+    if (page_tokens == 0 || page_tokens > (1u << 20) || trim > 1u ||
+        bad_sizes(pool_pages, n_requests, max_pages, table_stride, table_out_stride, free_capacity))
+        return SKV_ERR_INVALID_ARG;
+    if (!free_in || !free_out || !status || !workspace || (free_capacity && !free_pages) ||
+        (n_requests && (!ctx_len || !block_table || !n_pages_in || !table_out || !n_pages_out || !ctx_out || !copy_src || !copy_dst ||
+                        !copy_tokens)))
+        return SKV_ERR_INVALID_ARG;
+    const void *words[] = {parents, ctx_len, block_table, n_pages_in, table_out, n_pages_out, ctx_out, free_pages, free_in, free_out,
+                           copy_src, copy_dst, copy_tokens, status};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return SKV_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16) || ws_bytes < workspace_bytes(n_requests, pool_pages) || free_in == free_out ||
+        (n_requests && (block_table == table_out || n_pages_in == n_pages_out || ctx_len == ctx_out)))
+        return SKV_ERR_INVALID_ARG;
+    PlanArgs a{};
+    a.page = fast_div(page_tokens), a.pool_pages = pool_pages, a.n_requests = n_requests, a.max_pages = max_pages;
+    a.free_capacity = free_capacity, a.trim = trim, a.capacity = n_requests;
+    a.parents = parents, a.ctx_len = ctx_len, a.table = block_table, a.n_in = n_pages_in, a.free_in = free_in;
+    a.table_stride = table_stride, a.out_stride = table_out_stride;
+    a.table_out = table_out, a.n_out = n_pages_out, a.ctx_out = ctx_out, a.free_pages = free_pages, a.free_out = free_out;
+    a.src = copy_src, a.dst = copy_dst, a.count = copy_tokens, a.status = status;
+    a.bits = static_cast<uint32_t *>(workspace);
+    a.words = a.bits + bits_bytes(pool_pages) / 4u;
+    return launch_plan(fork_pages_kernel, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
+}
+
+extern "C" int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, const int32_t *block_table, uint64_t table_stride,
+                                    uint32_t max_pages, const int32_t *n_pages, int32_t *table_out, uint64_t table_out_stride,
+                                    int32_t *free_pages, uint32_t free_capacity, const int32_t *free_in, int32_t *free_out,
+                                    int32_t *copy_src, int32_t *copy_dst, uint32_t copy_capacity, int32_t *status, void *workspace,
+                                    uint64_t ws_bytes, void *stream) {
+    if (bad_sizes(pool_pages, n_requests, max_pages, table_stride, table_out_stride, free_capacity) || copy_capacity > 0x7FFFFFFFu)
+        return SKV_ERR_INVALID_ARG;
+    if (!free_in || !free_out || !status || !workspace || (free_capacity && !free_pages) || (copy_capacity && (!copy_src || !copy_dst)) ||
+        (n_requests && (!block_table || !n_pages || !table_out)))
+        return SKV_ERR_INVALID_ARG;
+    const void *words[] = {block_table, n_pages, table_out, free_pages, free_in, free_out, copy_src, copy_dst, status};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return SKV_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16) || ws_bytes < workspace_bytes(n_requests, pool_pages) || free_in == free_out ||
+        (n_requests && block_table == table_out))
+        return SKV_ERR_INVALID_ARG;
+    PlanArgs a{};
+    a.pool_pages = pool_pages, a.n_requests = n_requests, a.max_pages = max_pages;
+    a.free_capacity = free_capacity, a.capacity = copy_capacity;
+    a.table = block_table, a.n_in = n_pages, a.free_in = free_in;
+    a.table_stride = table_stride, a.out_stride = table_out_stride;
+    a.table_out = table_out, a.free_pages = free_pages, a.free_out = free_out, a.src = copy_src, a.dst = copy_dst, a.status = status;
+    a.bits = static_cast<uint32_t *>(workspace);
+    a.words = a.bits + bits_bytes(pool_pages) / 4u;
+    return launch_plan(compact_pages_kernel, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
+}
+
+extern "C" int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, const int32_t *dst, const int32_t *tokens, uint32_t n,
+                                  int32_t *status, void *stream) {
+    const int32_t rc = skv_paged_check(cache);
+    if (rc != SKV_OK) return rc;
+    if (!status || !aligned(status, 4) || n > 0x7FFFFFFFu || (n && (!src || !dst)) || !aligned(src, 4) || !aligned(dst, 4) ||
+        !aligned(tokens, 4))
+        return SKV_ERR_INVALID_ARG;
+    const PagedView c = paged_view(*cache);
+    const uint32_t per_head = cache->head_dim / (c.e4m3 ? 16u : 8u);
+    const uint64_t per_page = (uint64_t)cache->page_tokens * cache->n_heads * per_head;
+    if (per_page > 0x7FFFFFFFu - kCopyUnits) return SKV_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
+    uint32_t sms = 0;
+    if (!device_sms(&sms)) return SKV_ERR_CUDA;
+    CopyArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
+               cache->page_tokens, cache->n_pages, n, (uint32_t)((per_page + kCopyUnits - 1) / kCopyUnits), {}, fast_div(cache->n_heads * per_head),
+               fast_div(per_head), src, dst, tokens, status, n <= 2048u};
+    a.by_chunks = fast_div(a.chunks);
+    if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
+    const uint64_t items = (uint64_t)n * a.chunks;
+    const unsigned grid = (unsigned)(items < 8u * sms ? items : 8u * sms);
+    copy_pages_kernel<<<grid, kCopyThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
+}
+
+extern "C" int32_t skv_cache_move(const skv_paged *cache, uint32_t n_requests, const int32_t *cu_new, uint32_t n_rows,
+                                  const int32_t *rows, const int64_t *slots, const int64_t *kept, int32_t *status, void *stream) {
+    const int32_t rc = skv_paged_check(cache);
+    if (rc != SKV_OK) return rc;
+    if (!status || !aligned(status, 4) || n_rows > 0x7FFFFFFFu || (n_requests && !cu_new) || !aligned(cu_new, 4) || !aligned(rows, 4) ||
+        !aligned(slots, 8) || !aligned(kept, 8) || (n_rows && (!rows || !slots || !kept)))
+        return SKV_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
+    const PagedView c = paged_view(*cache);
+    const uint32_t per_head = cache->head_dim / (c.e4m3 ? 16u : 8u), units = cache->n_heads * per_head;
+    const uint32_t per_request = (2u * units + kMoveThreads - 1u) / kMoveThreads;
+    if ((uint64_t)n_requests * per_request >= 0x7FFFFFFFu) return SKV_ERR_INVALID_ARG;
+    MoveArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
+               c.page, fast_div(per_head), (uint64_t)cache->n_pages * cache->page_tokens, n_requests, n_rows, units, per_request, cu_new, rows,
+               slots, kept, status, n_rows <= 16384u && n_requests <= 1024u};
+    if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
+    move_tokens_kernel<<<n_requests * per_request + a.checked, kMoveThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
+}

@@ -1,0 +1,59 @@
+// skv_rows.cuh -- what the operators on rows and pages of a paged cache share: the
+// e4m3 quantiser, and small host checks.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "skv_paged.h"
+
+namespace skv {
+
+// A head's scale s, brought between 2^-85 and 2^64 together with the values (`by`, a power of two):
+// there 1 / s and the remainders below are exact enough at either end of binary32. A value that
+// leaves binary32 on the way saturates, or is 0, like its quotient.
+struct ScaleOf {
+    float by, s, r;
+};
+
+__device__ __forceinline__ ScaleOf scale_of(float s) {
+    ScaleOf o;
+    o.by = s < 0x1p-64f ? 0x1p64f : s > 0x1p64f ? 0x1p-64f : 1.0f;
+    o.s = s * o.by;
+    o.r = __fdiv_rn(1.0f, o.s);
+    return o;
+}
+
+// The e4m3 code nearest to x / s. The binary32 quotient alone can land on a tie
+// that the real quotient only comes near, so it is rounded to odd first: the
+// remainder x - q s is exact in an fma for any q within a step of the quotient, and
+// where it is not 0 the quotient is cut towards 0 and its last bit set, which keeps it
+// off every border of the much coarser code grid. q: one product with the
+// reciprocal of s and one correction by the remainder.
+__device__ __forceinline__ uint32_t e4m3_of(float value, const ScaleOf &c) {
+    const float x = value * c.by;
+    float q = x * c.r;
+    if (fabsf(q) >= 1.0e-30f && fabsf(q) < 1.0e30f) {
+        q = fmaf(fmaf(-q, c.s, x), c.r, q);
+        const float rem = fmaf(-q, c.s, x);
+        uint32_t b = __float_as_uint(q);
+        // the remainder's sign against the quotient's (s > 0): q is too large in magnitude
+        if ((__float_as_uint(rem) ^ b) >> 31) --b;
+        if (rem != 0.0f) q = __uint_as_float(b | 1u);
+    }
+    return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+inline bool device_sms(uint32_t *sms) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return false;
+    *sms = (uint32_t)n;
+    return true;
+}
+
+inline bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+}  // namespace skv

@@ -80,15 +80,39 @@ class _Status:
 
 class PageTable(_Status):
     """A block table [n_requests][max_pages] (int32) over a pool of `pool_pages`
-    pages of `page_tokens` tokens, kept on the GPU (skv_page_map)."""
+    pages of `page_tokens` tokens, kept on the GPU (skv_page_map). workspace=True makes the
+    workspace of fork and compact (a first call makes it otherwise, which a capture cannot)."""
 
-    def __init__(self, block_table: torch.Tensor, page_tokens: int, pool_pages: int):
+    def __init__(self, block_table: torch.Tensor, page_tokens: int, pool_pages: int, workspace: bool = False):
         self._stride = _table_rows(block_table)
         self.block_table, self._table = block_table, block_table.data_ptr()
         self.page_tokens, self.pool_pages = int(page_tokens), int(pool_pages)
         self.n_requests, self.max_pages = block_table.shape
         self._new_status(block_table.device)
+        self.workspace = None
+        if workspace:
+            self._make_workspace()
         self._settle()
+
+    def _make_workspace(self, stream=None):
+        """The workspace, which any content suits; it stays as long as the object: a captured graph holds
+        its address."""
+        v = C.c_uint64()
+        B.check("skv_page_workspace_bytes", B.lib().skv_page_workspace_bytes(self.n_requests, self.pool_pages, C.byref(v)))
+        self.workspace = torch.empty(v.value, dtype=torch.uint8, device=self.block_table.device)
+        _after_current(stream)
+        self._workspace, self._workspace_bytes = self.workspace.data_ptr(), v.value
+
+    def _ready(self, table_out, stream):
+        """What fork and compact need beside their arrays; table_out's row stride."""
+        out = _table_rows(table_out)
+        if table_out.shape != self.block_table.shape or table_out.get_device() != self._device or table_out.data_ptr() == self._table:
+            raise ValueError("table_out must be another tensor of the block_table's shape and device")
+        if self.workspace is None:
+            if _capturing(stream):
+                raise ValueError("give PageTable workspace=True before a capture")
+            self._make_workspace(stream)
+        return out
 
     def map_into(self, ctx_len, new_len, n_pages, free_pages, free_state, cu_new, slots, n_pages_out,
                  free_state_out, stream=None):
@@ -108,10 +132,49 @@ class PageTable(_Status):
                                   cu_new.data_ptr(), slots.data_ptr(), room, self._status, _stream_of(stream, self._device))
         B.check("skv_page_map", rc)
 
+    def fork_into(self, parents, ctx_len, n_pages, free_pages, free_state, table_out, n_pages_out, ctx_out, free_state_out,
+                  copy_src, copy_dst, copy_tokens, trim: bool = False, stream=None):
+        """Enqueue skv_page_fork: row s of table_out goes on from row parents[s] (None: from
+        itself; -1, or a row of ctx_len < 0: empty), sharing its full pages; pages that no row holds any
+        more go back to the ring. copy_src, copy_dst and copy_tokens are for PagedKV.copy_into, once for
+        each layer's pools. Outputs are other tensors than the inputs."""
+        n, size, dev = self.n_requests, free_pages.numel(), self._device
+        _check_words("ctx_len, n_pages, n_pages_out, ctx_out and the copies", _I32, n, dev, ctx_len, n_pages, n_pages_out, ctx_out,
+                     copy_src, copy_dst, copy_tokens)
+        _check_words("free_state and free_state_out", _I32, 2, dev, free_state, free_state_out)
+        _check_words("free_pages", _I32, size, dev, free_pages)
+        if parents is not None:
+            _check_words("parents", _I32, n, dev, parents)
+            parents = parents.data_ptr()
+        out = self._ready(table_out, stream)
+        rc = B.lib().skv_page_fork(self.page_tokens, self.pool_pages, n, parents, ctx_len.data_ptr(), self._table, self._stride,
+                                   self.max_pages, n_pages.data_ptr(), trim, table_out.data_ptr(), out, n_pages_out.data_ptr(),
+                                   ctx_out.data_ptr(), free_pages.data_ptr(), size, free_state.data_ptr(), free_state_out.data_ptr(),
+                                   copy_src.data_ptr(), copy_dst.data_ptr(), copy_tokens.data_ptr(), self._status, self._workspace,
+                                   self._workspace_bytes, _stream_of(stream, dev))
+        B.check("skv_page_fork", rc)
+
+    def compact_into(self, n_pages, free_pages, free_state, table_out, free_state_out, copy_src, copy_dst, stream=None):
+        """Enqueue skv_page_compact: the held pages move to the front of the pool; table_out has their new
+        numbers and the ring the pages behind them. copy_src and copy_dst (room for the moves: as many as
+        pages are held is always enough) are for PagedKV.copy_into, once for each layer's pools."""
+        size, room, dev = free_pages.numel(), copy_src.numel(), self._device
+        _check_words("n_pages", _I32, self.n_requests, dev, n_pages)
+        _check_words("free_state and free_state_out", _I32, 2, dev, free_state, free_state_out)
+        _check_words("free_pages", _I32, size, dev, free_pages)
+        _check_words("copy_src and copy_dst", _I32, room, dev, copy_src, copy_dst)
+        out = self._ready(table_out, stream)
+        rc = B.lib().skv_page_compact(self.pool_pages, self.n_requests, self._table, self._stride, self.max_pages, n_pages.data_ptr(),
+                                      table_out.data_ptr(), out, free_pages.data_ptr(), size, free_state.data_ptr(),
+                                      free_state_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), room, self._status,
+                                      self._workspace, self._workspace_bytes, _stream_of(stream, dev))
+        B.check("skv_page_compact", rc)
+
 
 class PagePool(PageTable):
     """A PageTable with its page counts and its ring of free pages: all pages free
-    at first, counts swapped by every step."""
+    at first, counts swapped by every step. Rows that share pages (fork) give them back when the last of
+    them has ended."""
 
     def __init__(self, n_requests: int, max_pages: int, page_tokens: int, pool_pages: int, device="cuda"):
         super().__init__(torch.full((n_requests, max_pages), -1, dtype=torch.int32, device=device), page_tokens,
@@ -120,6 +183,7 @@ class PagePool(PageTable):
         self.free_pages = torch.arange(pool_pages, dtype=torch.int32, device=device)
         self.free_state = torch.tensor([0, pool_pages], dtype=torch.int32, device=device)
         self._next = (torch.empty_like(self.n_pages), torch.empty_like(self.free_state))
+        self._shared = False
         self._settle()
 
     def step(self, ctx_len, new_len, max_new: int, check: bool = True, stream=None):
@@ -129,6 +193,9 @@ class PagePool(PageTable):
         dev = self.block_table.device
         if _capturing(stream):
             raise ValueError("PagePool.step swaps its counts on the host; capture map_into")
+        if self._shared:
+            # a page of an ended request may be another one's: the map would give it back all the same
+            self.fork(None, ctx_len, check=check, stream=stream)
         cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
         slots = torch.empty(max_new, dtype=torch.int64, device=dev)
         _after_current(stream)
@@ -143,6 +210,58 @@ class PagePool(PageTable):
             cu.record_stream(stream)
             slots.record_stream(stream)
         return cu, slots
+
+    def fork(self, parents, ctx_len, trim: bool = False, check: bool = True, stream=None):
+        """Row s goes on from row parents[s] (None: from itself; -1 or ctx_len < 0: it ends) and shares its
+        full pages. Returns (ctx_len of the new rows, copy_src, copy_dst, copy_tokens): give the
+        last three to copy of every layer's PagedKV before the rows are used. The block_table is
+        rewritten in place. Not for a capture: capture fork_into."""
+        if _capturing(stream):
+            raise ValueError("PagePool.fork swaps its counts on the host; capture fork_into")
+        ctx, src, dst, tokens = torch.empty((4, self.n_requests), dtype=torch.int32, device=self.block_table.device).unbind()
+        table = self.block_table.clone()
+        if self.workspace is None:
+            self._make_workspace(stream)
+        _after_current(stream)
+        self.fork_into(parents, ctx_len, self.n_pages, self.free_pages, self.free_state, table, self._next[0], ctx, self._next[1], src, dst,
+                       tokens, trim=trim, stream=stream)
+        self._take(table, self._next[0], stream)
+        self._shared = True
+        if check:
+            self.check_status("skv_page_fork", stream)
+        elif stream is not None:
+            for t in (table, ctx, src, dst, tokens):
+                t.record_stream(stream)
+        return ctx, src, dst, tokens
+
+    def compact(self, check: bool = True, stream=None):
+        """The held pages move to the front of the pool. Returns (copy_src, copy_dst): give them to
+        copy of every layer's PagedKV before the pages are used. Not for a capture."""
+        if _capturing(stream):
+            raise ValueError("PagePool.compact swaps its counts on the host; capture compact_into")
+        src, dst = torch.empty((2, self.pool_pages), dtype=torch.int32, device=self.block_table.device).unbind()
+        table = self.block_table.clone()
+        if self.workspace is None:
+            self._make_workspace(stream)
+        _after_current(stream)
+        self.compact_into(self.n_pages, self.free_pages, self.free_state, table, self._next[1], src, dst, stream=stream)
+        self._take(table, self.n_pages, stream)
+        if check:
+            self.check_status("skv_page_compact", stream)
+        elif stream is not None:
+            for t in (table, src, dst):
+                t.record_stream(stream)
+        return src, dst
+
+    def _take(self, table, n_pages, stream):
+        """The rows of `table`, n_pages (self.n_pages, or what a call left in _next) and the ring state
+        that the call left become the pool's."""
+        with torch.cuda.stream(stream):
+            self.block_table.copy_(table)
+        spare = self._next[0] if n_pages is self.n_pages else self.n_pages
+        now = (spare, self.free_state)
+        self.n_pages, self.free_state = n_pages, self._next[1]
+        self._next = now
 
 
 class PagedKV(_Status):
@@ -224,6 +343,79 @@ class PagedKV(_Status):
         """append_into, waited for and checked."""
         self.append_into(k, v, slots, rows, stream)
         self.check_status("skv_cache_append", stream)
+
+    def rotate_append_into(self, rotary, q, k, v, positions, slots, q_out, stream=None):
+        """Enqueue skv_rotate_append: the heads of q and k normalised and rotated (`rotary`, a Rotary),
+        q into q_out (contiguous, of q's shape; None with q None: no queries), k and v into the slots as
+        append_into writes them. positions: int32 [n], or [n_axes][n]; -1 in slots: queries only."""
+        shape, stride, dev = k.shape, k.stride(), self._device
+        if v.shape != shape or v.stride() != stride or k.dtype is not _BF16 or v.dtype is not _BF16 or k.get_device() != dev \
+                or v.get_device() != dev or len(shape) != 3 or shape[1:] != self._row_shape or stride[2] != 1:
+            raise ValueError("k and v must be bf16 tensors [n][%d][%d] on the pools' device, of the same strides, the last 1"
+                             % tuple(self._row_shape))
+        n = shape[0]
+        if rotary._device != dev or rotary.head_dim != self.head_dim:
+            raise ValueError("the Rotary must be on the pools' device and of their head_dim")
+        q_ptr = out_ptr = None
+        heads = q_row = q_head = 0
+        if q is not None:
+            q_shape, q_stride = q.shape, q.stride()
+            if len(q_shape) != 3 or q.dtype is not _BF16 or q.get_device() != dev or q_shape[0] != n or q_shape[2] != self.head_dim \
+                    or q_stride[2] != 1:
+                raise ValueError(f"q must be a bf16 tensor [{n}][q_heads][{self.head_dim}] on cuda:{dev}")
+            if q_out is None or q_out.shape != q_shape or q_out.dtype is not _BF16 or q_out.get_device() != dev or not q_out.is_contiguous():
+                raise ValueError("q_out must be a contiguous bf16 tensor of q's shape and device")
+            q_ptr, out_ptr, heads, q_row, q_head = q.data_ptr(), q_out.data_ptr(), q_shape[1], q_stride[0], q_stride[1]
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        _check_words("positions", _I32, rotary.n_axes * n, dev, positions)
+        _check_words("slots", _I64, n, dev, slots)
+        rc = B.lib().skv_rotate_append(self._ref, rotary._ref, q_ptr, q_row, q_head, heads, k.data_ptr(), v.data_ptr(), stride[0], stride[1],
+                                       positions.data_ptr(), slots.data_ptr(), n, out_ptr, self._status, _stream_of(stream, dev))
+        B.check("skv_rotate_append", rc)
+
+    def rotate_append(self, rotary, q, k, v, positions, slots, stream=None):
+        """rotate_append_into a new tensor, waited for and checked; returns the queries."""
+        out = None if q is None else torch.empty(q.shape, dtype=_BF16, device=q.device)
+        _after_current(stream)
+        self.rotate_append_into(rotary, q, k, v, positions, slots, out, stream)
+        self.check_status("skv_rotate_append", stream)
+        return out
+
+    def move_into(self, cu_new, rows, slots, kept, stream=None):
+        """Enqueue skv_cache_move: the accepted tokens' K and V to the places that `kept` names (rows and
+        kept as Verifier.verify_into leaves them, slots those of the new tokens)."""
+        n, dev = rows.numel(), self._device
+        _check_words("rows", _I32, n, dev, rows)
+        _check_words("slots and kept", _I64, n, dev, slots, kept)
+        requests = cu_new.numel() - 1
+        if requests < 0:
+            raise ValueError("cu_new needs an entry")
+        _check_words("cu_new", _I32, requests + 1, dev, cu_new)
+        rc = B.lib().skv_cache_move(self._ref, requests, cu_new.data_ptr(), n, rows.data_ptr(), slots.data_ptr(), kept.data_ptr(),
+                                    self._status, _stream_of(stream, dev))
+        B.check("skv_cache_move", rc)
+
+    def move(self, cu_new, rows, slots, kept, stream=None):
+        """move_into, waited for and checked."""
+        self.move_into(cu_new, rows, slots, kept, stream)
+        self.check_status("skv_cache_move", stream)
+
+    def copy_into(self, src, dst, tokens=None, stream=None):
+        """Enqueue skv_cache_copy: K and V pages src (int32, -1 skips) to pages dst, the first tokens[i]
+        tokens of each (None: whole pages)."""
+        n, dev = src.numel(), self._device
+        _check_words("src and dst", _I32, n, dev, src, dst)
+        if tokens is not None:
+            _check_words("tokens", _I32, n, dev, tokens)
+            tokens = tokens.data_ptr()
+        rc = B.lib().skv_cache_copy(self._ref, src.data_ptr(), dst.data_ptr(), tokens, n, self._status, _stream_of(stream, dev))
+        B.check("skv_cache_copy", rc)
+
+    def copy(self, src, dst, tokens=None, stream=None):
+        """copy_into, waited for and checked."""
+        self.copy_into(src, dst, tokens, stream)
+        self.check_status("skv_cache_copy", stream)
 
     def attend_into(self, q, ctx_len, cu_new, out, mask=None, max_nodes: int | None = None,
                     scale: float | None = None, lse=None, stream=None):
