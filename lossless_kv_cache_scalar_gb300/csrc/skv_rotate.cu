@@ -21,6 +21,7 @@ struct RotateArgs {
     uint16_t *q_out;
     uint32_t n_q_heads, n_heads, head_dim;
     uint32_t n, parts;                                                  // rows, warps per row
+    uint32_t q_steps, kv_steps;                                         // a warp's steps over the heads of a kind
     FastDiv by_parts;
     // rotation
     const uint64_t *turns;
@@ -40,40 +41,52 @@ struct RotateArgs {
     uint32_t checked;                                                   // 1: block 0 reports the errors
 };
 
-constexpr uint32_t kRotateThreads = 256;
+constexpr uint32_t kRotateThreads = 256, kRotateWarps = kRotateThreads / 32u, kRotateBlocks = 3;      // blocks per SM
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
+// Two binary32 numbers that one instruction works on; each is rounded as by itself.
+__device__ __forceinline__ uint64_t bits2(float2 a) { return (uint64_t)__float_as_uint(a.y) << 32 | __float_as_uint(a.x); }
+__device__ __forceinline__ float2 floats2(uint64_t b) { return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return floats2(r);
+}
+
+__device__ __forceinline__ uint32_t pack2(float2 x) {
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
     return r;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float *x) {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(a[i] << 16);
-        x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-    }
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float2 *x) {
+    x[0] = unpack2(w.x), x[1] = unpack2(w.y), x[2] = unpack2(w.z), x[3] = unpack2(w.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float *x) {
-    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-}
+__device__ __forceinline__ uint4 pack8(const float2 *x) { return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3])); }
 
-__device__ __forceinline__ uint2 quantise8(const float *x, const ScaleOf &s) {
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        o[i] = e4m3_of(x[4 * i], s) | (e4m3_of(x[4 * i + 1], s) << 8) | (e4m3_of(x[4 * i + 2], s) << 16) |
-               (e4m3_of(x[4 * i + 3], s) << 24);
-    return make_uint2(o[0], o[1]);
+__device__ __forceinline__ uint2 quantise8(const float2 *x, const ScaleOf &s) {
+    return make_uint2(e4m3x4_of(x[0], x[1], s), e4m3x4_of(x[2], x[3], s));
 }
 
 // LANES lanes to a head.
 template <uint32_t LANES, bool E4M3>
-__global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kRotateThreads, kRotateBlocks) rotate_kernel(const RotateArgs a) {
     constexpr uint32_t HPW = 32u / LANES;
+    __shared__ float4 weight[2][16 * LANES / 4];                        // norms of q and k
+    // cosines and sines of four frequencies of each unit side by side, a unit's eight in two rows
+    __shared__ float4 cosine[kRotateWarps][2 * LANES], sine[kRotateWarps][2 * LANES];
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, u = lane % LANES, own = lane / LANES;
+    if (threadIdx.x < a.head_dim / 4u) {
+        if (a.q_norm) weight[0][threadIdx.x] = __ldg(reinterpret_cast<const float4 *>(a.q_norm) + threadIdx.x);
+        if (a.k_norm) weight[1][threadIdx.x] = __ldg(reinterpret_cast<const float4 *>(a.k_norm) + threadIdx.x);
+    }
     if (a.checked && blockIdx.x == 0) {
         // loads of eight rounds in flight at once (checked: n <= 2,048)
         bool bad = false;
@@ -86,113 +99,135 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateArgs
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
     }
-    const uint64_t item = (uint64_t)blockIdx.x * (kRotateThreads / 32u) + (threadIdx.x >> 5);
-    if (item >= (uint64_t)a.n * a.parts) return;
-    const uint32_t lane = threadIdx.x & 31u, u = lane % LANES, own = lane / LANES;
-    const uint32_t i = item >> 31 ? (uint32_t)(item / a.parts) : div_by((uint32_t)item, a.by_parts);
-    const uint32_t part = (uint32_t)(item - (uint64_t)i * a.parts);
+    __syncthreads();
     const bool live = u < a.head_dim / 16u;
     const bool turned = u < a.rot_units;
     // channels of the unit's two vectors
     const uint32_t lo = turned && !a.interleaved ? 8u * u : 16u * u;
     const uint32_t hi = lo + (turned && !a.interleaved ? 8u * a.rot_units : 8u);
-
-    const int64_t slot = __ldg(a.slots + i);
-    float c[8], s[8];
-    if (turned) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t ax = a.axis ? __ldg(a.axis + 8u * u + j) : 0u;
-            if (ax >= a.n_axes) ax = 0u;
-            const int64_t pos = __ldg(a.positions + (uint64_t)ax * a.n + i);
-            const uint64_t t = __ldg(a.turns + 8u * u + j) * (uint64_t)pos;
-            sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s[j], &c[j]);
-            c[j] *= a.amplitude;
-            s[j] *= a.amplitude;
-        }
-    }
-    uint64_t dst = 0;
-    bool to_pages = slot >= 0;
-    if (to_pages && (uint64_t)slot >= a.pool_tokens) {
-        to_pages = false;
-        if (!a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
-    }
-    if (to_pages) {
-        const uint64_t p = a.pool_tokens >> 31 ? (uint64_t)slot / a.page.d : div_by((uint32_t)slot, a.page);
-        dst = p * a.page_stride + ((uint64_t)slot - p * a.page.d) * a.token_stride;
-    }
-    const uint32_t heads = a.n_q_heads + (to_pages ? 2u * a.n_heads : 0u);
-    float w[16];
-    uint32_t kind = 3u;                                     // whose weights w holds
+    const uint64_t items = (uint64_t)a.n * a.parts;
 #pragma unroll 1
-    for (uint32_t h0 = part * HPW; h0 < heads; h0 += a.parts * HPW) {
-        const uint32_t h = h0 + own;
-        const bool on = live && h < heads;
-        const uint32_t what = h < a.n_q_heads ? 0u : h < a.n_q_heads + a.n_heads ? 1u : 2u;
-        const uint32_t g = what == 0 ? h : what == 1 ? h - a.n_q_heads : h - a.n_q_heads - a.n_heads;
-        const uint16_t *src = what == 0 ? a.q + (uint64_t)i * a.q_row_stride + (uint64_t)g * a.q_head_stride
-                                        : (what == 1 ? a.k : a.v) + (uint64_t)i * a.row_stride + (uint64_t)g * a.head_stride;
+    for (uint64_t item = (uint64_t)blockIdx.x * kRotateWarps + warp; item < items; item += (uint64_t)gridDim.x * kRotateWarps) {
+        const uint32_t i = items >> 31 ? (uint32_t)(item / a.parts) : div_by((uint32_t)item, a.by_parts);
+        const uint32_t part = (uint32_t)(item - (uint64_t)i * a.parts);
+        const int64_t slot = __ldg(a.slots + i);
+        bool to_pages = slot >= 0;
+        if (to_pages && (uint64_t)slot >= a.pool_tokens) {
+            to_pages = false;
+            if (!a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
+        }
+        // Steps of HPW heads of one kind (0 queries, 1 keys, 2 values).
+        const uint32_t steps = a.q_steps + (to_pages ? 2u * a.kv_steps : 0u);
+        const auto kind_of = [&](uint32_t t, uint32_t *g0) {
+            const uint32_t what = t < a.q_steps ? 0u : t < a.q_steps + a.kv_steps ? 1u : 2u;
+            *g0 = (what == 0 ? t : what == 1 ? t - a.q_steps : t - a.q_steps - a.kv_steps) * HPW;
+            return what;
+        };
         uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-        if (on) {
+        const auto fetch = [&](uint32_t t) {
+            uint32_t g0;
+            const uint32_t what = kind_of(t, &g0);
+            if (t >= steps || !live || g0 + own >= (what ? a.n_heads : a.n_q_heads)) return;
+            const uint16_t *row = what == 0 ? a.q + (uint64_t)i * a.q_row_stride + (uint64_t)g0 * a.q_head_stride
+                                            : (what == 1 ? a.k : a.v) + (uint64_t)i * a.row_stride + (uint64_t)g0 * a.head_stride;
+            const uint16_t *src = row + own * (what ? a.head_stride : a.q_head_stride);
             x0 = *reinterpret_cast<const uint4 *>(src + lo);
             x1 = *reinterpret_cast<const uint4 *>(src + hi);
+        };
+        fetch(part);
+        __syncwarp();                                   // the last row's angles are read
+#pragma unroll 1
+        for (uint32_t j = lane; j < 8u * a.rot_units; j += 32u) {
+            uint32_t ax = a.axis ? __ldg(a.axis + j) : 0u;
+            if (ax >= a.n_axes) ax = 0u;
+            const int64_t pos = __ldg(a.positions + (uint64_t)ax * a.n + i);
+            const uint64_t t = __ldg(a.turns + j) * (uint64_t)pos;
+            float2 z;
+            sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &z.y, &z.x);
+            const uint32_t at = ((j >> 2 & 1u) * LANES + (j >> 3)) * 4u + (j & 3u);
+            reinterpret_cast<float *>(cosine[warp])[at] = z.x * a.amplitude;
+            reinterpret_cast<float *>(sine[warp])[at] = z.y * a.amplitude;
         }
-        float x[16];
-        unpack8(x0, x);
-        unpack8(x1, x + 8);
-        const float *norm = what == 0 ? a.q_norm : a.k_norm;
-        if (on && kind != what && what < 2u && norm) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 y = __ldg(reinterpret_cast<const float4 *>(norm + (j < 2 ? lo : hi)) + (j & 1));
-                w[4 * j] = y.x, w[4 * j + 1] = y.y, w[4 * j + 2] = y.z, w[4 * j + 3] = y.w;
-            }
+        __syncwarp();
+        uint64_t dst = 0;
+        if (to_pages) {
+            const uint64_t p = a.pool_tokens >> 31 ? (uint64_t)slot / a.page.d : div_by((uint32_t)slot, a.page);
+            dst = p * a.page_stride + ((uint64_t)slot - p * a.page.d) * a.token_stride;
         }
-        kind = what;
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sum = fmaf(x[j], x[j], sum);
-#pragma unroll
-        for (uint32_t d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        if (!on) continue;
-        if (what < 2u) {
-            if (norm) {
-                const float r = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= r * w[j];
+#pragma unroll 1
+        for (uint32_t t = part; t < steps; t += a.parts) {
+            uint32_t g0;
+            const uint32_t what = kind_of(t, &g0), g = g0 + own;
+            const bool on = live && g < (what ? a.n_heads : a.n_q_heads);
+            if (!E4M3 && what == 2u) {                  // bits as they are
+                uint8_t *to = a.v_pages + dst + (uint64_t)g * a.page_head_stride;
+                if (on) {
+                    *reinterpret_cast<uint4 *>(to + 2u * lo) = x0;
+                    *reinterpret_cast<uint4 *>(to + 2u * hi) = x1;
+                }
+                fetch(t + a.parts);
+                continue;
             }
-            if (turned) {
-                if (a.interleaved) {
+            float2 x[8];
+            unpack8(x0, x);
+            unpack8(x1, x + 4);
+            fetch(t + a.parts);
+            if (what < 2u) {
+                if (what ? a.k_norm != nullptr : a.q_norm != nullptr) {
+                    float2 sum2 = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float p = x[2 * j], q = x[2 * j + 1];
-                        x[2 * j] = p * c[j] - q * s[j];
-                        x[2 * j + 1] = p * s[j] + q * c[j];
+                    for (int j = 1; j < 8; ++j) sum2 = fma2(x[j], x[j], sum2);
+                    float sum = sum2.x + sum2.y;
+#pragma unroll
+                    for (uint32_t d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+                    const float r = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
+                    const float2 r2 = make_float2(r, r);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 w = live ? weight[what][((j < 2 ? lo : hi) >> 2) + (j & 1)] : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[2 * j] = mul2(mul2(x[2 * j], r2), make_float2(w.x, w.y));
+                        x[2 * j + 1] = mul2(mul2(x[2 * j + 1], r2), make_float2(w.z, w.w));
                     }
-                } else {
+                }
+                if (turned) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float p = x[j], q = x[j + 8];
-                        x[j] = p * c[j] - q * s[j];
-                        x[j + 8] = p * s[j] + q * c[j];
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 c = cosine[warp][k * LANES + u], s = sine[warp][k * LANES + u];
+                        if (a.interleaved) {
+                            const float cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 p = x[4 * k + j];
+                                x[4 * k + j] = fma2(p, make_float2(cs[j], cs[j]), mul2(make_float2(p.y, p.x), make_float2(-ss[j], ss[j])));
+                            }
+                        } else {
+                            const float2 c2[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)}, s2[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float2 p = x[2 * k + j], q = x[2 * k + j + 4];
+                                x[2 * k + j] = fma2(p, c2[j], mul2(q, make_float2(-s2[j].x, -s2[j].y)));
+                                x[2 * k + j + 4] = fma2(p, s2[j], mul2(q, c2[j]));
+                            }
+                        }
                     }
                 }
             }
-        }
-        if (what == 0) {
-            uint16_t *out = a.q_out + ((uint64_t)i * a.n_q_heads + g) * a.head_dim;
-            *reinterpret_cast<uint4 *>(out + lo) = pack8(x);
-            *reinterpret_cast<uint4 *>(out + hi) = pack8(x + 8);
-        } else {
-            uint8_t *to = (what == 1 ? a.k_pages : a.v_pages) + dst + (uint64_t)g * a.page_head_stride;
-            if (E4M3) {
-                const float *scale = what == 1 ? a.k_scale : a.v_scale;
-                const ScaleOf sc = scale_of(scale ? __ldg(scale + g) : 1.0f);
-                *reinterpret_cast<uint2 *>(to + lo) = quantise8(x, sc);
-                *reinterpret_cast<uint2 *>(to + hi) = quantise8(x + 8, sc);
+            if (!on) continue;
+            if (what == 0) {
+                uint16_t *out = a.q_out + ((uint64_t)i * a.n_q_heads + g) * a.head_dim;
+                *reinterpret_cast<uint4 *>(out + lo) = pack8(x);
+                *reinterpret_cast<uint4 *>(out + hi) = pack8(x + 4);
             } else {
-                *reinterpret_cast<uint4 *>(to + 2u * lo) = what == 1 ? pack8(x) : x0;
-                *reinterpret_cast<uint4 *>(to + 2u * hi) = what == 1 ? pack8(x + 8) : x1;
+                uint8_t *to = (what == 1 ? a.k_pages : a.v_pages) + dst + (uint64_t)g * a.page_head_stride;
+                if (E4M3) {
+                    const float *scale = what == 1 ? a.k_scale : a.v_scale;
+                    const ScaleOf sc = scale_of(scale ? __ldg(scale + g) : 1.0f);
+                    *reinterpret_cast<uint2 *>(to + lo) = quantise8(x, sc);
+                    *reinterpret_cast<uint2 *>(to + hi) = quantise8(x + 4, sc);
+                } else {
+                    *reinterpret_cast<uint4 *>(to + 2u * lo) = pack8(x);
+                    *reinterpret_cast<uint4 *>(to + 2u * hi) = pack8(x + 4);
+                }
             }
         }
     }
@@ -243,15 +278,29 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     const uint32_t lanes = units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : units <= 8 ? 8 : 16;
     // A warp takes a row's heads one group after the other; with few rows a row's groups go to several
     // warps, up to 16 warps per SM, each of which works the angles out again.
-    const uint32_t groups = (n_q_heads + 2u * cache->n_heads + 32u / lanes - 1u) / (32u / lanes);
+    const uint32_t per_step = 32u / lanes, q_steps = (n_q_heads + per_step - 1u) / per_step;
+    const uint32_t kv_steps = (cache->n_heads + per_step - 1u) / per_step, groups = q_steps + 2u * kv_steps;
     uint32_t parts = 16u * sms / n;
-    parts = parts < 1 ? 1 : parts > groups ? groups : parts;
+    if (parts < 2u) {
+        // From there on the warps of a full GPU make several rounds: two or three parts where the last
+        // round would be a poor one (twice the angles cost 2%, three times 8%).
+        const uint64_t warps = (uint64_t)kRotateBlocks * kRotateWarps * sms;
+        uint64_t best = ~uint64_t(0);
+        for (uint32_t p = 1; p <= 3u; ++p) {
+            const uint64_t cost = ((uint64_t)n * p + warps - 1u) / warps * (99u + p * p) * (6u / p);
+            if (cost < best) {
+                best = cost;
+                parts = p;
+            }
+        }
+    }
+    parts = parts > groups ? groups : parts;
     RotateArgs a{};
     a.q = static_cast<const uint16_t *>(q), a.k = static_cast<const uint16_t *>(k), a.v = static_cast<const uint16_t *>(v);
     a.q_row_stride = q_row_stride, a.q_head_stride = q_head_stride, a.row_stride = row_stride, a.head_stride = row_head_stride;
     a.q_out = static_cast<uint16_t *>(q_out);
     a.n_q_heads = n_q_heads, a.n_heads = cache->n_heads, a.head_dim = cache->head_dim;
-    a.n = n, a.parts = parts, a.by_parts = fast_div(parts);
+    a.n = n, a.parts = parts, a.by_parts = fast_div(parts), a.q_steps = q_steps, a.kv_steps = kv_steps;
     a.turns = rotary->turns, a.axis = rotary->axis, a.q_norm = rotary->q_norm, a.k_norm = rotary->k_norm, a.positions = positions;
     a.rot_units = rotary->rot_dim / 16u, a.n_axes = rotary->n_axes, a.interleaved = rotary->interleaved;
     a.eps = rotary->eps, a.inv_dim = 1.0f / (float)cache->head_dim, a.amplitude = rotary->amplitude;
@@ -261,8 +310,8 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     a.pool_tokens = (uint64_t)cache->n_pages * cache->page_tokens;
     a.slots = slots, a.status = status, a.checked = n <= 2048u;
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    const uint64_t blocks = ((uint64_t)n * parts + kRotateThreads / 32u - 1) / (kRotateThreads / 32u);
-    const unsigned grid = (unsigned)blocks;               // below 2^29
+    const uint64_t blocks = ((uint64_t)n * parts + kRotateWarps - 1) / kRotateWarps;
+    const unsigned grid = (unsigned)(blocks < kRotateBlocks * sms ? blocks : kRotateBlocks * sms);
     bool ok;
     switch (lanes) {
         case 1: ok = launch_rotate<1>(a, c.e4m3, grid, st); break;

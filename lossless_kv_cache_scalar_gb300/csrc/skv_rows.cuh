@@ -45,6 +45,24 @@ __device__ __forceinline__ uint32_t e4m3_of(float value, const ScaleOf &c) {
 
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
+// Four codes, the same as e4m3_of's. The product with the reciprocal is within 2^-22 of the real quotient, so where a
+// little more and a little less than it have one code, that is the code; only a value next to a border (one
+// in some 60,000) takes the long way.
+__device__ __forceinline__ uint32_t e4m3x4_of(const float2 &a, const float2 &b, const ScaleOf &c) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float d = i ? 1.0f - 0x1p-21f : 1.0f + 0x1p-21f, r = c.r;
+        uint16_t lo, hi;
+        const float x = a.x * c.by * r, y = a.y * c.by * r, z = b.x * c.by * r, t = b.y * c.by * r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y * d), "f"(x * d));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(t * d), "f"(z * d));
+        w[i] = (uint32_t)hi << 16 | lo;
+    }
+    if (w[0] == w[1]) return w[0];
+    return e4m3_of(a.x, c) | (e4m3_of(a.y, c) << 8) | (e4m3_of(b.x, c) << 16) | (e4m3_of(b.y, c) << 24);
+}
+
 inline bool device_sms(uint32_t *sms) {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

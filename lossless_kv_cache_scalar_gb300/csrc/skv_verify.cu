@@ -1,12 +1,17 @@
 // skv_verify.cu -- verification of drafted trees.
 //
-// A cluster of CTAs takes a request. Every CTA walks the tree for itself, from the same few scalars (the
+// A cluster of CTAs takes a request. Every warp walks the tree for itself, from the same few scalars (the
 // probabilities of the drafted tokens, all gathered at once before the walk): nothing has to be
-// passed on. Only a sum over the vocabulary is shared: each CTA sums its range of the row as whole numbers of
-// 2^-44, so that no order of adding matters, and hands the sum to the others through distributed
-// shared memory. The CTA and the warp in whose ranges the drawn number falls find the token.
+// passed on. Only a sum over the vocabulary is shared: each warp sums its range of the row as whole numbers of
+// 2^-44, so that no order of adding matters, and hands the sum to every CTA through distributed
+// shared memory. The warp in whose range the drawn number falls finds the token.
+//
+// Rows come by asynchronous copies into shared memory, all of a CTA's part on its way at once; where it fits, a
+// further sum over the same node, after another rejection, reads nothing.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "skv_rows.cuh"
 
@@ -14,11 +19,13 @@ namespace skv {
 
 namespace cg = cooperative_groups;
 
+bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready);      // skv_attend.cu
+
 constexpr uint32_t kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32u;
-constexpr uint32_t kNodes = 512;                 // nodes of a request that are gathered at once
+constexpr uint32_t kNodes = 256;                 // nodes of a request that are gathered at once
 constexpr uint32_t kGone = 4096;                 // nodes of a request without draft probabilities
-constexpr uint32_t kVerifyCluster = 8;
-constexpr float kUnit = 0x1p44f;
+constexpr uint32_t kVerifyCluster = 16;
+constexpr uint32_t kRowBytes = 80u * 1024u;      // shared memory for rows: two CTAs to an SM
 
 struct VerifyArgs {
     const void *probs, *draft;
@@ -32,20 +39,81 @@ struct VerifyArgs {
     int64_t *kept;
     int32_t *ctx_out, *next, *status;
     uint32_t checked;                            // 1: a cluster behind the requests' reports the errors
+    uint32_t per_cta, per_chunk, per_warp;       // elements: of a CTA's part, of what it holds at a time, of a warp's run of that
 };
 
-// A probability as it counts: the nearer end outside [0, 1], NaN as 0.
-__device__ __forceinline__ float clamp01(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }
-__device__ __forceinline__ float prob_of(const float *p) { return clamp01(__ldg(p)); }
-__device__ __forceinline__ float prob_of(const uint16_t *p) { return clamp01(__uint_as_float((uint32_t)__ldg(p) << 16)); }
+// A probability as it counts: the nearer end outside [0, 1], NaN as 0 (what saturation does).
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
+__device__ __forceinline__ float prob(uint16_t x) { return __saturatef(__uint_as_float((uint32_t)x << 16)); }
 
-__device__ __forceinline__ uint64_t units_of_prob(float r) { return (uint64_t)__float2ull_rn(r * kUnit); }
+// m elements from src into dst, from dst[returned] on, by the CTA: 16 bytes at a time, asynchronously, where src is
+// aligned, the ends one by one.
+template <typename T>
+__device__ __forceinline__ uint32_t fetch_run(T *dst, const T *src, uint32_t m) {
+    constexpr uint32_t V = 16u / sizeof(T);
+    const uint32_t tid = threadIdx.x, shift = (uint32_t)((16u - ((uintptr_t)src & 15u)) & 15u) / (uint32_t)sizeof(T);
+    const uint32_t lead = min(shift, m), units = (m - lead) / V, done = lead + units * V, at = V - shift;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + V);
+    for (uint32_t i = tid; i < units; i += kVerifyThreads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * i), "l"(src + lead + i * V) : "memory");
+    if (tid < lead) dst[at + tid] = __ldg(src + tid);
+    if (tid >= 32u && tid - 32u < m - done) dst[at + done + tid - 32u] = __ldg(src + done + tid - 32u);
+    return at;
+}
 
-// R(y) of a row: with c 0 (no rejection yet) p itself, whatever q holds.
-__device__ __forceinline__ float rest_of(float p, float q, float c) { return fmaxf(fmaf(-c, q, p), 0.0f); }
+// R(y) = max(p - c q, 0), in [0, 1] like p.
+__device__ __forceinline__ float rest_of(float p, float q, float c) {
+    float r;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(-c), "f"(q), "f"(p));
+    return r;
+}
 
-struct Node {
-    int32_t parent, token;
+// Sums of numbers of [0, 1] in units of 2^-44, each rounded to one, ties to even, without a conversion (a quarter
+// of the rate of an addition at best): r + 3 is r rounded to 2^-22, in the low bits of its word; what that
+// leaves, at most 2^-23 and exact, added to 1.5 2^-21 is rounded to 2^-44. The two words are summed by
+// themselves, modulo 2^32: up to 512 numbers, of at most 2^22 and 2^21 units beyond the constants, leave no doubt.
+constexpr uint32_t kHigh = 0x40400000u, kLow = 0x35400000u;          // 3 and 1.5 2^-21
+struct Units {
+    uint32_t high, low;
+};
+__device__ __forceinline__ void add_units(Units &u, float r) {
+    const float t = r + __uint_as_float(kHigh), rest = r - (t - __uint_as_float(kHigh));
+    u.high += __float_as_uint(t) - kHigh;
+    u.low += __float_as_uint(rest + __uint_as_float(kLow)) - kLow;
+}
+__device__ __forceinline__ unsigned long long total_of(uint64_t high, int64_t low) { return (high << 22) + (unsigned long long)low; }
+__device__ __forceinline__ unsigned long long units_of_prob(float r) {
+    Units u{0u, 0u};
+    add_units(u, r);
+    return total_of(u.high, (int32_t)u.low);
+}
+// The warp's sum of up to 512 numbers per lane (high below 2^31, low of either sign): in pieces that
+// a 32-bit reduction holds.
+__device__ __forceinline__ unsigned long long warp_total(const Units &u) {
+    const uint32_t a = __reduce_add_sync(~0u, u.high >> 16), b = __reduce_add_sync(~0u, u.high & 0xFFFFu);
+    const int32_t c = __reduce_add_sync(~0u, (int32_t)u.low >> 16);
+    const uint32_t d = __reduce_add_sync(~0u, u.low & 0xFFFFu);
+    return total_of(((uint64_t)a << 16) + b, ((int64_t)c << 16) + d);
+}
+
+__device__ __forceinline__ unsigned long long sum_of_warp(unsigned long long x) {
+#pragma unroll
+    for (uint32_t d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+    return x;
+}
+__device__ __forceinline__ unsigned long long prefix_of_warp(unsigned long long x) {
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+        const unsigned long long y = __shfl_up_sync(~0u, x, d);
+        if ((threadIdx.x & 31u) >= d) x += y;
+    }
+    return x;
+}
+
+// A node's token, its u, and the token's probabilities at the parent. The sign of u tells whether the token is
+// accepted as the first of its siblings to be tried.
+struct __align__(16) Node {
+    int32_t token;
     float u, p, q;
 };
 
@@ -68,19 +136,39 @@ __device__ __forceinline__ bool node_ok(const VerifyArgs &a, int32_t parent, int
     return (uint32_t)token < a.vocab && (uint32_t)parent < i;
 }
 
+// u q Z < r s, with Z in units of 2^-44 and the products in binary64. Those take a warp most of a microsecond a test, so
+// binary32 decides where it can: each of its products is off by 2^-21 at most where it is not tiny.
+__device__ __forceinline__ int decided(float left, float right) {
+    if (fmaxf(left, right) > 0x1p-90f) {
+        if (left < right * (1.0f - 0x1p-20f)) return 1;
+        if (left * (1.0f - 0x1p-20f) > right) return 0;
+    }
+    return -1;
+}
+// `whole`: s is 1.
+__device__ __forceinline__ bool below(float u, float q, unsigned long long Z, float r, bool whole, double s) {
+    const int d = decided(u * q * (__ull2float_rn(Z) * 0x1p-44f), whole ? r : r * (float)s);
+    return d >= 0 ? d : (double)u * (double)q * ((double)Z * 0x1p-44) < (double)r * s;
+}
+// u Z < r
+__device__ __forceinline__ bool below(float u, double Z, float r) {
+    const int d = decided(u * (float)Z, r);
+    return d >= 0 ? d : (double)u * Z < (double)r;
+}
+
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t request = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     __shared__ Node node[kNodes];
-    __shared__ unsigned long long warp_sum[kVerifyWarps + 1];
-    __shared__ unsigned long long cta_sum[2][kVerifyCluster];
+    __shared__ int32_t parent[kNodes];
+    extern __shared__ uint4 row_memory[];
+    __shared__ unsigned long long sums[2][kVerifyCluster * kVerifyWarps];      // of every warp of the cluster
+    __shared__ unsigned long long run_sum[kVerifyWarps];
     __shared__ int32_t gone[DRAFT ? 1 : kGone];  // rejected tokens of the node (no draft probabilities)
     __shared__ struct {
-        uint32_t todo, cur, at, taken, n_gone;
-        float c;
-        double Z, s;
+        uint32_t cur, taken, n_gone;
     } walk;
 
     if (request == a.n_requests) {               // the errors of every request
@@ -103,26 +191,28 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
     const T *P = static_cast<const T *>(a.probs) + (uint64_t)row0 * a.probs_stride;
     const T *Q = DRAFT ? static_cast<const T *>(a.draft) + (uint64_t)row0 * a.draft_stride : nullptr;
 
-    // The scalars of nodes [first, first + kNodes).
-    const auto gather = [&](uint32_t first) {
-        const uint32_t i = first + tid;
-        if (i < n) {
-            Node x{-1, 0, __ldg(a.uniform + row0 + i), 0.0f, 0.0f};
+    // The scalars of nodes [first, first + kNodes), by `threads` threads.
+    const auto gather = [&](uint32_t first, uint32_t mine, uint32_t threads) {
+        for (uint32_t i = first + mine; i < min(n, first + kNodes); i += threads) {
+            Node x{0, __saturatef(__ldg(a.uniform + row0 + i)), 0.0f, 0.0f};
+            int32_t up = -1;
             if (i) {
-                x.parent = parent_of(a, row0, i);
+                up = parent_of(a, row0, i);
                 x.token = __ldg(a.tokens + row0 + i);
-                if (node_ok(a, x.parent, x.token, i)) {
-                    x.p = prob_of(P + (uint64_t)x.parent * a.probs_stride + x.token);
-                    if (DRAFT) x.q = prob_of(Q + (uint64_t)x.parent * a.draft_stride + x.token);
+                if (node_ok(a, up, x.token, i)) {
+                    x.p = prob(__ldg(P + (uint64_t)up * a.probs_stride + x.token));
+                    if (DRAFT) x.q = prob(__ldg(Q + (uint64_t)up * a.draft_stride + x.token));
+                    if (DRAFT ? below(x.u, x.q, 1ull << 44, x.p, true, 1.0) : x.u < x.p) x.u = -x.u;
+                    else x.u = fabsf(x.u);
                 } else {
                     bad = true;
                 }
             }
-            node[tid] = x;
+            parent[i - first] = up;
+            node[i - first] = x;
         }
     };
-    static_assert(kNodes == kVerifyThreads, "a thread per node");
-    gather(0);
+    gather(0, tid, kVerifyThreads);
 #pragma unroll 1
     for (uint32_t i = kNodes + tid; i < n; i += kVerifyThreads)
         bad |= !node_ok(a, parent_of(a, row0, i), __ldg(a.tokens + row0 + i), i);
@@ -146,206 +236,195 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
     bool started = false;
     const float u0 = node[0].u;
 
-    // Ranges of the vocabulary: a run per CTA, in it a run of whole 32s per warp.
-    const uint32_t per_warp = (a.vocab + C * kVerifyThreads - 1u) / (C * kVerifyThreads) * 32u, per_cta = per_warp * kVerifyWarps;
-    const uint32_t first = min(rank * per_cta, a.vocab), last = min(first + per_cta, a.vocab);
-    const uint32_t w0 = min(first + warp * per_warp, last), w1 = min(w0 + per_warp, last);
-    uint32_t parity = 0;
+    // A part of the vocabulary per CTA, in chunks that shared memory holds; of a chunk, a run per warp.
+    const uint32_t first = min(rank * a.per_cta, a.vocab), last = min(first + a.per_cta, a.vocab);
+    const uint32_t chunks = (a.per_cta + a.per_chunk - 1u) / a.per_chunk;
+    T *const sp = reinterpret_cast<T *>(row_memory), *const sq = sp + a.per_chunk + 32u / sizeof(T);
+    const T *run_p = sp, *run_q = sq;            // this warp's run
+    uint32_t run = 0, run0 = 0;                  // its length, and its first element
+    uint32_t parity = 0, n_gone = 0;
+    uint32_t held = ~0u;                         // whose rows, both, shared memory holds
 
-    // Sum of R over the row of `cur`: of each warp's range, of each CTA's; returns the whole.
-    const auto sum_row = [&](uint32_t cur, float c) -> unsigned long long {
-        const T *p = P + (uint64_t)cur * a.probs_stride;
-        const T *q = DRAFT ? Q + (uint64_t)cur * a.draft_stride : nullptr;
-        const bool with = DRAFT && c != 0.0f;
-        unsigned long long sum = 0;
-        constexpr uint32_t U = 8;
-#pragma unroll 1
-        for (uint32_t y = w0 + lane; y < w1; y += 32u * U) {
-            float x[U], z[U];
-#pragma unroll
-            for (uint32_t j = 0; j < U; ++j) {
-                const bool in = y + 32u * j < w1;
-                x[j] = in ? prob_of(p + y + 32u * j) : 0.0f;
-                z[j] = with && in ? prob_of(q + y + 32u * j) : 0.0f;
-            }
-#pragma unroll
-            for (uint32_t j = 0; j < U; ++j) sum += units_of_prob(rest_of(x[j], z[j], c));
-        }
-#pragma unroll
-        for (uint32_t d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        __syncthreads();                         // the last sums are read
-        if (lane == 0) warp_sum[warp] = sum;
+    const auto load = [&](uint32_t cur, uint32_t k, bool both) {
+        const uint32_t e0 = min(first + k * a.per_chunk, last), m = min(a.per_chunk, last - e0);
+        __syncthreads();                         // what was here is read
+        const uint32_t at_p = fetch_run(sp, P + (uint64_t)cur * a.probs_stride + e0, m);
+        uint32_t at_q = 0;
+        if (DRAFT && both) at_q = fetch_run(sq, Q + (uint64_t)cur * a.draft_stride + e0, m);
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        // rejected tokens weigh nothing
-        if (!DRAFT) {
-            for (uint32_t j = tid; j < walk.n_gone; j += kVerifyThreads) {
-                const uint32_t y = (uint32_t)gone[j];
-                if (y >= first && y < last) atomicAdd(&warp_sum[(y - first) / per_warp], 0ull - units_of_prob(prob_of(p + y)));
-            }
+        if (!DRAFT && n_gone) {                  // rejected tokens weigh nothing
+            for (uint32_t g = tid; g < n_gone; g += kVerifyThreads)
+                if ((uint32_t)gone[g] - e0 < m) sp[at_p + (uint32_t)gone[g] - e0] = T(0);
             __syncthreads();
         }
+        const uint32_t r0 = min(warp * a.per_warp, m);
+        run = min(a.per_warp, m - r0);
+        run0 = e0 + r0;
+        run_p = sp + at_p + r0;
+        run_q = sq + at_q + r0;
+    };
+    const auto rest = [&](uint32_t i, float c) { return DRAFT && c != 0.0f ? rest_of(prob(run_p[i]), prob(run_q[i]), c) : prob(run_p[i]); };
+    // The warp's sum of R over its run.
+    const auto sum_run = [&](float c) {
+        Units u{0u, 0u};
+        if (DRAFT && c != 0.0f) {
+#pragma unroll 4
+            for (uint32_t i = lane; i < run; i += 32u) add_units(u, rest_of(prob(run_p[i]), prob(run_q[i]), c));
+        } else {
+#pragma unroll 8
+            for (uint32_t i = lane; i < run; i += 32u) add_units(u, prob(run_p[i]));
+        }
+        return warp_total(u);
+    };
+    // Sum of R over the row of `cur`; every warp's own is in sums[parity ^ 1] then.
+    const auto sum_row = [&](uint32_t cur, float c) -> unsigned long long {
+        unsigned long long sum = 0;
+        for (uint32_t k = 0; k < chunks; ++k) {
+            if (chunks > 1u || held != cur) load(cur, k, c != 0.0f);
+            sum += sum_run(c);
+        }
+        held = DRAFT && c != 0.0f ? cur : ~0u;
         if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         started = true;
-        if (warp == 0) {
-            unsigned long long t = lane < kVerifyWarps ? warp_sum[lane] : 0ull;
-#pragma unroll
-            for (uint32_t d = 16; d; d >>= 1) t += __shfl_xor_sync(~0u, t, d);
-            if (lane < C) *cluster.map_shared_rank(&cta_sum[parity][rank], lane) = t;
-        }
+        if (lane < C) *cluster.map_shared_rank(&sums[parity][rank * kVerifyWarps + warp], lane) = sum;
         cluster.sync();
         unsigned long long whole = 0;
-        for (uint32_t j = 0; j < C; ++j) whole += cta_sum[parity][j];
+        for (uint32_t j = lane; j < C * kVerifyWarps; j += 32u) whole += sums[parity][j];
         parity ^= 1u;
-        return whole;
+        return sum_of_warp(whole);
     };
 
-    if (tid == 0) {
-        walk.cur = 0, walk.at = 1, walk.taken = 1, walk.n_gone = 0;
-        walk.c = 0.0f, walk.Z = 1.0, walk.s = 1.0;
-        if (rank == 0) a.rows[row0] = (int32_t)row0;
-    }
-    constexpr uint32_t kDone = 0, kSum = 1, kMore = 2;
-    uint32_t batch = 0;                          // first node in shared memory
+    // The walk, the same in every warp of the cluster (without draft probabilities one warp's, for the others of its CTA).
+    uint32_t batch = 0, at = 1, cur = 0, taken = 1;      // batch: first node in shared memory
+    float c = 0.0f;
     unsigned long long total = 0;
     bool fresh = false;                          // total and the sums are those of (cur, c)
-    uint32_t cur = 0;
-    float c = 0.0f;
+    double Z = 1.0, s = 1.0;                     // Z: without draft probabilities
+    bool whole = true;                           // s is 1 (a warp's test of it in binary64 costs a hundred clocks)
+    if (rank == 0 && tid == 0) a.rows[row0] = (int32_t)row0;
 #pragma unroll 1
-    while (true) {
-        __syncthreads();
-        if (warp == 0) {
-            uint32_t at = walk.at, taken = walk.taken, n_gone = walk.n_gone, todo = kDone;
-            uint32_t here = walk.cur;
-            float cc = walk.c;
-            double Z = walk.Z, s = walk.s;
-            bool have = !DRAFT || cc == 0.0f || fresh;      // Z is that of (here, cc)
-            if (fresh) Z = (double)total * 0x1p-44;
-            const uint32_t end = min(n, batch + kNodes);
+    while (DRAFT || warp == 0) {
+        // the next child
+        const uint32_t end = min(n, batch + kNodes);
+        uint32_t found = end;
 #pragma unroll 1
-            while (true) {
-                // the next child of `here`
-                uint32_t found = end;
-#pragma unroll 1
-                for (uint32_t b = at; b < end; b += 32u) {
-                    const uint32_t i = b + lane;
-                    const uint32_t m = __ballot_sync(~0u, i < end && node[i - batch].parent == (int32_t)here);
-                    if (m) {
-                        found = b + __ffs(m) - 1u;
-                        break;
-                    }
-                }
-                at = found;
-                if (found == end) {
-                    todo = end < n ? kMore : kDone;
-                    break;
-                }
-                if (!have) {
-                    todo = kSum;
-                    break;
-                }
-                const Node x = node[found - batch];
-                bool take;
-                if (DRAFT) {
-                    const double rest = (double)rest_of(x.p, x.q, cc);
-                    take = (double)x.u * (double)x.q * Z < rest * s;
-                    if (!take) {
-                        if (s > 0.0) cc = (float)((double)cc + Z / s);
-                        if (a.distinct) s = fmax(s - (double)x.q, 0.0);
-                        have = false;
-                    }
-                } else {
-                    bool again = false;
-                    for (uint32_t j = lane; j < n_gone; j += 32u) again |= gone[j] == x.token;
-                    again = __any_sync(~0u, again);
-                    const double p = again ? 0.0 : (double)x.p;
-                    take = (double)x.u * Z < p;
-                    if (!take && !again) {
-                        Z = fmax(Z - p, 0.0);
-                        if (lane == 0) gone[n_gone] = x.token;
-                        ++n_gone;
-                        __syncwarp();
-                    }
-                }
-                if (take) {
-                    if (rank == 0 && lane == 0) a.rows[row0 + taken] = (int32_t)(row0 + found);
-                    ++taken;
-                    here = found;
-                    cc = 0.0f, Z = 1.0, s = 1.0, n_gone = 0, have = true;
-                }
-                at = found + 1u;
-            }
-            if (lane == 0) {
-                walk.todo = todo, walk.cur = here, walk.at = at, walk.taken = taken, walk.n_gone = n_gone;
-                walk.c = cc, walk.Z = Z, walk.s = s;
+        for (uint32_t b = at; b < end; b += 32u) {
+            const uint32_t i = b + lane;
+            const uint32_t m = __ballot_sync(~0u, i < end && parent[i - batch] == (int32_t)cur);
+            if (m) {
+                found = b + __ffs(m) - 1u;
+                break;
             }
         }
-        __syncthreads();
-        const uint32_t todo = walk.todo;
-        fresh = fresh && cur == walk.cur && c == walk.c;
-        cur = walk.cur, c = walk.c;
-        if (todo == kDone) break;
-        if (todo == kMore) {
+        at = found;
+        if (found == end) {
+            if (end == n) break;
             batch += kNodes;
-            gather(batch);
-        } else {
-            total = sum_row(cur, c);
-            fresh = true;
+            if (DRAFT) {
+                __syncthreads();
+                gather(batch, tid, kVerifyThreads);
+                __syncthreads();
+            } else {
+                __syncwarp();
+                gather(batch, lane, 32u);
+                __syncwarp();
+            }
+            continue;
         }
+        const Node x = node[found - batch];
+        bool take;
+        if (DRAFT) {
+            if (c != 0.0f && !fresh) {
+                total = sum_row(cur, c);
+                fresh = true;
+            }
+            take = c == 0.0f ? signbit(x.u) : below(fabsf(x.u), x.q, total, rest_of(x.p, x.q, c), whole, s);
+            if (!take) {
+                // c + Z / s: c and Z are whole numbers of 2^-44 (c is 0, or from 1 on)
+                float to = c;
+                if (whole && c < 0x1p18f) to = __ull2float_rn((unsigned long long)(c * 0x1p44f) + (c == 0.0f ? 1ull << 44 : total)) * 0x1p-44f;
+                else if (s > 0.0) to = (float)((double)c + (c == 0.0f ? 1.0 : (double)total * 0x1p-44) / s);
+                fresh = fresh && to == c;
+                c = to;
+                if (a.distinct) {
+                    s = fmax(s - (double)x.q, 0.0);
+                    whole = false;
+                }
+            }
+        } else {
+            bool again = false;
+            for (uint32_t j = lane; j < n_gone; j += 32u) again |= gone[j] == x.token;
+            again = __any_sync(~0u, again);
+            const float r = again ? 0.0f : x.p;
+            take = n_gone ? below(fabsf(x.u), Z, r) : signbit(x.u);
+            if (!take && !again) {
+                Z = fmax(Z - (double)r, 0.0);
+                if (lane == 0) gone[n_gone] = x.token;
+                ++n_gone;
+                __syncwarp();
+            }
+        }
+        if (take) {
+            if (rank == 0 && tid == 0) a.rows[row0 + taken] = (int32_t)(row0 + found);
+            ++taken;
+            cur = found;
+            c = 0.0f, Z = 1.0, s = 1.0, whole = true, n_gone = 0, fresh = false;
+        }
+        at = found + 1u;
+    }
+    if (!DRAFT) {
+        if (tid == 0) walk = {cur, taken, n_gone};
+        __syncthreads();
+        cur = walk.cur, taken = walk.taken, n_gone = walk.n_gone;
     }
     if (!fresh) total = sum_row(cur, c);
-    if (total == 0ull && (c != 0.0f || walk.n_gone)) {            // nothing left of the target: its own row
-        __syncthreads();
-        if (tid == 0) walk.n_gone = 0;
-        c = 0.0f;
-        __syncthreads();
+    if (total == 0ull && (c != 0.0f || n_gone)) {                 // nothing left of the target: its own row
+        c = 0.0f, n_gone = 0;
+        held = ~0u;
         total = sum_row(cur, c);
     }
-    const uint32_t taken = walk.taken;
 
-    // The drawn number: floor(u total), from u's bits.
+    // The drawn number: floor(u total). The CTA in whose part it falls finds the warp's run, the warp the element.
     const float u = u0 > 0.0f ? fminf(u0, 0x1.fffffep-1f) : 0.0f;
-    const unsigned long long t = min((unsigned long long)__double2ull_rd((double)u * (double)total), total ? total - 1ull : 0ull);
+    unsigned long long left = min((unsigned long long)__double2ull_rd((double)u * (double)total), total ? total - 1ull : 0ull);
+    const unsigned long long *all = sums[parity ^ 1u];
     unsigned long long before = 0;
-    for (uint32_t j = 0; j < rank; ++j) before += cta_sum[parity ^ 1u][j];
-    const bool mine = total && t >= before && t - before < cta_sum[parity ^ 1u][rank];
-    if (mine) {
-        // the warp's range, then the element: strips of 32, dealt to the warps
-        uint32_t w = 0;
-        unsigned long long left = t - before;
-        while (left >= warp_sum[w]) left -= warp_sum[w++];
-        const uint32_t v0 = first + w * per_warp, v1 = min(v0 + per_warp, last);
-        const T *p = P + (uint64_t)cur * a.probs_stride;
-        const T *q = DRAFT ? Q + (uint64_t)cur * a.draft_stride : nullptr;
-        const auto weight = [&](uint32_t y) -> unsigned long long {
-            if (y >= v1) return 0ull;
-            const unsigned long long x = units_of_prob(rest_of(prob_of(p + y), DRAFT && c != 0.0f ? prob_of(q + y) : 0.0f, c));
-            if (!DRAFT)
-                for (uint32_t j = 0; j < walk.n_gone; ++j)
-                    if ((uint32_t)gone[j] == y) return 0ull;
-            return x;
-        };
-        __syncthreads();                         // (the same CTA-wide condition) warp_sum is read
-        for (uint32_t y0 = v0; y0 < v1; y0 += kVerifyThreads) {
-            const uint32_t y = y0 + tid;
-            const unsigned long long x = weight(y);
-            unsigned long long run = x;
-#pragma unroll
-            for (uint32_t d = 1; d < 32; d <<= 1) {
-                const unsigned long long z = __shfl_up_sync(~0u, run, d);
-                if (lane >= d) run += z;
+    for (uint32_t j = lane; j < rank * kVerifyWarps; j += 32u) before += all[j];
+    before = sum_of_warp(before);
+    const unsigned long long mine = sum_of_warp(lane < kVerifyWarps ? all[rank * kVerifyWarps + lane] : 0ull);
+    if (total && left >= before && left - before < mine) {
+        left -= before;
+        const unsigned long long *runs = all + rank * kVerifyWarps;
+        for (uint32_t k = 0; k < chunks; ++k) {
+            if (chunks > 1u) {
+                load(cur, k, c != 0.0f);
+                const unsigned long long sum = sum_run(c);
+                if (lane == 0) run_sum[warp] = sum;
+                __syncthreads();
+                runs = run_sum;
             }
-            if (lane == 31) warp_sum[warp] = run;
-            __syncthreads();
-            unsigned long long low = 0, all = 0;
-            for (uint32_t j = 0; j < kVerifyWarps; ++j) {
-                if (j < warp) low += warp_sum[j];
-                all += warp_sum[j];
-            }
-            run += low;
-            if (left >= run - x && left < run) a.next[request] = (int32_t)y;
-            __syncthreads();
-            if (left < all) break;
-            left -= all;
+            const unsigned long long here = sum_of_warp(lane < kVerifyWarps ? runs[lane] : 0ull);
+            if (left < here) break;
+            left -= here;
+        }
+        const unsigned long long low = sum_of_warp(lane < warp ? runs[lane] : 0ull);
+        if (left >= low && left - low < runs[warp]) {
+            left -= low;
+            // a stretch of up to 32 elements per lane, then an element per lane of the stretch
+            const uint32_t each = (run + 31u) / 32u;
+            const auto stretch_sum = [&](uint32_t from, uint32_t to) {
+                Units x{0u, 0u};
+                for (uint32_t i = from; i < to; ++i) add_units(x, rest(i, c));
+                return total_of(x.high, (int32_t)x.low);
+            };
+            unsigned long long x = stretch_sum(min(lane * each, run), min((lane + 1u) * each, run)), upto = prefix_of_warp(x);
+            const uint32_t l = __ffs(__ballot_sync(~0u, left >= upto - x && left < upto)) - 1u;
+            left -= __shfl_sync(~0u, upto - x, l);
+            const uint32_t from = min(l * each, run), i = from + lane;
+            x = i < min(from + each, run) ? units_of_prob(rest(i, c)) : 0ull;
+            upto = prefix_of_warp(x);
+            if (left >= upto - x && left < upto) a.next[request] = (int32_t)(run0 + i);
         }
     }
     if (rank == 0) {
@@ -361,11 +440,29 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
     }
 }
 
+// Clusters of more than eight CTAs, once per kernel and device.
+static bool allow_cluster(const void *kernel, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (ready.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return false;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
 template <typename T, bool DRAFT>
-static bool launch_verify(const VerifyArgs &a, uint32_t cluster, cudaStream_t st) {
+static bool launch_verify(const VerifyArgs &a, uint32_t cluster, uint32_t bytes, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0}, large{0};
+    if (!allow_cluster(reinterpret_cast<const void *>(verify_kernel<T, DRAFT>), ready) ||
+        !raise_smem(reinterpret_cast<const void *>(verify_kernel<T, DRAFT>), kRowBytes, large))
+        return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.n_requests + a.checked) * cluster);
     cfg.blockDim = dim3(kVerifyThreads);
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -401,12 +498,27 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     VerifyArgs a{probs, draft_probs, probs_stride, draft_stride, vocab, distinct, n_rows, n_requests, cu_new, tokens, parents, uniform,
-                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 8192u && n_requests <= 1024u};
+                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 8192u && n_requests <= 1024u, 0u, 0u, 0u};
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
+    uint32_t sms = 0;
+    if (!device_sms(&sms)) return SKV_ERR_CUDA;
+    // CTAs to a request, up to 16 of 2,048 elements or more: as many as find a place at once (seven to four SMs), and with draft
+    // probabilities as many as hold their parts of both rows. 24 requests with 30 nodes and 50,257 tokens take 16.7 us with 8
+    // to each, 30.3 with 4 and 24.0 with 16; 64 with 151,936 tokens, which 16 CTAs hold, 70 with 16 and 81 with 4. Without
+    // draft probabilities a row is read once: 64 of those take 20.3 with 4 and 38 with 16.
+    const uint32_t sides = draft_probs ? 2u : 1u, fits = kRowBytes / (sides * size) - 32u / size - 16u;
+    const uint32_t room = fits < 32u * kVerifyThreads ? fits : 32u * kVerifyThreads;      // a run of 1,024 per warp at most
     uint32_t cluster = 1;
-    while (cluster < kVerifyCluster && cluster * 4096u < vocab) cluster *= 2u;
+    while (cluster < kVerifyCluster && cluster * 2048u < vocab &&
+           (8ull * cluster * n_requests <= 7ull * sms || (draft_probs && cluster * room < vocab)))
+        cluster *= 2u;
+    a.per_cta = (vocab + cluster - 1u) / cluster;
+    const uint32_t chunks = (a.per_cta + room - 1u) / room;
+    a.per_chunk = ((a.per_cta + chunks - 1u) / chunks + 15u) & ~15u;
+    a.per_warp = (a.per_chunk + kVerifyThreads - 1u) / kVerifyThreads * 32u;
+    const uint32_t bytes = sides * (a.per_chunk * size + 32u);
     bool ok;
-    if (dtype == SKV_PROB_F32) ok = draft_probs ? launch_verify<float, true>(a, cluster, st) : launch_verify<float, false>(a, cluster, st);
-    else ok = draft_probs ? launch_verify<uint16_t, true>(a, cluster, st) : launch_verify<uint16_t, false>(a, cluster, st);
+    if (dtype == SKV_PROB_F32) ok = draft_probs ? launch_verify<float, true>(a, cluster, bytes, st) : launch_verify<float, false>(a, cluster, bytes, st);
+    else ok = draft_probs ? launch_verify<uint16_t, true>(a, cluster, bytes, st) : launch_verify<uint16_t, false>(a, cluster, bytes, st);
     return ok ? SKV_OK : SKV_ERR_CUDA;
 }
