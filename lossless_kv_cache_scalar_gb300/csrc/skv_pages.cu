@@ -1,10 +1,12 @@
 // skv_pages.cu -- pages of a paged cache shared, moved and copied: fork, compact, copy, move.
 //
 // fork and compact plan on block tables alone: one cluster of CTAs walks the tables with a bit per page of the
-// pool in the workspace. A page comes free iff its bit, set for every page that some row held, is not cleared for the
-// rows that go on; no count per page is kept between calls that could drift from the tables. Between its
-// steps the cluster passes a barrier (some hundred nanoseconds, where a launch costs microseconds).
+// pool. A page comes free iff its bit, set for every page that some row held, is not cleared for the
+// rows that go on; no count per page is kept between calls that could drift from the tables.
 // Everything comes out in a fixed order: prefix sums over rows and over the words of bits.
+// Pools of up to 32,768 pages keep the bits in shared memory: every CTA marks its share of the rows, reads the
+// others' bits after the one barrier and works the rest out for itself. Larger ones keep them in the workspace, with
+// a barrier of the cluster (half a microsecond, where a launch costs two) after each step.
 //
 // copy and move bring the K and V: 16 bytes per thread and step, bound by HBM.
 #include <cooperative_groups.h>
@@ -389,6 +391,259 @@ __global__ void __launch_bounds__(kPlanThreads) compact_pages_kernel(const PlanA
     }
 }
 
+// ---- both, for pools whose bits fit shared memory
+
+constexpr uint32_t kSmallPool = 32768, kSmallWords = kSmallPool / 32u, kSmallRows = 1024;
+static_assert(kSmallWords == 2u * kPlanThreads && kSmallRows == 2u * kPlanThreads, "two words and two rows to a thread");
+
+// Word i of the union of the CTAs' bits (every CTA's, after a barrier).
+__device__ __forceinline__ uint32_t union_of(uint32_t *bits, uint32_t i, uint32_t C) {
+    cg::cluster_group cluster = cg::this_cluster();
+    uint32_t w = 0;
+#pragma unroll 8
+    for (uint32_t j = 0; j < C; ++j) w |= cluster.map_shared_rank(bits, j)[i];
+    return w;
+}
+
+// The last of a kernel that reads other CTAs' shared memory: nobody leaves before everybody has read.
+__device__ __forceinline__ void leave_together(uint32_t C) {
+    if (C > 1u) cg::this_cluster().sync();
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs a) {
+    __shared__ uint32_t was[kSmallWords], now[kSmallWords];
+    __shared__ int32_t parent[kSmallRows], ctx[kSmallRows], have[kSmallRows], taken[kSmallRows];
+    __shared__ uint32_t heir[kSmallRows], part[kPlanWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, n = a.n_requests;
+    const int32_t head = __ldg(a.free_in), count = __ldg(a.free_in + 1);
+    bool bad = ring_bad(a, head, count), corrupt = false;
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t r = k * kPlanThreads + tid;
+        was[r] = now[r] = 0u;
+        heir[r] = ~0u;
+        if (r >= n) continue;
+        const int32_t p = a.parents ? __ldg(a.parents + r) : (int32_t)r, c = __ldg(a.ctx_len + r), h = __ldg(a.n_in + r);
+        parent[r] = p, ctx[r] = c, have[r] = h;
+        bad |= p < -1 || p >= (int32_t)n || h < 0 || (uint32_t)h > a.max_pages || (int64_t)c > (int64_t)h * a.page.d;
+    }
+    if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
+    if (__syncthreads_or(bad)) {                          // the same in every CTA
+        hand_on(a, t, SKV_ERR_INVALID_ARG);
+        return;
+    }
+    const auto from_of = [&](uint32_t s) -> uint32_t { return parent[s] < 0 || ctx[parent[s]] < 0 ? ~0u : (uint32_t)parent[s]; };
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t s = k * kPlanThreads + tid;
+        if (s >= n) continue;
+        const uint32_t f = from_of(s);
+        if (f != ~0u) atomicMin(heir + f, f == s ? 0u : s + 1u);
+    }
+    __syncthreads();
+    // Entries that an heir of row r keeps, and what row s has.
+    const auto kept_of = [&](uint32_t r) -> uint32_t {
+        if (!a.trim) return (uint32_t)have[r];
+        const uint32_t whole = div_by((uint32_t)ctx[r], a.page);
+        return whole + ((uint32_t)ctx[r] != whole * a.page.d);
+    };
+    const auto row_of = [&](uint32_t s) {
+        Fork f{from_of(s), 0u, 0u, 0u, false};
+        if (f.from == ~0u) return f;
+        const uint32_t c = (uint32_t)ctx[f.from], whole = div_by(c, a.page);
+        f.heir = heir[f.from] == (f.from == s ? 0u : s + 1u);
+        f.part = f.heir ? 0u : c - whole * a.page.d;
+        f.copies = f.part != 0u;
+        f.keep = f.heir ? kept_of(f.from) : whole;
+        return f;
+    };
+    // Copies ranked in order of rows, two rows to a thread; a CTA takes the pages of its share of them.
+    Fork mine[2];
+    uint32_t took, k0;
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) mine[k] = 2u * tid + k < n ? row_of(2u * tid + k) : Fork{~0u, 0u, 0u, 0u, false};
+    k0 = block_scan(mine[0].copies + mine[1].copies, &took, part);
+    if (took > (uint32_t)count) {
+        hand_on(a, t, SKV_ERR_CAPACITY);
+        return;
+    }
+    int32_t src[2], dst[2];
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t s = 2u * tid + k;
+        src[k] = dst[k] = -1;
+        if (s < n && s % t.C == t.rank && mine[k].copies) {
+            uint64_t e = (uint64_t)head + k0 + (k ? mine[0].copies : 0u);
+            if (e >= a.free_capacity) e -= a.free_capacity;
+            src[k] = __ldg(a.table + (uint64_t)mine[k].from * a.table_stride + mine[k].keep);
+            dst[k] = __ldg(a.free_pages + e);
+            taken[s] = dst[k];
+            if ((uint32_t)dst[k] < a.pool_pages) atomicOr(now + ((uint32_t)dst[k] >> 5), 1u << (dst[k] & 31));
+            if ((uint32_t)src[k] >= a.pool_pages || (uint32_t)dst[k] >= a.pool_pages) {
+                corrupt = true;
+                src[k] = dst[k] = -1;
+                mine[k].part = 0u;
+            }
+        }
+    }
+    // Pages that rows held, and those that their heirs go on with (all others' are among them).
+#pragma unroll 1
+    for (uint32_t r = warp * t.C + t.rank; r < n; r += kPlanWarps * t.C) {
+        const uint32_t h = (uint32_t)have[r], keep = heir[r] == ~0u ? 0u : kept_of(r);
+        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < h; j += 32u) {
+            const uint32_t p = (uint32_t)__ldg(row + j);
+            if (p < a.pool_pages) {
+                atomicOr(was + (p >> 5), 1u << (p & 31u));
+                if (j < keep) atomicOr(now + (p >> 5), 1u << (p & 31u));
+            } else {
+                corrupt = true;
+            }
+        }
+    }
+    cluster.sync();
+    uint32_t w[2];
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) w[k] = union_of(was, 2u * tid + k, t.C) & ~union_of(now, 2u * tid + k, t.C);
+    uint32_t freed;
+    const uint32_t at0 = block_scan(__popc(w[0]) + __popc(w[1]), &freed, part);
+    if ((uint64_t)count - took + freed > a.free_capacity) {
+        hand_on(a, t, SKV_ERR_CAPACITY);
+        leave_together(t.C);
+        return;
+    }
+    if (tid % t.C == t.rank) {
+        uint32_t at = at0;
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) {
+            for (uint32_t m = w[k]; m; m &= m - 1u) {
+                uint64_t e = (uint64_t)head + (uint32_t)count + at++;
+                while (e >= a.free_capacity) e -= a.free_capacity;
+                a.free_pages[e] = (int32_t)(32u * (2u * tid + k) + __ffs(m) - 1u);
+            }
+        }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t s = 2u * tid + k;
+        if (s < n && s % t.C == t.rank) {
+            a.src[s] = src[k], a.dst[s] = dst[k], a.count[s] = (int32_t)mine[k].part;
+            a.n_out[s] = (int32_t)(mine[k].keep + mine[k].copies);
+            a.ctx_out[s] = mine[k].from == ~0u ? -1 : ctx[mine[k].from];
+        }
+    }
+#pragma unroll 1
+    for (uint32_t s = warp * t.C + t.rank; s < n; s += kPlanWarps * t.C) {
+        const Fork f = row_of(s);
+        if (f.from == ~0u) continue;
+        const int32_t *row = a.table + (uint64_t)f.from * a.table_stride;
+        int32_t *out = a.table_out + (uint64_t)s * a.out_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < f.keep; j += 32u) out[j] = __ldg(row + j);
+        if (f.copies && lane == 0) out[f.keep] = taken[s];
+    }
+    if (t.rank == 0 && tid == 0) {
+        uint64_t e = (uint64_t)head + took;
+        const uint32_t cap = max(a.free_capacity, 1u);
+        if (e >= cap) e -= cap;
+        a.free_out[0] = (int32_t)e;
+        a.free_out[1] = (int32_t)((uint32_t)count - took + freed);
+    }
+    if (corrupt) set_first(a.status, SKV_ERR_CORRUPT);    // (after the barrier that the first CTA's OK came before)
+    leave_together(t.C);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanArgs a) {
+    __shared__ uint32_t bits[kSmallWords], held[kSmallWords], part[kPlanWarps];
+    __shared__ uint16_t far_before[kSmallWords], hole[kSmallPool / 2u];
+    cg::cluster_group cluster = cg::this_cluster();
+    const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    bits[tid] = bits[kPlanThreads + tid] = 0u;
+    bool bad = false, corrupt = false;
+    for (uint32_t r = tid; r < a.n_requests; r += kPlanThreads) {
+        const int32_t h = __ldg(a.n_in + r);
+        bad |= h < 0 || (uint32_t)h > a.max_pages;
+    }
+    if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
+    if (__syncthreads_or(bad)) {                          // the same in every CTA
+        hand_on(a, t, SKV_ERR_INVALID_ARG);
+        return;
+    }
+#pragma unroll 1
+    for (uint32_t r = warp * t.C + t.rank; r < a.n_requests; r += kPlanWarps * t.C) {
+        const uint32_t h = (uint32_t)__ldg(a.n_in + r);
+        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < h; j += 32u) {
+            const uint32_t p = (uint32_t)__ldg(row + j);
+            if (p < a.pool_pages) atomicOr(bits + (p >> 5), 1u << (p & 31u));
+            else corrupt = true;
+        }
+    }
+    cluster.sync();
+    uint32_t w[2], live, all;
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) held[2u * tid + k] = w[k] = union_of(bits, 2u * tid + k, t.C);
+    block_scan(__popc(w[0]) + __popc(w[1]), &live, part);
+    // holes below `live` and held pages from it on, counted together (2^15 of either at most)
+    uint32_t low[2], x = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+        low[k] = below(2u * tid + k, live);
+        x += (uint32_t)__popc(~w[k] & low[k]) << 16 | (uint32_t)__popc(w[k] & ~low[k]);
+    }
+    x = block_scan(x, &all, part);
+    const uint32_t moves = all & 0xFFFFu;
+    if (moves > a.capacity || a.pool_pages - live > a.free_capacity) {
+        hand_on(a, t, SKV_ERR_CAPACITY);
+        leave_together(t.C);
+        return;
+    }
+    uint32_t holes = x >> 16, far = x & 0xFFFFu;
+    const bool tells = tid % t.C == t.rank;
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t first = 32u * (2u * tid + k);
+        far_before[2u * tid + k] = (uint16_t)far;
+        for (uint32_t m = ~w[k] & low[k]; m; m &= m - 1u) {
+            const uint32_t p = first + __ffs(m) - 1u;
+            hole[holes] = (uint16_t)p;
+            if (tells) a.dst[holes] = (int32_t)p;
+            ++holes;
+        }
+        for (uint32_t m = w[k] & ~low[k]; m; m &= m - 1u, ++far)
+            if (tells) a.src[far] = (int32_t)(first + __ffs(m) - 1u);
+    }
+    __syncthreads();
+    for (uint32_t i = moves + t.rank * kPlanThreads + tid; i < a.capacity; i += t.C * kPlanThreads) a.src[i] = a.dst[i] = -1;
+    for (uint32_t i = t.rank * kPlanThreads + tid; i < a.pool_pages - live; i += t.C * kPlanThreads) a.free_pages[i] = (int32_t)(live + i);
+#pragma unroll 1
+    for (uint32_t r = warp * t.C + t.rank; r < a.n_requests; r += kPlanWarps * t.C) {
+        const uint32_t h = (uint32_t)__ldg(a.n_in + r);
+        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
+        int32_t *out = a.table_out + (uint64_t)r * a.out_stride;
+#pragma unroll 4
+        for (uint32_t j = lane; j < h; j += 32u) {
+            uint32_t p = (uint32_t)__ldg(row + j);
+            if (p >= live && p < a.pool_pages) {
+                const uint32_t i = p >> 5, under = held[i] & ~below(i, live) & ((1u << (p & 31u)) - 1u);
+                p = hole[far_before[i] + __popc(under)];
+            }
+            out[j] = (int32_t)p;
+        }
+    }
+    if (t.rank == 0 && tid == 0) {
+        a.free_out[0] = 0;
+        a.free_out[1] = (int32_t)(a.pool_pages - live);
+    }
+    if (corrupt) set_first(a.status, SKV_ERR_CORRUPT);
+    leave_together(t.C);
+}
+
 // ---- copies of pages
 
 struct CopyArgs {
@@ -522,7 +777,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveArg
     int64_t from, to;
     uint32_t lo, hi;
     if (blockIdx.x >= a.n_requests * a.per_request) {         // the errors of every request
-        for (uint32_t r = threadIdx.x >> 5; r < a.n_requests; r += kMoveThreads / 32u) {
+        for (uint32_t r = threadIdx.x >> 5; r < a.n_requests; r += blockDim.x / 32u) {
             bad |= !move_rows_of(a, r, &lo, &hi);
             for (uint32_t i = lo + lane; i < hi; i += 32u) move_of(a, i, &from, &to, &bad);
         }
@@ -531,7 +786,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveArg
         return;
     }
     const uint32_t r = blockIdx.x / a.per_request;
-    const uint32_t column = (blockIdx.x - r * a.per_request) * kMoveThreads + threadIdx.x;
+    const uint32_t column = (blockIdx.x - r * a.per_request) * blockDim.x + threadIdx.x;
     bad |= !move_rows_of(a, r, &lo, &hi);
     const bool on = column < 2u * a.units;
     const uint32_t u = column < a.units ? column : column - a.units, h = div_by(u, a.per_head);
@@ -578,10 +833,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveArg
     if (bad && !a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
 }
 
-static bool launch_plan(void (*kernel)(PlanArgs), const PlanArgs &a, cudaStream_t st) {
+static bool launch_plan(void (*kernel)(PlanArgs), bool small, const PlanArgs &a, cudaStream_t st) {
     // One CTA where a small table and pool leave little for more: a barrier of several costs more.
     const uint64_t entries = (uint64_t)a.n_requests * a.max_pages;
-    const uint32_t cluster = entries <= 2048u && a.pool_pages <= 32768u ? 1u : kPlanCluster;
+    const uint32_t cluster = entries <= 2048u && (small || a.pool_pages <= 32768u) ? 1u : kPlanCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(kPlanThreads);
@@ -647,7 +902,8 @@ extern "C" int32_t skv_page_fork(uint32_t page_tokens, uint32_t pool_pages, uint
     a.src = copy_src, a.dst = copy_dst, a.count = copy_tokens, a.status = status;
     a.bits = static_cast<uint32_t *>(workspace);
     a.words = a.bits + bits_bytes(pool_pages) / 4u;
-    return launch_plan(fork_pages_kernel, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
+    const bool small = pool_pages <= kSmallPool && n_requests <= kSmallRows;
+    return launch_plan(small ? fork_small_kernel : fork_pages_kernel, small, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
 }
 
 extern "C" int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, const int32_t *block_table, uint64_t table_stride,
@@ -674,7 +930,8 @@ extern "C" int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, co
     a.table_out = table_out, a.free_pages = free_pages, a.free_out = free_out, a.src = copy_src, a.dst = copy_dst, a.status = status;
     a.bits = static_cast<uint32_t *>(workspace);
     a.words = a.bits + bits_bytes(pool_pages) / 4u;
-    return launch_plan(compact_pages_kernel, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
+    const bool small = pool_pages <= kSmallPool;
+    return launch_plan(small ? compact_small_kernel : compact_pages_kernel, small, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
 }
 
 extern "C" int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, const int32_t *dst, const int32_t *tokens, uint32_t n,
@@ -714,12 +971,13 @@ extern "C" int32_t skv_cache_move(const skv_paged *cache, uint32_t n_requests, c
     if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     const PagedView c = paged_view(*cache);
     const uint32_t per_head = cache->head_dim / (c.e4m3 ? 16u : 8u), units = cache->n_heads * per_head;
-    const uint32_t per_request = (2u * units + kMoveThreads - 1u) / kMoveThreads;
+    const uint32_t threads = 2u * units < kMoveThreads ? (2u * units + 31u) & ~31u : kMoveThreads;
+    const uint32_t per_request = (2u * units + threads - 1u) / threads;
     if ((uint64_t)n_requests * per_request >= 0x7FFFFFFFu) return SKV_ERR_INVALID_ARG;
     MoveArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
                c.page, fast_div(per_head), (uint64_t)cache->n_pages * cache->page_tokens, n_requests, n_rows, units, per_request, cu_new, rows,
-               slots, kept, status, n_rows <= 16384u && n_requests <= 1024u};
+               slots, kept, status, n_rows <= 2048u && n_requests <= 32u};
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    move_tokens_kernel<<<n_requests * per_request + a.checked, kMoveThreads, 0, st>>>(a);
+    move_tokens_kernel<<<n_requests * per_request + a.checked, threads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
 }

@@ -498,7 +498,7 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     VerifyArgs a{probs, draft_probs, probs_stride, draft_stride, vocab, distinct, n_rows, n_requests, cu_new, tokens, parents, uniform,
-                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 8192u && n_requests <= 1024u, 0u, 0u, 0u};
+                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 8192u && n_requests <= 128u, 0u, 0u, 0u};
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     uint32_t sms = 0;
     if (!device_sms(&sms)) return SKV_ERR_CUDA;

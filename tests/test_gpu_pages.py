@@ -75,7 +75,7 @@ def check_fork(got, want, width):
     assert list(zip(got["copy_src"], got["copy_dst"], got["copy_tokens"])) == copies
 
 
-@pytest.mark.parametrize("n,width,page", [(1, 1, 1), (2, 3, 16), (8, 20, 256), (33, 7, 5), (100, 30, 24), (700, 50, 64), (1300, 3, 16), (5, 900, 2)])
+@pytest.mark.parametrize("n,width,page", [(1, 1, 1), (2, 3, 16), (8, 20, 256), (33, 7, 5), (100, 30, 24), (700, 50, 64), (1300, 3, 16), (5, 900, 2), (40, 1000, 4), (1024, 20, 8)])
 def test_fork(n, width, page):
     for seed in range(12 if n < 500 else 4):
         rng = random.Random(1000 * n + seed)
@@ -155,7 +155,7 @@ def call_compact(pool, rows, have, width, ring, state, room):
     return got, int(t.status)
 
 
-@pytest.mark.parametrize("n,width", [(1, 1), (2, 3), (8, 20), (33, 7), (100, 30), (700, 50), (1300, 3), (3, 2000)])
+@pytest.mark.parametrize("n,width", [(1, 1), (2, 3), (8, 20), (33, 7), (100, 30), (700, 50), (1300, 3), (3, 2000), (40, 1000), (16, 2046)])
 def test_compact(n, width):
     for seed in range(10 if n < 500 else 3):
         rng = random.Random(77 * n + seed)
