@@ -96,10 +96,11 @@ __device__ __forceinline__ unsigned long long warp_total(const Units &u) {
     return total_of(((uint64_t)a << 16) + b, ((int64_t)c << 16) + d);
 }
 
+// In pieces of 24 bits, which 32-bit reductions hold.
 __device__ __forceinline__ unsigned long long sum_of_warp(unsigned long long x) {
-#pragma unroll
-    for (uint32_t d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-    return x;
+    const uint32_t lo = __reduce_add_sync(~0u, (uint32_t)x & 0xFFFFFFu), mid = __reduce_add_sync(~0u, (uint32_t)(x >> 24) & 0xFFFFFFu);
+    const uint32_t hi = __reduce_add_sync(~0u, (uint32_t)(x >> 48));
+    return lo + ((unsigned long long)mid << 24) + ((unsigned long long)hi << 48);
 }
 __device__ __forceinline__ unsigned long long prefix_of_warp(unsigned long long x) {
 #pragma unroll
@@ -290,7 +291,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
         if (lane < C) *cluster.map_shared_rank(&sums[parity][rank * kVerifyWarps + warp], lane) = sum;
         cluster.sync();
         unsigned long long whole = 0;
-        for (uint32_t j = lane; j < C * kVerifyWarps; j += 32u) whole += sums[parity][j];
+#pragma unroll
+        for (uint32_t j = 0; j < kVerifyCluster * kVerifyWarps / 32u; ++j)
+            if (32u * j + lane < C * kVerifyWarps) whole += sums[parity][32u * j + lane];
         parity ^= 1u;
         return sum_of_warp(whole);
     };

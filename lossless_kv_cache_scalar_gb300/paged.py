@@ -87,7 +87,8 @@ class PageTable(_Status):
         self._stride = _table_rows(block_table)
         self.block_table, self._table = block_table, block_table.data_ptr()
         self.page_tokens, self.pool_pages = int(page_tokens), int(pool_pages)
-        self.n_requests, self.max_pages = block_table.shape
+        self._shape = block_table.shape
+        self.n_requests, self.max_pages = self._shape
         self._new_status(block_table.device)
         self.workspace = None
         if workspace:
@@ -105,14 +106,17 @@ class PageTable(_Status):
 
     def _ready(self, table_out, stream):
         """What fork and compact need beside their arrays; table_out's row stride."""
-        out = _table_rows(table_out)
-        if table_out.shape != self.block_table.shape or table_out.get_device() != self._device or table_out.data_ptr() == self._table:
-            raise ValueError("table_out must be another tensor of the block_table's shape and device")
+        rows, cols = self._shape
+        if table_out.dtype is not _I32 or table_out.shape != self._shape or table_out.get_device() != self._device:
+            raise ValueError("table_out must be an int32 tensor of the block_table's shape and device")
+        down, across = table_out.stride()
+        if (cols > 1 and across != 1) or (rows > 1 and down < cols) or table_out.data_ptr() == self._table:
+            raise ValueError("table_out must have whole rows and be another tensor than the block_table")
         if self.workspace is None:
             if _capturing(stream):
                 raise ValueError("give PageTable workspace=True before a capture")
             self._make_workspace(stream)
-        return out
+        return down if rows > 1 else cols
 
     def map_into(self, ctx_len, new_len, n_pages, free_pages, free_state, cu_new, slots, n_pages_out,
                  free_state_out, stream=None):

@@ -11,6 +11,8 @@ from . import _binding as B
 from .api import _after_current
 from .paged import _F32, _I32, _I64, _Status, _check_words, _stream_of
 
+_PROBS = {torch.float32: B.SKV_PROB_F32, torch.bfloat16: B.SKV_PROB_BF16}
+
 # 2^192 / (2 pi), rounded down
 _TURN = 0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E410
 
@@ -73,10 +75,15 @@ class Verifier(_Status):
             raise ValueError("a Verifier lives on a GPU")
         self._settle()
 
-    def _probs(self, what, t, n):
-        if t.dim() != 2 or t.shape[1] != self.vocab or t.shape[0] != n or t.get_device() != self._device or t.stride(1) != 1 \
-                or (n > 1 and t.stride(0) < self.vocab) or t.dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError(f"{what} must be a float32 or bfloat16 tensor [{n}][{self.vocab}] of whole rows on cuda:{self._device}")
+    def _probs(self, t, n):
+        """The kind of whole rows of probabilities, and their stride."""
+        kind = _PROBS.get(t.dtype)
+        if kind is None or t.shape != (n, self.vocab) or t.get_device() != self._device:
+            raise ValueError(f"probabilities must be float32 or bfloat16 tensors [{n}][{self.vocab}] on cuda:{self._device}")
+        down, across = t.stride()
+        if across != 1 or (n > 1 and down < self.vocab):
+            raise ValueError("probabilities must be whole rows")
+        return kind, down
 
     def verify_into(self, probs, tokens, cu_new, uniform, accepted, rows, next_tokens, parents=None, draft_probs=None,
                     distinct: bool = False, slots=None, kept=None, ctx_len=None, ctx_out=None, stream=None):
@@ -87,11 +94,11 @@ class Verifier(_Status):
         replacement. Out: accepted and next_tokens int32 [n_requests], rows int32 [n_rows], and with
         slots (int64 [n_rows]) kept, with ctx_len (int32 [n_requests]) ctx_out."""
         n, dev = tokens.numel(), self._device
-        self._probs("probs", probs, n)
-        draft = None
+        kind, stride = self._probs(probs, n)
+        draft, draft_stride = None, 0
         if draft_probs is not None:
-            self._probs("draft_probs", draft_probs, n)
-            if draft_probs.dtype != probs.dtype:
+            draft_kind, draft_stride = self._probs(draft_probs, n)
+            if draft_kind != kind:
                 raise ValueError("probs and draft_probs must have one type")
             draft = draft_probs.data_ptr()
         _check_words("tokens and rows", _I32, n, dev, tokens, rows)
@@ -109,8 +116,7 @@ class Verifier(_Status):
         if ctx_len is not None:
             _check_words("ctx_len and ctx_out", _I32, self.n_requests, dev, ctx_len, ctx_out)
             ctx_len, ctx_out = ctx_len.data_ptr(), ctx_out.data_ptr()
-        rc = B.lib().skv_tree_verify(B.SKV_PROB_BF16 if probs.dtype is torch.bfloat16 else B.SKV_PROB_F32, probs.data_ptr(), probs.stride(0),
-                                     draft, 0 if draft is None else draft_probs.stride(0), self.vocab, bool(distinct), n, self.n_requests,
+        rc = B.lib().skv_tree_verify(kind, probs.data_ptr(), stride, draft, draft_stride, self.vocab, bool(distinct), n, self.n_requests,
                                      cu_new.data_ptr(), tokens.data_ptr(), parents, uniform.data_ptr(), slots, ctx_len,
                                      accepted.data_ptr(), rows.data_ptr(), kept, ctx_out, next_tokens.data_ptr(), self._status,
                                      _stream_of(stream, dev))
