@@ -4,11 +4,17 @@
 // other (channels 8 u .. and rot_dim / 2 + 8 u .., or 16 neighbours), so a lane that holds a unit
 // has both sides of its 8 pairs, and the angles of its 8 frequencies serve every head of the token.
 // head_dim / 16 lanes (rounded up to a power of two) hold a head, a warp 32 / that many heads at
-// once; the norm's sum is a few shuffles among them.
+// once; the norm's sum is a few shuffles among them. Norm's weights and angle of a pair come as
+// four products, worked out once per row; the root is multiplied in at the end.
 //
 // Angles: position x frequency grows far beyond the bits that binary32 keeps of it. In turns, as a fraction of
 // 2^64, the product modulo one turn is the low word of an integer product, and the sine
 // is taken of a reduced angle in [-1/2, 1/2) turns.
+//
+// Bound by HBM, and close behind by issue (some 200 instructions for a warp's 4 heads of 128 channels): 65,536 rows of 32
+// query and 8 KV heads, bf16, 250 us (6.4 TB/s, 0.95 of a copy); 56,008 rows into e4m3 218 us (0.85). Blocks
+// of 4 warps, 7 to an SM (72 registers): with 6 257 us, with 8 (64 registers, some of them spilled) 253 and 210. The loads of the
+// next step are on their way while a step is worked on; two steps ahead gave nothing.
 #include <cuda_bf16.h>
 
 #include "skv_rows.cuh"
@@ -41,21 +47,8 @@ struct RotateArgs {
     uint32_t checked;                                                   // 1: block 0 reports the errors
 };
 
-constexpr uint32_t kRotateThreads = 256, kRotateWarps = kRotateThreads / 32u, kRotateBlocks = 3;      // blocks per SM
-
-// Two binary32 numbers that one instruction works on; each is rounded as by itself.
-__device__ __forceinline__ uint64_t bits2(float2 a) { return (uint64_t)__float_as_uint(a.y) << 32 | __float_as_uint(a.x); }
-__device__ __forceinline__ float2 floats2(uint64_t b) { return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return floats2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return floats2(r);
-}
+constexpr uint32_t kRotateThreads = 128, kRotateWarps = kRotateThreads / 32u, kRotateBlocks = 7;      // blocks per SM
+constexpr uint32_t kRotateChecked = 2048;        // rows that one block looks through for errors
 
 __device__ __forceinline__ uint32_t pack2(float2 x) {
     uint32_t r;
@@ -79,19 +72,16 @@ __device__ __forceinline__ uint2 quantise8(const float2 *x, const ScaleOf &s) {
 template <uint32_t LANES, bool E4M3>
 __global__ void __launch_bounds__(kRotateThreads, kRotateBlocks) rotate_kernel(const RotateArgs a) {
     constexpr uint32_t HPW = 32u / LANES;
-    __shared__ float4 weight[2][16 * LANES / 4];                        // norms of q and k
-    // cosines and sines of four frequencies of each unit side by side, a unit's eight in two rows
-    __shared__ float4 cosine[kRotateWarps][2 * LANES], sine[kRotateWarps][2 * LANES];
+    // What a pair (x, y) of a row's frequency is multiplied with, the norm's weights w among it, for queries and for
+    // keys: x' = x (w_x cos) + y (-w_y sin), y' = x (w_x sin) + y (w_y cos). Four frequencies of each unit
+    // side by side, a unit's eight in two rows of each of the four.
+    __shared__ float4 coef[kRotateWarps][2][8][LANES];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, u = lane % LANES, own = lane / LANES;
-    if (threadIdx.x < a.head_dim / 4u) {
-        if (a.q_norm) weight[0][threadIdx.x] = __ldg(reinterpret_cast<const float4 *>(a.q_norm) + threadIdx.x);
-        if (a.k_norm) weight[1][threadIdx.x] = __ldg(reinterpret_cast<const float4 *>(a.k_norm) + threadIdx.x);
-    }
     if (a.checked && blockIdx.x == 0) {
-        // loads of eight rounds in flight at once (checked: n <= 2,048)
+        // loads of every round in flight at once
         bool bad = false;
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
+        for (uint32_t j = 0; j < kRotateChecked / kRotateThreads; ++j) {
             const uint32_t i = j * kRotateThreads + threadIdx.x;
             const int64_t s = i < a.n ? __ldg(a.slots + i) : -1;
             bad |= s >= 0 && (uint64_t)s >= a.pool_tokens;
@@ -99,135 +89,158 @@ __global__ void __launch_bounds__(kRotateThreads, kRotateBlocks) rotate_kernel(c
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
     }
-    __syncthreads();
     const bool live = u < a.head_dim / 16u;
     const bool turned = u < a.rot_units;
     // channels of the unit's two vectors
     const uint32_t lo = turned && !a.interleaved ? 8u * u : 16u * u;
-    const uint32_t hi = lo + (turned && !a.interleaved ? 8u * a.rot_units : 8u);
-    const uint64_t items = (uint64_t)a.n * a.parts;
+    const uint32_t apart = turned && !a.interleaved ? 8u * a.rot_units : 8u, hi = lo + apart;
+    const uint64_t items = (uint64_t)a.n * a.parts, q_next = (uint64_t)a.parts * HPW * a.q_head_stride;
+    const uint32_t out_next = a.parts * HPW * a.head_dim;
 #pragma unroll 1
     for (uint64_t item = (uint64_t)blockIdx.x * kRotateWarps + warp; item < items; item += (uint64_t)gridDim.x * kRotateWarps) {
         const uint32_t i = items >> 31 ? (uint32_t)(item / a.parts) : div_by((uint32_t)item, a.by_parts);
         const uint32_t part = (uint32_t)(item - (uint64_t)i * a.parts);
+        // Steps of HPW heads of one kind: queries, then keys, then values.
+        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+        const auto fetch = [&](const uint16_t *src, bool on) {
+            if (!on) return;
+            x0 = *reinterpret_cast<const uint4 *>(src);
+            x1 = *reinterpret_cast<const uint4 *>(src + apart);
+        };
+        const auto fetch_kv = [&](uint32_t t) {
+            const uint32_t is_v = t >= a.kv_steps, h = (is_v ? t - a.kv_steps : t) * HPW + own;
+            fetch((is_v ? a.v : a.k) + (uint64_t)i * a.row_stride + (uint64_t)h * a.head_stride + lo, live && t < 2u * a.kv_steps && h < a.n_heads);
+        };
+        const uint16_t *src = a.q + (uint64_t)i * a.q_row_stride + (uint64_t)(part * HPW + own) * a.q_head_stride + lo;
+        if (part < a.q_steps) fetch(src, live && part * HPW + own < a.n_q_heads);
         const int64_t slot = __ldg(a.slots + i);
         bool to_pages = slot >= 0;
         if (to_pages && (uint64_t)slot >= a.pool_tokens) {
             to_pages = false;
             if (!a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
         }
-        // Steps of HPW heads of one kind (0 queries, 1 keys, 2 values).
-        const uint32_t steps = a.q_steps + (to_pages ? 2u * a.kv_steps : 0u);
-        const auto kind_of = [&](uint32_t t, uint32_t *g0) {
-            const uint32_t what = t < a.q_steps ? 0u : t < a.q_steps + a.kv_steps ? 1u : 2u;
-            *g0 = (what == 0 ? t : what == 1 ? t - a.q_steps : t - a.q_steps - a.kv_steps) * HPW;
-            return what;
-        };
-        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-        const auto fetch = [&](uint32_t t) {
-            uint32_t g0;
-            const uint32_t what = kind_of(t, &g0);
-            if (t >= steps || !live || g0 + own >= (what ? a.n_heads : a.n_q_heads)) return;
-            const uint16_t *row = what == 0 ? a.q + (uint64_t)i * a.q_row_stride + (uint64_t)g0 * a.q_head_stride
-                                            : (what == 1 ? a.k : a.v) + (uint64_t)i * a.row_stride + (uint64_t)g0 * a.head_stride;
-            const uint16_t *src = row + own * (what ? a.head_stride : a.q_head_stride);
-            x0 = *reinterpret_cast<const uint4 *>(src + lo);
-            x1 = *reinterpret_cast<const uint4 *>(src + hi);
-        };
-        fetch(part);
-        __syncwarp();                                   // the last row's angles are read
+        if (part >= a.q_steps && to_pages) fetch_kv(part - a.q_steps);
+        __syncwarp();                                   // the last row's coefficients are read
 #pragma unroll 1
         for (uint32_t j = lane; j < 8u * a.rot_units; j += 32u) {
             uint32_t ax = a.axis ? __ldg(a.axis + j) : 0u;
             if (ax >= a.n_axes) ax = 0u;
             const int64_t pos = __ldg(a.positions + (uint64_t)ax * a.n + i);
             const uint64_t t = __ldg(a.turns + j) * (uint64_t)pos;
-            float2 z;
-            sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &z.y, &z.x);
-            const uint32_t at = ((j >> 2 & 1u) * LANES + (j >> 3)) * 4u + (j & 3u);
-            reinterpret_cast<float *>(cosine[warp])[at] = z.x * a.amplitude;
-            reinterpret_cast<float *>(sine[warp])[at] = z.y * a.amplitude;
+            float c, s;
+            sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s, &c);
+            c *= a.amplitude;
+            s *= a.amplitude;
+            const uint32_t x = a.interleaved ? 2u * j : j, y = a.interleaved ? x + 1u : j + 8u * a.rot_units;
+#pragma unroll
+            for (uint32_t k = 0; k < 2; ++k) {
+                const float *w = k ? a.k_norm : a.q_norm;
+                const float wx = w ? __ldg(w + x) : 1.0f, wy = w ? __ldg(w + y) : 1.0f;
+                float *to = reinterpret_cast<float *>(&coef[warp][k][j >> 2 & 1u][j >> 3]) + (j & 3u);
+                constexpr uint32_t next = 2u * LANES * 4u;
+                to[0] = wx * c;
+                to[next] = -wy * s;
+                to[2u * next] = wx * s;
+                to[3u * next] = wy * c;
+            }
         }
         __syncwarp();
-        uint64_t dst = 0;
-        if (to_pages) {
-            const uint64_t p = a.pool_tokens >> 31 ? (uint64_t)slot / a.page.d : div_by((uint32_t)slot, a.page);
-            dst = p * a.page_stride + ((uint64_t)slot - p * a.page.d) * a.token_stride;
-        }
+        // Norm and rotation of a unit of a head: `of` 0 a query's, 1 a key's.
+        const auto turn = [&](float2 (&x)[8], uint32_t of) {
+            const float *norm = of ? a.k_norm : a.q_norm;
+            float2 r2 = make_float2(1.0f, 1.0f);
+            if (norm) {
+                float2 sum2 = mul2(x[0], x[0]);
+#pragma unroll
+                for (int j = 1; j < 8; ++j) sum2 = fma2(x[j], x[j], sum2);
+                float sum = sum2.x + sum2.y;
+#pragma unroll
+                for (uint32_t d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+                r2.x = r2.y = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
+            }
+            if (turned) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float4 A = coef[warp][of][k][u], B = coef[warp][of][2 + k][u], C = coef[warp][of][4 + k][u], D = coef[warp][of][6 + k][u];
+                    if (a.interleaved) {
+                        const float ca[4] = {A.x, A.y, A.z, A.w}, cb[4] = {B.x, B.y, B.z, B.w}, cc[4] = {C.x, C.y, C.z, C.w}, cd[4] = {D.x, D.y, D.z, D.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 p = x[4 * k + j];
+                            x[4 * k + j] = make_float2(fmaf(p.x, ca[j], p.y * cb[j]), fmaf(p.x, cc[j], p.y * cd[j]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 p = x[2 * k + j], q = x[2 * k + j + 4];
+                            x[2 * k + j] = fma2(p, j ? make_float2(A.z, A.w) : make_float2(A.x, A.y), mul2(q, j ? make_float2(B.z, B.w) : make_float2(B.x, B.y)));
+                            x[2 * k + j + 4] = fma2(p, j ? make_float2(C.z, C.w) : make_float2(C.x, C.y), mul2(q, j ? make_float2(D.z, D.w) : make_float2(D.x, D.y)));
+                        }
+                    }
+                }
+            } else if (norm && live) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w = __ldg(reinterpret_cast<const float4 *>(norm + lo) + j);        // (lo and hi side by side)
+                    x[2 * j] = mul2(x[2 * j], make_float2(w.x, w.y));
+                    x[2 * j + 1] = mul2(x[2 * j + 1], make_float2(w.z, w.w));
+                }
+            }
+            if (norm) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], r2);
+            }
+        };
+        uint16_t *out = a.q_out + ((uint64_t)i * a.n_q_heads + part * HPW + own) * a.head_dim + lo;
+        uint32_t t = part;
 #pragma unroll 1
-        for (uint32_t t = part; t < steps; t += a.parts) {
-            uint32_t g0;
-            const uint32_t what = kind_of(t, &g0), g = g0 + own;
-            const bool on = live && g < (what ? a.n_heads : a.n_q_heads);
-            if (!E4M3 && what == 2u) {                  // bits as they are
-                uint8_t *to = a.v_pages + dst + (uint64_t)g * a.page_head_stride;
+        for (; t < a.q_steps; t += a.parts, out += out_next) {
+            const bool on = live && t * HPW + own < a.n_q_heads;
+            float2 x[8];
+            unpack8(x0, x);
+            unpack8(x1, x + 4);
+            if (t + a.parts < a.q_steps) {
+                src += q_next;
+                fetch(src, live && (t + a.parts) * HPW + own < a.n_q_heads);
+            } else if (to_pages) {
+                fetch_kv(t + a.parts - a.q_steps);
+            }
+            turn(x, 0u);
+            if (on) {
+                *reinterpret_cast<uint4 *>(out) = pack8(x);
+                *reinterpret_cast<uint4 *>(out + apart) = pack8(x + 4);
+            }
+        }
+        if (!to_pages) continue;
+        const uint64_t p = a.pool_tokens >> 31 ? (uint64_t)slot / a.page.d : div_by((uint32_t)slot, a.page);
+        const uint64_t dst = p * a.page_stride + ((uint64_t)slot - p * a.page.d) * a.token_stride;
+#pragma unroll 1
+        for (t -= a.q_steps; t < 2u * a.kv_steps; t += a.parts) {
+            const uint32_t is_v = t >= a.kv_steps, g = (is_v ? t - a.kv_steps : t) * HPW + own;
+            const bool on = live && g < a.n_heads;
+            uint8_t *to = (is_v ? a.v_pages : a.k_pages) + dst + (uint64_t)g * a.page_head_stride;
+            if (!E4M3 && is_v) {                        // bits as they are
                 if (on) {
                     *reinterpret_cast<uint4 *>(to + 2u * lo) = x0;
                     *reinterpret_cast<uint4 *>(to + 2u * hi) = x1;
                 }
-                fetch(t + a.parts);
+                fetch_kv(t + a.parts);
                 continue;
             }
             float2 x[8];
             unpack8(x0, x);
             unpack8(x1, x + 4);
-            fetch(t + a.parts);
-            if (what < 2u) {
-                if (what ? a.k_norm != nullptr : a.q_norm != nullptr) {
-                    float2 sum2 = mul2(x[0], x[0]);
-#pragma unroll
-                    for (int j = 1; j < 8; ++j) sum2 = fma2(x[j], x[j], sum2);
-                    float sum = sum2.x + sum2.y;
-#pragma unroll
-                    for (uint32_t d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-                    const float r = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
-                    const float2 r2 = make_float2(r, r);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 w = live ? weight[what][((j < 2 ? lo : hi) >> 2) + (j & 1)] : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[2 * j] = mul2(mul2(x[2 * j], r2), make_float2(w.x, w.y));
-                        x[2 * j + 1] = mul2(mul2(x[2 * j + 1], r2), make_float2(w.z, w.w));
-                    }
-                }
-                if (turned) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 c = cosine[warp][k * LANES + u], s = sine[warp][k * LANES + u];
-                        if (a.interleaved) {
-                            const float cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 p = x[4 * k + j];
-                                x[4 * k + j] = fma2(p, make_float2(cs[j], cs[j]), mul2(make_float2(p.y, p.x), make_float2(-ss[j], ss[j])));
-                            }
-                        } else {
-                            const float2 c2[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)}, s2[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float2 p = x[2 * k + j], q = x[2 * k + j + 4];
-                                x[2 * k + j] = fma2(p, c2[j], mul2(q, make_float2(-s2[j].x, -s2[j].y)));
-                                x[2 * k + j + 4] = fma2(p, s2[j], mul2(q, c2[j]));
-                            }
-                        }
-                    }
-                }
-            }
+            fetch_kv(t + a.parts);
+            if (!is_v) turn(x, 1u);
             if (!on) continue;
-            if (what == 0) {
-                uint16_t *out = a.q_out + ((uint64_t)i * a.n_q_heads + g) * a.head_dim;
-                *reinterpret_cast<uint4 *>(out + lo) = pack8(x);
-                *reinterpret_cast<uint4 *>(out + hi) = pack8(x + 4);
+            if (E4M3) {
+                const float *scale = is_v ? a.v_scale : a.k_scale;
+                const ScaleOf sc = scale_of(scale ? __ldg(scale + g) : 1.0f);
+                *reinterpret_cast<uint2 *>(to + lo) = quantise8(x, sc);
+                *reinterpret_cast<uint2 *>(to + hi) = quantise8(x + 4, sc);
             } else {
-                uint8_t *to = (what == 1 ? a.k_pages : a.v_pages) + dst + (uint64_t)g * a.page_head_stride;
-                if (E4M3) {
-                    const float *scale = what == 1 ? a.k_scale : a.v_scale;
-                    const ScaleOf sc = scale_of(scale ? __ldg(scale + g) : 1.0f);
-                    *reinterpret_cast<uint2 *>(to + lo) = quantise8(x, sc);
-                    *reinterpret_cast<uint2 *>(to + hi) = quantise8(x + 4, sc);
-                } else {
-                    *reinterpret_cast<uint4 *>(to + 2u * lo) = pack8(x);
-                    *reinterpret_cast<uint4 *>(to + 2u * hi) = pack8(x + 4);
-                }
+                *reinterpret_cast<uint4 *>(to + 2u * lo) = pack8(x);
+                *reinterpret_cast<uint4 *>(to + 2u * hi) = pack8(x + 4);
             }
         }
     }
@@ -308,7 +321,7 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     a.page_stride = c.page_stride, a.token_stride = c.token_stride, a.page_head_stride = c.head_stride;
     a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.page = c.page;
     a.pool_tokens = (uint64_t)cache->n_pages * cache->page_tokens;
-    a.slots = slots, a.status = status, a.checked = n <= 2048u;
+    a.slots = slots, a.status = status, a.checked = n <= kRotateChecked;
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     const uint64_t blocks = ((uint64_t)n * parts + kRotateWarps - 1) / kRotateWarps;
     const unsigned grid = (unsigned)(blocks < kRotateBlocks * sms ? blocks : kRotateBlocks * sms);

@@ -45,18 +45,34 @@ __device__ __forceinline__ uint32_t e4m3_of(float value, const ScaleOf &c) {
 
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
+// Two binary32 numbers that one instruction works on; each is rounded as by itself.
+__device__ __forceinline__ uint64_t bits2(float2 a) { return (uint64_t)__float_as_uint(a.y) << 32 | __float_as_uint(a.x); }
+__device__ __forceinline__ float2 floats2(uint64_t b) { return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return floats2(r);
+}
+
 // Four codes, the same as e4m3_of's. The product with the reciprocal is within 2^-22 of the real quotient, so where a
 // little more and a little less than it have one code, that is the code; only a value next to a border (one
 // in some 60,000) takes the long way.
 __device__ __forceinline__ uint32_t e4m3x4_of(const float2 &a, const float2 &b, const ScaleOf &c) {
+    const float2 r = make_float2(c.r, c.r), up = make_float2(1.0f + 0x1p-21f, 1.0f + 0x1p-21f), down = make_float2(1.0f - 0x1p-21f, 1.0f - 0x1p-21f);
+    const bool plain = c.by == 1.0f;
+    const float2 x = mul2(plain ? a : make_float2(a.x * c.by, a.y * c.by), r), y = mul2(plain ? b : make_float2(b.x * c.by, b.y * c.by), r);
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float d = i ? 1.0f - 0x1p-21f : 1.0f + 0x1p-21f, r = c.r;
+        const float2 u = mul2(x, i ? up : down), v = mul2(y, i ? up : down);
         uint16_t lo, hi;
-        const float x = a.x * c.by * r, y = a.y * c.by * r, z = b.x * c.by * r, t = b.y * c.by * r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y * d), "f"(x * d));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(t * d), "f"(z * d));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(u.y), "f"(u.x));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v.y), "f"(v.x));
         w[i] = (uint32_t)hi << 16 | lo;
     }
     if (w[0] == w[1]) return w[0];
