@@ -410,15 +410,39 @@ __device__ __forceinline__ void leave_together(uint32_t C) {
     if (C > 1u) cg::this_cluster().sync();
 }
 
+// f(row, column, page) of the first len(row) entries of the table's row from(row), for every row, dealt to the warps of
+// the cluster in pieces of 32 entries, four of them on their way at once; most: the largest len.
+template <typename Len, typename From, typename F>
+__device__ __forceinline__ void each_entry(const PlanArgs &a, const Team &t, uint32_t most, Len len, From from, F f) {
+    const uint32_t lane = threadIdx.x & 31u, pieces = (most + 31u) / 32u, items = a.n_requests * pieces, warps = kPlanWarps * t.C;
+#pragma unroll 1
+    for (uint32_t m0 = (threadIdx.x >> 5) * t.C + t.rank; m0 < items; m0 += 4u * warps) {
+        uint32_t row[4], column[4];
+        int32_t page[4];
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t m = m0 + k * warps, r = m / pieces;
+            column[k] = 32u * (m - r * pieces) + lane;
+            row[k] = m < items && column[k] < len(r) ? r : ~0u;
+            page[k] = row[k] != ~0u ? __ldg(a.table + (uint64_t)from(r) * a.table_stride + column[k]) : 0;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (row[k] != ~0u) f(row[k], column[k], page[k]);
+    }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs a) {
     __shared__ uint32_t was[kSmallWords], now[kSmallWords];
-    __shared__ int32_t parent[kSmallRows], ctx[kSmallRows], have[kSmallRows], taken[kSmallRows];
-    __shared__ uint32_t heir[kSmallRows], part[kPlanWarps];
+    __shared__ int32_t parent[kSmallRows], ctx[kSmallRows], have[kSmallRows];
+    __shared__ uint32_t heir[kSmallRows], from[kSmallRows], keep[kSmallRows], part[kPlanWarps], most;
     cg::cluster_group cluster = cg::this_cluster();
     const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, n = a.n_requests;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, n = a.n_requests;
     const int32_t head = __ldg(a.free_in), count = __ldg(a.free_in + 1);
     bool bad = ring_bad(a, head, count), corrupt = false;
+    uint32_t longest = 0;
+    if (tid == 0) most = 0u;
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) {
         const uint32_t r = k * kPlanThreads + tid;
@@ -427,6 +451,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         if (r >= n) continue;
         const int32_t p = a.parents ? __ldg(a.parents + r) : (int32_t)r, c = __ldg(a.ctx_len + r), h = __ldg(a.n_in + r);
         parent[r] = p, ctx[r] = c, have[r] = h;
+        longest = max(longest, (uint32_t)h);
         bad |= p < -1 || p >= (int32_t)n || h < 0 || (uint32_t)h > a.max_pages || (int64_t)c > (int64_t)h * a.page.d;
     }
     if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
@@ -442,6 +467,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         const uint32_t f = from_of(s);
         if (f != ~0u) atomicMin(heir + f, f == s ? 0u : s + 1u);
     }
+    longest = __reduce_max_sync(~0u, longest);
+    if (lane == 0) atomicMax(&most, longest);
     __syncthreads();
     // Entries that an heir of row r keeps, and what row s has.
     const auto kept_of = [&](uint32_t r) -> uint32_t {
@@ -463,13 +490,17 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
     Fork mine[2];
     uint32_t took, k0;
 #pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) mine[k] = 2u * tid + k < n ? row_of(2u * tid + k) : Fork{~0u, 0u, 0u, 0u, false};
+    for (uint32_t k = 0; k < 2; ++k) {
+        mine[k] = 2u * tid + k < n ? row_of(2u * tid + k) : Fork{~0u, 0u, 0u, 0u, false};
+        from[2u * tid + k] = mine[k].from;
+        keep[2u * tid + k] = mine[k].keep;
+    }
     k0 = block_scan(mine[0].copies + mine[1].copies, &took, part);
     if (took > (uint32_t)count) {
         hand_on(a, t, SKV_ERR_CAPACITY);
         return;
     }
-    int32_t src[2], dst[2];
+    int32_t src[2], dst[2], fresh[2];
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) {
         const uint32_t s = 2u * tid + k;
@@ -478,8 +509,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
             uint64_t e = (uint64_t)head + k0 + (k ? mine[0].copies : 0u);
             if (e >= a.free_capacity) e -= a.free_capacity;
             src[k] = __ldg(a.table + (uint64_t)mine[k].from * a.table_stride + mine[k].keep);
-            dst[k] = __ldg(a.free_pages + e);
-            taken[s] = dst[k];
+            fresh[k] = dst[k] = __ldg(a.free_pages + e);
             if ((uint32_t)dst[k] < a.pool_pages) atomicOr(now + ((uint32_t)dst[k] >> 5), 1u << (dst[k] & 31));
             if ((uint32_t)src[k] >= a.pool_pages || (uint32_t)dst[k] >= a.pool_pages) {
                 corrupt = true;
@@ -489,21 +519,15 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         }
     }
     // Pages that rows held, and those that their heirs go on with (all others' are among them).
-#pragma unroll 1
-    for (uint32_t r = warp * t.C + t.rank; r < n; r += kPlanWarps * t.C) {
-        const uint32_t h = (uint32_t)have[r], keep = heir[r] == ~0u ? 0u : kept_of(r);
-        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < h; j += 32u) {
-            const uint32_t p = (uint32_t)__ldg(row + j);
-            if (p < a.pool_pages) {
-                atomicOr(was + (p >> 5), 1u << (p & 31u));
-                if (j < keep) atomicOr(now + (p >> 5), 1u << (p & 31u));
-            } else {
-                corrupt = true;
-            }
+    each_entry(a, t, most, [&](uint32_t r) { return (uint32_t)have[r]; }, [](uint32_t r) { return r; }, [&](uint32_t r, uint32_t j, int32_t p) {
+        if ((uint32_t)p < a.pool_pages) {
+            const uint32_t bit = 1u << (p & 31);
+            atomicOr(was + ((uint32_t)p >> 5), bit);
+            if (heir[r] != ~0u && j < kept_of(r)) atomicOr(now + ((uint32_t)p >> 5), bit);
+        } else {
+            corrupt = true;
         }
-    }
+    });
     cluster.sync();
     uint32_t w[2];
 #pragma unroll
@@ -533,18 +557,11 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
             a.src[s] = src[k], a.dst[s] = dst[k], a.count[s] = (int32_t)mine[k].part;
             a.n_out[s] = (int32_t)(mine[k].keep + mine[k].copies);
             a.ctx_out[s] = mine[k].from == ~0u ? -1 : ctx[mine[k].from];
+            if (mine[k].copies) a.table_out[(uint64_t)s * a.out_stride + mine[k].keep] = fresh[k];
         }
     }
-#pragma unroll 1
-    for (uint32_t s = warp * t.C + t.rank; s < n; s += kPlanWarps * t.C) {
-        const Fork f = row_of(s);
-        if (f.from == ~0u) continue;
-        const int32_t *row = a.table + (uint64_t)f.from * a.table_stride;
-        int32_t *out = a.table_out + (uint64_t)s * a.out_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < f.keep; j += 32u) out[j] = __ldg(row + j);
-        if (f.copies && lane == 0) out[f.keep] = taken[s];
-    }
+    each_entry(a, t, most, [&](uint32_t s) { return keep[s]; }, [&](uint32_t s) { return from[s]; },
+               [&](uint32_t s, uint32_t j, int32_t p) { a.table_out[(uint64_t)s * a.out_stride + j] = p; });
     if (t.rank == 0 && tid == 0) {
         uint64_t e = (uint64_t)head + took;
         const uint32_t cap = max(a.free_capacity, 1u);
@@ -559,31 +576,33 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
 __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanArgs a) {
     __shared__ uint32_t bits[kSmallWords], held[kSmallWords], part[kPlanWarps];
     __shared__ uint16_t far_before[kSmallWords], hole[kSmallPool / 2u];
+    __shared__ int32_t have[kSmallRows];
+    __shared__ uint32_t most;
     cg::cluster_group cluster = cg::this_cluster();
     const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u;
     bits[tid] = bits[kPlanThreads + tid] = 0u;
     bool bad = false, corrupt = false;
+    uint32_t longest = 0;
+    if (tid == 0) most = 0u;
     for (uint32_t r = tid; r < a.n_requests; r += kPlanThreads) {
         const int32_t h = __ldg(a.n_in + r);
         bad |= h < 0 || (uint32_t)h > a.max_pages;
+        have[r] = h;
+        longest = max(longest, (uint32_t)h);
     }
     if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
     if (__syncthreads_or(bad)) {                          // the same in every CTA
         hand_on(a, t, SKV_ERR_INVALID_ARG);
         return;
     }
-#pragma unroll 1
-    for (uint32_t r = warp * t.C + t.rank; r < a.n_requests; r += kPlanWarps * t.C) {
-        const uint32_t h = (uint32_t)__ldg(a.n_in + r);
-        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < h; j += 32u) {
-            const uint32_t p = (uint32_t)__ldg(row + j);
-            if (p < a.pool_pages) atomicOr(bits + (p >> 5), 1u << (p & 31u));
-            else corrupt = true;
-        }
-    }
+    longest = __reduce_max_sync(~0u, longest);
+    if (lane == 0) atomicMax(&most, longest);
+    __syncthreads();
+    each_entry(a, t, most, [&](uint32_t r) { return (uint32_t)have[r]; }, [](uint32_t r) { return r; }, [&](uint32_t, uint32_t, int32_t p) {
+        if ((uint32_t)p < a.pool_pages) atomicOr(bits + ((uint32_t)p >> 5), 1u << (p & 31));
+        else corrupt = true;
+    });
     cluster.sync();
     uint32_t w[2], live, all;
 #pragma unroll
@@ -621,21 +640,13 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanA
     __syncthreads();
     for (uint32_t i = moves + t.rank * kPlanThreads + tid; i < a.capacity; i += t.C * kPlanThreads) a.src[i] = a.dst[i] = -1;
     for (uint32_t i = t.rank * kPlanThreads + tid; i < a.pool_pages - live; i += t.C * kPlanThreads) a.free_pages[i] = (int32_t)(live + i);
-#pragma unroll 1
-    for (uint32_t r = warp * t.C + t.rank; r < a.n_requests; r += kPlanWarps * t.C) {
-        const uint32_t h = (uint32_t)__ldg(a.n_in + r);
-        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
-        int32_t *out = a.table_out + (uint64_t)r * a.out_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < h; j += 32u) {
-            uint32_t p = (uint32_t)__ldg(row + j);
-            if (p >= live && p < a.pool_pages) {
-                const uint32_t i = p >> 5, under = held[i] & ~below(i, live) & ((1u << (p & 31u)) - 1u);
-                p = hole[far_before[i] + __popc(under)];
-            }
-            out[j] = (int32_t)p;
+    each_entry(a, t, most, [&](uint32_t r) { return (uint32_t)have[r]; }, [](uint32_t r) { return r; }, [&](uint32_t r, uint32_t j, int32_t p) {
+        if ((uint32_t)p >= live && (uint32_t)p < a.pool_pages) {
+            const uint32_t i = (uint32_t)p >> 5, under = held[i] & ~below(i, live) & ((1u << (p & 31)) - 1u);
+            p = hole[far_before[i] + __popc(under)];
         }
-    }
+        a.table_out[(uint64_t)r * a.out_stride + j] = p;
+    });
     if (t.rank == 0 && tid == 0) {
         a.free_out[0] = 0;
         a.free_out[1] = (int32_t)(a.pool_pages - live);
@@ -656,7 +667,7 @@ struct CopyArgs {
     uint32_t checked;
 };
 
-constexpr uint32_t kCopyThreads = 256, kCopyDeep = 4, kCopyUnits = kCopyThreads * kCopyDeep;
+constexpr uint32_t kCopyThreads = 256, kCopyDeep = 2, kCopyUnits = kCopyThreads * kCopyDeep;
 
 // A pair's pages and how many tokens of them; false: nothing to copy (bad: not as it should be).
 __device__ __forceinline__ bool pair_of(const CopyArgs &a, uint32_t i, int32_t *src, int32_t *dst, uint32_t *n, bool *bad) {
@@ -850,6 +861,10 @@ static bool launch_plan(void (*kernel)(PlanArgs), bool small, const PlanArgs &a,
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess;
 }
 
+static bool fits_small(uint32_t pool_pages, uint32_t n_requests, uint32_t max_pages) {
+    return pool_pages <= kSmallPool && n_requests <= kSmallRows && max_pages <= (1u << 20);
+}
+
 static uint64_t bits_bytes(uint32_t pool_pages) { return ((uint64_t)pool_pages + 511u) / 512u * 64u; }
 
 static uint64_t workspace_bytes(uint32_t n_requests, uint32_t pool_pages) {
@@ -902,7 +917,7 @@ extern "C" int32_t skv_page_fork(uint32_t page_tokens, uint32_t pool_pages, uint
     a.src = copy_src, a.dst = copy_dst, a.count = copy_tokens, a.status = status;
     a.bits = static_cast<uint32_t *>(workspace);
     a.words = a.bits + bits_bytes(pool_pages) / 4u;
-    const bool small = pool_pages <= kSmallPool && n_requests <= kSmallRows;
+    const bool small = fits_small(pool_pages, n_requests, max_pages);
     return launch_plan(small ? fork_small_kernel : fork_pages_kernel, small, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
 }
 
@@ -930,7 +945,7 @@ extern "C" int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, co
     a.table_out = table_out, a.free_pages = free_pages, a.free_out = free_out, a.src = copy_src, a.dst = copy_dst, a.status = status;
     a.bits = static_cast<uint32_t *>(workspace);
     a.words = a.bits + bits_bytes(pool_pages) / 4u;
-    const bool small = pool_pages <= kSmallPool;
+    const bool small = fits_small(pool_pages, n_requests, max_pages);
     return launch_plan(small ? compact_small_kernel : compact_pages_kernel, small, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
 }
 
@@ -955,7 +970,7 @@ extern "C" int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, co
     a.by_chunks = fast_div(a.chunks);
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     const uint64_t items = (uint64_t)n * a.chunks;
-    const unsigned grid = (unsigned)(items < 8u * sms ? items : 8u * sms);
+    const unsigned grid = (unsigned)(items < 16u * sms ? items : 16u * sms);
     copy_pages_kernel<<<grid, kCopyThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
 }

@@ -223,18 +223,15 @@ class PagePool(PageTable):
         if _capturing(stream):
             raise ValueError("PagePool.fork swaps its counts on the host; capture fork_into")
         ctx, src, dst, tokens = torch.empty((4, self.n_requests), dtype=torch.int32, device=self.block_table.device).unbind()
-        table = self.block_table.clone()
-        if self.workspace is None:
-            self._make_workspace(stream)
-        _after_current(stream)
+        table = self._other_table(stream)
         self.fork_into(parents, ctx_len, self.n_pages, self.free_pages, self.free_state, table, self._next[0], ctx, self._next[1], src, dst,
                        tokens, trim=trim, stream=stream)
         self._take(table, self._next[0], stream)
         self._shared = True
         if check:
             self.check_status("skv_page_fork", stream)
-        elif stream is not None:
-            for t in (table, ctx, src, dst, tokens):
+        elif stream is not None:                         # given up early, they are not handed out early
+            for t in (ctx, src, dst, tokens):
                 t.record_stream(stream)
         return ctx, src, dst, tokens
 
@@ -244,21 +241,27 @@ class PagePool(PageTable):
         if _capturing(stream):
             raise ValueError("PagePool.compact swaps its counts on the host; capture compact_into")
         src, dst = torch.empty((2, self.pool_pages), dtype=torch.int32, device=self.block_table.device).unbind()
-        table = self.block_table.clone()
-        if self.workspace is None:
-            self._make_workspace(stream)
-        _after_current(stream)
+        table = self._other_table(stream)
         self.compact_into(self.n_pages, self.free_pages, self.free_state, table, self._next[1], src, dst, stream=stream)
         self._take(table, self.n_pages, stream)
         if check:
             self.check_status("skv_page_compact", stream)
         elif stream is not None:
-            for t in (table, src, dst):
+            for t in (src, dst):
                 t.record_stream(stream)
         return src, dst
 
+    def _other_table(self, stream):
+        """A second table for a call on `stream`, in that stream's memory and order: earlier calls on it
+        may still be writing the first."""
+        if self.workspace is None:
+            self._make_workspace(stream)
+        _after_current(stream)
+        with torch.cuda.stream(stream):
+            return self.block_table.clone()
+
     def _take(self, table, n_pages, stream):
-        """The rows of `table`, n_pages (self.n_pages, or what a call left in _next) and the ring state
+        """The rows of `table`, n_pages (self.n_pages, or what the call left in _next) and the ring state
         that the call left become the pool's."""
         with torch.cuda.stream(stream):
             self.block_table.copy_(table)
