@@ -104,7 +104,7 @@ def test_far_and_negative_positions():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-@pytest.mark.parametrize("n", [5, 3000])
+@pytest.mark.parametrize("n", [5, 3000, 9001])
 def test_without_rotation_it_is_append(n, dtype):
     """No norm and no frequencies: the pages get what append writes, bit for bit."""
     s = made(3, n, 4, 2, 96, 16, dtype)

@@ -131,6 +131,21 @@ def test_more_nodes_than_are_gathered_at_once(draft, n):
         compare(s)
 
 
+@pytest.mark.parametrize("draft,dtype", [("best", "f32"), ("best", "bf16"), ("drawn", "f32")])
+def test_many_requests_of_a_large_vocabulary(draft, dtype):
+    """Few CTAs to a request: a part of the row comes in several pieces."""
+    compare(made(3, [2, 1, 3, 0] * 25, 60001, dtype, draft, spread=4.0))
+
+
+def test_no_rows():
+    v = Verifier(3, 100)
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    acc, rows, nxt, after = v.verify(torch.zeros(0, 100, device="cuda"), e, i32([0, 0, 0, 0]), e.float(), ctx_len=i32([4, 5, -1]))
+    assert acc.tolist() == [0, 0, 0] and nxt.tolist() == [-1, -1, -1] and rows.numel() == 0 and after.tolist() == [4, 5, -1]
+    v = Verifier(0, 100)
+    assert v.verify(torch.zeros(2, 100, device="cuda"), i32([1, 1]), i32([0]), torch.zeros(2, device="cuda"))[1].tolist() == [-1, -1]
+
+
 def test_uniform_numbers_at_the_ends():
     for u in (0.0, 1.0 - 2.0 ** -24, 2.0 ** -149, 0.5):
         for draft in ("drawn", "distinct", "best"):
