@@ -497,6 +497,8 @@ int32_t skv_decode_noalloc(const skv_layout *lay, const void *bitstream, uint64_
  *   skv_page_map        which page and slot each new token gets, on the GPU
  *   skv_cache_append    the new K and V rows go to those slots
  *   skv_tree_attention  the new tokens' queries read the pages
+ * and behind them the calls of a whole step: skv_rotate_append, skv_tree_verify, skv_cache_move, skv_page_fork,
+ * skv_page_compact and skv_cache_copy.
  *
  * skv_paged: a K and a V pool of n_pages pages, both with the same strides.
  * The value of token t of a page, KV head h, channel d is at

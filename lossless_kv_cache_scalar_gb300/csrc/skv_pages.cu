@@ -8,7 +8,11 @@
 // others' bits after the one barrier and works the rest out for itself. Larger ones keep them in the workspace, with
 // a barrier of the cluster (half a microsecond, where a launch costs two) after each step.
 //
-// copy and move bring the K and V: 16 bytes per thread and step, bound by HBM.
+// On the device 6.0 us for a fork of 8 rows (one CTA), 11.5 for one of 700 rows of 48 pages (a cluster of 8, two barriers), 10.6 for a compaction
+// of 200 rows of 47: latency, some 2.5 us of it the launch and as much the cluster's.
+//
+// copy and move bring the K and V: 16 bytes per thread and step. Copies are bound by HBM: 2,422 pages of 64 x 8 x 128 codes, K and V, in 99 us
+// (6.4 TB/s, 0.94 of a copy). Moves are five dependent loads: 3 us for 8 paths, 10 for 256 (with the status cleared before them).
 #include <cooperative_groups.h>
 
 #include "skv_rows.cuh"

@@ -375,6 +375,8 @@ class PagedKV(_Status):
             q_ptr, out_ptr, heads, q_row, q_head = q.data_ptr(), q_out.data_ptr(), q_shape[1], q_stride[0], q_stride[1]
         elif q_out is not None:
             raise ValueError("q_out without q")
+        if rotary.n_axes > 1 and positions.shape != (rotary.n_axes, n):
+            raise ValueError(f"positions must be an int32 tensor [{rotary.n_axes}][{n}]")
         _check_words("positions", _I32, rotary.n_axes * n, dev, positions)
         _check_words("slots", _I64, n, dev, slots)
         rc = B.lib().skv_rotate_append(self._ref, rotary._ref, q_ptr, q_row, q_head, heads, k.data_ptr(), v.data_ptr(), stride[0], stride[1],

@@ -448,6 +448,33 @@ def test_plans_in_a_graph():
     check_fork(got, fork(page, pool + n, parents, ctx, rows, have, ring, state, False), width)
 
 
+def test_tables_with_wider_rows_and_an_empty_ring():
+    """Rows of wider tensors, in and out; what lies beside them stays."""
+    wide = torch.full((3, 9), 77, dtype=torch.int32, device="cuda")
+    wide[:, 2:6] = i32([[4, 1, -9, -9], [0, -9, -9, -9], [4, 3, 2, -9]])
+    other = torch.full((3, 12), 55, dtype=torch.int32, device="cuda")
+    t = PageTable(wide[:, 2:6], 4, 6)
+    empty, st, st2 = i32([]), i32([0, 0]), i32([-9, -9])
+    ctx, have = i32([8, 4, 11]), i32([2, 1, 3])
+    out = [i32([0] * 3) for _ in range(5)]
+    t.fork_into(i32([0, 0, 2]), ctx, have, empty, st, other[:, 1:5], out[0], out[1], st2, *out[2:])
+    torch.cuda.synchronize()
+    assert int(t.status) == 6                              # page 0 comes free, and the ring has no room
+    t.fork_into(i32([0, 1, 0]), ctx, have, empty, st, other[:, 1:5], out[0], out[1], st2, *out[2:])
+    torch.cuda.synchronize()
+    assert int(t.status) == 6
+    t.fork_into(None, ctx, have, empty, st, other[:, 1:5], out[0], out[1], st2, *out[2:])
+    t.check_status("fork")
+    assert other.tolist() == [[55, 4, 1] + [55] * 9, [55, 0] + [55] * 10, [55, 4, 3, 2] + [55] * 8]
+    assert out[0].tolist() == [2, 1, 3] and st2.tolist() == [0, 0]
+    ring, other = i32([-1] * 6), other.fill_(55)
+    t.compact_into(have, ring, st, other[:, 3:7], st2, out[2], out[3])
+    t.check_status("compact")
+    assert other.tolist() == [[55] * 3 + [4, 1] + [55] * 7, [55] * 3 + [0] + [55] * 8, [55] * 3 + [4, 3, 2] + [55] * 6]
+    assert ring.tolist() == [5] + [-1] * 5 and st2.tolist() == [0, 1] and out[2].tolist() == [-1] * 3
+    assert wide[:, :2].eq(77).all() and wide[:, 6:].eq(77).all()
+
+
 def test_what_the_wrappers_refuse():
     t = PageTable(i32([[0, 1], [2, 3]]), 4, 8)
     a = dict(parents=i32([0, 1]), ctx_len=i32([5, 6]), n_pages=i32([2, 2]), free_pages=i32([4, 5, 6, 7]), free_state=i32([0, 4]),

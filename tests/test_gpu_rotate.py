@@ -188,6 +188,25 @@ def test_pools_with_strides_and_far_pages():
     assert torch.equal(pool[slots // 64, 0, slots % 64], s["kn"]) and torch.equal(pool[slots // 64, 1, slots % 64], s["vn"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_pages_with_heads_before_tokens(dtype):
+    """Strides of their own for heads and tokens, K and V in one tensor: the same rows as in a plain pool."""
+    s = made(15, 70, 4, 3, 96, 24, dtype)
+    pages = s["k"].shape[0]
+    both = torch.zeros(pages, 2, 3, 24, 96, dtype=s["k"].dtype, device="cuda")
+    k, v = both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2)
+    rotary, pos = Rotary(96, freqs(64), torch.ones(96), torch.ones(96)), torch.arange(70, dtype=torch.int32, device="cuda")
+    want = s["cache"].rotate_append(rotary, s["q"], s["kn"], s["vn"], pos, s["slots"])
+    got = PagedKV(k, v, k_scale=s["ks"], v_scale=s["vs"]).rotate_append(rotary, s["q"], s["kn"], s["vn"], pos, s["slots"])
+    assert torch.equal(got, want)
+    at = s["slots"][s["slots"] >= 0]
+    for mine, plain in ((k, s["k"]), (v, s["v"])):
+        assert torch.equal(mine[at // 24, at % 24].view(torch.uint8), plain[at // 24, at % 24].view(torch.uint8))
+    left = torch.ones(pages * 24, dtype=torch.bool, device="cuda")
+    left[at] = False
+    assert not k.reshape(pages * 24, 3, 96)[left].float().any() and not v.reshape(pages * 24, 3, 96)[left].float().any()
+
+
 def test_in_a_graph_and_on_another_stream():
     s = made(13, 30, 4, 2, 128, 16, "e4m3", skip=0.0)
     w = torch.ones(128)
@@ -221,7 +240,8 @@ def test_what_the_wrapper_refuses():
     c.rotate_append_into(**good)
     for kw in (dict(rotary=Rotary(96, freqs(96))), dict(q=s["q"].float()), dict(q=s["q"][:3]), dict(q_out=out[:, :2]), dict(q_out=None), dict(q=None),
                dict(k=s["kn"][:, :1]), dict(v=s["vn"].contiguous()), dict(positions=pos.long()), dict(positions=pos[:3]), dict(slots=s["slots"].int()),
-               dict(rotary=Rotary(64, freqs(64), axes=[0, 1] * 16))):
+               dict(rotary=Rotary(64, freqs(64), axes=[0, 1] * 16)),
+               dict(rotary=Rotary(64, freqs(64), axes=[0, 1] * 16), positions=torch.zeros(4, 2, dtype=torch.int32, device="cuda"))):
         with pytest.raises(ValueError):
             c.rotate_append_into(**dict(good, **kw))
     for a in (dict(inv_freq=freqs(80)), dict(inv_freq=[1.0] * 7), dict(inv_freq=[math.nan] * 8), dict(inv_freq=freqs(64), axes=[0]),
