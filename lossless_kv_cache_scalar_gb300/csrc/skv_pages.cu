@@ -5,11 +5,13 @@
 // rows that go on; no count per page is kept between calls that could drift from the tables.
 // Everything comes out in a fixed order: prefix sums over rows and over the words of bits.
 // Pools of up to 32,768 pages keep the bits in shared memory: every CTA marks its share of the rows, reads the
-// others' bits after the one barrier and works the rest out for itself. Larger ones keep them in the workspace, with
-// a barrier of the cluster (half a microsecond, where a launch costs two) after each step.
+// others' bits after the one barrier and works the rest out for itself. Larger ones (or more than 1,024 rows) keep them in
+// the workspace, with a barrier of a cluster of 16 (half a microsecond, where a launch costs two) after each step.
 //
-// On the device 6.0 us for a fork of 8 rows (one CTA), 11.5 for one of 700 rows of 48 pages (a cluster of 8, two barriers), 10.6 for a compaction
-// of 200 rows of 47: latency, some 2.5 us of it the launch and as much the cluster's.
+// On the device 6.0 us for a fork of 8 rows (one CTA), 10.0 for one of 700 rows of 48 pages (a cluster of 8, two barriers), 9.8 for a compaction
+// of 200 rows of 47: latency, some 2.5 us of it the launch and as much the cluster's. In the workspace 17 for a compaction of 200 rows of
+// 188 pages in a pool of 63,120, 23 for a fork of 4,000 rows of 189. A warp takes two rows at a time, two pieces of 32 entries of
+// each on their way; with a warp per row and its lengths looked up anew for each piece these two took 30 and 73.
 //
 // copy and move bring the K and V: 16 bytes per thread and step. Copies are bound by HBM: 2,422 pages of 64 x 8 x 128 codes, K and V, in 99 us
 // (6.4 TB/s, 0.94 of a copy). Moves are five dependent loads: 3 us for 8 paths, 10 for 256 (with the status cleared before them).
@@ -21,7 +23,8 @@ namespace skv {
 
 namespace cg = cooperative_groups;
 
-constexpr uint32_t kPlanThreads = 512, kPlanWarps = kPlanThreads / 32u, kPlanCluster = 8;
+constexpr uint32_t kPlanThreads = 512, kPlanWarps = kPlanThreads / 32u, kPlanCluster = 8;      // pools whose bits fit shared memory
+constexpr uint32_t kLargeThreads = 1024, kLargeWarps = kLargeThreads / 32u, kLargeCluster = 16;
 
 struct PlanArgs {
     FastDiv page;
@@ -29,50 +32,50 @@ struct PlanArgs {
     const int32_t *parents, *ctx_len, *table, *n_in, *free_in;
     uint64_t table_stride, out_stride;
     int32_t *table_out, *n_out, *ctx_out, *free_pages, *free_out, *src, *dst, *count, *status;
-    uint32_t *bits;                     // workspace: a bit per page
-    uint32_t *words;                    // fork: the heir of each row; compact: rank of a far page, then the holes
+    uint32_t *bits, *now;               // workspace: a bit per page, twice
+    uint32_t *words;                    // fork: each row's heir, old row and entries of it; compact: rank of a far page, then the holes
 };
 
-// What the CTAs of the cluster tell each other: a word each, in every CTA's shared memory.
+// What the CTAs of the cluster tell each other: two numbers each, in every CTA's shared memory.
 struct Told {
-    uint32_t word[2][kPlanCluster];
+    uint2 word[2][kLargeCluster];
 };
 
 struct Team {
     uint32_t C, rank, parity;
     Told *told;
 
-    // Every thread calls; w is thread 0's. All writes of the cluster before it are seen after it.
-    __device__ __forceinline__ const uint32_t *tell(uint32_t w) {
+    // The sums of the CTAs' two numbers (thread 0's), and those of the CTAs before this one. Every thread calls; all writes of
+    // the cluster before it, to global memory too, are seen after it (release and acquire of the cluster's barrier).
+    __device__ __forceinline__ uint2 sum(uint32_t x, uint32_t y, uint2 *before) {
         cg::cluster_group cluster = cg::this_cluster();
-        if (threadIdx.x == 0)
-            for (uint32_t j = 0; j < C; ++j) *cluster.map_shared_rank(&told->word[parity][rank], j) = w;
-        __threadfence();
+        if (threadIdx.x < C) *cluster.map_shared_rank(&told->word[parity][rank], threadIdx.x) = make_uint2(x, y);
         cluster.sync();
-        const uint32_t *all = told->word[parity];
+        uint2 all = make_uint2(0u, 0u);
+        for (uint32_t j = 0; j < C; ++j) {
+            const uint2 w = told->word[parity][j];
+            if (j == rank) *before = all;
+            all.x += w.x;
+            all.y += w.y;
+        }
         parity ^= 1u;
         return all;
     }
-    __device__ __forceinline__ uint32_t any(uint32_t w) {
-        const uint32_t *all = tell(w);
-        uint32_t x = 0;
-        for (uint32_t j = 0; j < C; ++j) x |= all[j];
-        return x;
+    __device__ __forceinline__ uint32_t sum(uint32_t x, uint32_t *before) {
+        uint2 b;
+        const uint32_t all = sum(x, 0u, &b).x;
+        *before = b.x;
+        return all;
     }
-    // The sum of the CTAs' words, and of those before this one.
-    __device__ __forceinline__ uint32_t sum(uint32_t w, uint32_t *before) {
-        const uint32_t *all = tell(w);
-        uint32_t x = 0;
-        *before = 0;
-        for (uint32_t j = 0; j < C; ++j) {
-            if (j == rank) *before = x;
-            x += all[j];
-        }
-        return x;
+    __device__ __forceinline__ bool any(bool x) {
+        uint32_t b;
+        return sum(x, &b) != 0u;
     }
+    __device__ __forceinline__ void meet() { cg::this_cluster().sync(); }
 };
 
-// Exclusive prefix sum over the block, and the total. part: a word per warp.
+// Exclusive prefix sum over a block of WARPS warps, and the total. part: a word per warp.
+template <uint32_t WARPS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *total, uint32_t *part) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, in = x;
 #pragma unroll
@@ -83,42 +86,63 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *total, uint
     __syncthreads();
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    const uint32_t p = lane < kPlanWarps ? part[lane] : 0u;
+    const uint32_t p = lane < WARPS ? part[lane] : 0u;
     *total = __reduce_add_sync(~0u, p);
     return x - in + __reduce_add_sync(~0u, lane < warp ? p : 0u);
 }
 
-__device__ __forceinline__ uint32_t *bit_word(const PlanArgs &a, uint32_t page) { return a.bits + (page >> 5); }
+__device__ __forceinline__ void set_bit(uint32_t *bits, uint32_t page) { atomicOr(bits + (page >> 5), 1u << (page & 31u)); }
 
-// Sets the bit of every page that a row holds; whether all of them lie in the pool.
-__device__ __forceinline__ bool mark_rows(const PlanArgs &a, const Team &t) {
-    const uint32_t lane = threadIdx.x & 31u;
-    bool ok = true;
+// What a walk over the table needs of a row: how many entries, of which row of the old table, and a number of the caller's.
+struct Head {
+    uint32_t len, from, extra;
+};
+
+// f(row, its head, column, g(page)) of every entry: two rows to a warp at a time, two pieces of 32 entries of each on their way.
+template <uint32_t WARPS, typename HeadOf, typename G, typename F>
+__device__ __forceinline__ void each_entry(const PlanArgs &a, const Team &t, HeadOf head_of, G g, F f) {
+    const uint32_t lane = threadIdx.x & 31u, warps = WARPS * t.C;
 #pragma unroll 1
-    for (uint32_t r = t.rank * kPlanWarps + (threadIdx.x >> 5); r < a.n_requests; r += t.C * kPlanWarps) {
-        const uint32_t n = (uint32_t)__ldg(a.n_in + r);
-        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < n; j += 32u) {
-            const uint32_t p = (uint32_t)__ldg(row + j);
-            if (p < a.pool_pages) atomicOr(bit_word(a, p), 1u << (p & 31u));
-            else ok = false;
+    for (uint64_t r0 = (threadIdx.x >> 5) * t.C + t.rank; r0 < a.n_requests; r0 += 2u * warps) {
+        Head h[2];
+        uint32_t most = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) {
+            h[k] = r0 + k * warps < a.n_requests ? head_of((uint32_t)r0 + k * warps) : Head{0u, 0u, 0u};
+            most = max(most, h[k].len);
+        }
+#pragma unroll 1
+        for (uint32_t j0 = 0; j0 < most; j0 += 64u) {
+            int32_t page[2][2];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t j = j0 + 32u * (k & 1u) + lane;
+                const Head &x = h[k >> 1];
+                page[k >> 1][k & 1u] = j < x.len ? __ldg(a.table + (uint64_t)x.from * a.table_stride + j) : 0;
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+                if (j0 + 32u * (k & 1u) + lane < h[k >> 1].len) page[k >> 1][k & 1u] = g(page[k >> 1][k & 1u]);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t j = j0 + 32u * (k & 1u) + lane;
+                const Head &x = h[k >> 1];
+                if (j < x.len) f((uint32_t)r0 + (k >> 1) * warps, x, j, page[k >> 1][k & 1u]);
+            }
         }
     }
-    return ok;
 }
 
-__device__ __forceinline__ void clear_bits(const PlanArgs &a, const Team &t) {
-    const uint32_t n = (a.pool_pages + 31u) >> 5;
-    for (uint32_t i = t.rank * kPlanThreads + threadIdx.x; i < n; i += t.C * kPlanThreads) a.bits[i] = 0u;
-}
+struct AsItIs {
+    __device__ __forceinline__ int32_t operator()(int32_t p) const { return p; }
+};
 
 // Words of bits of this CTA and, in them, of this thread: runs in order.
 __device__ __forceinline__ void run_of(const PlanArgs &a, const Team &t, uint32_t *from, uint32_t *to) {
-    const uint32_t n = (a.pool_pages + 31u) >> 5, each = (n + t.C * kPlanThreads - 1u) / (t.C * kPlanThreads);
-    const uint64_t at = (uint64_t)(t.rank * kPlanThreads + threadIdx.x) * each;
-    *from = (uint32_t)min(at, (uint64_t)n);
-    *to = (uint32_t)min(at + each, (uint64_t)n);
+    const uint32_t n = (a.pool_pages + 31u) >> 5, per_cta = (n + t.C - 1u) / t.C, each = (per_cta + blockDim.x - 1u) / blockDim.x;
+    const uint32_t end = min((t.rank + 1u) * per_cta, n);
+    *from = min(t.rank * per_cta + threadIdx.x * each, end);
+    *to = min(*from + each, end);
 }
 
 __device__ __forceinline__ bool ring_bad(const PlanArgs &a, int32_t head, int32_t count) {
@@ -129,7 +153,7 @@ __device__ __forceinline__ bool ring_bad(const PlanArgs &a, int32_t head, int32_
 // The tables handed on as they were, after an error (page counts clamped to the rows).
 __device__ __forceinline__ void hand_on(const PlanArgs &a, const Team &t, int32_t err) {
     const uint32_t lane = threadIdx.x & 31u;
-    for (uint32_t r = t.rank * kPlanWarps + (threadIdx.x >> 5); r < a.n_requests; r += t.C * kPlanWarps) {
+    for (uint32_t r = t.rank * (blockDim.x >> 5) + (threadIdx.x >> 5); r < a.n_requests; r += t.C * (blockDim.x >> 5)) {
         const uint32_t n = min((uint32_t)max(__ldg(a.n_in + r), 0), a.max_pages);
         for (uint32_t j = lane; j < n; j += 32u)
             a.table_out[(uint64_t)r * a.out_stride + j] = __ldg(a.table + (uint64_t)r * a.table_stride + j);
@@ -138,7 +162,7 @@ __device__ __forceinline__ void hand_on(const PlanArgs &a, const Team &t, int32_
             a.ctx_out[r] = __ldg(a.ctx_len + r);
         }
     }
-    for (uint32_t i = t.rank * kPlanThreads + threadIdx.x; i < a.capacity; i += t.C * kPlanThreads) {
+    for (uint32_t i = t.rank * blockDim.x + threadIdx.x; i < a.capacity; i += t.C * blockDim.x) {
         a.src[i] = a.dst[i] = -1;
         if (a.count) a.count[i] = 0;
     }
@@ -155,6 +179,11 @@ __device__ __forceinline__ void hand_on(const PlanArgs &a, const Team &t, int32_
 __device__ __forceinline__ uint32_t parent_row(const PlanArgs &a, uint32_t s) {
     const int32_t p = a.parents ? __ldg(a.parents + s) : (int32_t)s;
     return p < 0 || __ldg(a.ctx_len + p) < 0 ? ~0u : (uint32_t)p;
+}
+
+__device__ __forceinline__ uint32_t pages_of(const PlanArgs &a, uint32_t tokens) {
+    const uint32_t whole = div_by(tokens, a.page);
+    return whole + (tokens != whole * a.page.d);
 }
 
 struct Fork {
@@ -181,129 +210,125 @@ __device__ __forceinline__ Fork fork_of(const PlanArgs &a, uint32_t s) {
     return f;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) fork_pages_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kLargeThreads) fork_pages_kernel(const PlanArgs a) {
     __shared__ Told told;
-    __shared__ uint32_t part[kPlanWarps];
+    __shared__ uint32_t part[kLargeWarps];
     cg::cluster_group cluster = cg::this_cluster();
     Team t{cluster.num_blocks(), cluster.block_rank(), 0u, &told};
-    const uint32_t tid = threadIdx.x, lane = tid & 31u;
+    const uint32_t tid = threadIdx.x, all_threads = t.C * kLargeThreads, mine_of_all = t.rank * kLargeThreads + tid;
     const int32_t head = __ldg(a.free_in), count = __ldg(a.free_in + 1);
+    if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
     cluster.sync();                                       // every CTA has started
 
     // Errors of the lengths; the workspace is made ready.
     bool bad = ring_bad(a, head, count);
-    for (uint32_t r = t.rank * kPlanThreads + tid; r < a.n_requests; r += t.C * kPlanThreads) {
+    for (uint32_t r = mine_of_all; r < a.n_requests; r += all_threads) {
         const int32_t p = a.parents ? __ldg(a.parents + r) : (int32_t)r, c = __ldg(a.ctx_len + r), h = __ldg(a.n_in + r);
         bad |= p < -1 || p >= (int32_t)a.n_requests || h < 0 || (uint32_t)h > a.max_pages || (int64_t)c > (int64_t)h * a.page.d;
         a.words[r] = ~0u;
     }
-    clear_bits(a, t);
-    bad = __syncthreads_or(bad);
-    if (t.any(bad)) {
+    for (uint32_t i = mine_of_all; i < (a.pool_pages + 31u) >> 5; i += all_threads) a.bits[i] = a.now[i] = 0u;
+    if (t.any(__syncthreads_or(bad) != 0)) {
         hand_on(a, t, SKV_ERR_INVALID_ARG);
         return;
     }
-    // Heirs, and the pages that are held.
-    for (uint32_t s = t.rank * kPlanThreads + tid; s < a.n_requests; s += t.C * kPlanThreads) {
+    for (uint32_t s = mine_of_all; s < a.n_requests; s += all_threads) {
         const uint32_t p = parent_row(a, s);
         if (p != ~0u) atomicMin(a.words + p, p == s ? 0u : s + 1u);
     }
-    bool corrupt = !mark_rows(a, t);
-    __syncthreads();
-    t.tell(0u);
-    // The bits of what rows go on with are cleared (an heir's pages: the others' are among them); the first CTA
-    // ranks the copies, in order of rows, and takes their pages off the ring.
-#pragma unroll 1
-    for (uint32_t s = t.rank * kPlanWarps + (tid >> 5); s < a.n_requests; s += t.C * kPlanWarps) {
-        const Fork f = fork_of(a, s);
-        if (!f.heir) continue;
-        const int32_t *row = a.table + (uint64_t)f.from * a.table_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < f.keep; j += 32u) {
-            const uint32_t p = (uint32_t)__ldg(row + j);
-            if (p < a.pool_pages) atomicAnd(bit_word(a, p), ~(1u << (p & 31u)));
+    t.meet();
+    // Pages that rows held, and those that their heirs go on with (all others' are among them).
+    bool corrupt = false;
+    each_entry<kLargeWarps>(a, t, [&](uint32_t r) {
+        const uint32_t n = (uint32_t)__ldg(a.n_in + r), heir = __ldcg(a.words + r);
+        const int32_t c = __ldg(a.ctx_len + r);
+        return Head{n, r, heir == ~0u ? 0u : a.trim ? pages_of(a, (uint32_t)c) : n};
+    }, AsItIs{}, [&](uint32_t, const Head &h, uint32_t j, int32_t p) {
+        if ((uint32_t)p >= a.pool_pages) {
+            corrupt = true;
+            return;
         }
+        set_bit(a.bits, (uint32_t)p);
+        if (j < h.extra) set_bit(a.now, (uint32_t)p);
+    });
+    // Copies ranked in order of rows, a stretch of them to a CTA; their pages come off the ring.
+    const uint32_t stretch = a.n_requests / t.C + 1u;
+    const uint32_t s0 = (uint32_t)min((uint64_t)t.rank * stretch, (uint64_t)a.n_requests), s1 = (uint32_t)min((uint64_t)s0 + stretch, (uint64_t)a.n_requests);
+    uint32_t mine = 0, here, before;
+    for (uint32_t s = s0 + tid; s < s1; s += kLargeThreads) mine += fork_of(a, s).copies;
+    block_scan<kLargeWarps>(mine, &here, part);
+    const uint32_t took = t.sum(here, &before);
+    if (took > (uint32_t)count) {
+        hand_on(a, t, SKV_ERR_CAPACITY);
+        return;
     }
-    uint32_t took = 0;
-    if (t.rank == 0) {
+    uint32_t k0 = before, *const from_of = a.words + a.n_requests, *const keep_of = from_of + a.n_requests;
 #pragma unroll 1
-        for (uint32_t base = 0; base < a.n_requests; base += kPlanThreads) {
-            const uint32_t s = base + tid;
-            Fork f{~0u, 0u, 0u, 0u, false};
-            if (s < a.n_requests) f = fork_of(a, s);
-            uint32_t all;
-            const uint32_t k = took + block_scan(f.copies, &all, part);
-            took += all;
-            if (s < a.n_requests) {
-                int32_t from = -1, to = -1;
-                if (f.copies && k < (uint32_t)count) {
-                    uint64_t e = (uint64_t)head + k;
-                    if (e >= a.free_capacity) e -= a.free_capacity;
-                    from = __ldg(a.table + (uint64_t)f.from * a.table_stride + f.keep);
-                    to = __ldg(a.free_pages + e);
-                    // (a ring that names a held page is not made worse)
-                    if ((uint32_t)to < a.pool_pages) atomicAnd(bit_word(a, (uint32_t)to), ~(1u << (to & 31)));
-                }
-                // both as they are until the rows are written; a pair outside the pool is left out then
-                a.src[s] = from;
-                a.dst[s] = to;
-                a.count[s] = (int32_t)f.part;
-                a.n_out[s] = (int32_t)(f.keep + f.copies);
-                a.ctx_out[s] = f.from == ~0u ? -1 : __ldg(a.ctx_len + f.from);
-            }
+    for (uint32_t base = s0; base < s1; base += kLargeThreads) {
+        const uint32_t s = base + tid;
+        Fork f{~0u, 0u, 0u, 0u, false};
+        if (s < s1) f = fork_of(a, s);
+        const uint32_t k = k0 + block_scan<kLargeWarps>(f.copies, &here, part);
+        k0 += here;
+        if (s >= s1) continue;
+        from_of[s] = f.from;
+        keep_of[s] = f.keep;
+        int32_t from = -1, to = -1;
+        if (f.copies) {
+            uint64_t e = (uint64_t)head + k;
+            if (e >= a.free_capacity) e -= a.free_capacity;
+            from = __ldg(a.table + (uint64_t)f.from * a.table_stride + f.keep);
+            to = __ldg(a.free_pages + e);
+            if ((uint32_t)to < a.pool_pages) set_bit(a.now, (uint32_t)to);
         }
+        // both as they are until the rows are written; a pair outside the pool is left out then
+        a.src[s] = from;
+        a.dst[s] = to;
+        a.count[s] = (int32_t)f.part;
+        a.n_out[s] = (int32_t)(f.keep + f.copies);
+        a.ctx_out[s] = f.from == ~0u ? -1 : __ldg(a.ctx_len + f.from);
     }
-    __syncthreads();
-    took = t.tell(took)[0];
+    t.meet();
     // Freed pages, counted.
-    uint32_t from, to, mine = 0, freed_here;
+    uint32_t from, to;
     run_of(a, t, &from, &to);
-    for (uint32_t i = from; i < to; ++i) mine += __popc(__ldcg(a.bits + i));
-    uint32_t at = block_scan(mine, &freed_here, part), before;
-    const uint32_t freed = t.sum(freed_here, &before);
+    mine = 0;
+    for (uint32_t i = from; i < to; ++i) mine += __popc(__ldcg(a.bits + i) & ~__ldcg(a.now + i));
+    uint32_t at = block_scan<kLargeWarps>(mine, &here, part);
+    const uint32_t freed = t.sum(here, &before);
     at += before;
-    if (took > (uint32_t)count || (uint64_t)count - took + freed > a.free_capacity) {
+    if ((uint64_t)count - took + freed > a.free_capacity) {
         hand_on(a, t, SKV_ERR_CAPACITY);
         return;
     }
     // Into the ring behind its end, the rows, the counts.
     for (uint32_t i = from; i < to; ++i) {
-        uint32_t w = __ldcg(a.bits + i);
-        while (w) {
+        for (uint32_t w = __ldcg(a.bits + i) & ~__ldcg(a.now + i); w; w &= w - 1u) {
             uint64_t e = (uint64_t)head + (uint32_t)count + at++;
             while (e >= a.free_capacity) e -= a.free_capacity;
             a.free_pages[e] = (int32_t)(32u * i + __ffs(w) - 1u);
-            w &= w - 1u;
         }
     }
-#pragma unroll 1
-    for (uint32_t s = t.rank * kPlanWarps + (tid >> 5); s < a.n_requests; s += t.C * kPlanWarps) {
-        const Fork f = fork_of(a, s);
-        if (f.from == ~0u) continue;
-        const int32_t *row = a.table + (uint64_t)f.from * a.table_stride;
-        int32_t *out = a.table_out + (uint64_t)s * a.out_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < f.keep; j += 32u) out[j] = __ldg(row + j);
-        if (f.copies && lane == 0) {
-            const int32_t x = __ldcg(a.src + s), y = __ldcg(a.dst + s);
-            out[f.keep] = y;
-            if ((uint32_t)x >= a.pool_pages || (uint32_t)y >= a.pool_pages) {
-                corrupt = true;
-                a.src[s] = a.dst[s] = -1;
-                a.count[s] = 0;
-            }
+    each_entry<kLargeWarps>(a, t, [&](uint32_t s) { return Head{__ldcg(keep_of + s), __ldcg(from_of + s), 0u}; }, AsItIs{},
+                            [&](uint32_t s, const Head &, uint32_t j, int32_t p) { a.table_out[(uint64_t)s * a.out_stride + j] = p; });
+    for (uint32_t s = s0 + tid; s < s1; s += kLargeThreads) {
+        if (a.count[s] == 0) continue;
+        const int32_t x = a.src[s], y = a.dst[s];
+        a.table_out[(uint64_t)s * a.out_stride + keep_of[s]] = y;
+        if ((uint32_t)x >= a.pool_pages || (uint32_t)y >= a.pool_pages) {
+            corrupt = true;
+            a.src[s] = a.dst[s] = -1;
+            a.count[s] = 0;
         }
     }
-    corrupt = __syncthreads_or(corrupt);
-    corrupt = t.any(corrupt);
     if (t.rank == 0 && tid == 0) {
         uint64_t e = (uint64_t)head + took;
         const uint32_t cap = max(a.free_capacity, 1u);
         if (e >= cap) e -= cap;
         a.free_out[0] = (int32_t)e;
         a.free_out[1] = (int32_t)((uint32_t)count - took + freed);
-        *a.status = corrupt ? SKV_ERR_CORRUPT : SKV_OK;
     }
+    if (corrupt) set_first(a.status, SKV_ERR_CORRUPT);    // (the first CTA's OK came barriers ago)
 }
 
 // ---- compact
@@ -314,32 +339,35 @@ __device__ __forceinline__ uint32_t below(uint32_t i, uint32_t limit) {
     return limit <= first ? 0u : limit - first >= 32u ? ~0u : (1u << (limit - first)) - 1u;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) compact_pages_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kLargeThreads) compact_pages_kernel(const PlanArgs a) {
     __shared__ Told told;
-    __shared__ uint32_t part[kPlanWarps];
+    __shared__ uint32_t part[kLargeWarps];
     cg::cluster_group cluster = cg::this_cluster();
     Team t{cluster.num_blocks(), cluster.block_rank(), 0u, &told};
-    const uint32_t tid = threadIdx.x, lane = tid & 31u;
-    cluster.sync();
-    bool bad = false;
-    for (uint32_t r = t.rank * kPlanThreads + tid; r < a.n_requests; r += t.C * kPlanThreads) {
+    const uint32_t tid = threadIdx.x, all_threads = t.C * kLargeThreads, mine_of_all = t.rank * kLargeThreads + tid;
+    if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
+    cluster.sync();                                       // every CTA has started
+    bool bad = false, corrupt = false;
+    for (uint32_t r = mine_of_all; r < a.n_requests; r += all_threads) {
         const int32_t h = __ldg(a.n_in + r);
         bad |= h < 0 || (uint32_t)h > a.max_pages;
     }
-    clear_bits(a, t);
-    bad = __syncthreads_or(bad);
-    if (t.any(bad)) {
+    for (uint32_t i = mine_of_all; i < (a.pool_pages + 31u) >> 5; i += all_threads) a.bits[i] = 0u;
+    if (t.any(__syncthreads_or(bad) != 0)) {
         hand_on(a, t, SKV_ERR_INVALID_ARG);
         return;
     }
-    bool corrupt = !mark_rows(a, t);
-    corrupt = __syncthreads_or(corrupt);
-    corrupt = t.any(corrupt);
+    const auto row_head = [&](uint32_t r) { return Head{(uint32_t)__ldg(a.n_in + r), r, 0u}; };
+    each_entry<kLargeWarps>(a, t, row_head, AsItIs{}, [&](uint32_t, const Head &, uint32_t, int32_t p) {
+        if ((uint32_t)p < a.pool_pages) set_bit(a.bits, (uint32_t)p);
+        else corrupt = true;
+    });
+    t.meet();
     // Held pages in all, then holes below that number and held pages from it on.
     uint32_t from, to, mine = 0, here, before;
     run_of(a, t, &from, &to);
     for (uint32_t i = from; i < to; ++i) mine += __popc(__ldcg(a.bits + i));
-    block_scan(mine, &here, part);
+    block_scan<kLargeWarps>(mine, &here, part);
     const uint32_t live = t.sum(here, &before);
     uint32_t holes = 0, far = 0;
     for (uint32_t i = from; i < to; ++i) {
@@ -348,12 +376,12 @@ __global__ void __launch_bounds__(kPlanThreads) compact_pages_kernel(const PlanA
         far += __popc(w & ~low);
     }
     uint32_t here_holes, here_far;
-    holes = block_scan(holes, &here_holes, part);
-    far = block_scan(far, &here_far, part);
-    t.sum(here_holes, &before);
-    holes += before;
-    const uint32_t moves = t.sum(here_far, &before);
-    far += before;
+    uint2 others;
+    holes = block_scan<kLargeWarps>(holes, &here_holes, part);
+    far = block_scan<kLargeWarps>(far, &here_far, part);
+    const uint32_t moves = t.sum(here_holes, here_far, &others).y;
+    holes += others.x;
+    far += others.y;
     if (moves > a.capacity || a.pool_pages - live > a.free_capacity) {
         hand_on(a, t, SKV_ERR_CAPACITY);
         return;
@@ -372,27 +400,17 @@ __global__ void __launch_bounds__(kPlanThreads) compact_pages_kernel(const PlanA
             a.src[far++] = (int32_t)p;
         }
     }
-    for (uint32_t i = moves + t.rank * kPlanThreads + tid; i < a.capacity; i += t.C * kPlanThreads) a.src[i] = a.dst[i] = -1;
-    for (uint32_t i = t.rank * kPlanThreads + tid; i < a.pool_pages - live; i += t.C * kPlanThreads) a.free_pages[i] = (int32_t)(live + i);
-    __syncthreads();
-    t.tell(0u);
-#pragma unroll 1
-    for (uint32_t r = t.rank * kPlanWarps + (tid >> 5); r < a.n_requests; r += t.C * kPlanWarps) {
-        const uint32_t n = (uint32_t)__ldg(a.n_in + r);
-        const int32_t *row = a.table + (uint64_t)r * a.table_stride;
-        int32_t *out = a.table_out + (uint64_t)r * a.out_stride;
-#pragma unroll 4
-        for (uint32_t j = lane; j < n; j += 32u) {
-            int32_t p = __ldg(row + j);
-            if ((uint32_t)p >= live && (uint32_t)p < a.pool_pages) p = (int32_t)__ldcg(hole + __ldcg(rank_of + p));
-            out[j] = p;
-        }
-    }
+    for (uint32_t i = moves + mine_of_all; i < a.capacity; i += all_threads) a.src[i] = a.dst[i] = -1;
+    for (uint32_t i = mine_of_all; i < a.pool_pages - live; i += all_threads) a.free_pages[i] = (int32_t)(live + i);
+    t.meet();
+    each_entry<kLargeWarps>(a, t, row_head, [&](int32_t p) {
+        return (uint32_t)p >= live && (uint32_t)p < a.pool_pages ? (int32_t)__ldcg(hole + __ldcg(rank_of + p)) : p;
+    }, [&](uint32_t r, const Head &, uint32_t j, int32_t p) { a.table_out[(uint64_t)r * a.out_stride + j] = p; });
     if (t.rank == 0 && tid == 0) {
         a.free_out[0] = 0;
         a.free_out[1] = (int32_t)(a.pool_pages - live);
-        *a.status = corrupt ? SKV_ERR_CORRUPT : SKV_OK;
     }
+    if (corrupt) set_first(a.status, SKV_ERR_CORRUPT);
 }
 
 // ---- both, for pools whose bits fit shared memory
@@ -414,39 +432,15 @@ __device__ __forceinline__ void leave_together(uint32_t C) {
     if (C > 1u) cg::this_cluster().sync();
 }
 
-// f(row, column, page) of the first len(row) entries of the table's row from(row), for every row, dealt to the warps of
-// the cluster in pieces of 32 entries, four of them on their way at once; most: the largest len.
-template <typename Len, typename From, typename F>
-__device__ __forceinline__ void each_entry(const PlanArgs &a, const Team &t, uint32_t most, Len len, From from, F f) {
-    const uint32_t lane = threadIdx.x & 31u, pieces = (most + 31u) / 32u, items = a.n_requests * pieces, warps = kPlanWarps * t.C;
-#pragma unroll 1
-    for (uint32_t m0 = (threadIdx.x >> 5) * t.C + t.rank; m0 < items; m0 += 4u * warps) {
-        uint32_t row[4], column[4];
-        int32_t page[4];
-#pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) {
-            const uint32_t m = m0 + k * warps, r = m / pieces;
-            column[k] = 32u * (m - r * pieces) + lane;
-            row[k] = m < items && column[k] < len(r) ? r : ~0u;
-            page[k] = row[k] != ~0u ? __ldg(a.table + (uint64_t)from(r) * a.table_stride + column[k]) : 0;
-        }
-#pragma unroll
-        for (uint32_t k = 0; k < 4; ++k)
-            if (row[k] != ~0u) f(row[k], column[k], page[k]);
-    }
-}
-
 __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs a) {
     __shared__ uint32_t was[kSmallWords], now[kSmallWords];
     __shared__ int32_t parent[kSmallRows], ctx[kSmallRows], have[kSmallRows];
-    __shared__ uint32_t heir[kSmallRows], from[kSmallRows], keep[kSmallRows], part[kPlanWarps], most;
+    __shared__ uint32_t heir[kSmallRows], from[kSmallRows], keep[kSmallRows], part[kPlanWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
     const uint32_t tid = threadIdx.x, lane = tid & 31u, n = a.n_requests;
     const int32_t head = __ldg(a.free_in), count = __ldg(a.free_in + 1);
     bool bad = ring_bad(a, head, count), corrupt = false;
-    uint32_t longest = 0;
-    if (tid == 0) most = 0u;
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) {
         const uint32_t r = k * kPlanThreads + tid;
@@ -455,7 +449,6 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         if (r >= n) continue;
         const int32_t p = a.parents ? __ldg(a.parents + r) : (int32_t)r, c = __ldg(a.ctx_len + r), h = __ldg(a.n_in + r);
         parent[r] = p, ctx[r] = c, have[r] = h;
-        longest = max(longest, (uint32_t)h);
         bad |= p < -1 || p >= (int32_t)n || h < 0 || (uint32_t)h > a.max_pages || (int64_t)c > (int64_t)h * a.page.d;
     }
     if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
@@ -471,15 +464,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         const uint32_t f = from_of(s);
         if (f != ~0u) atomicMin(heir + f, f == s ? 0u : s + 1u);
     }
-    longest = __reduce_max_sync(~0u, longest);
-    if (lane == 0) atomicMax(&most, longest);
     __syncthreads();
     // Entries that an heir of row r keeps, and what row s has.
-    const auto kept_of = [&](uint32_t r) -> uint32_t {
-        if (!a.trim) return (uint32_t)have[r];
-        const uint32_t whole = div_by((uint32_t)ctx[r], a.page);
-        return whole + ((uint32_t)ctx[r] != whole * a.page.d);
-    };
+    const auto kept_of = [&](uint32_t r) -> uint32_t { return a.trim ? pages_of(a, (uint32_t)ctx[r]) : (uint32_t)have[r]; };
     const auto row_of = [&](uint32_t s) {
         Fork f{from_of(s), 0u, 0u, 0u, false};
         if (f.from == ~0u) return f;
@@ -499,7 +486,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         from[2u * tid + k] = mine[k].from;
         keep[2u * tid + k] = mine[k].keep;
     }
-    k0 = block_scan(mine[0].copies + mine[1].copies, &took, part);
+    k0 = block_scan<kPlanWarps>(mine[0].copies + mine[1].copies, &took, part);
     if (took > (uint32_t)count) {
         hand_on(a, t, SKV_ERR_CAPACITY);
         return;
@@ -523,11 +510,11 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
         }
     }
     // Pages that rows held, and those that their heirs go on with (all others' are among them).
-    each_entry(a, t, most, [&](uint32_t r) { return (uint32_t)have[r]; }, [](uint32_t r) { return r; }, [&](uint32_t r, uint32_t j, int32_t p) {
+    each_entry<kPlanWarps>(a, t, [&](uint32_t r) { return Head{(uint32_t)have[r], r, heir[r] == ~0u ? 0u : kept_of(r)}; }, AsItIs{},
+                           [&](uint32_t, const Head &h, uint32_t j, int32_t p) {
         if ((uint32_t)p < a.pool_pages) {
-            const uint32_t bit = 1u << (p & 31);
-            atomicOr(was + ((uint32_t)p >> 5), bit);
-            if (heir[r] != ~0u && j < kept_of(r)) atomicOr(now + ((uint32_t)p >> 5), bit);
+            set_bit(was, (uint32_t)p);
+            if (j < h.extra) set_bit(now, (uint32_t)p);
         } else {
             corrupt = true;
         }
@@ -537,7 +524,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) w[k] = union_of(was, 2u * tid + k, t.C) & ~union_of(now, 2u * tid + k, t.C);
     uint32_t freed;
-    const uint32_t at0 = block_scan(__popc(w[0]) + __popc(w[1]), &freed, part);
+    const uint32_t at0 = block_scan<kPlanWarps>(__popc(w[0]) + __popc(w[1]), &freed, part);
     if ((uint64_t)count - took + freed > a.free_capacity) {
         hand_on(a, t, SKV_ERR_CAPACITY);
         leave_together(t.C);
@@ -564,8 +551,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
             if (mine[k].copies) a.table_out[(uint64_t)s * a.out_stride + mine[k].keep] = fresh[k];
         }
     }
-    each_entry(a, t, most, [&](uint32_t s) { return keep[s]; }, [&](uint32_t s) { return from[s]; },
-               [&](uint32_t s, uint32_t j, int32_t p) { a.table_out[(uint64_t)s * a.out_stride + j] = p; });
+    each_entry<kPlanWarps>(a, t, [&](uint32_t s) { return Head{keep[s], from[s], 0u}; }, AsItIs{},
+                           [&](uint32_t s, const Head &, uint32_t j, int32_t p) { a.table_out[(uint64_t)s * a.out_stride + j] = p; });
     if (t.rank == 0 && tid == 0) {
         uint64_t e = (uint64_t)head + took;
         const uint32_t cap = max(a.free_capacity, 1u);
@@ -581,37 +568,31 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanA
     __shared__ uint32_t bits[kSmallWords], held[kSmallWords], part[kPlanWarps];
     __shared__ uint16_t far_before[kSmallWords], hole[kSmallPool / 2u];
     __shared__ int32_t have[kSmallRows];
-    __shared__ uint32_t most;
     cg::cluster_group cluster = cg::this_cluster();
     const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
     const uint32_t tid = threadIdx.x, lane = tid & 31u;
     bits[tid] = bits[kPlanThreads + tid] = 0u;
     bool bad = false, corrupt = false;
-    uint32_t longest = 0;
-    if (tid == 0) most = 0u;
     for (uint32_t r = tid; r < a.n_requests; r += kPlanThreads) {
         const int32_t h = __ldg(a.n_in + r);
         bad |= h < 0 || (uint32_t)h > a.max_pages;
         have[r] = h;
-        longest = max(longest, (uint32_t)h);
     }
     if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
     if (__syncthreads_or(bad)) {                          // the same in every CTA
         hand_on(a, t, SKV_ERR_INVALID_ARG);
         return;
     }
-    longest = __reduce_max_sync(~0u, longest);
-    if (lane == 0) atomicMax(&most, longest);
-    __syncthreads();
-    each_entry(a, t, most, [&](uint32_t r) { return (uint32_t)have[r]; }, [](uint32_t r) { return r; }, [&](uint32_t, uint32_t, int32_t p) {
-        if ((uint32_t)p < a.pool_pages) atomicOr(bits + ((uint32_t)p >> 5), 1u << (p & 31));
+    const auto row_head = [&](uint32_t r) { return Head{(uint32_t)have[r], r, 0u}; };
+    each_entry<kPlanWarps>(a, t, row_head, AsItIs{}, [&](uint32_t, const Head &, uint32_t, int32_t p) {
+        if ((uint32_t)p < a.pool_pages) set_bit(bits, (uint32_t)p);
         else corrupt = true;
     });
     cluster.sync();
     uint32_t w[2], live, all;
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) held[2u * tid + k] = w[k] = union_of(bits, 2u * tid + k, t.C);
-    block_scan(__popc(w[0]) + __popc(w[1]), &live, part);
+    block_scan<kPlanWarps>(__popc(w[0]) + __popc(w[1]), &live, part);
     // holes below `live` and held pages from it on, counted together (2^15 of either at most)
     uint32_t low[2], x = 0;
 #pragma unroll
@@ -619,7 +600,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanA
         low[k] = below(2u * tid + k, live);
         x += (uint32_t)__popc(~w[k] & low[k]) << 16 | (uint32_t)__popc(w[k] & ~low[k]);
     }
-    x = block_scan(x, &all, part);
+    x = block_scan<kPlanWarps>(x, &all, part);
     const uint32_t moves = all & 0xFFFFu;
     if (moves > a.capacity || a.pool_pages - live > a.free_capacity) {
         hand_on(a, t, SKV_ERR_CAPACITY);
@@ -644,13 +625,11 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanA
     __syncthreads();
     for (uint32_t i = moves + t.rank * kPlanThreads + tid; i < a.capacity; i += t.C * kPlanThreads) a.src[i] = a.dst[i] = -1;
     for (uint32_t i = t.rank * kPlanThreads + tid; i < a.pool_pages - live; i += t.C * kPlanThreads) a.free_pages[i] = (int32_t)(live + i);
-    each_entry(a, t, most, [&](uint32_t r) { return (uint32_t)have[r]; }, [](uint32_t r) { return r; }, [&](uint32_t r, uint32_t j, int32_t p) {
-        if ((uint32_t)p >= live && (uint32_t)p < a.pool_pages) {
-            const uint32_t i = (uint32_t)p >> 5, under = held[i] & ~below(i, live) & ((1u << (p & 31)) - 1u);
-            p = hole[far_before[i] + __popc(under)];
-        }
-        a.table_out[(uint64_t)r * a.out_stride + j] = p;
-    });
+    each_entry<kPlanWarps>(a, t, row_head, [&](int32_t p) -> int32_t {
+        if ((uint32_t)p < live || (uint32_t)p >= a.pool_pages) return p;
+        const uint32_t i = (uint32_t)p >> 5, under = held[i] & ~below(i, live) & ((1u << (p & 31)) - 1u);
+        return hole[far_before[i] + __popc(under)];
+    }, [&](uint32_t r, const Head &, uint32_t j, int32_t p) { a.table_out[(uint64_t)r * a.out_stride + j] = p; });
     if (t.rank == 0 && tid == 0) {
         a.free_out[0] = 0;
         a.free_out[1] = (int32_t)(a.pool_pages - live);
@@ -848,13 +827,17 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveArg
     if (bad && !a.checked) set_first(a.status, SKV_ERR_INVALID_ARG);
 }
 
-static bool launch_plan(void (*kernel)(PlanArgs), bool small, const PlanArgs &a, cudaStream_t st) {
-    // One CTA where a small table and pool leave little for more: a barrier of several costs more.
+template <void (*KERNEL)(PlanArgs), bool SMALL>
+static bool launch_plan(const PlanArgs &a, cudaStream_t st) {
+    // One CTA where a small table leaves little for more: a barrier of several costs more (8 rows of 17 pages 6.2 us with one,
+    // 9.7 with 8; 700 rows of 48 27 and 11.5, before two rows went at a time).
     const uint64_t entries = (uint64_t)a.n_requests * a.max_pages;
-    const uint32_t cluster = entries <= 2048u && (small || a.pool_pages <= 32768u) ? 1u : kPlanCluster;
+    const uint32_t cluster = !SMALL ? kLargeCluster : entries <= 2048u ? 1u : kPlanCluster;
+    static std::atomic<uint64_t> ready{0};
+    if (!SMALL && !allow_cluster(reinterpret_cast<const void *>(KERNEL), ready)) return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster);
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.blockDim = dim3(SMALL ? kPlanThreads : kLargeThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -862,7 +845,7 @@ static bool launch_plan(void (*kernel)(PlanArgs), bool small, const PlanArgs &a,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, KERNEL, a) == cudaSuccess;
 }
 
 static bool fits_small(uint32_t pool_pages, uint32_t n_requests, uint32_t max_pages) {
@@ -872,8 +855,8 @@ static bool fits_small(uint32_t pool_pages, uint32_t n_requests, uint32_t max_pa
 static uint64_t bits_bytes(uint32_t pool_pages) { return ((uint64_t)pool_pages + 511u) / 512u * 64u; }
 
 static uint64_t workspace_bytes(uint32_t n_requests, uint32_t pool_pages) {
-    const uint64_t fork = 4ull * n_requests, compact = 8ull * pool_pages;
-    return (bits_bytes(pool_pages) + (fork > compact ? fork : compact) + 255u) & ~uint64_t(255);
+    const uint64_t fork = 12ull * n_requests, compact = 8ull * pool_pages;
+    return (2u * bits_bytes(pool_pages) + (fork > compact ? fork : compact) + 255u) & ~uint64_t(255);
 }
 
 static bool bad_sizes(uint32_t pool_pages, uint32_t n_requests, uint32_t max_pages, uint64_t stride, uint64_t out_stride,
@@ -920,9 +903,11 @@ extern "C" int32_t skv_page_fork(uint32_t page_tokens, uint32_t pool_pages, uint
     a.table_out = table_out, a.n_out = n_pages_out, a.ctx_out = ctx_out, a.free_pages = free_pages, a.free_out = free_out;
     a.src = copy_src, a.dst = copy_dst, a.count = copy_tokens, a.status = status;
     a.bits = static_cast<uint32_t *>(workspace);
-    a.words = a.bits + bits_bytes(pool_pages) / 4u;
+    a.now = a.bits + bits_bytes(pool_pages) / 4u;
+    a.words = a.now + bits_bytes(pool_pages) / 4u;
     const bool small = fits_small(pool_pages, n_requests, max_pages);
-    return launch_plan(small ? fork_small_kernel : fork_pages_kernel, small, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return (small ? launch_plan<fork_small_kernel, true>(a, st) : launch_plan<fork_pages_kernel, false>(a, st)) ? SKV_OK : SKV_ERR_CUDA;
 }
 
 extern "C" int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, const int32_t *block_table, uint64_t table_stride,
@@ -948,9 +933,11 @@ extern "C" int32_t skv_page_compact(uint32_t pool_pages, uint32_t n_requests, co
     a.table_stride = table_stride, a.out_stride = table_out_stride;
     a.table_out = table_out, a.free_pages = free_pages, a.free_out = free_out, a.src = copy_src, a.dst = copy_dst, a.status = status;
     a.bits = static_cast<uint32_t *>(workspace);
-    a.words = a.bits + bits_bytes(pool_pages) / 4u;
+    a.now = a.bits + bits_bytes(pool_pages) / 4u;
+    a.words = a.now + bits_bytes(pool_pages) / 4u;
     const bool small = fits_small(pool_pages, n_requests, max_pages);
-    return launch_plan(small ? compact_small_kernel : compact_pages_kernel, small, a, static_cast<cudaStream_t>(stream)) ? SKV_OK : SKV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return (small ? launch_plan<compact_small_kernel, true>(a, st) : launch_plan<compact_pages_kernel, false>(a, st)) ? SKV_OK : SKV_ERR_CUDA;
 }
 
 extern "C" int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, const int32_t *dst, const int32_t *tokens, uint32_t n,

@@ -4,6 +4,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "skv_paged.h"
 
 namespace skv {
@@ -85,6 +87,19 @@ inline bool device_sms(uint32_t *sms) {
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return false;
     *sms = (uint32_t)n;
+    return true;
+}
+
+// Clusters of more than eight CTAs and as much shared memory as there is, once per kernel and device.
+inline bool allow_cluster(const void *kernel, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (ready.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return false;
+    ready.fetch_or(bit, std::memory_order_relaxed);
     return true;
 }
 

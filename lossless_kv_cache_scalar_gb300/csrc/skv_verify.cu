@@ -448,19 +448,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     }
 }
 
-// Clusters of more than eight CTAs, once per kernel and device.
-static bool allow_cluster(const void *kernel, std::atomic<uint64_t> &ready) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (bit && (ready.load(std::memory_order_relaxed) & bit)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-        return false;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-    return true;
-}
-
 template <typename T, bool DRAFT>
 static bool launch_verify(const VerifyArgs &a, uint32_t cluster, uint32_t bytes, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0}, large{0};

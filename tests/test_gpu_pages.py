@@ -75,7 +75,7 @@ def check_fork(got, want, width):
     assert list(zip(got["copy_src"], got["copy_dst"], got["copy_tokens"])) == copies
 
 
-@pytest.mark.parametrize("n,width,page", [(1, 1, 1), (2, 3, 16), (8, 20, 256), (33, 7, 5), (100, 30, 24), (700, 50, 64), (1300, 3, 16), (5, 900, 2), (40, 1000, 4), (1024, 20, 8)])
+@pytest.mark.parametrize("n,width,page", [(1, 1, 1), (2, 3, 16), (8, 20, 256), (33, 7, 5), (100, 30, 24), (700, 50, 64), (1300, 3, 16), (5, 900, 2), (40, 1000, 4), (1024, 20, 8), (2100, 40, 8)])
 def test_fork(n, width, page):
     for seed in range(12 if n < 500 else 4):
         rng = random.Random(1000 * n + seed)
@@ -98,7 +98,7 @@ def unchanged(got, ctx, rows, have, width, ring, state):
     assert got["copy_src"] == [-1] * n and got["copy_dst"] == [-1] * n and got["copy_tokens"] == [0] * n
 
 
-@pytest.mark.parametrize("n", [6, 600])
+@pytest.mark.parametrize("n", [6, 600, 1100])
 def test_fork_errors_leave_everything(n):
     rng = random.Random(n)
     width, page = 12, 8
@@ -155,7 +155,7 @@ def call_compact(pool, rows, have, width, ring, state, room):
     return got, int(t.status)
 
 
-@pytest.mark.parametrize("n,width", [(1, 1), (2, 3), (8, 20), (33, 7), (100, 30), (700, 50), (1300, 3), (3, 2000), (40, 1000), (16, 2046)])
+@pytest.mark.parametrize("n,width", [(1, 1), (2, 3), (8, 20), (33, 7), (100, 30), (700, 50), (1300, 3), (3, 2000), (40, 1000), (16, 2046), (2100, 40)])
 def test_compact(n, width):
     for seed in range(10 if n < 500 else 3):
         rng = random.Random(77 * n + seed)
@@ -171,9 +171,10 @@ def test_compact(n, width):
         assert list(zip(got["copy_src"], got["copy_dst"])) == moves + [(-1, -1)] * (room - len(moves))
 
 
-def test_compact_errors_leave_everything():
+@pytest.mark.parametrize("n", [40, 1100])
+def test_compact_errors_leave_everything(n):
     rng = random.Random(5)
-    _, have, rows, free, pool = tables(rng, 40, 10, 16, idle=0.0)
+    _, have, rows, free, pool = tables(rng, n, 10, 16, idle=0.0)
     ring, state = ring_of(rng, free, pool)
     _, tail, moves = compact(pool, rows, have)
     assert len(moves) > 1
@@ -185,7 +186,7 @@ def test_compact_errors_leave_everything():
         assert [t for t in got["table_out"][:-1]] == table[:-1]
         assert got["free"] == rg and got["free_state_out"] == state and got["copy_src"] == [-1] * room and got["copy_dst"] == [-1] * room
     rows[0][0] = pool
-    got, status = call_compact(pool, rows, have, 10, ring, state, 400)
+    got, status = call_compact(pool, rows, have, 10, ring, state, 10 * n)
     assert status == 7 and got["table_out"][0][0] == pool
 
 

@@ -188,6 +188,20 @@ def test_pools_with_strides_and_far_pages():
     assert torch.equal(pool[slots // 64, 0, slots % 64], s["kn"]) and torch.equal(pool[slots // 64, 1, slots % 64], s["vn"])
 
 
+def test_rows_far_into_a_large_tensor():
+    """Rows whose elements lie beyond 2^31 of the first's."""
+    n, wide = 3000, torch.empty(3000, 6000, 128, dtype=torch.bfloat16, device="cuda")          # 4.6 GB
+    s = made(16, n, 2, 1, 128, 16, "bf16", skip=0.0)
+    wide[:, 5996:5998], wide[:, 5998:5999], wide[:, 5999:] = s["q"], s["kn"], s["vn"]
+    w, pos = torch.ones(128), torch.arange(n, dtype=torch.int32, device="cuda")
+    rotary = Rotary(128, freqs(128), w, w)
+    want = s["cache"].rotate_append(rotary, s["q"], s["kn"], s["vn"], pos, s["slots"])
+    k = s["k"].clone()
+    s["k"].fill_(1)
+    got = s["cache"].rotate_append(rotary, wide[:, 5996:5998], wide[:, 5998:5999], wide[:, 5999:], pos, s["slots"])
+    assert torch.equal(got, want) and torch.equal(s["k"], k)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_pages_with_heads_before_tokens(dtype):
     """Strides of their own for heads and tokens, K and V in one tensor: the same rows as in a plain pool."""

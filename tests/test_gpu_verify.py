@@ -137,6 +137,37 @@ def test_many_requests_of_a_large_vocabulary(draft, dtype):
     compare(made(3, [2, 1, 3, 0] * 25, 60001, dtype, draft, spread=4.0))
 
 
+@pytest.mark.parametrize("draft", ["drawn", "best"])
+def test_the_same_in_any_company(draft):
+    """The number of requests chooses how a row is split; the answer does not depend on it."""
+    s = made(21, [7], 70000, draft=draft, pad=0)
+    want = plain(s)
+    for n in (1, 9, 20, 70):
+        t = dict(s, probs=s["probs"].cuda().repeat(n, 1), tokens=s["tokens"].repeat(n), parents=s["parents"].repeat(n), uniform=s["uniform"].repeat(n),
+                 cu=list(range(0, 7 * n + 1, 7)), rows=7 * n)
+        if draft == "drawn":
+            t["draft"] = s["draft"].cuda().repeat(n, 1)
+        out, _, _ = call(t)
+        assert out["accepted"].tolist() == want[0] * n and out["next_tokens"].tolist() == want[2] * n
+
+
+def test_rows_far_into_a_large_tensor():
+    """More than 2^32 probabilities: the last rows of 29,000."""
+    rows, vocab = 29000, 151937
+    s = made(22, [4], vocab, dtype="bf16", pad=0)
+    big = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    big[-4:] = s["probs"].cuda()
+    tokens, uniform, parents = torch.zeros(rows, dtype=torch.int32), torch.zeros(rows), torch.zeros(rows, dtype=torch.int32)
+    tokens[-4:], uniform[-4:], parents[-4:] = s["tokens"], s["uniform"], s["parents"]
+    draft = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    draft[-4:] = s["draft"].cuda()
+    v = Verifier(1, vocab)
+    got = v.verify(big, tokens.cuda(), i32([rows - 4, rows]), uniform.cuda(), parents=parents.cuda(), draft_probs=draft)
+    want = plain(s)
+    assert got[0].tolist() == want[0] and got[2].tolist() == want[2]
+    assert got[1][-4:].tolist() == [p + rows - 4 for p in want[1][0]] + [-1] * (4 - want[0][0])
+
+
 def test_no_rows():
     v = Verifier(3, 100)
     e = torch.zeros(0, dtype=torch.int32, device="cuda")
