@@ -44,11 +44,11 @@ struct RotateArgs {
     uint64_t pool_tokens;
     const int64_t *slots;
     int32_t *status;
-    uint32_t checked;                                                   // 1: block 0 reports the errors
+    uint32_t checked;                                                   // 1: block 0 reports the errors, 2: and does nothing else
 };
 
 constexpr uint32_t kRotateThreads = 128, kRotateWarps = kRotateThreads / 32u, kRotateBlocks = 7;      // blocks per SM
-constexpr uint32_t kRotateChecked = 2048;        // rows that one block looks through for errors
+constexpr uint32_t kRotateChecked = 2048;        // rows that a block looks through for errors beside its own
 
 __device__ __forceinline__ uint32_t pack2(float2 x) {
     uint32_t r;
@@ -78,17 +78,22 @@ __global__ void __launch_bounds__(kRotateThreads, kRotateBlocks) rotate_kernel(c
     __shared__ float4 coef[kRotateWarps][2][8][LANES];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, u = lane % LANES, own = lane / LANES;
     if (a.checked && blockIdx.x == 0) {
-        // loads of every round in flight at once
+        // every slot, loads of 16 rounds in flight at once
         bool bad = false;
+#pragma unroll 1
+        for (uint32_t i0 = threadIdx.x; i0 < a.n; i0 += kRotateChecked) {
 #pragma unroll
-        for (uint32_t j = 0; j < kRotateChecked / kRotateThreads; ++j) {
-            const uint32_t i = j * kRotateThreads + threadIdx.x;
-            const int64_t s = i < a.n ? __ldg(a.slots + i) : -1;
-            bad |= s >= 0 && (uint64_t)s >= a.pool_tokens;
+            for (uint32_t j = 0; j < kRotateChecked / kRotateThreads; ++j) {
+                const uint32_t i = i0 + j * kRotateThreads;
+                const int64_t s = i < a.n ? __ldg(a.slots + i) : -1;
+                bad |= s >= 0 && (uint64_t)s >= a.pool_tokens;
+            }
         }
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
+        if (a.checked == 2u) return;
     }
+    const uint32_t first = a.checked == 2u ? blockIdx.x - 1u : blockIdx.x, blocks = a.checked == 2u ? gridDim.x - 1u : gridDim.x;
     const bool live = u < a.head_dim / 16u;
     const bool turned = u < a.rot_units;
     // channels of the unit's two vectors
@@ -97,7 +102,7 @@ __global__ void __launch_bounds__(kRotateThreads, kRotateBlocks) rotate_kernel(c
     const uint64_t items = (uint64_t)a.n * a.parts, q_next = (uint64_t)a.parts * HPW * a.q_head_stride;
     const uint32_t out_next = a.parts * HPW * a.head_dim;
 #pragma unroll 1
-    for (uint64_t item = (uint64_t)blockIdx.x * kRotateWarps + warp; item < items; item += (uint64_t)gridDim.x * kRotateWarps) {
+    for (uint64_t item = (uint64_t)first * kRotateWarps + warp; item < items; item += (uint64_t)blocks * kRotateWarps) {
         const uint32_t i = items >> 31 ? (uint32_t)(item / a.parts) : div_by((uint32_t)item, a.by_parts);
         const uint32_t part = (uint32_t)(item - (uint64_t)i * a.parts);
         // Steps of HPW heads of one kind: queries, then keys, then values.
@@ -289,24 +294,13 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     const PagedView c = paged_view(*cache);
     const uint32_t units = cache->head_dim / 16u;
     const uint32_t lanes = units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : units <= 8 ? 8 : 16;
-    // A warp takes a row's heads one group after the other; with few rows a row's groups go to several
-    // warps, up to 16 warps per SM, each of which works the angles out again.
+    // A row's groups of heads go to two warps (each works the angles out for itself, but the last round over the GPU is
+    // shorter: 7,001 rows 39.1 us, 39.3 with one and 41.0 with three; 4,300 27.7, 30.8 and 27.3; 30,000 138, 136 and 147), with few rows to
+    // more, up to 24 warps per SM (1,000 rows: 7.0 us with three, 7.6 with two, 8.0 with five).
     const uint32_t per_step = 32u / lanes, q_steps = (n_q_heads + per_step - 1u) / per_step;
     const uint32_t kv_steps = (cache->n_heads + per_step - 1u) / per_step, groups = q_steps + 2u * kv_steps;
-    uint32_t parts = 16u * sms / n;
-    if (parts < 2u) {
-        // From there on the warps of a full GPU make several rounds: two or three parts where the last
-        // round would be a poor one (twice the angles cost 2%, three times 8%).
-        const uint64_t warps = (uint64_t)kRotateBlocks * kRotateWarps * sms;
-        uint64_t best = ~uint64_t(0);
-        for (uint32_t p = 1; p <= 3u; ++p) {
-            const uint64_t cost = ((uint64_t)n * p + warps - 1u) / warps * (99u + p * p) * (6u / p);
-            if (cost < best) {
-                best = cost;
-                parts = p;
-            }
-        }
-    }
+    uint32_t parts = 24u * sms / n;
+    parts = parts < 2u ? 2u : parts;
     parts = parts > groups ? groups : parts;
     RotateArgs a{};
     a.q = static_cast<const uint16_t *>(q), a.k = static_cast<const uint16_t *>(k), a.v = static_cast<const uint16_t *>(v);
@@ -321,10 +315,14 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     a.page_stride = c.page_stride, a.token_stride = c.token_stride, a.page_head_stride = c.head_stride;
     a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.page = c.page;
     a.pool_tokens = (uint64_t)cache->n_pages * cache->page_tokens;
-    a.slots = slots, a.status = status, a.checked = n <= kRotateChecked;
+    // Errors are looked for by one block (it writes the status once, where clearing it first is a launch of its own, 2 us): up to
+    // 2,048 rows on its way, beyond as all it does, where rows of 4 KB or more take the others ten times as long.
+    const uint64_t row_bytes = (uint64_t)cache->head_dim * (4u * n_q_heads + (c.e4m3 ? 6u : 8u) * cache->n_heads);
+    a.slots = slots, a.status = status, a.checked = n <= kRotateChecked ? 1u : row_bytes >= 4096u ? 2u : 0u;
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     const uint64_t blocks = ((uint64_t)n * parts + kRotateWarps - 1) / kRotateWarps;
-    const unsigned grid = (unsigned)(blocks < kRotateBlocks * sms ? blocks : kRotateBlocks * sms);
+    const uint64_t all = blocks + (a.checked == 2u);
+    const unsigned grid = (unsigned)(all < kRotateBlocks * sms ? all : kRotateBlocks * sms);
     bool ok;
     switch (lanes) {
         case 1: ok = launch_rotate<1>(a, c.e4m3, grid, st); break;
