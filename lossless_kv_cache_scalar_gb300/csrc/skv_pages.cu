@@ -647,7 +647,7 @@ struct CopyArgs {
     FastDiv by_chunks, per_token, per_head;               // units of a token and of a head
     const int32_t *src, *dst, *tokens;
     int32_t *status;
-    uint32_t checked;
+    uint32_t checked;                                     // 1: block 0 reports the errors, 2: and does nothing else
 };
 
 constexpr uint32_t kCopyThreads = 256, kCopyDeep = 2, kCopyUnits = kCopyThreads * kCopyDeep;
@@ -669,17 +669,20 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs
     int32_t src, dst;
     uint32_t n;
     if (a.checked && blockIdx.x == 0) {
+#pragma unroll 8
         for (uint32_t i = threadIdx.x; i < a.n; i += kCopyThreads) pair_of(a, i, &src, &dst, &n, &bad);
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
+        if (a.checked == 2u) return;
         bad = false;
     }
+    const uint32_t first = a.checked == 2u ? blockIdx.x - 1u : blockIdx.x, blocks = a.checked == 2u ? gridDim.x - 1u : gridDim.x;
     // Chunks are dealt to the CTAs in turn. A warp looks 32 of its chunks up at once, so that pairs without a copy
     // cost little; all warps of a CTA find the same.
     const uint64_t items = (uint64_t)a.n * a.chunks;
 #pragma unroll 1
-    for (uint64_t m0 = blockIdx.x; m0 < items; m0 += 32ull * gridDim.x) {
-        const uint64_t m = m0 + (uint64_t)lane * gridDim.x;
+    for (uint64_t m0 = first; m0 < items; m0 += 32ull * blocks) {
+        const uint64_t m = m0 + (uint64_t)lane * blocks;
         bool live = false;
         uint32_t chunk = 0;
         src = dst = 0;
@@ -728,14 +731,14 @@ struct MoveArgs {
     uint64_t page_stride, token_stride, head_stride;      // bytes
     FastDiv page, per_head;                               // units of 16 bytes per head
     uint64_t pool_tokens;
-    uint32_t n_requests, n_rows, units, per_request;      // units of a token; CTAs of a request
+    uint32_t n_requests, n_rows, units, threads, per_request;      // units of a token; threads of a team, teams of a request
     const int32_t *cu, *rows;
     const int64_t *slots, *kept;
     int32_t *status;
-    uint32_t checked;
+    uint32_t checked;                                     // 1: one more block, the first, reports the errors
 };
 
-constexpr uint32_t kMoveThreads = 256, kMoveDeep = 8;
+constexpr uint32_t kMoveThreads = 512, kMoveTeam = 256, kMoveDeep = 8;
 
 // Entry i's places; false: nothing to move (bad: not as it should be).
 __device__ __forceinline__ bool move_of(const MoveArgs &a, uint32_t i, int64_t *from, int64_t *to, bool *bad) {
@@ -770,17 +773,35 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveArg
     bool bad = false;
     int64_t from, to;
     uint32_t lo, hi;
-    if (blockIdx.x >= a.n_requests * a.per_request) {         // the errors of every request
-        for (uint32_t r = threadIdx.x >> 5; r < a.n_requests; r += blockDim.x / 32u) {
-            bad |= !move_rows_of(a, r, &lo, &hi);
-            for (uint32_t i = lo + lane; i < hi; i += 32u) move_of(a, i, &from, &to, &bad);
+    if (a.checked && blockIdx.x == 0) {                       // the errors of every request, row by row
+#pragma unroll 4
+        for (uint32_t r = threadIdx.x; r < a.n_requests; r += kMoveThreads) bad |= !move_rows_of(a, r, &lo, &hi);
+        bad = __syncthreads_or(bad);
+        const uint32_t end = bad ? 0u : (uint32_t)__ldg(a.cu + a.n_requests);
+#pragma unroll 1
+        for (uint32_t i0 = (uint32_t)__ldg(a.cu) + threadIdx.x; i0 < end; i0 += 8u * kMoveThreads) {
+            // loads of eight rounds in flight at once
+            int64_t to_[8], from_[8];
+            uint32_t row[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                const uint32_t i = i0 + k * kMoveThreads;
+                to_[k] = i < end ? __ldg(a.kept + i) : -1;
+                row[k] = i < end ? (uint32_t)__ldg(a.rows + i) : 0u;
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) from_[k] = to_[k] >= 0 && row[k] < a.n_rows ? __ldg(a.slots + row[k]) : -1;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) bad |= to_[k] >= 0 && ((uint64_t)to_[k] >= a.pool_tokens || (uint64_t)from_[k] >= a.pool_tokens);
         }
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
         return;
     }
-    const uint32_t r = blockIdx.x / a.per_request;
-    const uint32_t column = (blockIdx.x - r * a.per_request) * blockDim.x + threadIdx.x;
+    const uint32_t in_block = threadIdx.x / a.threads, team = (blockIdx.x - a.checked) * (kMoveThreads / a.threads) + in_block;
+    const uint32_t r = team / a.per_request;
+    const uint32_t column = (team - r * a.per_request) * a.threads + threadIdx.x - in_block * a.threads;
+    if (in_block >= kMoveThreads / a.threads || r >= a.n_requests) return;
     bad |= !move_rows_of(a, r, &lo, &hi);
     const bool on = column < 2u * a.units;
     const uint32_t u = column < a.units ? column : column - a.units, h = div_by(u, a.per_head);
@@ -957,10 +978,12 @@ extern "C" int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, co
     if (!device_sms(&sms)) return SKV_ERR_CUDA;
     CopyArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
                cache->page_tokens, cache->n_pages, n, (uint32_t)((per_page + kCopyUnits - 1) / kCopyUnits), {}, fast_div(cache->n_heads * per_head),
-               fast_div(per_head), src, dst, tokens, status, n <= 2048u};
+               fast_div(per_head), src, dst, tokens, status, 0u};
+    // One block reports the errors: beside its copies up to 512 pairs, as all it does up to 65,536.
+    a.checked = n <= 512u ? 1u : n <= 65536u ? 2u : 0u;
     a.by_chunks = fast_div(a.chunks);
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    const uint64_t items = (uint64_t)n * a.chunks;
+    const uint64_t items = (uint64_t)n * a.chunks + (a.checked == 2u);
     const unsigned grid = (unsigned)(items < 16u * sms ? items : 16u * sms);
     copy_pages_kernel<<<grid, kCopyThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
@@ -977,13 +1000,14 @@ extern "C" int32_t skv_cache_move(const skv_paged *cache, uint32_t n_requests, c
     if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     const PagedView c = paged_view(*cache);
     const uint32_t per_head = cache->head_dim / (c.e4m3 ? 16u : 8u), units = cache->n_heads * per_head;
-    const uint32_t threads = 2u * units < kMoveThreads ? (2u * units + 31u) & ~31u : kMoveThreads;
+    const uint32_t threads = 2u * units < kMoveTeam ? (2u * units + 31u) & ~31u : kMoveTeam;
     const uint32_t per_request = (2u * units + threads - 1u) / threads;
     if ((uint64_t)n_requests * per_request >= 0x7FFFFFFFu) return SKV_ERR_INVALID_ARG;
     MoveArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
-               c.page, fast_div(per_head), (uint64_t)cache->n_pages * cache->page_tokens, n_requests, n_rows, units, per_request, cu_new, rows,
-               slots, kept, status, n_rows <= 2048u && n_requests <= 32u};
+               c.page, fast_div(per_head), (uint64_t)cache->n_pages * cache->page_tokens, n_requests, n_rows, units, threads, per_request, cu_new, rows,
+               slots, kept, status, n_rows <= 65536u && n_requests <= 65536u};
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
-    move_tokens_kernel<<<n_requests * per_request + a.checked, threads, 0, st>>>(a);
+    const uint32_t teams = kMoveThreads / threads, blocks = (n_requests * per_request + teams - 1u) / teams;
+    move_tokens_kernel<<<blocks + a.checked, kMoveThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
 }

@@ -177,18 +177,30 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
         uint32_t cur, taken, n_gone;
     } walk;
 
-    if (request == a.n_requests) {               // the errors of every request
+    if (request == a.n_requests) {               // the errors of every request, row by row
+        if (rank) return;
+        int32_t *cu = reinterpret_cast<int32_t *>(node);
+        for (uint32_t r = tid; r <= a.n_requests; r += kVerifyThreads) cu[r] = __ldg(a.cu + r);
+        __syncthreads();
         bool bad = false;
-        if (rank == 0) {
-            for (uint32_t r = warp; r < a.n_requests; r += kVerifyWarps) {
-                uint32_t row0, n;
-                bad |= !rows_of(a, r, &row0, &n);
-                for (uint32_t i = 1 + lane; i < n; i += 32u)
-                    bad |= !node_ok(a, parent_of(a, row0, i), __ldg(a.tokens + row0 + i), i);
-            }
-            bad = __syncthreads_or(bad);
-            if (tid == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
+        for (uint32_t r = tid; r < a.n_requests; r += kVerifyThreads) {
+            const int32_t lo = cu[r], hi = cu[r + 1u];
+            bad |= lo < 0 || hi < lo || (uint32_t)hi > a.n_rows || (!DRAFT && (uint32_t)(hi - lo) > kGone);
         }
+        bad = __syncthreads_or(bad);
+        const uint32_t end = bad ? 0u : (uint32_t)cu[a.n_requests];
+        for (uint32_t i = (uint32_t)cu[0] + tid; i < end; i += kVerifyThreads) {
+            uint32_t r = 0, m = a.n_requests;                             // last request with cu <= i
+            while (m > 1u) {
+                const uint32_t h = m >> 1;
+                if ((uint32_t)cu[r + h] <= i) r += h;
+                m -= h;
+            }
+            const uint32_t row = (uint32_t)cu[r], j = i - row;
+            if (j) bad |= !node_ok(a, parent_of(a, row, j), __ldg(a.tokens + i), j);
+        }
+        bad = __syncthreads_or(bad);
+        if (tid == 0) *a.status = bad ? SKV_ERR_INVALID_ARG : SKV_OK;
         return;
     }
     uint32_t row0, n;
@@ -493,7 +505,7 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     VerifyArgs a{probs, draft_probs, probs_stride, draft_stride, vocab, distinct, n_rows, n_requests, cu_new, tokens, parents, uniform,
-                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 8192u && n_requests <= 128u, 0u, 0u, 0u};
+                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 32768u && n_requests < kNodes * 4u, 0u, 0u, 0u};
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     uint32_t sms = 0;
     if (!device_sms(&sms)) return SKV_ERR_CUDA;

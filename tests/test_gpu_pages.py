@@ -315,6 +315,29 @@ def test_move_errors(many):
             assert torch.equal(flat[4], old[5])
 
 
+def test_more_entries_than_one_block_looks_through():
+    k, v = pools("e4m3", 70000, 1, 1, 16)
+    k0, cache = k.clone(), PagedKV(k, v)
+    n = 69000
+    src, dst = torch.full((n,), -1, dtype=torch.int32), torch.arange(1000, 70000, dtype=torch.int32)
+    src[::701] = torch.arange(len(src[::701]), dtype=torch.int32)
+    cache.copy(src.cuda(), dst.cuda())
+    assert torch.equal(k[1000::701], k0[:len(src[::701])]) and torch.equal(k[1001:1701], k0[1001:1701])
+    src[5] = 70000
+    with pytest.raises(SKVError, match="INVALID_ARG"):
+        cache.copy(src.cuda(), dst.cuda())
+    k.copy_(k0)
+    cu, rows = torch.arange(35001, dtype=torch.int32).cuda() * 2, torch.arange(70000, dtype=torch.int32).cuda()
+    slots, kept = torch.arange(70000).cuda(), torch.full((70000,), -1).cuda()
+    rows[0::2] += 1
+    kept[0::2] = slots[0::2]
+    cache.move(cu, rows, slots, kept)
+    assert torch.equal(k[0::2], k0[1::2]) and torch.equal(k[1::2], k0[1::2])
+    rows[69998] = -2
+    with pytest.raises(SKVError, match="INVALID_ARG"):
+        cache.move(cu, rows, slots, kept)
+
+
 def test_far_pages_are_copied_and_moved():
     pool = torch.empty(4200, 2, 64, 8, 128, dtype=torch.bfloat16, device="cuda")         # 11 GB
     pool[7].normal_(), pool[4100].normal_()

@@ -164,9 +164,9 @@ def test_channels_beyond_the_rotated_ones_take_nothing_from_them():
     assert torch.equal(out[:, :, 32:], s["q"][:, :, 32:]) and out[:, :, :32].isfinite().all()
 
 
-@pytest.mark.parametrize("n", [40, 2100])
-def test_a_slot_beyond_the_pool(n):
-    s = made(11, n, 2, 2, 64, 16, "bf16", skip=0.0)
+@pytest.mark.parametrize("n,heads", [(40, 2), (2100, 2), (2100, 16), (5000, 16)])
+def test_a_slot_beyond_the_pool(n, heads):
+    s = made(11, n, heads, 2, 64, 16, "bf16", skip=0.0)
     pos = torch.zeros(n, dtype=torch.int32, device="cuda")
     good = s["slots"].clone()
     s["slots"][n - 2] = s["k"].shape[0] * 16
