@@ -12,7 +12,7 @@
 // is taken of a reduced angle in [-1/2, 1/2) turns.
 //
 // Bound by HBM, and close behind by issue (some 200 instructions for a warp's 4 heads of 128 channels): 65,536 rows of 32
-// query and 8 KV heads, bf16, 250 us (6.4 TB/s, 0.95 of a copy); 56,008 rows into e4m3 218 us (0.85). Blocks
+// query and 8 KV heads, bf16, 246 us (6.5 TB/s, 0.96 of a copy); 30,000 rows of 40 and 8 into e4m3 134 us (0.87). Blocks
 // of 4 warps, 7 to an SM (72 registers): with 6 257 us, with 8 (64 registers, some of them spilled) 253 and 210. The loads of the
 // next step are on their way while a step is worked on; two steps ahead gave nothing.
 #include <cuda_bf16.h>
@@ -315,7 +315,7 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     a.page_stride = c.page_stride, a.token_stride = c.token_stride, a.page_head_stride = c.head_stride;
     a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.page = c.page;
     a.pool_tokens = (uint64_t)cache->n_pages * cache->page_tokens;
-    // Errors are looked for by one block (it writes the status once, where clearing it first is a launch of its own, 2 us): up to
+    // Errors are looked for by one block (it writes the status once, where clearing it first is a launch of its own: 2,500 rows 11.6 us, 16.3 with it): up to
     // 2,048 rows on its way, beyond as all it does, where rows of 4 KB or more take the others ten times as long.
     const uint64_t row_bytes = (uint64_t)cache->head_dim * (4u * n_q_heads + (c.e4m3 ? 6u : 8u) * cache->n_heads);
     a.slots = slots, a.status = status, a.checked = n <= kRotateChecked ? 1u : row_bytes >= 4096u ? 2u : 0u;

@@ -43,7 +43,7 @@ struct VerifyArgs {
     int32_t *accepted, *rows;
     int64_t *kept;
     int32_t *ctx_out, *next, *status;
-    uint32_t checked;                            // 1: a cluster behind the requests' reports the errors
+    uint32_t checked;                            // 1: a cluster behind the requests' reports the errors (a launch that clears the status: 4 us)
     uint32_t per_cta, per_chunk, per_warp;       // elements: of a CTA's part, of what it holds at a time, of a warp's run of that
 };
 
