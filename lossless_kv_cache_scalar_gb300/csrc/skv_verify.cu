@@ -6,13 +6,13 @@
 // 2^-44, so that no order of adding matters, and hands the sum to every CTA through distributed
 // shared memory. The warp in whose range the drawn number falls finds the token.
 //
-// Rows come by asynchronous copies into shared memory, all of a CTA's part on its way at once; where it fits, a
-// further sum over the same node, after another rejection, reads nothing.
+// Rows come by asynchronous copies into shared memory, all that it holds of a CTA's part on its way at once: a further sum over
+// the same node, after another rejection, reads only what did not fit.
 //
 // Bound by latency: a chain of 5 nodes over 151,936 tokens takes 7.3 us on the device (launch and end 2.5, then scalars, tests, row, sum,
 // the cluster's barrier and the token's search, 0.5 to 1 us each), 24 trees of 27 nodes over 50,257 tokens without draft probabilities 9.7;
-// 64 trees of up to 60 nodes over 151,936 tokens 79, where some 14 clusters of 16 run at a time and a request takes 2.7 sums on average,
-// 6 at most, of 2.5 us each (HBM would bring the rows in 11.5).
+// 64 trees of up to 60 nodes over 151,936 tokens 61: a request takes 2.7 sums on average, 6 at most, one after the other, with 4 CTAs to each,
+// whose parts of the two rows (304 KB) fit shared memory by a quarter (HBM would bring the rows in 11.5).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -30,6 +30,7 @@ constexpr uint32_t kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32u;
 constexpr uint32_t kNodes = 256;                 // nodes of a request that are gathered at once
 constexpr uint32_t kGone = 4096;                 // nodes of a request without draft probabilities
 constexpr uint32_t kVerifyCluster = 16;
+constexpr uint32_t kMostPart = 16384u * kVerifyWarps, kPieces = kMostPart / (32u * kVerifyThreads);      // of a CTA's part: 512 numbers to a lane at most
 constexpr uint32_t kRowBytes = 80u * 1024u;      // shared memory for rows: two CTAs to an SM
 
 struct VerifyArgs {
@@ -44,26 +45,33 @@ struct VerifyArgs {
     int64_t *kept;
     int32_t *ctx_out, *next, *status;
     uint32_t checked;                            // 1: a cluster behind the requests' reports the errors (a launch that clears the status: 4 us)
-    uint32_t per_cta, per_chunk, per_warp;       // elements: of a CTA's part, of what it holds at a time, of a warp's run of that
+    uint32_t per_cta, per_held, per_warp, per_warp_far;      // elements: of a CTA's part, of what it holds of it, of a warp's
+                                                             // run of that and of the rest
 };
 
 // A probability as it counts: the nearer end outside [0, 1], NaN as 0 (what saturation does).
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 __device__ __forceinline__ float prob(uint16_t x) { return __saturatef(__uint_as_float((uint32_t)x << 16)); }
 
-// m elements from src into dst, from dst[returned] on, by the CTA: 16 bytes at a time, asynchronously, where src is
-// aligned, the ends one by one.
+// Elements [e0, e0 + m) of a row of `vocab` into dst, by the CTA: whole 16-byte units, asynchronously, from the one that e0 lies
+// in on (so that it comes to lie at dst[place_in_unit]); the row's first and last unit element by element where they
+// are not all the row's.
 template <typename T>
-__device__ __forceinline__ uint32_t fetch_run(T *dst, const T *src, uint32_t m) {
+__device__ __forceinline__ uint32_t place_in_unit(const T *p) { return (uint32_t)((uintptr_t)p & 15u) / (uint32_t)sizeof(T); }
+template <typename T>
+__device__ __forceinline__ void fetch_run(T *dst, const T *row, uint32_t vocab, uint32_t e0, uint32_t m) {
     constexpr uint32_t V = 16u / sizeof(T);
-    const uint32_t tid = threadIdx.x, shift = (uint32_t)((16u - ((uintptr_t)src & 15u)) & 15u) / (uint32_t)sizeof(T);
-    const uint32_t lead = min(shift, m), units = (m - lead) / V, done = lead + units * V, at = V - shift;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + V);
-    for (uint32_t i = tid; i < units; i += kVerifyThreads)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * i), "l"(src + lead + i * V) : "memory");
-    if (tid < lead) dst[at + tid] = __ldg(src + tid);
-    if (tid >= 32u && tid - 32u < m - done) dst[at + done + tid - 32u] = __ldg(src + done + tid - 32u);
-    return at;
+    const uint32_t at = place_in_unit(row + e0), units = m ? (at + m + V - 1u) / V : 0u;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    for (uint32_t i = threadIdx.x; i < units; i += kVerifyThreads) {
+        const int32_t e = (int32_t)(e0 + i * V) - (int32_t)at;
+        if (e >= 0 && (uint32_t)e + V <= vocab) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * i), "l"(row + e) : "memory");
+        } else {
+            for (int32_t j = 0; j < (int32_t)V; ++j)
+                if (e + j >= 0 && (uint32_t)(e + j) < vocab) dst[i * V + j] = __ldg(row + e + j);
+        }
+    }
 }
 
 // R(y) = max(p - c q, 0), in [0, 1] like p.
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     __shared__ int32_t parent[kNodes];
     extern __shared__ uint4 row_memory[];
     __shared__ unsigned long long sums[2][kVerifyCluster * kVerifyWarps];      // of every warp of the cluster
-    __shared__ unsigned long long run_sum[kVerifyWarps];
+    __shared__ unsigned long long run_sum[(DRAFT ? 2u : kPieces) * kVerifyWarps];      // of this CTA's runs, in order
     __shared__ int32_t gone[DRAFT ? 1 : kGone];  // rejected tokens of the node (no draft probabilities)
     __shared__ struct {
         uint32_t cur, taken, n_gone;
@@ -254,55 +262,105 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     bool started = false;
     const float u0 = node[0].u;
 
-    // A part of the vocabulary per CTA, in chunks that shared memory holds; of a chunk, a run per warp.
+    // A part of the vocabulary per CTA, of which shared memory holds a piece. With draft probabilities the rest is read
+    // anew for each sum; without them the only sum passes through shared memory piece by piece. A run per warp
+    // of each piece, and of the rest.
     const uint32_t first = min(rank * a.per_cta, a.vocab), last = min(first + a.per_cta, a.vocab);
-    const uint32_t chunks = (a.per_cta + a.per_chunk - 1u) / a.per_chunk;
-    T *const sp = reinterpret_cast<T *>(row_memory), *const sq = sp + a.per_chunk + 32u / sizeof(T);
-    const T *run_p = sp, *run_q = sq;            // this warp's run
-    uint32_t run = 0, run0 = 0;                  // its length, and its first element
+    const uint32_t m = min(a.per_held, last - first), far0 = first + m;
+    const uint32_t pieces = DRAFT ? 1u : (a.per_cta + a.per_held - 1u) / a.per_held;
+    T *const sp = reinterpret_cast<T *>(row_memory), *const sq = sp + a.per_held + 32u / sizeof(T);
     uint32_t parity = 0, n_gone = 0;
     uint32_t held = ~0u;                         // whose rows, both, shared memory holds
 
-    const auto load = [&](uint32_t cur, uint32_t k, bool both) {
-        const uint32_t e0 = min(first + k * a.per_chunk, last), m = min(a.per_chunk, last - e0);
-        __syncthreads();                         // what was here is read
-        const uint32_t at_p = fetch_run(sp, P + (uint64_t)cur * a.probs_stride + e0, m);
-        uint32_t at_q = 0;
-        if (DRAFT && both) at_q = fetch_run(sq, Q + (uint64_t)cur * a.draft_stride + e0, m);
+    struct Run {
+        const T *p, *q;
+        uint32_t n, e0;                          // its length, and its first element
+    };
+    // This warp's run of the piece of `here` elements from e0 on that shared memory holds, and of the rest.
+    const auto held_run = [&](uint32_t cur, uint32_t e0, uint32_t here) {
+        const uint32_t r0 = min(warp * a.per_warp, here);
+        Run r{sp + place_in_unit(P + (uint64_t)cur * a.probs_stride + e0) + r0, nullptr, min(a.per_warp, here - r0), e0 + r0};
+        if (DRAFT) r.q = sq + place_in_unit(Q + (uint64_t)cur * a.draft_stride + e0) + r0;
+        return r;
+    };
+    const auto far_run = [&](uint32_t cur) {
+        const uint32_t r0 = min(warp * a.per_warp_far, last - far0);
+        Run r{P + (uint64_t)cur * a.probs_stride + far0 + r0, nullptr, min(a.per_warp_far, last - far0 - r0), far0 + r0};
+        if (DRAFT) r.q = Q + (uint64_t)cur * a.draft_stride + far0 + r0;
+        return r;
+    };
+    // Every copy is in; without draft probabilities rejected tokens weigh nothing.
+    const auto arrive = [&](uint32_t cur, uint32_t e0, uint32_t here) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        if (!DRAFT && n_gone) {                  // rejected tokens weigh nothing
+        if (!DRAFT && n_gone) {
+            T *p = sp + place_in_unit(P + (uint64_t)cur * a.probs_stride + e0);
             for (uint32_t g = tid; g < n_gone; g += kVerifyThreads)
-                if ((uint32_t)gone[g] - e0 < m) sp[at_p + (uint32_t)gone[g] - e0] = T(0);
+                if ((uint32_t)gone[g] - e0 < here) p[(uint32_t)gone[g] - e0] = T(0);
             __syncthreads();
         }
-        const uint32_t r0 = min(warp * a.per_warp, m);
-        run = min(a.per_warp, m - r0);
-        run0 = e0 + r0;
-        run_p = sp + at_p + r0;
-        run_q = sq + at_q + r0;
     };
-    const auto rest = [&](uint32_t i, float c) { return DRAFT && c != 0.0f ? rest_of(prob(run_p[i]), prob(run_q[i]), c) : prob(run_p[i]); };
-    // The warp's sum of R over its run.
-    const auto sum_run = [&](float c) {
+    // The warp's sum of R over its run of the rest, from global memory: up to 16 loads of a lane on their way.
+    const auto sum_far = [&](const Run &r, float c) {
         Units u{0u, 0u};
-        if (DRAFT && c != 0.0f) {
-#pragma unroll 4
-            for (uint32_t i = lane; i < run; i += 32u) add_units(u, rest_of(prob(run_p[i]), prob(run_q[i]), c));
+        if (c != 0.0f) {
+#pragma unroll 1
+            for (uint32_t i0 = lane; i0 < r.n; i0 += 256u) {
+                T x[8], y[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const bool in = i0 + 32u * j < r.n;
+                    x[j] = in ? r.p[i0 + 32u * j] : T(0);
+                    y[j] = in ? r.q[i0 + 32u * j] : T(0);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) add_units(u, rest_of(prob(x[j]), prob(y[j]), c));
+            }
         } else {
-#pragma unroll 8
-            for (uint32_t i = lane; i < run; i += 32u) add_units(u, prob(run_p[i]));
+#pragma unroll 1
+            for (uint32_t i0 = lane; i0 < r.n; i0 += 512u) {
+                T x[16];
+#pragma unroll
+                for (uint32_t j = 0; j < 16; ++j) x[j] = i0 + 32u * j < r.n ? r.p[i0 + 32u * j] : T(0);
+#pragma unroll
+                for (uint32_t j = 0; j < 16; ++j) add_units(u, prob(x[j]));
+            }
         }
         return warp_total(u);
     };
-    // Sum of R over the row of `cur`; every warp's own is in sums[parity ^ 1] then.
+    // Sum of R over the row of `cur`; every warp's own is in sums[parity ^ 1] then, of this CTA's runs in run_sum.
     const auto sum_row = [&](uint32_t cur, float c) -> unsigned long long {
+        const bool both = DRAFT && c != 0.0f, reload = held != cur;
         unsigned long long sum = 0;
-        for (uint32_t k = 0; k < chunks; ++k) {
-            if (chunks > 1u || held != cur) load(cur, k, c != 0.0f);
-            sum += sum_run(c);
+#pragma unroll 1
+        for (uint32_t k = 0; k < pieces; ++k) {
+            const uint32_t e0 = min(first + k * a.per_held, last), here = min(a.per_held, last - e0);
+            if (reload) {
+                __syncthreads();                 // what was here is read
+                fetch_run(sp, P + (uint64_t)cur * a.probs_stride, a.vocab, e0, here);
+                if (both) fetch_run(sq, Q + (uint64_t)cur * a.draft_stride, a.vocab, e0, here);
+            }
+            if (DRAFT) {
+                unsigned long long far = 0;
+                if (a.per_warp_far) far = sum_far(far_run(cur), c);
+                if (lane == 0) run_sum[kVerifyWarps + warp] = far;
+                sum += far;
+            }
+            if (reload) arrive(cur, e0, here);
+            const Run r = held_run(cur, e0, here);
+            Units u{0u, 0u};
+            if (both) {
+#pragma unroll 4
+                for (uint32_t i = lane; i < r.n; i += 32u) add_units(u, rest_of(prob(r.p[i]), prob(r.q[i]), c));
+            } else {
+#pragma unroll 8
+                for (uint32_t i = lane; i < r.n; i += 32u) add_units(u, prob(r.p[i]));
+            }
+            const unsigned long long near = warp_total(u);
+            if (lane == 0) run_sum[k * kVerifyWarps + warp] = near;
+            sum += near;
         }
-        held = DRAFT && c != 0.0f ? cur : ~0u;
+        held = both ? cur : ~0u;
         if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         started = true;
         if (lane < C) *cluster.map_shared_rank(&sums[parity][rank * kVerifyWarps + warp], lane) = sum;
@@ -415,36 +473,48 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     const unsigned long long mine = sum_of_warp(lane < kVerifyWarps ? all[rank * kVerifyWarps + lane] : 0ull);
     if (total && left >= before && left - before < mine) {
         left -= before;
-        const unsigned long long *runs = all + rank * kVerifyWarps;
-        for (uint32_t k = 0; k < chunks; ++k) {
-            if (chunks > 1u) {
-                load(cur, k, c != 0.0f);
-                const unsigned long long sum = sum_run(c);
-                if (lane == 0) run_sum[warp] = sum;
-                __syncthreads();
-                runs = run_sum;
-            }
-            const unsigned long long here = sum_of_warp(lane < kVerifyWarps ? runs[lane] : 0ull);
-            if (left < here) break;
-            left -= here;
-        }
-        const unsigned long long low = sum_of_warp(lane < warp ? runs[lane] : 0ull);
-        if (left >= low && left - low < runs[warp]) {
-            left -= low;
-            // a stretch of up to 32 elements per lane, then an element per lane of the stretch
-            const uint32_t each = (run + 31u) / 32u;
-            const auto stretch_sum = [&](uint32_t from, uint32_t to) {
-                Units x{0u, 0u};
-                for (uint32_t i = from; i < to; ++i) add_units(x, rest(i, c));
-                return total_of(x.high, (int32_t)x.low);
-            };
-            unsigned long long x = stretch_sum(min(lane * each, run), min((lane + 1u) * each, run)), upto = prefix_of_warp(x);
-            const uint32_t l = __ffs(__ballot_sync(~0u, left >= upto - x && left < upto)) - 1u;
-            left -= __shfl_sync(~0u, upto - x, l);
-            const uint32_t from = min(l * each, run), i = from + lane;
-            x = i < min(from + each, run) ? units_of_prob(rest(i, c)) : 0ull;
+        // the run, of this CTA's in order
+        const uint32_t runs = (DRAFT ? 2u : pieces) * kVerifyWarps;
+        uint32_t e = 0;
+        unsigned long long x, upto;
+        while (true) {
+            x = e + lane < runs ? run_sum[e + lane] : 0ull;
             upto = prefix_of_warp(x);
-            if (left >= upto - x && left < upto) a.next[request] = (int32_t)(run0 + i);
+            const uint32_t in = __ballot_sync(~0u, left >= upto - x && left < upto);
+            if (in) {
+                const uint32_t l = __ffs(in) - 1u;
+                left -= __shfl_sync(~0u, upto - x, l);
+                e += l;
+                break;
+            }
+            left -= __shfl_sync(~0u, upto, 31);
+            e += 32u;
+        }
+        const uint32_t k = DRAFT ? 0u : e / kVerifyWarps, e0 = min(first + k * a.per_held, last), here = min(a.per_held, last - e0);
+        if (k + 1u < pieces) {                   // (the last piece is there)
+            __syncthreads();
+            fetch_run(sp, P + (uint64_t)cur * a.probs_stride, a.vocab, e0, here);
+            arrive(cur, e0, here);
+        }
+        if (warp == e % kVerifyWarps) {
+            const Run r = DRAFT && e >= kVerifyWarps ? far_run(cur) : held_run(cur, e0, here);
+            const auto rest = [&](uint32_t i) { return DRAFT ? rest_of(prob(r.p[i]), c != 0.0f ? prob(r.q[i]) : 0.0f, c) : prob(r.p[i]); };
+            // stretches of it, one per lane, until a lane has one element
+            uint32_t from = 0, n = r.n;
+            while (n > 32u) {
+                const uint32_t each = (n + 31u) / 32u;
+                Units u{0u, 0u};
+                for (uint32_t i = min(lane * each, n); i < min((lane + 1u) * each, n); ++i) add_units(u, rest(from + i));
+                x = total_of(u.high, (int32_t)u.low);
+                upto = prefix_of_warp(x);
+                const uint32_t l = __ffs(__ballot_sync(~0u, left >= upto - x && left < upto)) - 1u;
+                left -= __shfl_sync(~0u, upto - x, l);
+                from += l * each;
+                n = min(each, n - l * each);
+            }
+            x = lane < n ? units_of_prob(rest(from + lane)) : 0ull;
+            upto = prefix_of_warp(x);
+            if (left >= upto - x && left < upto) a.next[request] = (int32_t)(r.e0 + from + lane);
         }
     }
     if (rank == 0) {
@@ -505,25 +575,25 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (n_requests == 0) return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? SKV_OK : SKV_ERR_CUDA;
     VerifyArgs a{probs, draft_probs, probs_stride, draft_stride, vocab, distinct, n_rows, n_requests, cu_new, tokens, parents, uniform,
-                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 32768u && n_requests < kNodes * 4u, 0u, 0u, 0u};
+                 slots, ctx_len, accepted, rows, kept, ctx_out, next, status, n_rows <= 32768u && n_requests < kNodes * 4u, 0u, 0u, 0u, 0u};
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     uint32_t sms = 0;
     if (!device_sms(&sms)) return SKV_ERR_CUDA;
-    // CTAs to a request, up to 16 of 2,048 elements or more: as many as find a place at once (seven to four SMs), and with draft
-    // probabilities as many as hold their parts of both rows. 24 requests with 30 nodes and 50,257 tokens take 16.7 us with 8
-    // to each, 30.3 with 4 and 24.0 with 16; 64 with 151,936 tokens, which 16 CTAs hold, 70 with 16 and 81 with 4. Without
-    // draft probabilities a row is read once: 64 of those take 20.3 with 4 and 38 with 16.
+    // CTAs to a request, up to 16 of 2,048 elements or more: as many as about find a place at once, two to an SM. More of them hold more of
+    // the rows and have less to add up, but what waits for a place waits for whole requests. 64 requests of up to 60 nodes and
+    // 151,936 tokens take 61 us with 4 to each, 70 with 8 and 82 with 16; 12 of 30 nodes 34 with 4, 24 with 8 and 19 with 16; 40 with
+    // 8 33 and with 4 36. Without draft probabilities a row is read once, and fewer do: 40 requests 16 with 4 and 20 with 8.
     const uint32_t sides = draft_probs ? 2u : 1u, fits = kRowBytes / (sides * size) - 32u / size - 16u;
     const uint32_t room = fits < 32u * kVerifyThreads ? fits : 32u * kVerifyThreads;      // a run of 1,024 per warp at most
     uint32_t cluster = 1;
     while (cluster < kVerifyCluster && cluster * 2048u < vocab &&
-           (8ull * cluster * n_requests <= 7ull * sms || (draft_probs && cluster * room < vocab)))
+           (8ull * cluster * n_requests <= (draft_probs ? 9ull : 7ull) * sms || cluster * kMostPart < vocab))
         cluster *= 2u;
     a.per_cta = (vocab + cluster - 1u) / cluster;
-    const uint32_t chunks = (a.per_cta + room - 1u) / room;
-    a.per_chunk = ((a.per_cta + chunks - 1u) / chunks + 15u) & ~15u;
-    a.per_warp = (a.per_chunk + kVerifyThreads - 1u) / kVerifyThreads * 32u;
-    const uint32_t bytes = sides * (a.per_chunk * size + 32u);
+    a.per_held = ((a.per_cta < room ? a.per_cta : room) + 15u) & ~15u;
+    a.per_warp = (a.per_held + kVerifyThreads - 1u) / kVerifyThreads * 32u;
+    a.per_warp_far = draft_probs && a.per_cta > a.per_held ? (a.per_cta - a.per_held + kVerifyThreads - 1u) / kVerifyThreads * 32u : 0u;
+    const uint32_t bytes = sides * (a.per_held * size + 32u);
     bool ok;
     if (dtype == SKV_PROB_F32) ok = draft_probs ? launch_verify<float, true>(a, cluster, bytes, st) : launch_verify<float, false>(a, cluster, bytes, st);
     else ok = draft_probs ? launch_verify<uint16_t, true>(a, cluster, bytes, st) : launch_verify<uint16_t, false>(a, cluster, bytes, st);
