@@ -9,8 +9,8 @@
 // Rows come by asynchronous copies into shared memory, all that it holds of a CTA's part on its way at once: a further sum over
 // the same node, after another rejection, reads only what did not fit.
 //
-// Bound by latency: a chain of 5 nodes over 151,936 tokens takes 7.3 us on the device (launch and end 2.5, then scalars, tests, row, sum,
-// the cluster's barrier and the token's search, 0.5 to 1 us each), 24 trees of 27 nodes over 50,257 tokens without draft probabilities 9.7;
+// Bound by latency: a chain of 5 nodes over 151,936 tokens takes 7.1 us on the device (launch and end 2.5, then scalars, tests, row, sum,
+// the cluster's barrier and the token's search, 0.5 to 1 us each), 24 trees of 27 nodes over 50,257 tokens without draft probabilities 9.1;
 // 64 trees of up to 60 nodes over 151,936 tokens 61: a request takes 2.7 sums on average, 6 at most, one after the other, with 4 CTAs to each,
 // whose parts of the two rows (304 KB) fit shared memory by a quarter (HBM would bring the rows in 11.5).
 #include <cooperative_groups.h>
@@ -584,7 +584,7 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     // 151,936 tokens take 61 us with 4 to each, 70 with 8 and 82 with 16; 12 of 30 nodes 34 with 4, 24 with 8 and 19 with 16; 40 with
     // 8 33 and with 4 36. Without draft probabilities a row is read once, and fewer do: 40 requests 16 with 4 and 20 with 8.
     const uint32_t sides = draft_probs ? 2u : 1u, fits = kRowBytes / (sides * size) - 32u / size - 16u;
-    const uint32_t room = fits < 32u * kVerifyThreads ? fits : 32u * kVerifyThreads;      // a run of 1,024 per warp at most
+    const uint32_t room = fits < 32u * kVerifyThreads ? fits : 32u * kVerifyThreads;      // in kPieces pieces a part at most
     uint32_t cluster = 1;
     while (cluster < kVerifyCluster && cluster * 2048u < vocab &&
            (8ull * cluster * n_requests <= (draft_probs ? 9ull : 7ull) * sms || cluster * kMostPart < vocab))
