@@ -11,8 +11,8 @@
 //
 // Bound by latency: a chain of 5 nodes over 151,936 tokens takes 7.1 us on the device (launch and end 2.5, then scalars, tests, row, sum,
 // the cluster's barrier and the token's search, 0.5 to 1 us each), 24 trees of 27 nodes over 50,257 tokens without draft probabilities 9.1;
-// 64 trees of up to 60 nodes over 151,936 tokens 61: a request takes 2.7 sums on average, 6 at most, one after the other, with 4 CTAs to each,
-// whose parts of the two rows (304 KB) fit shared memory by a quarter (HBM would bring the rows in 11.5).
+// 64 trees of up to 60 nodes over 151,936 tokens 57: a request takes 2.7 sums on average, 6 at most, one after the other, with 8 CTAs to each,
+// whose parts of the two rows (152 KB) fit shared memory by a third (HBM would bring the rows in 11.5).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -26,12 +26,18 @@ namespace cg = cooperative_groups;
 
 bool raise_smem(const void *kernel, uint32_t bytes, std::atomic<uint64_t> &ready);      // skv_attend.cu
 
-constexpr uint32_t kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32u;
 constexpr uint32_t kNodes = 256;                 // nodes of a request that are gathered at once
 constexpr uint32_t kGone = 4096;                 // nodes of a request without draft probabilities
 constexpr uint32_t kVerifyCluster = 16;
-constexpr uint32_t kMostPart = 16384u * kVerifyWarps, kPieces = kMostPart / (32u * kVerifyThreads);      // of a CTA's part: 512 numbers to a lane at most
-constexpr uint32_t kRowBytes = 80u * 1024u;      // shared memory for rows: two CTAs to an SM
+// Threads of a CTA, 1,024 of an SM's: many requests with draft probabilities wait for the sums of the longest chains, and those
+// end sooner on more SMs (64 requests of 30 nodes over 151,936 tokens: 38 us with 256, 46 with 512); without draft
+// probabilities more of the only row is under way in larger ones (40 requests over 151,936 tokens: 16 us with 512, 18 with 256).
+template <bool DRAFT>
+constexpr uint32_t kThreads = DRAFT ? 256u : 512u;
+template <bool DRAFT>
+constexpr uint32_t kRowBytes = (DRAFT ? 46u : 80u) * 1024u;      // shared memory for rows
+constexpr uint32_t kPieces = 16;                 // of a CTA's part without draft probabilities
+constexpr uint32_t most_part(uint32_t threads) { return 512u * threads; }      // elements: 512 to a lane
 
 struct VerifyArgs {
     const void *probs, *draft;
@@ -63,7 +69,7 @@ __device__ __forceinline__ void fetch_run(T *dst, const T *row, uint32_t vocab, 
     constexpr uint32_t V = 16u / sizeof(T);
     const uint32_t at = place_in_unit(row + e0), units = m ? (at + m + V - 1u) / V : 0u;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
-    for (uint32_t i = threadIdx.x; i < units; i += kVerifyThreads) {
+    for (uint32_t i = threadIdx.x; i < units; i += blockDim.x) {
         const int32_t e = (int32_t)(e0 + i * V) - (int32_t)at;
         if (e >= 0 && (uint32_t)e + V <= vocab) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * i), "l"(row + e) : "memory");
@@ -171,7 +177,8 @@ __device__ __forceinline__ bool below(float u, double Z, float r) {
 }
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads<DRAFT>, 1024u / kThreads<DRAFT>) verify_kernel(const VerifyArgs a) {
+    constexpr uint32_t kVerifyThreads = kThreads<DRAFT>, kVerifyWarps = kVerifyThreads / 32u;
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t request = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -534,11 +541,11 @@ template <typename T, bool DRAFT>
 static bool launch_verify(const VerifyArgs &a, uint32_t cluster, uint32_t bytes, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0}, large{0};
     if (!allow_cluster(reinterpret_cast<const void *>(verify_kernel<T, DRAFT>), ready) ||
-        !raise_smem(reinterpret_cast<const void *>(verify_kernel<T, DRAFT>), kRowBytes, large))
+        !raise_smem(reinterpret_cast<const void *>(verify_kernel<T, DRAFT>), kRowBytes<DRAFT>, large))
         return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.n_requests + a.checked) * cluster);
-    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.blockDim = dim3(kThreads<DRAFT>);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -579,20 +586,22 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     uint32_t sms = 0;
     if (!device_sms(&sms)) return SKV_ERR_CUDA;
-    // CTAs to a request, up to 16 of 2,048 elements or more: as many as about find a place at once, two to an SM. More of them hold more of
-    // the rows and have less to add up, but what waits for a place waits for whole requests. 64 requests of up to 60 nodes and
-    // 151,936 tokens take 61 us with 4 to each, 70 with 8 and 82 with 16; 12 of 30 nodes 34 with 4, 24 with 8 and 19 with 16; 40 with
-    // 8 33 and with 4 36. Without draft probabilities a row is read once, and fewer do: 40 requests 16 with 4 and 20 with 8.
-    const uint32_t sides = draft_probs ? 2u : 1u, fits = kRowBytes / (sides * size) - 32u / size - 16u;
-    const uint32_t room = fits < 32u * kVerifyThreads ? fits : 32u * kVerifyThreads;      // in kPieces pieces a part at most
+    // CTAs to a request, up to 16 of 2,048 elements or more: as many as about find a place at once, 1,024 threads to an SM (up to seven
+    // eighths of it, as a cluster's CTAs need places near one another). More of them hold more of the rows and have less to add up, but what waits for a place
+    // waits for whole requests. With draft probabilities 64 requests of up to 60 nodes over 151,936 tokens take 57 us with 8 to
+    // each, 54 with 16, 82 with 4; 64 of 30 nodes over 50,257 tokens 23 with 8, 30 with 16, 27 with 4. Without, 24 requests of 27 nodes over
+    // 50,257 tokens take 9 with 8 and 15 with 16; 40 over 151,936 16 with 4 and 20 with 8.
+    const uint32_t sides = draft_probs ? 2u : 1u, threads = draft_probs ? kThreads<true> : kThreads<false>,
+                   fits = (draft_probs ? kRowBytes<true> : kRowBytes<false>) / (sides * size) - 32u / size - 16u;
+    const uint32_t room = draft_probs || fits < 32u * threads ? fits : 32u * threads;      // (kPieces to a part at most)
     uint32_t cluster = 1;
     while (cluster < kVerifyCluster && cluster * 2048u < vocab &&
-           (8ull * cluster * n_requests <= (draft_probs ? 9ull : 7ull) * sms || cluster * kMostPart < vocab))
+           ((uint64_t)cluster * n_requests * threads <= 448ull * sms || cluster * most_part(threads) < vocab))
         cluster *= 2u;
     a.per_cta = (vocab + cluster - 1u) / cluster;
     a.per_held = ((a.per_cta < room ? a.per_cta : room) + 15u) & ~15u;
-    a.per_warp = (a.per_held + kVerifyThreads - 1u) / kVerifyThreads * 32u;
-    a.per_warp_far = draft_probs && a.per_cta > a.per_held ? (a.per_cta - a.per_held + kVerifyThreads - 1u) / kVerifyThreads * 32u : 0u;
+    a.per_warp = (a.per_held + threads - 1u) / threads * 32u;
+    a.per_warp_far = draft_probs && a.per_cta > a.per_held ? (a.per_cta - a.per_held + threads - 1u) / threads * 32u : 0u;
     const uint32_t bytes = sides * (a.per_held * size + 32u);
     bool ok;
     if (dtype == SKV_PROB_F32) ok = draft_probs ? launch_verify<float, true>(a, cluster, bytes, st) : launch_verify<float, false>(a, cluster, bytes, st);
