@@ -151,6 +151,30 @@ def test_the_same_in_any_company(draft):
         assert out["accepted"].tolist() == want[0] * n and out["next_tokens"].tolist() == want[2] * n
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("draft", ["drawn", "best"])
+def test_full_sums_over_the_largest_vocabulary(draft, dtype):
+    """150 requests, the fewest CTAs to each: the longest runs of a warp, of probabilities of one (0.75 left of each behind a
+    rejection), whose sums pass 2^62."""
+    vocab, n = 1 << 19, 150
+    for seed, first in enumerate((0.0, 0.5, 0.999999)):
+        s = made(31 + seed, [2], vocab, dtype, draft, tree=False, pad=0)
+        s["probs"] = torch.ones_like(s["probs"])
+        if draft == "drawn":
+            s["draft"] = torch.full_like(s["probs"], 0.25)
+        if seed:
+            s["probs"][0, int(s["tokens"][1])] = 0           # the only drafted token is rejected
+        s["uniform"] = torch.tensor([first, 0.75])
+        want = plain(s)
+        t = dict(s, probs=s["probs"].cuda().repeat(n, 1), tokens=s["tokens"].repeat(n), uniform=s["uniform"].repeat(n),
+                 cu=list(range(0, 2 * n + 1, 2)), rows=2 * n)
+        if draft == "drawn":
+            t["draft"] = s["draft"].cuda().repeat(n, 1)
+        out, _, _ = call(t)
+        assert out["accepted"].tolist() == want[0] * n and out["next_tokens"].tolist() == want[2] * n
+        assert want[0] == [1 if seed else 2]
+
+
 def test_rows_far_into_a_large_tensor():
     """More than 2^32 probabilities: the last rows of 29,000."""
     rows, vocab = 29000, 151937
