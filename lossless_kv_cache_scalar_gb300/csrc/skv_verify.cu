@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kThreads<DRAFT>, 1024u / kThreads<DRAFT>) veri
     }
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // waited for before the first sum
     bool started = false;
-    const float u0 = node[0].u;
+    // (not from node[0]: the walking warp may be at later nodes, which take its place, before every warp has read it)
+    const float u0 = __saturatef(__ldg(a.uniform + row0));
 
     // A part of the vocabulary per CTA, of which shared memory holds a piece. With draft probabilities the rest is read
     // anew for each sum; without them the only sum passes through shared memory piece by piece. A run per warp
