@@ -777,7 +777,8 @@ int32_t skv_cache_move(const skv_paged *cache, uint32_t n_requests, const int32_
  * Sharing rows may be forked, trimmed and ended again by this call at will. skv_page_map gives the pages of
  * an ended request back whoever else holds them: end requests that may share pages by this call. Tokens
  * that are added to a row fall into no page of another one, as long as its ctx_len does not go back below
- * what it was when its pages were shared.
+ * what it was when its pages were shared, or goes back to a page's border (0 among them) and the row is trimmed to it
+ * first.
  *  n_pages_in, ring   as for skv_page_map; table_out, n_pages_out, ctx_out, free_out and the copies are other
  *                     arrays than the inputs
  *  workspace          device, 16-byte aligned, skv_page_workspace_bytes(n_requests, pool_pages) bytes; any content

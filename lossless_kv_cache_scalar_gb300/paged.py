@@ -178,7 +178,10 @@ class PageTable(_Status):
 class PagePool(PageTable):
     """A PageTable with its page counts and its ring of free pages: all pages free
     at first, counts swapped by every step. Rows that share pages (fork) give them back when the last of
-    them has ended."""
+    them has ended. A row's ctx_len may go back to any page's border (to 0: its request has ended and
+    another one takes the row), but not into the middle of a page that it shares: its new tokens would be
+    written over the other rows'. Of a pool that shares pages a step keeps no more of a row's pages
+    than its ctx_len tokens need."""
 
     def __init__(self, n_requests: int, max_pages: int, page_tokens: int, pool_pages: int, device="cuda"):
         super().__init__(torch.full((n_requests, max_pages), -1, dtype=torch.int32, device=device), page_tokens,
@@ -198,8 +201,9 @@ class PagePool(PageTable):
         if _capturing(stream):
             raise ValueError("PagePool.step swaps its counts on the host; capture map_into")
         if self._shared:
-            # a page of an ended request may be another one's: the map would give it back all the same
-            self.fork(None, ctx_len, check=check, stream=stream)
+            # A page of an ended request may be another one's: the map would give it back all the same. And a row
+            # that goes back, or starts again, would get its new tokens on pages that it shares: trimmed, it gives those up.
+            self.fork(None, ctx_len, trim=True, check=check, stream=stream)
         cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
         slots = torch.empty(max_new, dtype=torch.int64, device=dev)
         _after_current(stream)

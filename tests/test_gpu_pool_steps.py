@@ -1,0 +1,64 @@
+"""PagePool.step where rows share pages: rows that go back or are admitted anew, errors, and pools that
+share nothing any more."""
+import pytest
+import torch
+
+from lossless_kv_cache_scalar_gb300 import PagePool
+
+pytestmark = pytest.mark.gpu
+
+PAGE = 4
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+def rows_of(pool):
+    return [row[:h] for row, h in zip(pool.block_table.tolist(), pool.n_pages.tolist())]
+
+
+def ring_of(pool):
+    head, count = pool.free_state.tolist()
+    ring = pool.free_pages.tolist()
+    return [ring[(head + i) % len(ring)] for i in range(count)]
+
+
+def audit(pool):
+    """Every page of the pool is held or on the ring, once."""
+    held = {p for row in rows_of(pool) for p in row}
+    assert sorted(ring_of(pool) + sorted(held)) == list(range(pool.pool_pages))
+
+
+def shared_pool(tokens=10, rows=3, pages=24):
+    """`rows` rows of `tokens` tokens that share the first row's full pages, and an idle row."""
+    pool = PagePool(rows + 1, 8, PAGE, pages)
+    pool.step(i32([0] + [-1] * rows), i32([tokens] + [0] * rows), tokens)
+    pool.fork(i32([0] * rows + [-1]), i32([tokens] + [-1] * rows))
+    audit(pool)
+    return pool
+
+
+@pytest.mark.parametrize("back", [0, 4])
+@pytest.mark.parametrize("check", [True, False])
+def test_a_row_that_starts_again_leaves_the_shared_pages_alone(back, check):
+    """A row that ends and is admitted anew in one step, or goes back to a page's border: its new tokens fall into
+    pages that are its own."""
+    pool = shared_pool()
+    before = rows_of(pool)
+    cu, slots = pool.step(i32([back, 10, 10, -1]), i32([9, 1, 1, 0]), 11, check=check)
+    pool.check_status("step")
+    after, cu, slots = rows_of(pool), cu.tolist(), slots.tolist()
+    audit(pool)
+    assert after[1] == before[1] and after[2] == before[2]
+    for r in range(3):
+        for at in slots[cu[r]:cu[r + 1]]:
+            assert at // PAGE in after[r] and not any(at // PAGE in after[s] for s in range(4) if s != r), (r, at)
+    assert after[0][:back // PAGE] == before[0][:back // PAGE]
+
+
+def test_an_idle_row_is_admitted_beside_shared_ones():
+    pool = shared_pool()
+    pool.step(i32([-1, 10, 10, 0]), i32([0, 3, 0, 17]), 32)
+    audit(pool)
+    assert [len(r) for r in rows_of(pool)] == [0, 4, 3, 5]
