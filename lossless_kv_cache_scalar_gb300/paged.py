@@ -83,6 +83,8 @@ class PageTable(_Status):
     pages of `page_tokens` tokens, kept on the GPU (skv_page_map). workspace=True makes the
     workspace of fork and compact (a first call makes it otherwise, which a capture cannot)."""
 
+    _ended = False      # whether the last call was a step in two parts (PagePool)
+
     def __init__(self, block_table: torch.Tensor, page_tokens: int, pool_pages: int, workspace: bool = False):
         self._stride = _table_rows(block_table)
         self.block_table, self._table = block_table, block_table.data_ptr()
@@ -135,6 +137,7 @@ class PageTable(_Status):
                                   free_pages.data_ptr(), size, free_state.data_ptr(), free_state_out.data_ptr(),
                                   cu_new.data_ptr(), slots.data_ptr(), room, self._status, _stream_of(stream, self._device))
         B.check("skv_page_map", rc)
+        self._ended = False
 
     def fork_into(self, parents, ctx_len, n_pages, free_pages, free_state, table_out, n_pages_out, ctx_out, free_state_out,
                   copy_src, copy_dst, copy_tokens, trim: bool = False, stream=None):
@@ -157,6 +160,7 @@ class PageTable(_Status):
                                    copy_src.data_ptr(), copy_dst.data_ptr(), copy_tokens.data_ptr(), self._status, self._workspace,
                                    self._workspace_bytes, _stream_of(stream, dev))
         B.check("skv_page_fork", rc)
+        self._ended = False
 
     def compact_into(self, n_pages, free_pages, free_state, table_out, free_state_out, copy_src, copy_dst, stream=None):
         """Enqueue skv_page_compact: the held pages move to the front of the pool; table_out has their new
@@ -173,6 +177,7 @@ class PageTable(_Status):
                                       free_state_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), room, self._status,
                                       self._workspace, self._workspace_bytes, _stream_of(stream, dev))
         B.check("skv_page_compact", rc)
+        self._ended = False
 
 
 class PagePool(PageTable):
@@ -190,34 +195,60 @@ class PagePool(PageTable):
         self.free_pages = torch.arange(pool_pages, dtype=torch.int32, device=device)
         self.free_state = torch.tensor([0, pool_pages], dtype=torch.int32, device=device)
         self._next = (torch.empty_like(self.n_pages), torch.empty_like(self.free_state))
-        self._shared = False
+        self._shared, self._mid = False, None
+        self._ends = PageTable(self.block_table, page_tokens, pool_pages)      # what ends rows in a step, with a status of its own
         self._settle()
 
     def step(self, ctx_len, new_len, max_new: int, check: bool = True, stream=None):
         """Map one step's new tokens (max_new: room for so many slots). Returns
         (cu_new, slots), slots past the step's tokens -1. Not for a capture, whose replays would
-        all start from the same counts: capture map_into, and copy its counts back behind it."""
+        all start from the same counts: capture map_into, and copy its counts back behind it. A step
+        that is refused leaves everything as it was; with check=False, where rows share pages, rows that ended
+        have given theirs back all the same."""
         dev = self.block_table.device
         if _capturing(stream):
             raise ValueError("PagePool.step swaps its counts on the host; capture map_into")
-        if self._shared:
-            # A page of an ended request may be another one's: the map would give it back all the same. And a row
-            # that goes back, or starts again, would get its new tokens on pages that it shares: trimmed, it gives those up.
-            self.fork(None, ctx_len, trim=True, check=check, stream=stream)
         cu = torch.empty(self.n_requests + 1, dtype=torch.int32, device=dev)
         slots = torch.empty(max_new, dtype=torch.int64, device=dev)
+        counts = (self.n_pages, self.free_state)
+        if self._shared:
+            counts = self._end(ctx_len, stream)
         _after_current(stream)
-        self.map_into(ctx_len, new_len, self.n_pages, self.free_pages, self.free_state, cu, slots, *self._next,
-                      stream=stream)
-        now = (self.n_pages, self.free_state)
-        self.n_pages, self.free_state = self._next
-        self._next = now
+        self.map_into(ctx_len, new_len, counts[0], self.free_pages, counts[1], cu, slots, *self._next, stream=stream)
+        self._ended = self._shared
+        before, (self.n_pages, self.free_state) = (self.n_pages, self.free_state), self._next
+        self._next = before
         if check:
-            self.check_status("skv_page_map", stream)
+            try:
+                self.check_status("skv_page_map", stream)
+            except B.SKVError as e:
+                if e.name != "CORRUPT":                  # nothing was mapped, and nothing has ended
+                    self._next, (self.n_pages, self.free_state) = (self.n_pages, self.free_state), before
+                raise
         elif stream is not None:                         # given up early, they are not handed out early
             cu.record_stream(stream)
             slots.record_stream(stream)
         return cu, slots
+
+    def _end(self, ctx_len, stream):
+        """The page counts and the ring state of a step's rows without those that have ended, for its map. A page of
+        an ended request may be another one's: the map would give it back all the same. And a row that goes
+        back, or starts again, would get its new tokens on pages that it shares: trimmed, it gives those
+        up. (Every row is its own heir: entries of the table stay where they are, and of the ring those behind
+        its end are written.)"""
+        if self._mid is None:
+            words = torch.empty((5, self.n_requests), dtype=torch.int32, device=self.block_table.device)
+            self._mid = (torch.empty_like(self.block_table), *words.unbind(), torch.empty_like(self.free_state))
+        _after_current(stream)
+        table, n_pages, ctx_out, src, dst, tokens, state = self._mid
+        self._ends.fork_into(None, ctx_len, self.n_pages, self.free_pages, self.free_state, table, n_pages, ctx_out, state, src, dst, tokens,
+                             trim=True, stream=stream)
+        return n_pages, state
+
+    def check_status(self, where: str, stream=None):
+        super().check_status(where, stream)
+        if self._ended:                                  # the last call was a step in two parts
+            self._ends.check_status("skv_page_fork", stream)
 
     def fork(self, parents, ctx_len, trim: bool = False, check: bool = True, stream=None):
         """Row s goes on from row parents[s] (None: from itself; -1 or ctx_len < 0: it ends) and shares its

@@ -3,7 +3,7 @@ share nothing any more."""
 import pytest
 import torch
 
-from lossless_kv_cache_scalar_gb300 import PagePool
+from lossless_kv_cache_scalar_gb300 import PagePool, SKVError
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,59 @@ def test_an_idle_row_is_admitted_beside_shared_ones():
     pool.step(i32([-1, 10, 10, 0]), i32([0, 3, 0, 17]), 32)
     audit(pool)
     assert [len(r) for r in rows_of(pool)] == [0, 4, 3, 5]
+
+
+def state(pool):
+    return rows_of(pool), pool.n_pages.tolist(), pool.free_state.tolist(), ring_of(pool)
+
+
+@pytest.mark.parametrize("ctx,new,room,error", [([-1, 10, 10, -1], [0, 1, 1, 2], 8, "INVALID_ARG"), ([10, -1, 13, -1], [0, 0, 1, 0], 8, "INVALID_ARG"),
+                                                ([-1, 8, 10, 0], [0, 1, 1, 99], 101, "CAPACITY"), ([-1, 8, -1, 0], [0, 20, 0, 9], 29, "CAPACITY")])
+def test_a_refused_step_leaves_a_shared_pool_as_it_was(ctx, new, room, error):
+    pool = shared_pool(pages=9)
+    before = state(pool)
+    for _ in range(2):
+        with pytest.raises(SKVError, match=error):
+            pool.step(i32(ctx), i32(new), room)
+        assert state(pool) == before
+    pool.step(i32([-1, 10, 10, -1]), i32([0, 1, 3, 0]), 4)
+    audit(pool)
+    assert [len(r) for r in rows_of(pool)] == [0, 3, 4, 0]
+
+
+@pytest.mark.parametrize("check", [True, False])
+def test_a_bad_page_that_only_the_shared_rows_show(check):
+    """A page number outside the pool in a row without new tokens, before its last page: nothing but the walk over the shared
+    rows comes past it."""
+    pool = shared_pool()
+    good = int(pool.block_table[2, 0])
+    pool.block_table[2, 0] = 99
+    ctx, new = i32([10, 10, 10, -1]), i32([1, 0, 0, 0])
+    if check:
+        with pytest.raises(SKVError, match="CORRUPT"):
+            pool.step(ctx, new, 4)
+    else:
+        pool.step(ctx, new, 4, check=False)
+        with pytest.raises(SKVError, match="CORRUPT"):
+            pool.check_status("step")
+    pool.block_table[2, 0] = good
+    pool.step(i32([11, 10, 10, -1]), i32([1, 0, 0, 0]), 4)
+    pool.check_status("step")
+    pool.compact()
+    audit(pool)
+
+
+@pytest.mark.parametrize("check", [True, False])
+def test_a_step_on_another_stream(check):
+    pool, side = shared_pool(), torch.cuda.Stream()
+    ctx, new = i32([-1, 10, 0, -1]), i32([0, 1, 9, 0])
+    torch.cuda.synchronize()
+    for _ in range(2):
+        torch.cuda._sleep(100_000_000)
+        cu, slots = pool.step(ctx, new, 10, check=check, stream=side)
+        torch.cuda.synchronize()
+        pool.check_status("step", side)
+        audit(pool)
+        assert cu.tolist() == [0, 0, 1, 10, 10] and [len(r) for r in rows_of(pool)] == [0, 3, 3, 0]
+        held = rows_of(pool)
+        assert [at // PAGE for at in slots.tolist()] == [held[1][2]] + [held[2][i // PAGE] for i in range(9)]
