@@ -186,7 +186,8 @@ class PagePool(PageTable):
     them has ended. A row's ctx_len may go back to any page's border (to 0: its request has ended and
     another one takes the row), but not into the middle of a page that it shares: its new tokens would be
     written over the other rows'. Of a pool that shares pages a step keeps no more of a row's pages
-    than its ctx_len tokens need."""
+    than its ctx_len tokens need, and takes a second launch; every 16th one that is checked looks whether pages are shared
+    still."""
 
     def __init__(self, n_requests: int, max_pages: int, page_tokens: int, pool_pages: int, device="cuda"):
         super().__init__(torch.full((n_requests, max_pages), -1, dtype=torch.int32, device=device), page_tokens,
@@ -195,7 +196,7 @@ class PagePool(PageTable):
         self.free_pages = torch.arange(pool_pages, dtype=torch.int32, device=device)
         self.free_state = torch.tensor([0, pool_pages], dtype=torch.int32, device=device)
         self._next = (torch.empty_like(self.n_pages), torch.empty_like(self.free_state))
-        self._shared, self._mid = False, None
+        self._shared, self._steps, self._mid = False, 0, None
         self._ends = PageTable(self.block_table, page_tokens, pool_pages)      # what ends rows in a step, with a status of its own
         self._settle()
 
@@ -225,6 +226,10 @@ class PagePool(PageTable):
                 if e.name != "CORRUPT":                  # nothing was mapped, and nothing has ended
                     self._next, (self.n_pages, self.free_state) = (self.n_pages, self.free_state), before
                 raise
+            if self._shared:
+                self._steps += 1
+                if self._steps % 16 == 0:
+                    self._shared = self._sharing(stream)
         elif stream is not None:                         # given up early, they are not handed out early
             cu.record_stream(stream)
             slots.record_stream(stream)
@@ -245,6 +250,15 @@ class PagePool(PageTable):
                              trim=True, stream=stream)
         return n_pages, state
 
+    def _sharing(self, stream):
+        """Whether rows share a page: they have more entries than there are different pages in them (a compaction whose
+        results are dropped counts those)."""
+        with torch.cuda.stream(stream):
+            ring, src, dst = torch.empty((3, self.pool_pages), dtype=torch.int32, device=self.block_table.device).unbind()
+            state = torch.empty_like(self.free_state)
+            self._ends.compact_into(self.n_pages, ring, self.free_state, self._mid[0], state, src, dst)
+            return int(self.n_pages.sum() + state[1]) != self.pool_pages
+
     def check_status(self, where: str, stream=None):
         super().check_status(where, stream)
         if self._ended:                                  # the last call was a step in two parts
@@ -262,7 +276,8 @@ class PagePool(PageTable):
         self.fork_into(parents, ctx_len, self.n_pages, self.free_pages, self.free_state, table, self._next[0], ctx, self._next[1], src, dst,
                        tokens, trim=trim, stream=stream)
         self._take(table, self._next[0], stream)
-        self._shared = True
+        if parents is not None:
+            self._shared, self._steps = True, 0
         if check:
             self.check_status("skv_page_fork", stream)
         elif stream is not None:                         # given up early, they are not handed out early

@@ -118,3 +118,41 @@ def test_a_step_on_another_stream(check):
         assert cu.tolist() == [0, 0, 1, 10, 10] and [len(r) for r in rows_of(pool)] == [0, 3, 3, 0]
         held = rows_of(pool)
         assert [at // PAGE for at in slots.tolist()] == [held[1][2]] + [held[2][i // PAGE] for i in range(9)]
+
+
+def test_a_pool_that_shares_nothing_any_more_ends_its_rows_in_one_launch():
+    """Launches of a step are those of a pool that was never forked, some steps after the last sharing row has ended; while
+    rows share pages they stay two."""
+    pool = shared_pool()
+    two = []
+
+    class Ends:
+        def __init__(self, ends):
+            self.ends = ends
+
+        def __getattr__(self, name):
+            if name == "fork_into":
+                two.append(1)
+            return getattr(self.ends, name)
+
+    pool._ends = Ends(pool._ends)
+    length = 10
+    for step in range(40):                                 # two rows share pages
+        pool.step(i32([length, length, -1, -1]), i32([step % 2, step % 2, 0, 0]), 2)
+        length += step % 2
+    assert len(two) == 40
+    for step in range(40):                                 # one row's pages are its own
+        pool.step(i32([length, -1, -1, -1]), i32([0, 0, 0, 0]), 2)
+    assert 40 < len(two) <= 40 + 16
+    audit(pool)
+    pool.step(i32([-1, 0, -1, -1]), i32([0, 9, 0, 0]), 9)
+    audit(pool)
+    assert [len(r) for r in rows_of(pool)] == [0, 3, 0, 0]
+    pool.fork(None, i32([-1, 9, -1, -1]))                  # nobody shares: still one launch
+    n = len(two)
+    pool.step(i32([-1, 9, -1, -1]), i32([0, 9, 0, 0]), 9)
+    assert len(two) == n
+    pool.fork(i32([1, 1, -1, -1]), i32([-1, 18, -1, -1]))
+    pool.step(i32([-1, 18, -1, -1]), i32([0, 9, 0, 0]), 9)
+    assert len(two) == n + 1
+    audit(pool)
