@@ -404,7 +404,8 @@ class PagedKV(_Status):
     def rotate_append_into(self, rotary, q, k, v, positions, slots, q_out, stream=None):
         """Enqueue skv_rotate_append: the heads of q and k normalised and rotated (`rotary`, a Rotary),
         q into q_out (contiguous, of q's shape; None with q None: no queries), k and v into the slots as
-        append_into writes them. positions: int32 [n], or [n_axes][n]; -1 in slots: queries only."""
+        append_into writes them. positions: int32 [n], or [n_axes][n] (None where nothing is rotated); -1 in
+        slots: queries only."""
         shape, stride, dev = k.shape, k.stride(), self._device
         if v.shape != shape or v.stride() != stride or k.dtype is not _BF16 or v.dtype is not _BF16 or k.get_device() != dev \
                 or v.get_device() != dev or len(shape) != 3 or shape[1:] != self._row_shape or stride[2] != 1:
@@ -425,12 +426,17 @@ class PagedKV(_Status):
             q_ptr, out_ptr, heads, q_row, q_head = q.data_ptr(), q_out.data_ptr(), q_shape[1], q_stride[0], q_stride[1]
         elif q_out is not None:
             raise ValueError("q_out without q")
-        if rotary.n_axes > 1 and positions.shape != (rotary.n_axes, n):
-            raise ValueError(f"positions must be an int32 tensor [{rotary.n_axes}][{n}]")
-        _check_words("positions", _I32, rotary.n_axes * n, dev, positions)
+        at = None
+        if positions is not None:
+            if rotary.n_axes > 1 and positions.shape != (rotary.n_axes, n):
+                raise ValueError(f"positions must be an int32 tensor [{rotary.n_axes}][{n}]")
+            _check_words("positions", _I32, rotary.n_axes * n, dev, positions)
+            at = positions.data_ptr()
+        elif rotary.rot_dim:
+            raise ValueError(f"the Rotary turns {rotary.rot_dim} channels: positions are needed")
         _check_words("slots", _I64, n, dev, slots)
         rc = B.lib().skv_rotate_append(self._ref, rotary._ref, q_ptr, q_row, q_head, heads, k.data_ptr(), v.data_ptr(), stride[0], stride[1],
-                                       positions.data_ptr(), slots.data_ptr(), n, out_ptr, self._status, _stream_of(stream, dev))
+                                       at, slots.data_ptr(), n, out_ptr, self._status, _stream_of(stream, dev))
         B.check("skv_rotate_append", rc)
 
     def rotate_append(self, rotary, q, k, v, positions, slots, stream=None):
