@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
     }
     if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
     if (__syncthreads_or(bad)) {                          // the same in every CTA
+        cluster.sync();                                   // and every CTA has seen it, before anything is written
         hand_on(a, t, SKV_ERR_INVALID_ARG);
         return;
     }
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
     }
     k0 = block_scan<kPlanWarps>(mine[0].copies + mine[1].copies, &took, part);
     if (took > (uint32_t)count) {
+        cluster.sync();
         hand_on(a, t, SKV_ERR_CAPACITY);
         return;
     }
@@ -580,6 +582,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanA
     }
     if (t.rank == 0 && tid == 0) *a.status = SKV_OK;
     if (__syncthreads_or(bad)) {                          // the same in every CTA
+        cluster.sync();                                   // and every CTA has seen it, before anything is written
         hand_on(a, t, SKV_ERR_INVALID_ARG);
         return;
     }
@@ -916,6 +919,9 @@ extern "C" int32_t skv_page_fork(uint32_t page_tokens, uint32_t pool_pages, uint
     if (!aligned(workspace, 16) || ws_bytes < workspace_bytes(n_requests, pool_pages) || free_in == free_out ||
         (n_requests && (block_table == table_out || n_pages_in == n_pages_out || ctx_len == ctx_out)))
         return SKV_ERR_INVALID_ARG;
+    // the lengths written over others than their own are the mistake at hand (every CTA reads them all)
+    for (const int32_t *in : {parents, ctx_len, n_pages_in})
+        if (in && n_requests && (in == n_pages_out || in == ctx_out)) return SKV_ERR_INVALID_ARG;
     PlanArgs a{};
     a.page = fast_div(page_tokens), a.pool_pages = pool_pages, a.n_requests = n_requests, a.max_pages = max_pages;
     a.free_capacity = free_capacity, a.trim = trim, a.capacity = n_requests;
