@@ -5,8 +5,9 @@
 // rows that go on; no count per page is kept between calls that could drift from the tables.
 // Everything comes out in a fixed order: prefix sums over rows and over the words of bits.
 // Pools of up to 32,768 pages keep the bits in shared memory: every CTA marks its share of the rows, reads the
-// others' bits after the one barrier and works the rest out for itself. Larger ones (or more than 1,024 rows) keep them in
-// the workspace, with a barrier of a cluster of 16 (half a microsecond, where a launch costs two) after each step.
+// others' bits after a barrier and works the rest out for itself (a second barrier keeps all CTAs there until
+// everybody has read). Larger ones (or more than 1,024 rows) keep them in the workspace, with a barrier of a
+// cluster of 16 (half a microsecond, where a launch costs two) after each step.
 //
 // On the device 6.0 us for a fork of 8 rows (one CTA), 10.0 for one of 700 rows of 48 pages (a cluster of 8, two barriers), 9.8 for a compaction
 // of 200 rows of 47: latency, some 2.5 us of it the launch and as much the cluster's. In the workspace 17 for a compaction of 200 rows of
@@ -339,7 +340,7 @@ __device__ __forceinline__ uint32_t below(uint32_t i, uint32_t limit) {
     return limit <= first ? 0u : limit - first >= 32u ? ~0u : (1u << (limit - first)) - 1u;
 }
 
-__global__ void __launch_bounds__(kLargeThreads) compact_pages_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kLargeThreads, 1) compact_pages_kernel(const PlanArgs a) {
     __shared__ Told told;
     __shared__ uint32_t part[kLargeWarps];
     cg::cluster_group cluster = cg::this_cluster();
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PlanArgs
     __shared__ uint32_t heir[kSmallRows], from[kSmallRows], keep[kSmallRows], part[kPlanWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, n = a.n_requests;
+    const uint32_t tid = threadIdx.x, n = a.n_requests;
     const int32_t head = __ldg(a.free_in), count = __ldg(a.free_in + 1);
     bool bad = ring_bad(a, head, count), corrupt = false;
 #pragma unroll
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PlanA
     __shared__ int32_t have[kSmallRows];
     cg::cluster_group cluster = cg::this_cluster();
     const Team t{cluster.num_blocks(), cluster.block_rank(), 0u, nullptr};
-    const uint32_t tid = threadIdx.x, lane = tid & 31u;
+    const uint32_t tid = threadIdx.x;
     bits[tid] = bits[kPlanThreads + tid] = 0u;
     bool bad = false, corrupt = false;
     for (uint32_t r = tid; r < a.n_requests; r += kPlanThreads) {
