@@ -986,9 +986,10 @@ extern "C" int32_t skv_cache_copy(const skv_paged *cache, const int32_t *src, co
     CopyArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
                cache->page_tokens, cache->n_pages, n, (uint32_t)((per_page + kCopyUnits - 1) / kCopyUnits), {}, fast_div(cache->n_heads * per_head),
                fast_div(per_head), src, dst, tokens, status, 0u};
-    // One block reports the errors (it writes the status once; clearing it first is a launch of its own, 4 us): beside its copies up to 512
-    // pairs, as all it does up to 65,536, some 15 us beside the others' copies (4,809 pairs 99 us with the launch, 97 so).
-    a.checked = n <= 512u ? 1u : n <= 65536u ? 2u : 0u;
+    // One block reports the errors (it writes the status once; clearing it first is a launch of its own): beside its copies up to 512
+    // pairs, as all it does up to 16,384. Pairs of which none, or half, are copied (pages of 4 KB), with the launch and so: 2,000 pairs 6.3 and 3.4,
+    // 8.3 and 4.8 us; 16,000 6.8 and 5.7, 28.7 and 24.6; but 32,000 7.4 and 7.9, 65,536 8.4 and 12.4 where none is.
+    a.checked = n <= 512u ? 1u : n <= 16384u ? 2u : 0u;
     a.by_chunks = fast_div(a.chunks);
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     const uint64_t items = (uint64_t)n * a.chunks + (a.checked == 2u);
@@ -1013,8 +1014,9 @@ extern "C" int32_t skv_cache_move(const skv_paged *cache, uint32_t n_requests, c
     if ((uint64_t)n_requests * per_request >= 0x7FFFFFFFu) return SKV_ERR_INVALID_ARG;
     MoveArgs a{static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages), c.page_stride, c.token_stride, c.head_stride,
                c.page, fast_div(per_head), (uint64_t)cache->n_pages * cache->page_tokens, n_requests, n_rows, units, threads, per_request, cu_new, rows,
-               slots, kept, status, n_rows <= 65536u && n_requests <= 65536u};
-    // (one block looks through up to 65,536 entries for errors: 256 paths of 60 nodes 7.3 us, 10.2 with a launch that clears the status)
+               slots, kept, status, n_rows <= 16384u && n_requests <= 16384u};
+    // (One block looks through up to 16,384 entries for errors; beyond, a launch clears the status. With the launch and with the
+    // block: 8 requests of 16 nodes 6.3 and 3.9 us, 256 of 60 10.5 and 7.7, 1,000 of 16 6.4 and 6.4, 1,000 of 30 6.8 and 9.8, 1,000 of 60 7.2 and 15.3.)
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     const uint32_t teams = kMoveThreads / threads, blocks = (n_requests * per_request + teams - 1u) / teams;
     move_tokens_kernel<<<blocks + a.checked, kMoveThreads, 0, st>>>(a);
