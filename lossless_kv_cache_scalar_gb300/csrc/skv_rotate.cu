@@ -12,7 +12,7 @@
 // is taken of a reduced angle in [-1/2, 1/2) turns.
 //
 // Bound by HBM, and close behind by issue (some 200 instructions for a warp's 4 heads of 128 channels): 65,536 rows of 32
-// query and 8 KV heads, bf16, 246 us (6.5 TB/s, 0.96 of a copy); 30,000 rows of 40 and 8 into e4m3 134 us (0.87). Blocks
+// query and 8 KV heads, bf16, 244 us (6.6 TB/s, 0.97 of a copy); 30,000 rows of 40 and 8 into e4m3 131 us (0.90). Blocks
 // of 4 warps, 7 to an SM (72 registers): with 6 257 us, with 8 (64 registers, some of them spilled) 253 and 210. The loads of the
 // next step are on their way while a step is worked on; two steps ahead gave nothing.
 #include <cuda_bf16.h>
@@ -294,13 +294,20 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     const PagedView c = paged_view(*cache);
     const uint32_t units = cache->head_dim / 16u;
     const uint32_t lanes = units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : units <= 8 ? 8 : 16;
-    // A row's groups of heads go to two warps (each works the angles out for itself, but the last round over the GPU is
-    // shorter: 7,001 rows 39.1 us, 39.3 with one and 41.0 with three; 4,300 27.7, 30.8 and 27.3; 30,000 138, 136 and 147), with few rows to
-    // more, up to 24 warps per SM (1,000 rows: 7.0 us with three, 7.6 with two, 8.0 with five).
+    // Few rows' groups of heads go to several warps each, up to 24 warps per SM (1,000 rows of 32 query and 8 KV heads of 128 channels, bf16:
+    // 6.5 us with three, 6.8 with two, 8.4 with one). Each works the angles out for itself, which takes as long as some four groups. So
+    // where a warp to a row fills the GPU, two are better only by a shorter last round: the rounds of both are counted. One and two
+    // warps, us: 3,600 rows 13.0, 14.6; 4,300 21.5, 19.0; 6,000 29.2, 27.3; 16,384 65.0, 65.3; 65,536 244.5, 246.2. Into e4m3 from 4,300 on 21.2,
+    // 19.4; 29.1, 27.9; 64.6, 65.7; 235.6, 253.1; with 8 query heads 12.7, 13.4; 15.4, 18.3; 38.8, 44.6; 140.6, 170.0. Counted
+    // wrongly just behind two whole rounds: 8,600 rows 41.6 (taken), 38.2.
     const uint32_t per_step = 32u / lanes, q_steps = (n_q_heads + per_step - 1u) / per_step;
     const uint32_t kv_steps = (cache->n_heads + per_step - 1u) / per_step, groups = q_steps + 2u * kv_steps;
     uint32_t parts = 24u * sms / n;
-    parts = parts < 2u ? 2u : parts;
+    if (parts < 2u) {
+        const uint64_t warps = (kRotateBlocks * sms - 1u) * kRotateWarps;
+        const uint64_t one = (n + warps - 1u) / warps * (groups + 4u), two = (2ull * n + warps - 1u) / warps * ((groups + 1u) / 2u + 4u);
+        parts = two < one ? 2u : 1u;
+    }
     parts = parts > groups ? groups : parts;
     RotateArgs a{};
     a.q = static_cast<const uint16_t *>(q), a.k = static_cast<const uint16_t *>(k), a.v = static_cast<const uint16_t *>(v);
@@ -315,10 +322,10 @@ extern "C" int32_t skv_rotate_append(const skv_paged *cache, const skv_rotary *r
     a.page_stride = c.page_stride, a.token_stride = c.token_stride, a.page_head_stride = c.head_stride;
     a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.page = c.page;
     a.pool_tokens = (uint64_t)cache->n_pages * cache->page_tokens;
-    // Errors are looked for by one block (it writes the status once, where clearing it first is a launch of its own: 2,500 rows 11.6 us, 16.3 with it): up to
-    // 2,048 rows on its way, beyond as all it does, where rows of 4 KB or more take the others ten times as long.
-    const uint64_t row_bytes = (uint64_t)cache->head_dim * (4u * n_q_heads + (c.e4m3 ? 6u : 8u) * cache->n_heads);
-    a.slots = slots, a.status = status, a.checked = n <= kRotateChecked ? 1u : row_bytes >= 4096u ? 2u : 0u;
+    // Errors are looked for by one block (it writes the status once, where clearing it first is a launch of its own): up to 2,048 rows on
+    // its way, up to 65,536 as all it does, beyond by whoever meets them. With the launch and so: 2,049 rows of one head of 16 channels
+    // 6.4 and 3.7 us, 65,536 of them 65.7 and 62.2; 65,536 of 8 + 8 + 8 heads of 64 81.8 and 79.2, but 262,144 312 and 329.
+    a.slots = slots, a.status = status, a.checked = n <= kRotateChecked ? 1u : n <= 65536u ? 2u : 0u;
     if (!a.checked && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return SKV_ERR_CUDA;
     const uint64_t blocks = ((uint64_t)n * parts + kRotateWarps - 1) / kRotateWarps;
     const uint64_t all = blocks + (a.checked == 2u);
