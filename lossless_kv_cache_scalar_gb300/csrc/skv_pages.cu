@@ -9,13 +9,14 @@
 // everybody has read). Larger ones (or more than 1,024 rows) keep them in the workspace, with a barrier of a
 // cluster of 16 (half a microsecond, where a launch costs two) after each step.
 //
-// On the device 6.0 us for a fork of 8 rows (one CTA), 10.0 for one of 700 rows of 48 pages (a cluster of 8, two barriers), 9.8 for a compaction
-// of 200 rows of 47: latency, some 2.5 us of it the launch and as much the cluster's. In the workspace 17 for a compaction of 200 rows of
-// 188 pages in a pool of 63,120, 23 for a fork of 4,000 rows of 189. A warp takes two rows at a time, two pieces of 32 entries of
+// On the device 6.0 us for a fork of 8 rows (one CTA), 10.0 for one of 700 rows, 90 of them live, of up to 48 pages (a cluster of 8, two barriers), 9.8
+// for a compaction of 200 rows of up to 47: latency, some 2.5 us of it the launch and as much the cluster's. In the workspace 16 for a compaction of
+// 200 rows of up to 188 pages in a pool of 63,120, 23 for a fork of 4,000 rows, 600 of them live, of up to 189. A warp takes two rows at a time, two pieces of 32 entries of
 // each on their way; with a warp per row and its lengths looked up anew for each piece these two took 30 and 73.
 //
 // copy and move bring the K and V: 16 bytes per thread and step. Copies are bound by HBM: 2,422 pages of 64 x 8 x 128 codes, K and V, in 99 us
-// (6.4 TB/s, 0.94 of a copy; 97 with the status written by one of the blocks). Moves are five dependent loads: 3 us for 8 paths, 7.3 for 256.
+// (6.4 TB/s, 0.94 of a copy; 97 with the status written by one of the blocks). Moves are five dependent loads: 3.5 us for 8
+// paths of 4; 256 of 13 of 60 nodes take 7.4, 2.6 of them for the block that looks through all entries and 1.9 for the second eight of a path.
 #include <cooperative_groups.h>
 
 #include "skv_rows.cuh"

@@ -9,9 +9,9 @@
 // Rows come by asynchronous copies into shared memory, all that it holds of a CTA's part on its way at once: a further sum over
 // the same node, after another rejection, reads only what did not fit.
 //
-// Bound by latency: a chain of 5 nodes over 151,936 tokens takes 7.1 us on the device (launch and end 2.5, then scalars, tests, row, sum,
-// the cluster's barrier and the token's search, 0.5 to 1 us each), 24 trees of 27 nodes over 50,257 tokens without draft probabilities 9.1;
-// 64 trees of up to 60 nodes over 151,936 tokens 57: a request takes 2.7 sums on average, 6 at most, one after the other, with 8 CTAs to each,
+// Bound by latency: a chain of 5 nodes over 151,936 tokens takes 7.3 us on the device (launch and end 2.5, then scalars, tests, row, sum,
+// the cluster's barrier and the token's search, 0.5 to 1 us each), 24 trees of 27 nodes over 50,257 tokens without draft probabilities 9.4;
+// 64 trees of up to 60 nodes over 151,936 tokens 55: a request takes 2.7 sums on average, 6 at most, one after the other, with 8 CTAs to each,
 // whose parts of the two rows (152 KB) fit shared memory by a third (HBM would bring the rows in 11.5).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -592,7 +592,7 @@ extern "C" int32_t skv_tree_verify(uint32_t dtype, const void *probs, uint64_t p
     if (!device_sms(&sms)) return SKV_ERR_CUDA;
     // CTAs to a request, up to 16 of 2,048 elements or more: as many as about find a place at once, 1,024 threads to an SM (up to seven
     // eighths of it, as a cluster's CTAs need places near one another). More of them hold more of the rows and have less to add up, but what waits for a place
-    // waits for whole requests. With draft probabilities 64 requests of up to 60 nodes over 151,936 tokens take 57 us with 8 to
+    // waits for whole requests. With draft probabilities 64 requests of up to 60 nodes over 151,936 tokens take 55 us with 8 to
     // each, 54 with 16, 82 with 4; 64 of 30 nodes over 50,257 tokens 23 with 8, 30 with 16, 27 with 4. Without, 24 requests of 27 nodes over
     // 50,257 tokens take 9 with 8 and 15 with 16; 40 over 151,936 16 with 4 and 20 with 8.
     const uint32_t sides = draft_probs ? 2u : 1u, threads = draft_probs ? kThreads<true> : kThreads<false>,
